@@ -61,7 +61,8 @@ typedef enum {
     TPS_ERR_UNSUPPORTED_V = 3, /* V is above tps_max_vocab(dtype)                               */
     TPS_ERR_ALIGN = 4,         /* logits, out_probs or a parameter array is not element-aligned */
     TPS_ERR_CUDA = 5,          /* the CUDA runtime refused the launch (see tps_last_cuda_error) */
-    TPS_ERR_SCRATCH = 6        /* tps_sample_noalloc: the call needs more than its fixed scratch   */
+    TPS_ERR_SCRATCH = 6        /* tps_sample_noalloc: the call needs more than its fixed scratch;
+                                  tps_prefix_attention: the workspace given is too small      */
 } tps_status;
 
 /* Per-row outcome written to out_status. */
@@ -296,6 +297,144 @@ int tps_sample_stall_test(const void* logits, int dtype, int64_t B, int64_t V, c
                           const int32_t* top_k, const float* top_p, const float* min_p, const uint64_t* seed,
                           uint64_t step, int32_t* out_token, int32_t* out_status, int64_t stall_chunk,
                           uint64_t wait_ns, void* stream);
+
+/* ------------------------------------------------------------------------------------------------
+ * The decode step in front of the sampler: per-head norm and rotation, a paged key/value cache that
+ * may hold 8-bit codes, and the attention of a batch that shares a long prefix.  Calling convention
+ * as above; the argument structs are read on the host before the call returns.
+ * ---------------------------------------------------------------------------------------------- */
+
+/*
+ * tps_norm_rope -- arguments of tps_qk_norm_rope.  Strides are in elements, the last axis (one
+ * head's D components) is contiguous.
+ *   q, k         [T, n_q_heads, D] and [T, n_k_heads, D] of `dtype` (TPS_F32 / TPS_BF16), e.g. cut out
+ *                of one fused projection.  Either head count may be 0 (its pointers are not used).
+ *   *_ld, *_hd   token and head strides; out_* likewise.  Writing in place (out_q == q with the same
+ *                strides) is allowed; other overlaps are not.
+ *   *_weight     [D] float, or NULL (ones).
+ *   positions    [T] int32.      cos_sin  [n_positions, rot_dim] float: cosines, then sines.
+ *   rot_dim      components that rotate, even, 0 .. D;  interleaved: pairs (2i, 2i+1) rather than
+ *                (i, i + rot_dim/2).
+ *   out_status   [T] int32 or NULL: TPS_ROW_BAD_PARAM for a token whose position lies outside
+ *                [0, n_positions) (its outputs are NaN), else TPS_ROW_OK.
+ */
+typedef struct {
+    const void* q;
+    const void* k;
+    void* out_q;
+    void* out_k;
+    int64_t q_ld, q_hd, k_ld, k_hd;
+    int64_t oq_ld, oq_hd, ok_ld, ok_hd;
+    const float* q_weight;
+    const float* k_weight;
+    const int32_t* positions;
+    const float* cos_sin;
+    int32_t* out_status;
+    int64_t T, n_positions;
+    int32_t n_q_heads, n_k_heads, head_dim, rot_dim, interleaved, dtype;
+    float eps;
+} tps_norm_rope;
+
+/*
+ * tps_qk_norm_rope -- for every token and head: y = x * rsqrt(mean(x^2) + eps) * w over the head's D
+ * components, then the first rot_dim components rotated pair by pair, (a, b) -> (a cos - b sin,
+ * b cos + a sin), at the token's position; float32 throughout, one rounding at the end.
+ * Returns TPS_ERR_ARG (a missing pointer, D < 1 or > 8192, rot_dim odd or outside [0, D], eps negative or
+ * not finite, more than 65535 heads), TPS_ERR_DTYPE, TPS_ERR_ALIGN (not element-aligned), TPS_ERR_CUDA.
+ */
+int tps_qk_norm_rope(const tps_norm_rope* args, void* stream);
+
+/* How the cache holds a (token, head) vector x of D components, a = max |x_i|:
+ *   BF16  as it is (float32 input rounded to nearest-even).
+ *   FP8   codes e4m3(x_i / s) with s = 2^e, e the least integer with a <= 448 * 2^e: the division is
+ *         exact, and a stored value is exact in bfloat16.
+ *   INT8  codes rint(x_i / s), s = a / 127 rounded up to bfloat16.
+ * Both scales are at least 2^-40 and stored as bfloat16; a vector with a NaN or an infinity gets the
+ * scale NaN and codes 0, so that it reads as NaN. */
+typedef enum { TPS_KV_BF16 = 0, TPS_KV_FP8 = 1, TPS_KV_INT8 = 2 } tps_kv_format;
+
+/*
+ * tps_kv_cache -- a paged cache of one layer (caller-owned device memory).
+ *   k, v              [n_pages, n_heads, page_size, head_dim] codes, 16-byte aligned.
+ *   k_scale, v_scale  [n_pages, n_heads, page_size] bfloat16, 4-byte aligned; NULL for TPS_KV_BF16.
+ *   page_size         16, 32, 64, 128 or 256.      head_dim  a multiple of 16, at most 512.
+ *   n_pages           at most 2^31 - 1.            n_heads   1 .. 65535.
+ * Token slot s lives in page s / page_size at row s % page_size.
+ */
+typedef struct {
+    void* k;
+    void* v;
+    void* k_scale;
+    void* v_scale;
+    int64_t n_pages;
+    int32_t n_heads, page_size, head_dim, format;
+} tps_kv_cache;
+
+/*
+ * tps_kv_write -- store T tokens' keys and values.  k, v: [T, n_heads, head_dim] of `dtype`, strides
+ * in elements (*_ld per token, *_hd per head), head_dim contiguous.  slots: [T] int64; a slot outside
+ * [0, n_pages * page_size) is skipped (-1 pads a batch).  Two tokens of one call must not name the same
+ * slot: which one is stored, and whether codes and scale are the same one's, is then not defined.
+ */
+int tps_kv_write(const tps_kv_cache* cache, const void* k, const void* v, int dtype, int64_t T, int64_t k_ld,
+                 int64_t k_hd, int64_t v_ld, int64_t v_hd, const int64_t* slots, void* stream);
+
+/*
+ * tps_kv_read -- the stored values (code * scale in float32, rounded to `dtype`) of T slots:
+ * out_k, out_v [T, n_heads, head_dim] dense, 16-byte aligned.  A slot outside the cache reads as zeros.
+ */
+int tps_kv_read(const tps_kv_cache* cache, const int64_t* slots, int64_t T, void* out_k, void* out_v, int dtype,
+                void* stream);
+
+/*
+ * tps_attention -- arguments of tps_prefix_attention.
+ *   q            [B, Tq, n_q_heads, D] bfloat16, dense, 16-byte aligned; n_q_heads a multiple of the
+ *                cache's n_heads (query head i reads key head i / (n_q_heads / n_heads)).
+ *   out          [B, Tq, n_q_heads, D] bfloat16, dense, 16-byte aligned.
+ *   out_lse      [B, Tq, n_q_heads] float or NULL: ln of the sum of e^{scale q.k} (-inf: no token).
+ *   prefix_pages the pages, in order, of the prefix_len tokens that all sequences share: int32.
+ *   page_table   [B, table_width] int32: the pages of each sequence's own tokens (ld table_ld).
+ *   suffix_len   [B] int32: own tokens of each sequence, its Tq query tokens among them.  Query t sees
+ *                the whole prefix and its first suffix_len - Tq + 1 + t own tokens (none if that is
+ *                not positive).  A query that sees nothing yields 0 and the log-sum -inf.
+ *   scale        of the products q.k.
+ *   out_status   [B] int32 or NULL: TPS_ROW_BAD_PARAM where a page of a token that is seen lies
+ *                outside [0, n_pages) or suffix_len outside [0, table_width * page_size], else TPS_ROW_OK.
+ *                The outputs of queries that such a page or length concerns are NaN.
+ *   workspace    device memory of tps_prefix_attention_workspace bytes, 256-byte aligned, or NULL: taken
+ *                from the library's stream-ordered pool and returned on the call's stream.
+ */
+typedef struct {
+    const void* q;
+    void* out;
+    float* out_lse;
+    const int32_t* prefix_pages;
+    const int32_t* page_table;
+    const int32_t* suffix_len;
+    int32_t* out_status;
+    void* workspace;
+    int64_t workspace_bytes;
+    int64_t B, prefix_len, table_width, table_ld;
+    int32_t q_len, n_q_heads;
+    float scale;
+} tps_attention;
+
+/*
+ * tps_prefix_attention -- softmax attention of B sequences of Tq query tokens each over a prefix they
+ * all share and their own tokens, both held in `cache` (head_dim 64 or 128).  The products with the
+ * shared keys and values are computed once for the whole batch.  Products are accumulated and
+ * softmax statistics held in float32; softmax weights are rounded to 16 bits for the second product
+ * (bfloat16 for TPS_KV_BF16, float16 for 8-bit formats).  No result depends on another sequence's
+ * data, and cache rows past a sequence's length are never used, whatever they hold; a NaN or an infinity
+ * in an own token's VALUE, though, also reaches those of the sequence's queries that causality hides the
+ * token from (0 * NaN in the second product).
+ * Returns TPS_ERR_ARG / _ALIGN / _SCRATCH (workspace too small) / _CUDA.
+ */
+int tps_prefix_attention(const tps_kv_cache* cache, const tps_attention* args, void* stream);
+
+/* Bytes of workspace tps_prefix_attention needs for these arguments on the current device (pointers
+ * are not looked at), or -1 for arguments it would reject.  Host-only query. */
+int64_t tps_prefix_attention_workspace(const tps_kv_cache* cache, const tps_attention* args);
 
 /* Kernels one tps_sample_kernel call with these arguments launches (0 for arguments the call would
  * reject): 1 for the cluster kernel alone; 2 for the streaming kernel (a one-CTA kernel clears its

@@ -14,7 +14,11 @@ import threading
 
 import torch
 
-__all__ = ["build", "load", "sample", "sample_rejection", "apply_penalties", "spec_accept", "TPS_F32", "TPS_BF16", "ROW_STATUS", "library_path", "max_vocab",
+from . import decode
+from .decode import KVCache, kv_read, kv_write, prefix_attention, prefix_attention_workspace, qk_norm_rope
+
+__all__ = ["build", "load", "sample", "sample_rejection", "apply_penalties", "spec_accept", "qk_norm_rope", "KVCache", "kv_write",
+           "kv_read", "prefix_attention", "prefix_attention_workspace", "TPS_F32", "TPS_BF16", "ROW_STATUS", "library_path", "max_vocab",
            "cluster_size", "kernels_per_call", "version"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -23,16 +27,18 @@ _LIB = os.path.join(_HERE, "libtps.so")
 _INCLUDE = os.path.join(os.path.dirname(_HERE), "include")
 # The ABI and launch code, and one translation unit per (kernel, element type): compiled in parallel.
 _SOURCES = ["tps_api.cu", "tps_k_cluster_f32.cu", "tps_k_cluster_bf16.cu", "tps_k_stream_f32.cu",
-            "tps_k_stream_bf16.cu", "tps_k_penalty.cu", "tps_k_spec.cu", "tps_k_reject.cu"]
+            "tps_k_stream_bf16.cu", "tps_k_penalty.cu", "tps_k_spec.cu", "tps_k_reject.cu",
+            "tps_api_decode.cu", "tps_k_norm_rope.cu", "tps_k_kv.cu", "tps_k_attn_rows.cu"]
 _HEADERS = ["tps_device.cuh", "tps_common.cuh", "tps_cluster.cuh", "tps_stream.cuh", "tps_penalty.cuh",
-            "tps_spec.cuh", "tps_reject.cuh", "tps_kernels.h"]
+            "tps_spec.cuh", "tps_reject.cuh", "tps_kernels.h", "tps_decode.h", "tps_norm_rope.cuh", "tps_kv.cuh",
+            "tps_attn_rows.cuh"]
 _NVCC = ["nvcc", "-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
          "-Xcompiler", "-fPIC"]
 
 TPS_F32, TPS_BF16 = 0, 1
 ROW_STATUS = {0: "ok", 1: "nan", 2: "all_masked", 3: "bad_param", 4: "timeout"}
 _ERRORS = {1: "invalid argument", 2: "unknown dtype", 3: "vocabulary too large", 4: "misaligned pointer",
-           5: "CUDA runtime error", 6: "more scratch than the fixed array of tps_sample_noalloc holds"}
+           5: "CUDA runtime error", 6: "more scratch than the fixed array of tps_sample_noalloc holds, or than the workspace given"}
 
 _lock = threading.Lock()
 _lib = None
@@ -101,6 +107,7 @@ def load():
             lib.tps_sample_rejection.argtypes = [P, I32, I64, I64, I64, P, P, P, P, P, U64, P, P, P, P, P, P]
             lib.tps_spec_accept.restype = I32
             lib.tps_spec_accept.argtypes = [P, P, I32, I64, I64, I64, P, P, P, P, P, P, P, P, P, P, U64, P, P, P, P]
+            decode.declare(lib)
             lib.tps_max_vocab.restype = I64
             lib.tps_max_vocab.argtypes = [I32]
             lib.tps_cluster_size.restype = I32

@@ -21,6 +21,7 @@
 
 #include "../../include/tps.h"
 #include "tps_cluster.cuh"
+#include "tps_decode.h"
 #include "tps_kernels.h"
 #include "tps_penalty.cuh"
 #include "tps_reject.cuh"
@@ -500,6 +501,28 @@ int sample_call(const Call& c, ScratchSource src, void* fixed = nullptr, size_t 
 }
 
 }  // namespace
+
+// What the decode-step entry points (tps_api_decode.cu) use of this file.
+namespace tps {
+
+bool host_sms(int* sms)
+{
+    DeviceInfo* d = nullptr;
+    if (!device_info(&d)) return false;
+    *sms = d->sms;
+    return true;
+}
+
+cudaError_t pool_alloc(void** p, size_t bytes, cudaStream_t stream)
+{
+    cudaMemPool_t pool = nullptr;
+    const cudaError_t e = scratch_pool(&pool);
+    return e == cudaSuccess ? cudaMallocFromPoolAsync(p, bytes, pool, stream) : e;
+}
+
+int report_cuda(cudaError_t e) { return fail_cuda(e); }
+
+}  // namespace tps
 
 extern "C" {
 

@@ -1,0 +1,198 @@
+// tps_api_decode.cu -- the C ABI of the decode-step operators declared in include/tps.h: argument
+// checks, the choice of kernels and launch shapes, and the launches.  Like tps_api.cu it never
+// synchronises the host and keeps no state between calls.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/tps.h"
+#include "tps_decode.h"
+
+namespace {
+
+constexpr int kMaxHeads = 65535;
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+int elem_bytes(int dtype) { return dtype == TPS_F32 ? 4 : (dtype == TPS_BF16 ? 2 : 0); }
+
+int check_cache(const tps_kv_cache* c, bool pointers)
+{
+    if (!c) return TPS_ERR_ARG;
+    const int ps = c->page_size;
+    if (c->format < TPS_KV_BF16 || c->format > TPS_KV_INT8) return TPS_ERR_ARG;
+    if (ps < 16 || ps > 256 || (ps & (ps - 1)) != 0) return TPS_ERR_ARG;
+    if (c->head_dim < 16 || c->head_dim > 512 || c->head_dim % 16 != 0) return TPS_ERR_ARG;
+    if (c->n_heads < 1 || c->n_heads > kMaxHeads || c->n_pages < 1 || c->n_pages > INT32_MAX) return TPS_ERR_ARG;
+    if (!pointers) return TPS_OK;
+    if (!c->k || !c->v) return TPS_ERR_ARG;
+    if (c->format != TPS_KV_BF16 && (!c->k_scale || !c->v_scale)) return TPS_ERR_ARG;
+    if (!aligned(c->k, 16) || !aligned(c->v, 16)) return TPS_ERR_ALIGN;
+    if (c->format != TPS_KV_BF16 && (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))) return TPS_ERR_ALIGN;
+    return TPS_OK;
+}
+
+// CTAs of the 16-row prefix kernel per SM, and the tokens of its blocks (one step of its four warps).
+constexpr int kRowsCtasPerSm = 2;
+constexpr int kRowsBlock = 64;
+
+int plan_attention(const tps_kv_cache& c, const tps_attention& a, int sms, tps::AttnPlan* out)
+{
+    tps::AttnPlan p = {};
+    const int G = a.n_q_heads / c.n_heads;
+    const int64_t own_rows = (int64_t)a.q_len * G;
+    if (own_rows > (1 << 24) || a.B > (int64_t(1) << 31) / (own_rows * c.n_heads)) return TPS_ERR_ARG;
+    p.R = a.B * own_rows;
+    p.suffix_tiles = (int)((own_rows + 15) / 16);
+    p.tensor = false;
+    p.tile_rows = 16;
+    p.block_keys = kRowsBlock;
+    p.n_tiles = (int)((p.R + p.tile_rows - 1) / p.tile_rows);
+    p.nblk = (a.prefix_len + p.block_keys - 1) / p.block_keys;
+    p.items = (int64_t)p.n_tiles * c.n_heads;
+    p.units = p.items * p.nblk;
+    p.ctas = std::min<int64_t>(p.units, (int64_t)sms * kRowsCtasPerSm);
+    p.pieces = p.units ? p.ctas + p.items : 0;
+    // Several CTAs share one sequence's own tokens where there are few sequences and many tokens.
+    const int64_t alone = a.B * c.n_heads * p.suffix_tiles;
+    const int64_t tokens = a.table_width * c.page_size;
+    p.cluster = 1;
+    while (p.cluster < 8 && alone * p.cluster < 2 * (int64_t)sms && tokens >= (int64_t)p.cluster * 512) p.cluster *= 2;
+    if (alone * p.cluster > INT32_MAX) return TPS_ERR_ARG;
+    p.off_ml = (size_t)p.pieces * p.tile_rows * c.head_dim * sizeof(float);
+    p.bytes = p.off_ml + (size_t)p.pieces * p.tile_rows * sizeof(float2);
+    *out = p;
+    return TPS_OK;
+}
+
+int check_attention(const tps_kv_cache* c, const tps_attention* a, bool pointers)
+{
+    if (!a) return TPS_ERR_ARG;
+    const int rc = check_cache(c, pointers);
+    if (rc != TPS_OK) return rc;
+    if (c->head_dim != 64 && c->head_dim != 128) return TPS_ERR_ARG;
+    if (a->B < 0 || a->prefix_len < 0 || a->prefix_len > INT32_MAX || a->table_width < 0 || a->table_width > INT32_MAX ||
+        a->table_ld < a->table_width || a->q_len < 1 || a->n_q_heads < 1 || a->n_q_heads % c->n_heads != 0 ||
+        !std::isfinite(a->scale))
+        return TPS_ERR_ARG;
+    if (!pointers || a->B == 0) return TPS_OK;
+    if (!a->q || !a->out || !a->suffix_len || (a->prefix_len > 0 && !a->prefix_pages) || (a->table_width > 0 && !a->page_table))
+        return TPS_ERR_ARG;
+    if (!aligned(a->q, 16) || !aligned(a->out, 16) || !aligned(a->out_lse, 4) || !aligned(a->prefix_pages, 4) ||
+        !aligned(a->page_table, 4) || !aligned(a->suffix_len, 4) || !aligned(a->out_status, 4) || !aligned(a->workspace, 256))
+        return TPS_ERR_ALIGN;
+    return TPS_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int tps_qk_norm_rope(const tps_norm_rope* args, void* stream)
+{
+    if (!args) return TPS_ERR_ARG;
+    const tps_norm_rope& a = *args;
+    const int es = elem_bytes(a.dtype);
+    if (a.T < 0 || a.T > INT32_MAX || a.n_q_heads < 0 || a.n_q_heads > kMaxHeads || a.n_k_heads < 0 || a.n_k_heads > kMaxHeads ||
+        a.head_dim < 1 || a.head_dim > 8192 || a.rot_dim < 0 || a.rot_dim > a.head_dim || a.rot_dim % 2 != 0 ||
+        a.n_positions < 0 || !(a.eps >= 0.f) || std::isinf(a.eps))
+        return TPS_ERR_ARG;
+    if (!es) return TPS_ERR_DTYPE;
+    if (a.T == 0 || a.n_q_heads + a.n_k_heads == 0) return TPS_OK;
+    if ((a.n_q_heads && (!a.q || !a.out_q)) || (a.n_k_heads && (!a.k || !a.out_k)) || !a.positions ||
+        (a.rot_dim && !a.cos_sin))
+        return TPS_ERR_ARG;
+    if ((a.n_q_heads && (!aligned(a.q, es) || !aligned(a.out_q, es))) ||
+        (a.n_k_heads && (!aligned(a.k, es) || !aligned(a.out_k, es))) || !aligned(a.q_weight, 4) || !aligned(a.k_weight, 4) ||
+        !aligned(a.positions, 4) || !aligned(a.cos_sin, 4) || !aligned(a.out_status, 4))
+        return TPS_ERR_ALIGN;
+    int sms = 0;
+    if (!tps::host_sms(&sms)) return tps::report_cuda(cudaGetLastError());
+    const cudaError_t e = tps::launch_norm_rope(a, sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? TPS_OK : tps::report_cuda(e);
+}
+
+int tps_kv_write(const tps_kv_cache* cache, const void* k, const void* v, int dtype, int64_t T, int64_t k_ld, int64_t k_hd,
+                 int64_t v_ld, int64_t v_hd, const int64_t* slots, void* stream)
+{
+    const int rc = check_cache(cache, true);
+    if (rc != TPS_OK) return rc;
+    if (T < 0) return TPS_ERR_ARG;
+    const int es = elem_bytes(dtype);
+    if (!es) return TPS_ERR_DTYPE;
+    if (T == 0) return TPS_OK;
+    if (!k || !v || !slots) return TPS_ERR_ARG;
+    if (!aligned(k, es) || !aligned(v, es) || !aligned(slots, 8)) return TPS_ERR_ALIGN;
+    int sms = 0;
+    if (!tps::host_sms(&sms)) return tps::report_cuda(cudaGetLastError());
+    const tps::KvWriteArgs a{*cache, k, v, T, k_ld, k_hd, v_ld, v_hd, slots};
+    const cudaError_t e = tps::launch_kv_write(a, dtype == TPS_BF16, sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? TPS_OK : tps::report_cuda(e);
+}
+
+int tps_kv_read(const tps_kv_cache* cache, const int64_t* slots, int64_t T, void* out_k, void* out_v, int dtype, void* stream)
+{
+    const int rc = check_cache(cache, true);
+    if (rc != TPS_OK) return rc;
+    if (T < 0) return TPS_ERR_ARG;
+    if (!elem_bytes(dtype)) return TPS_ERR_DTYPE;
+    if (T == 0) return TPS_OK;
+    if (!slots || !out_k || !out_v) return TPS_ERR_ARG;
+    if (!aligned(slots, 8) || !aligned(out_k, 16) || !aligned(out_v, 16)) return TPS_ERR_ALIGN;
+    int sms = 0;
+    if (!tps::host_sms(&sms)) return tps::report_cuda(cudaGetLastError());
+    const tps::KvReadArgs a{*cache, slots, T, out_k, out_v};
+    const cudaError_t e = tps::launch_kv_read(a, dtype == TPS_BF16, sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? TPS_OK : tps::report_cuda(e);
+}
+
+int64_t tps_prefix_attention_workspace(const tps_kv_cache* cache, const tps_attention* args)
+{
+    if (check_attention(cache, args, false) != TPS_OK) return -1;
+    if (args->B == 0) return 0;
+    int sms = 0;
+    tps::AttnPlan p;
+    if (!tps::host_sms(&sms) || plan_attention(*cache, *args, sms, &p) != TPS_OK) return -1;
+    return (int64_t)p.bytes;
+}
+
+int tps_prefix_attention(const tps_kv_cache* cache, const tps_attention* args, void* stream)
+{
+    int rc = check_attention(cache, args, true);
+    if (rc != TPS_OK) return rc;
+    if (args->B == 0) return TPS_OK;
+    int sms = 0;
+    if (!tps::host_sms(&sms)) return tps::report_cuda(cudaGetLastError());
+    tps::AttnArgs a;
+    rc = plan_attention(*cache, *args, sms, &a.p);
+    if (rc != TPS_OK) return rc;
+    a.c = *cache;
+    a.a = *args;
+    a.G = args->n_q_heads / cache->n_heads;
+    a.qk_scale = (float)((double)args->scale * 1.4426950408889634);
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    unsigned char* ws = static_cast<unsigned char*>(args->workspace);
+    cudaError_t e = cudaSuccess;
+    if (a.p.bytes) {
+        if (ws) {
+            if (args->workspace_bytes < (int64_t)a.p.bytes) return TPS_ERR_SCRATCH;
+        } else {
+            void* mem = nullptr;
+            e = tps::pool_alloc(&mem, a.p.bytes, st);
+            if (e != cudaSuccess) return tps::report_cuda(e);
+            ws = static_cast<unsigned char*>(mem);
+        }
+    }
+    a.part = reinterpret_cast<float*>(ws);
+    a.ml = reinterpret_cast<float2*>(ws + a.p.off_ml);
+    if (a.p.units) e = tps::launch_attn_prefix_rows(a, st);
+    if (e == cudaSuccess) e = tps::launch_attn_suffix(a, a.p.units > 0, st);
+    if (a.p.bytes && !args->workspace) {
+        const cudaError_t ef = cudaFreeAsync(ws, st);
+        if (e == cudaSuccess) e = ef;
+    }
+    return e == cudaSuccess ? TPS_OK : tps::report_cuda(e);
+}
+
+}  // extern "C"

@@ -1,0 +1,59 @@
+// The per-head norm and rotation on float32 and bfloat16, and its launch (its own translation unit).
+#include "tps_norm_rope.cuh"
+
+#include <algorithm>
+
+namespace tps {
+
+namespace {
+
+bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+template <typename T, int L>
+cudaError_t launch_units(const tps_norm_rope& a, int threads, cudaStream_t stream)
+{
+    if (a.interleaved)
+        norm_rope_kernel<T, L, true><<<(unsigned)a.T, threads, 0, stream>>>(a);
+    else
+        norm_rope_kernel<T, L, false><<<(unsigned)a.T, threads, 0, stream>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_type(const tps_norm_rope& a, cudaStream_t stream)
+{
+    constexpr int N = Pack<T>::kN;
+    const int H = a.n_q_heads + a.n_k_heads, units = a.head_dim / (2 * N);
+    const int64_t strides = (a.n_q_heads ? a.q_ld | a.q_hd | a.oq_ld | a.oq_hd : 0) |
+                            (a.n_k_heads ? a.k_ld | a.k_hd | a.ok_ld | a.ok_hd : 0);
+    const bool whole = a.head_dim % (2 * N) == 0 && a.rot_dim % (2 * N) == 0 && units <= 32 && strides % N == 0 &&
+                       (!a.n_q_heads || (on16(a.q) && on16(a.out_q))) && (!a.n_k_heads || (on16(a.k) && on16(a.out_k))) &&
+                       on16(a.q_weight) && on16(a.k_weight) && on16(a.cos_sin);
+    if (!whole) {
+        const int threads = 32 * std::min(H, kNormMaxThreads / 32);
+        norm_rope_any_kernel<T><<<(unsigned)a.T, threads, 0, stream>>>(a);
+        return cudaGetLastError();
+    }
+    int L = 1;
+    while (L < units) L *= 2;
+    // As few walks over the heads as 256 threads allow, and no more threads than those walks fill.
+    const int walks = (H * L + kNormMaxThreads - 1) / kNormMaxThreads;
+    const int threads = std::min(kNormMaxThreads, ((H + walks - 1) / walks * L + 31) / 32 * 32);
+    switch (L) {
+    case 1: return launch_units<T, 1>(a, threads, stream);
+    case 2: return launch_units<T, 2>(a, threads, stream);
+    case 4: return launch_units<T, 4>(a, threads, stream);
+    case 8: return launch_units<T, 8>(a, threads, stream);
+    case 16: return launch_units<T, 16>(a, threads, stream);
+    default: return launch_units<T, 32>(a, threads, stream);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_norm_rope(const tps_norm_rope& a, int, cudaStream_t stream)
+{
+    return a.dtype == TPS_BF16 ? launch_type<__nv_bfloat16>(a, stream) : launch_type<float>(a, stream);
+}
+
+}  // namespace tps

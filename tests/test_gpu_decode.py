@@ -1,0 +1,416 @@
+"""The decode-step operators against their plain 64-bit forms, through the C ABI.
+
+Tolerances.  A bfloat16 result is off by at most half a unit, 2^-8 of its magnitude.
+ - Norm and rotation: D float32 terms are summed (relative error up to D 2^-24, halved by the square
+   root) and a handful of operations follow, on components no larger than the head's largest: (D/2 + 16) 2^-24
+   of that.
+ - Cache: codes and scales are exact for bfloat16 input (quotients of two 8-bit significands lie at least 2^-9 of
+   a code away from a rounding boundary unless on it); for float32 input a code may be either neighbour
+   where the quotient lies within 2^-22 of a boundary.
+ - Attention: the weights are rounded to 8 bits (bfloat16) or 11 bits (float16): at most 2^-8 or 2^-11 of
+   sum p |v|; the scores' float32 sums are off by at most 2^-18 of the largest sum of |products|, and base-2
+   exponentials, the joins of parts and weights below 2^-31 of the largest by less than 2^-14.
+"""
+import math
+
+import pytest
+import torch
+
+import nucleus_token_sampler_gb300 as tps
+
+from . import _decode as plain
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA device")]
+
+DEV = "cuda:0"
+
+
+def _gen(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def _table(n, R):
+    f = torch.arange(n, dtype=torch.float64)[:, None] * 10000.0 ** (-torch.arange(R // 2, dtype=torch.float64) / max(1, R // 2))
+    return torch.cat([f.cos(), f.sin()], 1).float().to(DEV)
+
+
+# --------------------------------------------------------------------------------------------- norm
+def _check_norm(got, x, w, pos, table, eps, interleaved):
+    want = plain.norm_rope(x, w, pos, table, eps, interleaved)
+    D = x.shape[-1]
+    # a component is at most sqrt(2) times the largest before the rotation
+    top = want.abs().amax(-1, keepdim=True) * math.sqrt(2)
+    tol = (D / 2 + 16) * 2.0 ** -24 * top + (2.0 ** -8 * want.abs() if x.dtype == torch.bfloat16 else 0)
+    assert got.dtype == x.dtype and got.shape == x.shape
+    assert ((got.double() - want).abs() <= tol).all(), float(((got.double() - want).abs() - tol).max())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,Hq,Hk,D,R,interleaved", [
+    (1, 32, 8, 128, 128, False), (7, 32, 8, 128, 64, True), (130, 28, 4, 96, 96, False), (33, 5, 1, 256, 128, False),
+    (3, 1, 1, 64, 64, True), (9, 3, 2, 80, 80, False), (5, 2, 1, 80, 32, True), (4, 3, 3, 66, 66, False), (6, 2, 2, 7, 4, True),
+    (2, 1, 1, 1, 0, False), (3, 4, 0, 128, 128, False), (3, 0, 4, 128, 128, True), (2, 2, 2, 512, 512, False),
+    (2, 1, 1, 1000, 500, False), (1000, 9, 3, 128, 128, False), (2, 300, 1, 16, 16, False)])
+def test_norm_rope(dtype, T, Hq, Hk, D, R, interleaved):
+    g = _gen(T * 1000 + D)
+    qkv = (3 * torch.randn(T, Hq + 2 * Hk + 1, D, generator=g, device=DEV)).to(dtype)
+    q, k = qkv[:, :Hq], qkv[:, Hq:Hq + Hk]
+    wq, wk = torch.randn(D, generator=g, device=DEV), torch.randn(D, generator=g, device=DEV)
+    table = _table(50, R)
+    pos = torch.randint(0, 50, (T,), generator=g, device=DEV).int()
+    oq, ok = tps.qk_norm_rope(q, k, wq, wk, pos, table, eps=1e-5, interleaved=interleaved)
+    _check_norm(oq, q, wq, pos, table, 1e-5, interleaved)
+    _check_norm(ok, k, wk, pos, table, 1e-5, interleaved)
+
+
+def test_norm_rope_without_weights_unaligned_in_place_and_zero_rows():
+    g = _gen(5)
+    base = torch.randn(11 * 6 * 128 + 3, generator=g, device=DEV).bfloat16()
+    x = base[3:].view(11, 6, 128)  # rows start 6 bytes past a 16-byte boundary
+    x[2, 1] = 0
+    q, k = x[:, :4], x[:, 4:]
+    table, pos = _table(20, 128), torch.arange(11, device=DEV).int()
+    keep = x.clone()
+    a = tps.qk_norm_rope(q, k, None, None, pos, table)
+    _check_norm(a[0], keep[:, :4], None, pos, table, 1e-6, False)
+    assert (a[0][2, 1] == 0).all()
+    b = tps.qk_norm_rope(q, k, None, None, pos, table, out=(q, k))
+    assert b[0] is q and torch.equal(q, a[0]) and torch.equal(k, a[1])
+    # heads ahead of tokens in memory
+    y = torch.randn(6, 11, 128, generator=g, device=DEV).transpose(0, 1)
+    c = tps.qk_norm_rope(y[:, :4], y[:, 4:], None, None, pos, table)
+    _check_norm(c[0], y[:, :4], None, pos, table, 1e-6, False)
+    # the same in place, on the aligned path
+    z = y.contiguous()
+    d = tps.qk_norm_rope(z[:, :4], z[:, 4:], None, None, pos, table, out=(z[:, :4], z[:, 4:]))
+    assert torch.equal(d[0], c[0]) and torch.equal(d[1], c[1])
+
+
+@pytest.mark.parametrize("D", [128, 36])
+def test_norm_rope_positions_outside_the_table_and_values_that_are_not_finite(D):
+    q = torch.randn(5, 2, D, device=DEV)
+    q[3, 0, 5] = math.inf
+    q[4, 1, 0] = math.nan
+    pos = torch.tensor([0, -1, 9, 2, 3], dtype=torch.int32, device=DEV)
+    st = torch.full((5,), 77, dtype=torch.int32, device=DEV)
+    oq, ok = tps.qk_norm_rope(q, q, None, None, pos, _table(9, D), status=st)
+    assert st.tolist() == [0, 3, 3, 0, 0]
+    assert torch.isfinite(oq[0]).all() and oq[1].isnan().all() and oq[2].isnan().all()
+    assert oq[3, 0].isnan().any() and torch.isfinite(oq[3, 1]).all()
+    assert oq[4, 1].isnan().all() and torch.isfinite(oq[4, 0]).all()
+    assert torch.equal(oq.view(torch.int32), ok.view(torch.int32))
+    assert tps.qk_norm_rope(q[:0], q[:0], None, None, pos[:0], _table(9, D))[0].shape == (0, 2, D)
+
+
+# -------------------------------------------------------------------------------------------- cache
+def _vectors(g, T, H, D, dtype):
+    x = torch.randn(T, H, D, generator=g, device=DEV) * torch.exp(2 * torch.randn(T, H, 1, generator=g, device=DEV))
+    x[0, 0] = 0
+    if T > 2:
+        x[1, 0], x[1, 0, D // 2] = 0, 448.0       # the largest code itself
+        x[2, 0], x[2, 0, 0] = 2.0 ** -60, 2.0 ** -50  # below the smallest scale
+    if T > 4:
+        x[3, 0, 1] = 3e38
+        x[4, 0] = torch.arange(D, device=DEV) % 8 + 0.5  # ties
+        x[4, 0, 0] = 127.0
+    return x.to(dtype)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "int8"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,H,D,page", [(1, 1, 16, 16), (5, 8, 128, 64), (77, 3, 96, 16), (130, 2, 256, 128), (9, 1, 512, 256),
+                                        (6, 5, 80, 32), (3000, 4, 64, 32)])
+def test_cache_write_and_read(fmt, dtype, T, H, D, page):
+    g = _gen(T + D)
+    pages = -(-T // page) + 2
+    c = tps.KVCache.empty(pages, H, page, D, fmt, device=DEV)
+    k, v = _vectors(g, T, H, D, dtype), _vectors(g, T, 2 * H, D, dtype)[:, H - 1:2 * H - 1]
+    slots = torch.randperm(pages * page, generator=g, device=DEV)[:T].contiguous()
+    tps.kv_write(c, k, v, slots)
+    for x, code, scale in ((k, c.k, c.k_scale), (v, c.v, c.v_scale)):
+        at = (slots // page, slice(None), slots % page)
+        bits = code.view(torch.int16 if fmt == "bf16" else torch.uint8)[at].view(code.dtype)
+        got = bits.double()
+        if fmt == "bf16":
+            assert torch.equal(got, x.bfloat16().double())
+            continue
+        s = scale[at].double()
+        assert torch.equal(s, plain.scale_of(x, fmt))
+        y = x.double() / s.unsqueeze(-1)
+        want = plain.nearest(y, fmt)
+        if dtype == torch.bfloat16 or fmt == "fp8":
+            assert torch.equal(got, want)
+        else:
+            other = (got != want)
+            assert ((got - want).abs()[other] == 1).all() and ((y - y.floor() - 0.5).abs()[other] <= 127 * 2.0 ** -22).all()
+    for dt in (torch.bfloat16, torch.float32):
+        rk, rv = tps.kv_read(c, slots, dtype=dt)
+        K, V = plain.values(c)
+        at = (slots // page, slice(None), slots % page)
+        assert torch.equal(rk, K[at].float().to(dt)) and torch.equal(rv, V[at].float().to(dt))
+    # nothing else was touched
+    mask = torch.ones(pages * page, dtype=torch.bool, device=DEV)
+    mask[slots] = False
+    rest = mask.nonzero().flatten()
+    rk, rv = tps.kv_read(c, rest)
+    assert (rk == 0).all() and (rv == 0).all()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "int8"])
+def test_cache_padding_slots_unaligned_input_and_values_that_are_not_finite(fmt):
+    g = _gen(3)
+    c = tps.KVCache.empty(3, 2, 16, 64, fmt, device=DEV)
+    base = torch.randn(6 * 2 * 64 + 1, generator=g, device=DEV).bfloat16()
+    k = base[1:].view(6, 2, 64)
+    v = torch.randn(2, 6, 64, generator=g, device=DEV).bfloat16().transpose(0, 1)
+    k[4, 1, 7] = math.nan
+    k[5, 0, 3] = -math.inf
+    slots = torch.tensor([-1, 47, 48, 1 << 40, 5, 0], device=DEV)
+    tps.kv_write(c, k, v, slots)
+    rk, rv = tps.kv_read(c, torch.tensor([47, 5, 0, 48, -5, 3], device=DEV), dtype=torch.float32)
+    assert torch.equal(rk[0].double(), plain.stored(k[1], fmt)) and torch.equal(rv[0].double(), plain.stored(v[1], fmt))
+    assert torch.equal(rv[1].double(), plain.stored(v[4], fmt)) and torch.equal(rk[1, 0].double(), plain.stored(k[4, 0], fmt))
+    assert (rk[3:] == 0).all() and (rv[3:] == 0).all()
+    if fmt == "bf16":
+        assert rk[1, 1].isnan().sum() == 1 and rk[2, 0].isinf().sum() == 1
+    else:  # such a vector reads as NaN as a whole
+        assert rk[1, 1].isnan().all() and rk[2, 0].isnan().all() and torch.isfinite(rk[2, 1]).all()
+    tps.kv_write(c, k[:0], v[:0], slots[:0])
+    assert tps.kv_read(c, slots[:0])[0].shape == (0, 2, 64)
+
+
+def test_cache_past_four_gigabytes():
+    """Rows whose byte offset does not fit 32 bits, written, read and attended to."""
+    pages, H, page, D = 37000, 8, 128, 128  # 4.85 GB of codes each
+    k, v = (torch.empty((pages, H, page, D), dtype=torch.int8, device=DEV) for _ in range(2))
+    ks, vs = (torch.full((pages, H, page), math.nan, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    c = tps.KVCache(k, v, ks, vs)
+    g = _gen(8)
+    T = 300
+    ids = torch.tensor([36999, 2, 35000], device=DEV)
+    slots = ids[torch.arange(T, device=DEV) // page] * page + torch.arange(T, device=DEV) % page
+    x, y = torch.randn(T, H, D, generator=g, device=DEV).bfloat16(), torch.randn(T, H, D, generator=g, device=DEV).bfloat16()
+    tps.kv_write(c, x, y, slots)
+    rk, rv = tps.kv_read(c, slots, dtype=torch.float32)
+    assert torch.equal(rk.double(), plain.stored(x, "int8")) and torch.equal(rv.double(), plain.stored(y, "int8"))
+    q = torch.randn(6, 1, 16, D, generator=g, device=DEV).bfloat16()
+    near = [rk.view(T, H, D), rv.view(T, H, D)]
+    pad = torch.zeros(384 - T, H, D, device=DEV)
+    kv = [torch.cat([t, pad]).view(3, page, H, D).transpose(1, 2).double() for t in near]
+    lens = torch.zeros(6, dtype=torch.int32, device=DEV)
+    own = torch.zeros(6, 1, dtype=torch.int32, device=DEV)
+    _check_attention(tps.prefix_attention(q, c, ids.int(), T, own, lens, want_lse=True), q, kv,
+                     torch.arange(3, device=DEV), T, own, lens, D ** -0.5, "int8")
+    lens[:] = T
+    own = ids.int().expand(6, 3).contiguous()
+    local = torch.arange(3, device=DEV).expand(6, 3)
+    _check_attention(tps.prefix_attention(q, c, ids.int(), 0, own, lens, want_lse=True), q, kv, ids, 0, local, lens, D ** -0.5,
+                     "int8")
+
+
+# ---------------------------------------------------------------------------------------- attention
+def _check_attention(got, q, kv, prefix_pages, prefix_len, page_table, lens, scale, fmt):
+    out, lse = got
+    want, wl, mag, big = plain.attention(q, kv, prefix_pages, prefix_len, page_table, lens, scale)
+    rest = 2.0 ** -18 * big + 2.0 ** -14
+    tol = 2.0 ** -8 * want.abs() + ((2.0 ** -8 if fmt == "bf16" else 2.0 ** -11) + rest).unsqueeze(-1) * mag
+    err = (out.double() - want).abs()
+    assert (err <= tol).all(), (float((err - tol).max()), int((err > tol).sum()), err.numel())
+    seen = wl > -math.inf
+    assert torch.equal(lse > -math.inf, seen)
+    assert ((lse.double() - wl)[seen].abs() <= rest[seen] + 2.0 ** -22 * wl[seen].abs()).all()
+    assert (out[~seen] == 0).all()
+
+
+def _case(g, B, Tq, Hq, Hkv, D, prefix, lens, page, fmt, poison=True, spare=2):
+    """A cache that holds the prefix and the sequences' tokens in scattered pages; every row that is no
+    token of the call is NaN (or has a NaN scale)."""
+    lens = [lens[i % len(lens)] for i in range(B)]
+    shared, each = -(-prefix // page), max([1] + [-(-n // page) for n in lens])
+    pages = shared + B * each + spare
+    c = tps.KVCache.empty(pages, Hkv, page, D, fmt, device=DEV)
+    order = torch.randperm(pages, generator=g, device=DEV)
+    pp, table = order[:shared].int().contiguous(), order[shared:shared + B * each].int().reshape(B, each).contiguous()
+    if poison:
+        if fmt == "bf16":
+            c.k.fill_(math.nan), c.v.fill_(math.nan)
+        else:
+            c.k_scale.fill_(math.nan), c.v_scale.fill_(math.nan)
+    at = torch.arange(prefix, device=DEV)
+    slots = [pp.long()[at // page] * page + at % page]
+    for b in range(B):
+        at = torch.arange(lens[b], device=DEV)
+        slots.append(table[b].long()[at // page] * page + at % page)
+    slots = torch.cat(slots)
+    n = slots.shape[0]
+    k = torch.randn(n, Hkv, D, generator=g, device=DEV) * torch.exp(0.5 * torch.randn(1, Hkv, D, generator=g, device=DEV))
+    v = torch.randn(n, Hkv, D, generator=g, device=DEV) * torch.exp(torch.randn(n, Hkv, 1, generator=g, device=DEV))
+    tps.kv_write(c, k.bfloat16(), v.bfloat16(), slots)
+    q = (1.5 * torch.randn(B, Tq, Hq, D, generator=g, device=DEV)).bfloat16()
+    return c, q, pp, table, torch.tensor(lens, dtype=torch.int32, device=DEV)
+
+
+SHAPES = [  # B, Tq, Hq, Hkv, D, prefix, own lengths, page
+    (1, 1, 1, 1, 64, 1, [0], 16),
+    (1, 1, 4, 1, 128, 0, [1], 16),
+    (2, 1, 8, 8, 128, 17, [0, 33], 16),
+    (3, 1, 32, 8, 128, 1000, [0, 1, 40], 16),
+    (5, 1, 8, 2, 64, 0, [0, 1, 15, 16, 300], 32),
+    (8, 1, 28, 4, 128, 129, [64, 7], 64),
+    (4, 5, 20, 4, 64, 333, [5, 6, 2, 0, 70], 32),   # fewer own tokens than queries: some see none
+    (4, 3, 12, 4, 128, 0, [3, 1, 0], 16),           # and no prefix: nothing at all
+    (16, 1, 8, 1, 128, 640, [20], 128),             # 128 rows of one head
+    (33, 1, 8, 1, 128, 1023, [0, 5, 130], 256),     # 264 rows
+    (40, 1, 16, 2, 64, 511, [9, 0], 16),            # 320 rows
+    (70, 2, 10, 2, 128, 257, [2, 50], 32),          # 700 rows
+    (1, 1, 16, 1, 64, 5000, [3], 64),
+    (2, 1, 8, 2, 128, 100, [4000, 1], 16),          # a long own part: several CTAs for each sequence
+    (1, 40, 6, 1, 64, 200, [40], 16),               # 240 rows of one sequence
+    (257, 1, 4, 1, 64, 130, [1, 2, 3], 16),
+]
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "int8"])
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s[:6])))
+def test_attention(fmt, shape):
+    B, Tq, Hq, Hkv, D, prefix, lens, page = shape
+    g = _gen(B * 100 + prefix)
+    c, q, pp, table, n = _case(g, B, Tq, Hq, Hkv, D, prefix, lens, page, fmt)
+    st = torch.full((B,), 9, dtype=torch.int32, device=DEV)
+    got = tps.prefix_attention(q, c, pp, prefix, table, n, want_lse=True, status=st)
+    assert (st == 0).all()
+    _check_attention(got, q, plain.values(c), pp, prefix, table, n, D ** -0.5, fmt)
+    again = tps.prefix_attention(q, c, pp, prefix, table, n, want_lse=True)
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+    if Tq == 1:
+        assert torch.equal(tps.prefix_attention(q[:, 0].contiguous(), c, pp, prefix, table, n), got[0][:, 0])
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "int8"])
+@pytest.mark.parametrize("B", [2, 48])
+def test_attention_to_one_token_and_growing_scores(fmt, B):
+    """Scores that rise along the tokens by hundreds of units (every block raises the reference), and a
+    token whose score towers over the others."""
+    g = _gen(7)
+    D, prefix = 128, 700
+    c, q, pp, table, n = _case(g, B, 1, 8, 2, D, prefix, [40], 64, fmt)
+    at = torch.arange(prefix, device=DEV)
+    slots = pp.long()[at // 64] * 64 + at % 64
+    u = torch.randn(1, 2, D, generator=g, device=DEV)
+    q[:] = (u.repeat_interleave(4, 1) * torch.linspace(0.25, 2, B * 8, device=DEV).view(B, 8, 1)).unsqueeze(1).bfloat16()
+    k = (u * (at.view(-1, 1, 1) / 100 - 2)).bfloat16()
+    v = torch.randn(prefix, 2, D, generator=g, device=DEV).bfloat16()
+    tps.kv_write(c, k, v, slots)
+    _check_attention(tps.prefix_attention(q, c, pp, prefix, table, n, want_lse=True), q, plain.values(c), pp, prefix, table, n,
+                     D ** -0.5, fmt)
+    _check_attention(tps.prefix_attention(q, c, pp, prefix, table, n, want_lse=True, scale=3.0), q, plain.values(c), pp, prefix,
+                     table, n, 3.0, fmt)
+    _check_attention(tps.prefix_attention(q, c, pp, prefix, table, n, want_lse=True, scale=-0.5), q, plain.values(c), pp, prefix,
+                     table, n, -0.5, fmt)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "int8"])
+@pytest.mark.parametrize("B,mag", [(2, 2.0 ** -30), (2, 2.0 ** 20), (40, 2.0 ** -30), (40, 2.0 ** 20)])
+def test_attention_queries_outside_float16(fmt, B, mag):
+    g = _gen(9)
+    c, q, pp, table, n = _case(g, B, 1, 4, 1, 64, 200, [30], 32, fmt)
+    q[0] = (q[0].float() * mag).bfloat16()
+    q[1, 0, 0] = 0
+    kv = plain.values(c)
+    scale = 0.125 / max(1.0, mag)
+    _check_attention(tps.prefix_attention(q, c, pp, 200, table, n, want_lse=True, scale=scale), q, kv, pp, 200, table, n, scale, fmt)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "int8"])
+@pytest.mark.parametrize("B", [3, 40])
+def test_attention_bad_pages_lengths_and_values(fmt, B):
+    g = _gen(11)
+    c, q, pp, table, n = _case(g, B, 1, 8, 1, 128, 300, [40], 16, fmt)
+    good = tps.prefix_attention(q, c, pp, 300, table, n)
+    table[0, 1] = c.n_pages
+    table[1, 2] = -1
+    n2 = n.clone()
+    n2[1] = 32  # its bad page holds no token that is seen
+    n2[2] = table.shape[1] * 16 + 1
+    st = torch.empty(B, dtype=torch.int32, device=DEV)
+    out, lse = tps.prefix_attention(q, c, pp, 300, table, n2, status=st, want_lse=True)
+    assert st[:3].tolist() == [3, 0, 3] and (st[3:] == 0).all()
+    assert out[0].isnan().all() and out[2].isnan().all() and torch.isfinite(out[1]).all()
+    assert lse[0].isnan().all() and torch.isfinite(lse[1]).all()
+    assert torch.equal(out[3:], good[3:])
+    n2[0] = -1
+    tps.prefix_attention(q, c, pp, 300, table, n2, status=st)
+    assert st[:3].tolist() == [3, 0, 3]
+    bad = pp.clone()
+    bad[5] = c.n_pages + 7
+    out = tps.prefix_attention(q, c, bad, 300, table, n, status=st)
+    assert (st == 3).all() and out.isnan().all()
+    # NaN in one sequence's query and in another's own tokens stay there
+    table = torch.arange(table.numel(), device=DEV, dtype=torch.int32).reshape(table.shape)
+    c, q, pp, table, n = _case(_gen(11), B, 1, 8, 1, 128, 300, [40], 16, fmt)
+    q[1, 0, 3, 5] = math.nan
+    s = table[2, 1].long().reshape(1) * 16 + 3
+    tps.kv_write(c, torch.full((1, 1, 128), math.nan, device=DEV), torch.zeros(1, 1, 128, device=DEV), s)
+    out = tps.prefix_attention(q, c, pp, 300, table, n)
+    assert out[1, 0, 3].isnan().all() and out[2].isnan().all()
+    keep = torch.ones(B, 1, 8, dtype=torch.bool, device=DEV)
+    keep[1, 0, 3] = False
+    keep[2] = False
+    assert torch.equal(out[keep], good[keep])
+
+
+def test_attention_table_stride_workspace_stream_and_graph():
+    g = _gen(13)
+    c, q, pp, table, n = _case(g, 40, 1, 8, 2, 128, 777, [0, 33, 50], 16, "fp8")
+    want = tps.prefix_attention(q, c, pp, 777, table, n)
+    wide = torch.full((40, table.shape[1] + 5), -9, dtype=torch.int32, device=DEV)
+    wide[:, :table.shape[1]] = table
+    assert torch.equal(tps.prefix_attention(q, c, pp, 777, wide[:, :table.shape[1]], n), want)
+    size = tps.prefix_attention_workspace(q.shape, c, 777, table.shape[1])
+    ws = torch.empty(size, dtype=torch.uint8, device=DEV)
+    assert torch.equal(tps.prefix_attention(q, c, pp, 777, table, n, workspace=ws), want)
+    with pytest.raises(RuntimeError):
+        tps.prefix_attention(q, c, pp, 777, table, n, workspace=ws[:size - 1])
+    side = torch.cuda.Stream(DEV)
+    q2 = torch.empty_like(q)
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+        q2.copy_(q)
+    got = tps.prefix_attention(q2, c, pp, 777, table, n, stream=side)
+    side.synchronize()
+    assert torch.equal(got, want)
+    out = torch.empty_like(q)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        tps.prefix_attention(q, c, pp, 777, table, n, out=out)
+    for _ in range(2):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    assert tps.prefix_attention(q[:0].contiguous(), c, pp, 777, table[:0], n[:0]).shape == (0, 1, 8, 128)
+
+
+def test_attention_does_not_depend_on_the_other_sequences():
+    g = _gen(17)
+    c, q, pp, table, n = _case(g, 64, 1, 8, 2, 128, 900, [10, 33], 32, "int8")
+    want = tps.prefix_attention(q, c, pp, 900, table, n)
+    q2 = q.clone()
+    q2[:20] = (q2[:20].float() * 1000).bfloat16()
+    q2[20:40] = 0
+    assert torch.equal(tps.prefix_attention(q2, c, pp, 900, table, n)[40:], want[40:])
+
+
+def test_no_prefix_equals_all_prefix():
+    """The same tokens as one sequence's own and as its prefix give the same answer to rounding."""
+    g = _gen(19)
+    c, q, pp, table, n = _case(g, 1, 1, 8, 2, 128, 500, [0], 16, "bf16")
+    a, la = tps.prefix_attention(q, c, pp, 500, table, n, want_lse=True)
+    m = torch.tensor([500], dtype=torch.int32, device=DEV)
+    b, lb = tps.prefix_attention(q, c, pp[:0], 0, pp.view(1, -1), m, want_lse=True)
+    kv = plain.values(c)
+    _check_attention((a, la), q, kv, pp, 500, table, n, 128 ** -0.5, "bf16")
+    _check_attention((b, lb), q, kv, pp[:0], 0, pp.view(1, -1), m, 128 ** -0.5, "bf16")
