@@ -356,7 +356,7 @@ typedef enum { TPS_KV_BF16 = 0, TPS_KV_FP8 = 1, TPS_KV_INT8 = 2 } tps_kv_format;
 /*
  * tps_kv_cache -- a paged cache of one layer (caller-owned device memory).
  *   k, v              [n_pages, n_heads, page_size, head_dim] codes, 16-byte aligned.
- *   k_scale, v_scale  [n_pages, n_heads, page_size] bfloat16, 4-byte aligned; NULL for TPS_KV_BF16.
+ *   k_scale, v_scale  [n_pages, n_heads, page_size] bfloat16, 16-byte aligned; NULL for TPS_KV_BF16.
  *   page_size         16, 32, 64, 128 or 256.      head_dim  a multiple of 16, at most 512.
  *   n_pages           at most 2^31 - 1.            n_heads   1 .. 65535.
  * Token slot s lives in page s / page_size at row s % page_size.

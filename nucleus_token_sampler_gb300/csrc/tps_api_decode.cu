@@ -29,13 +29,17 @@ int check_cache(const tps_kv_cache* c, bool pointers)
     if (!c->k || !c->v) return TPS_ERR_ARG;
     if (c->format != TPS_KV_BF16 && (!c->k_scale || !c->v_scale)) return TPS_ERR_ARG;
     if (!aligned(c->k, 16) || !aligned(c->v, 16)) return TPS_ERR_ALIGN;
-    if (c->format != TPS_KV_BF16 && (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))) return TPS_ERR_ALIGN;
+    if (c->format != TPS_KV_BF16 && (!aligned(c->k_scale, 16) || !aligned(c->v_scale, 16))) return TPS_ERR_ALIGN;
     return TPS_OK;
 }
 
 // CTAs of the 16-row prefix kernel per SM, and the tokens of its blocks (one step of its four warps).
 constexpr int kRowsCtasPerSm = 2;
 constexpr int kRowsBlock = 64;
+// Query rows of one key head from which the tcgen05 kernel computes the shared part.
+constexpr int64_t kTensorRows = 33;
+// Sequences (times heads and row tiles) per SM from which each warp takes one for itself.
+constexpr int64_t kOneWarpItems = 8;
 
 int plan_attention(const tps_kv_cache& c, const tps_attention& a, int sms, tps::AttnPlan* out)
 {
@@ -45,21 +49,22 @@ int plan_attention(const tps_kv_cache& c, const tps_attention& a, int sms, tps::
     if (own_rows > (1 << 24) || a.B > (int64_t(1) << 31) / (own_rows * c.n_heads)) return TPS_ERR_ARG;
     p.R = a.B * own_rows;
     p.suffix_tiles = (int)((own_rows + 15) / 16);
-    p.tensor = false;
-    p.tile_rows = 16;
-    p.block_keys = kRowsBlock;
+    p.tensor = p.R >= kTensorRows;
+    p.tile_rows = !p.tensor ? 16 : (p.R <= 128 ? 128 : 256);
+    p.block_keys = p.tensor ? 128 : kRowsBlock;
     p.n_tiles = (int)((p.R + p.tile_rows - 1) / p.tile_rows);
     p.nblk = (a.prefix_len + p.block_keys - 1) / p.block_keys;
     p.items = (int64_t)p.n_tiles * c.n_heads;
     p.units = p.items * p.nblk;
-    p.ctas = std::min<int64_t>(p.units, (int64_t)sms * kRowsCtasPerSm);
+    p.ctas = std::min<int64_t>(p.units, (int64_t)sms * (p.tensor ? 1 : kRowsCtasPerSm));
     p.pieces = p.units ? p.ctas + p.items : 0;
     // Several CTAs share one sequence's own tokens where there are few sequences and many tokens.
     const int64_t alone = a.B * c.n_heads * p.suffix_tiles;
     const int64_t tokens = a.table_width * c.page_size;
+    p.one_warp = alone >= kOneWarpItems * (int64_t)sms;
     p.cluster = 1;
-    while (p.cluster < 8 && alone * p.cluster < 2 * (int64_t)sms && tokens >= (int64_t)p.cluster * 512) p.cluster *= 2;
-    if (alone * p.cluster > INT32_MAX) return TPS_ERR_ARG;
+    while (!p.one_warp && p.cluster < 8 && alone * p.cluster < 2 * (int64_t)sms && tokens >= (int64_t)p.cluster * 512) p.cluster *= 2;
+    if (alone * p.cluster > INT32_MAX - 4) return TPS_ERR_ARG;
     p.off_ml = (size_t)p.pieces * p.tile_rows * c.head_dim * sizeof(float);
     p.bytes = p.off_ml + (size_t)p.pieces * p.tile_rows * sizeof(float2);
     *out = p;
@@ -170,6 +175,8 @@ int tps_prefix_attention(const tps_kv_cache* cache, const tps_attention* args, v
     a.c = *cache;
     a.a = *args;
     a.G = args->n_q_heads / cache->n_heads;
+    a.page_shift = 4;
+    while ((1 << a.page_shift) < cache->page_size) ++a.page_shift;
     a.qk_scale = (float)((double)args->scale * 1.4426950408889634);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     unsigned char* ws = static_cast<unsigned char*>(args->workspace);
@@ -186,7 +193,14 @@ int tps_prefix_attention(const tps_kv_cache* cache, const tps_attention* args, v
     }
     a.part = reinterpret_cast<float*>(ws);
     a.ml = reinterpret_cast<float2*>(ws + a.p.off_ml);
-    if (a.p.units) e = tps::launch_attn_prefix_rows(a, st);
+    if (a.p.units) {
+        if (!a.p.tensor)
+            e = tps::launch_attn_prefix_rows(a, st);
+        else
+            e = cache->format == TPS_KV_BF16  ? tps::launch_attn_prefix_bf16(a, st)
+                : cache->format == TPS_KV_FP8 ? tps::launch_attn_prefix_fp8(a, st)
+                                              : tps::launch_attn_prefix_int8(a, st);
+    }
     if (e == cudaSuccess) e = tps::launch_attn_suffix(a, a.p.units > 0, st);
     if (a.p.bytes && !args->workspace) {
         const cudaError_t ef = cudaFreeAsync(ws, st);

@@ -1,0 +1,558 @@
+// tps_attn_prefix.cuh -- the shared part of tps_prefix_attention on the tcgen05 matrix unit: all query
+// rows of one key head (R = B Tq G of them) against the keys and values that every sequence shares.
+//
+// Mathematics.  As in tps_attn_rows.cuh: weights 2^(z - m) with a reference m per row that is raised only
+// when a score exceeds it by more than kSlack; m is a whole number here, so that raising it scales what
+// was already computed by an exact power of two.  8-bit formats become float16 on the way to the matrix
+// unit: for every block of 128 tokens the scales are taken relative to the block's largest, nk for keys
+// and nv for values (powers of two), so that code * scale / n is at most 448 (one rounding to 11
+// bits for int8, exact for fp8) whatever the magnitude of the cache's values.  The block's factors stay
+// scalars outside: z = (q.k') nk, and the weights take log2(nv) in their exponent (the row sum divides
+// by nv again).
+//
+// What bounds it: with R of some hundreds, the matrix unit (512 clocks per 128 x 128 tile at D = 128) and
+// next to it the exponentials (one for each of its 16,384 weights) and the conversion of 8-bit codes; with
+// fewer rows, the bytes of the cache.  One CTA per SM; the blocks of all items form one line that is
+// cut evenly (AttnPlan).  A CTA holds one or two tiles of 128 query rows: with two, one tile's softmax
+// runs while the other's products do, and each block of keys and values is loaded and converted once
+// for 256 rows.  Roles:
+//   warps 0 .. 4 kTiles - 1   softmax, one thread per query row: scores from TMEM, weights back to
+//                             TMEM over them, where they are the first operand of the second product
+//   the next warp             issues every product
+//   one warp                  loads tiles: bf16 by TMA into place, 8-bit codes by bulk copies
+//   8-bit: four warps         convert code tiles to float16 ones
+// Shared memory: the query tiles and a ring of 128-token tiles (keys, values, keys, ...), in the 128-byte
+// swizzle, and a ring of code tiles; TMEM: scores and outputs of each tile.  Every wait is bounded: a wait that runs
+// out makes all roles leave, and the pieces say so.
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_fp16.h>
+
+#include "tps_attn_rows.cuh"
+#include "tps_decode.h"
+#include "tps_tcgen05.cuh"
+
+namespace tps {
+
+constexpr int kBlockKeys = 128;
+constexpr int kRaw = 4;             // tiles of 8-bit codes in shared memory
+constexpr int kScalars = 4;         // blocks whose scale factors are kept
+
+template <int D, int kFormat, int kTiles> struct PrefixShape {
+    static constexpr bool k8 = kFormat != TPS_KV_BF16;
+    static constexpr int kMmaWarp = 4 * kTiles, kLoadWarp = kMmaWarp + 1, kConvertWarp = kMmaWarp + 2;
+    static constexpr int kThreads = (kConvertWarp + (k8 ? 4 : 0)) * 32;
+    static constexpr int kTileBytes = 128 * D * 2;         // a query, key or value tile
+    static constexpr int kRing = k8 && D == 128 && kTiles == 2 ? 3 : 4;  // key and value tiles in shared memory
+    static constexpr int kRawBytes = 128 * D + 128 * 2;    // codes and scales of a tile
+    static constexpr int kTmemCols = kTiles == 2 ? 512 : 256;
+    static constexpr int kScoreCol = 0, kOutCol = 128 * kTiles;  // tile m: scores at 128 m, outputs at kOutCol + D m
+    struct Control {
+        uint64_t q_full, full[kRing], empty[kRing], s_full[kTiles], p_full[kTiles], o_full[kTiles], tail, drain;
+        uint64_t raw_full[kRaw], raw_empty[kRaw], scalar_full[kScalars];
+        uint32_t tmem;
+        int abort, bad;
+        float key_unit[kScalars], value_exp[kScalars];
+        alignas(16) float warp_max[2][4];  // read as a float4
+        __half factor[2][128];  // [parity of the tile][token]
+    };
+    static constexpr size_t kSmem =
+        (size_t)(kTiles + kRing) * kTileBytes + (k8 ? (size_t)kRaw * kRawBytes : 0) + sizeof(Control) + 1024;
+    static_assert(kSmem <= 232448, "fits one CTA's shared memory");
+};
+
+// Byte of 16-byte chunk c of row r in a tile: 64-element column blocks of 128 rows, 128-byte swizzle.
+__device__ __forceinline__ uint32_t tile_byte(int r, int c)
+{
+    return (uint32_t)((c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+template <int D, int kFormat, int kTiles>
+__global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
+    attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap)
+{
+    using Shape = PrefixShape<D, kFormat, kTiles>;
+    using Control = typename Shape::Control;
+    constexpr bool k8 = Shape::k8;
+    constexpr int kRing = Shape::kRing;
+    extern __shared__ unsigned char raw_smem[];
+    unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~(uintptr_t)1023);
+    unsigned char* q_tile = smem;
+    unsigned char* ring = smem + kTiles * Shape::kTileBytes;
+    unsigned char* raw_ring = ring + kRing * Shape::kTileBytes;
+    Control& ctl = *reinterpret_cast<Control*>(raw_ring + (k8 ? kRaw * Shape::kRawBytes : 0));
+
+    const AttnPlan& p = a.p;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t u0 = (int64_t)blockIdx.x * p.units / p.ctas, u1 = ((int64_t)blockIdx.x + 1) * p.units / p.ctas;
+
+    if (threadIdx.x == 0) {
+        mbar_init(&ctl.q_full, 128 * kTiles);
+        for (int i = 0; i < kRing; ++i) mbar_init(&ctl.full[i], k8 ? 4 : 1), mbar_init(&ctl.empty[i], 1);
+        for (int i = 0; i < kTiles; ++i) mbar_init(&ctl.s_full[i], 1), mbar_init(&ctl.p_full[i], 128), mbar_init(&ctl.o_full[i], 1);
+        for (int i = 0; i < kScalars; ++i) mbar_init(&ctl.scalar_full[i], 4);
+        for (int i = 0; i < kRaw; ++i) mbar_init(&ctl.raw_full[i], 1), mbar_init(&ctl.raw_empty[i], 4);
+        mbar_init(&ctl.tail, 1);
+        mbar_init(&ctl.drain, 1);
+        ctl.abort = 0;
+        ctl.bad = 0;
+        fence_proxy_async();
+    }
+    if (warp == Shape::kMmaWarp) tmem_alloc(&ctl.tmem, Shape::kTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ctl.tmem;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    volatile int* abort_flag = &ctl.abort;
+    // Wait for a phase; false once any role has given up (this one after kAttnWaitNs).
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (mbar_try_wait(bar, parity)) return true;
+        const uint64_t t0 = globaltimer_ns();
+        for (uint32_t i = 1;; ++i) {  // no suspend hint: a hand-over every few hundred nanoseconds wants a quick wake-up
+            if (mbar_try_wait(bar, parity)) return true;
+            if ((i & 15u) != 0) continue;
+            if (*abort_flag) return false;
+            if (globaltimer_ns() - t0 > kAttnWaitNs) {
+                *abort_flag = 1;
+                return false;
+            }
+        }
+    };
+    // The same for a whole warp, whose lanes go on or give up together.
+    auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait(bar, parity)) != 0; };
+    bool alive = true;
+
+    if (warp < 4 * kTiles) {
+        // ---------------------------------------------------------------------------- softmax
+        const int m = warp >> 2;
+        const int in_tile = (int)threadIdx.x;  // row of the CTA's kTiles * 128
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t s_addr = tmem + lanes + Shape::kScoreCol + 128 * m, o_addr = tmem + lanes + Shape::kOutCol + D * m;
+        const float neg = -__int_as_float(0x7F800000);
+        unsigned char* my_q = q_tile + m * Shape::kTileBytes;
+        uint32_t s_phase = 0, o_phase = 0;
+        int64_t block = 0;  // blocks this CTA has passed
+        const bool flip = a.qk_scale < 0.f;
+        const float unit = fmaxf(fabsf(a.qk_scale), 1e-30f);  // never 0: a masked score times it stays -inf
+        for (int64_t u = u0; u < u1 && alive;) {
+            const int64_t item = u / p.nblk, end = min(u1, (item + 1) * p.nblk);
+            const int head = (int)(item / p.n_tiles);
+            const int64_t row = (item - (int64_t)head * p.n_tiles) * (128 * kTiles) + in_tile;
+            // the query row, as it is (bf16) or brought into float16's range
+            float row_unit = unit;
+            {
+                uint4 w[D / 8];
+                if (row < p.R) {
+                    const int64_t bt = row / a.G;
+                    const uint4* src = reinterpret_cast<const uint4*>(
+                        static_cast<const __nv_bfloat16*>(a.a.q) + (bt * a.a.n_q_heads + (int64_t)head * a.G + (row - bt * a.G)) * D);
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c) w[c] = src[c];
+                } else {
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c) w[c] = make_uint4(0u, 0u, 0u, 0u);
+                }
+                const uint32_t sign = flip ? 0x80008000u : 0u;
+                float f = 1.f;
+                if (k8) {
+                    float amax = 0.f;
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c) {
+                        const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float lo = fabsf(__uint_as_float(x[i] << 16)), hi = fabsf(__uint_as_float(x[i] & 0xFFFF0000u));
+                            amax = lo < -neg ? fmaxf(amax, lo) : amax;
+                            amax = hi < -neg ? fmaxf(amax, hi) : amax;
+                        }
+                    }
+                    f = f16_row_scale(amax);
+                    row_unit = unit / f;
+                }
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) {
+                    uint32_t x[4] = {w[c].x ^ sign, w[c].y ^ sign, w[c].z ^ sign, w[c].w ^ sign};
+                    if (k8) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const __half2 h = __floats2half2_rn(__uint_as_float(x[i] << 16) * f, __uint_as_float(x[i] & 0xFFFF0000u) * f);
+                            x[i] = *reinterpret_cast<const uint32_t*>(&h);
+                        }
+                    }
+                    *reinterpret_cast<uint4*>(my_q + tile_byte(in_tile & 127, c)) = make_uint4(x[0], x[1], x[2], x[3]);
+                }
+                fence_proxy_async();
+                mbar_arrive(&ctl.q_full);
+            }
+            float ref = neg, sum = 0.f;
+            for (int64_t v = u; v < end; ++v, ++block) {
+                if (!(alive = wait_all(&ctl.s_full[m], s_phase & 1))) break;
+                ++s_phase;
+                tc_fence_after();
+                float c = row_unit, add = 0.f, inv = 1.f;
+                if (k8) {
+                    const int slot = (int)(block % kScalars);
+                    if (!(alive = wait_all(&ctl.scalar_full[slot], (uint32_t)(block / kScalars) & 1))) break;
+                    c *= ctl.key_unit[slot];
+                    add = ctl.value_exp[slot];
+                    inv = exp2_fast(-add);
+                }
+                const int64_t left = a.a.prefix_len - (v - item * p.nblk) * kBlockKeys;
+                float2 part = make_float2(0.f, 0.f);
+                auto chunk = [&](float (&s)[32], int ch) {
+                    if (left < ch * 32 + 32) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (ch * 32 + i >= left) s[i] = neg;
+                    }
+                    float top = fmaxf(s[0], s[1]);
+#pragma unroll
+                    for (int i = 2; i < 32; i += 2) top = fmaxf(fmaxf(top, s[i]), s[i + 1]);
+                    top = fmaf(top, c, add);
+                    if (__any_sync(0xFFFFFFFFu, top > ref + kSlack)) {
+                        // raise the references that need it: scale the sum, the output and this block's weights
+                        const float to = top > ref + kSlack ? ceilf(top) : ref;
+                        const float f = to == ref ? 1.f : exp2_fast(ref - to);
+                        ref = to;
+                        sum *= f;
+                        part.x *= f, part.y *= f;
+                        if (v > u) {
+#pragma unroll 1
+                            for (int i = 0; i < D; i += 16) {
+                                uint32_t o[16];
+                                tmem_ld16(o_addr + i, o);
+                                tmem_wait_ld(o);
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                                tmem_st16(o_addr + i, o);
+                            }
+                        }
+#pragma unroll 1
+                        for (int i = 0; i < ch; ++i) {
+                            uint32_t w[16];
+                            tmem_wait_st();
+                            tmem_ld16(s_addr + i * 16, w);
+                            tmem_wait_ld(w);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                if (k8) {
+                                    const __half2 h = __hmul2(*reinterpret_cast<__half2*>(&w[j]), __float2half2_rn(f));
+                                    w[j] = *reinterpret_cast<const uint32_t*>(&h);
+                                } else {
+                                    const __nv_bfloat162 h = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&w[j]), __float2bfloat162_rn(f));
+                                    w[j] = *reinterpret_cast<const uint32_t*>(&h);
+                                }
+                            }
+                            tmem_st16(s_addr + i * 16, w);
+                        }
+                    }
+                    const float b = add - (ref == neg ? 0.f : ref) + (k8 ? kLift : 0.f);
+                    uint32_t w[16];
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        float2 x = fma2(make_float2(s[i], s[i + 1]), make_float2(c, c), make_float2(b, b));
+                        x.x = exp2_fast(x.x), x.y = exp2_fast(x.y);
+                        part = add2(part, x);
+                        if (k8) {
+                            const __half2 h = __floats2half2_rn(x.x, x.y);
+                            w[i / 2] = *reinterpret_cast<const uint32_t*>(&h);
+                        } else {
+                            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i / 2]) : "f"(x.y), "f"(x.x));
+                        }
+                    }
+                    tmem_st16(s_addr + ch * 16, w);
+                };
+                // 32 scores at a time, the next ones on their way meanwhile.  The weights of a chunk go over
+                // scores that have been read: chunk ch's over columns [16 ch, 16 ch + 16).
+                float sa[32], sb[32];
+                tmem_ld32(s_addr, sa);
+#pragma unroll 1
+                for (int ch = 0; ch < 4; ch += 2) {
+                    tmem_wait_ld(sa);
+                    tmem_ld32(s_addr + (ch + 1) * 32, sb);
+                    chunk(sa, ch);
+                    tmem_wait_ld(sb);
+                    if (ch == 0) tmem_ld32(s_addr + 64, sa);
+                    chunk(sb, ch + 1);
+                }
+                sum = fmaf(part.x + part.y, inv, sum);
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(&ctl.p_full[m]);
+            }
+            if (alive) alive = wait_all(&ctl.o_full[m], o_phase & 1);
+            ++o_phase;
+            const int64_t piece = blockIdx.x + item;
+            const int64_t at = piece * p.tile_rows + in_tile;
+            if (alive) {
+                tc_fence_after();
+                float4* dst = reinterpret_cast<float4*>(a.part + piece * p.tile_rows * D) + in_tile;
+#pragma unroll 1
+                for (int i = 0; i < D; i += 32) {
+                    float o[32];
+                    tmem_ld32(o_addr + i, o);
+                    tmem_wait_ld(o);
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4)
+                        dst[(int64_t)((i + j) / 4) * p.tile_rows] = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                }
+                tc_fence_before();
+            }
+            a.ml[at] = make_float2(ref, !alive ? kPieceTimeout : (*(volatile int*)&ctl.bad ? kPieceBadPage : sum));
+            u = end;
+        }
+        if (!alive)  // the pieces of the items that were not reached
+            for (int64_t u = u0; u < u1;) {
+                const int64_t item = u / p.nblk;
+                a.ml[(blockIdx.x + item) * p.tile_rows + in_tile] = make_float2(neg, kPieceTimeout);
+                u = min(u1, (item + 1) * p.nblk);
+            }
+    } else if (warp == Shape::kMmaWarp) {
+        // ---------------------------------------------------------------------------- products
+        if (lane == 0) {
+            constexpr uint32_t kScoreDesc = mma_desc(128, 128, !k8, false), kOutDesc = mma_desc(128, D, !k8, true);
+            const uint32_t q_addr = smem_u32(q_tile), ring_addr = smem_u32(ring);
+            uint32_t q_phase = 0, p_phase = 0, tail_phase = 0;
+            int64_t tile = 0;  // tiles consumed from the ring
+            auto scores = [&](int m, int slot) {
+#pragma unroll
+                for (int s = 0; s < D / 16; ++s) {
+                    const uint32_t off = (uint32_t)((s >> 2) * (128 * 128) + (s & 3) * 32);
+                    mma_ss(tmem + Shape::kScoreCol + 128 * m, smem_desc(q_addr + m * Shape::kTileBytes + off, 16),
+                           smem_desc(ring_addr + slot * Shape::kTileBytes + off, 16), kScoreDesc, s > 0);
+                }
+                tc_commit(&ctl.s_full[m]);
+            };
+            for (int64_t u = u0; u < u1 && alive;) {
+                const int64_t item = u / p.nblk, end = min(u1, (item + 1) * p.nblk);
+                if (!(alive = wait(&ctl.q_full, q_phase++ & 1))) break;
+                int kslot = (int)(tile % kRing);
+                if (!(alive = wait(&ctl.full[kslot], (uint32_t)(tile / kRing) & 1))) break;
+                ++tile;
+                tc_fence_after();
+                for (int m = 0; m < kTiles; ++m) scores(m, kslot);
+                tc_commit(&ctl.empty[kslot]);
+                for (int64_t v = u; v < end && alive; ++v) {
+                    const int vslot = (int)(tile % kRing);
+                    if (!(alive = wait(&ctl.full[vslot], (uint32_t)(tile / kRing) & 1))) break;
+                    ++tile;
+                    if (!k8 && a.a.prefix_len < (v - item * p.nblk + 1) * kBlockKeys)  // its rows past the prefix are zeroed
+                        if (!(alive = wait(&ctl.tail, tail_phase++ & 1))) break;
+                    for (int m = 0; m < kTiles; ++m) {
+                        if (!(alive = wait(&ctl.p_full[m], p_phase & 1))) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int s = 0; s < kBlockKeys / 16; ++s)
+                            mma_ts(tmem + Shape::kOutCol + D * m, tmem + Shape::kScoreCol + 128 * m + s * 8,
+                                   smem_desc(ring_addr + vslot * Shape::kTileBytes + s * 2048, 128 * 128), kOutDesc, v > u || s > 0);
+                        if (v + 1 == end) {
+                            tc_commit(&ctl.o_full[m]);
+                        } else {
+                            if (m == 0) {
+                                kslot = (int)(tile % kRing);
+                                if (!(alive = wait(&ctl.full[kslot], (uint32_t)(tile / kRing) & 1))) break;
+                                ++tile;
+                                tc_fence_after();
+                            }
+                            scores(m, kslot);
+                        }
+                    }
+                    if (!alive) break;
+                    ++p_phase;
+                    tc_commit(&ctl.empty[vslot]);
+                    if (v + 1 < end) tc_commit(&ctl.empty[kslot]);
+                }
+                u = end;
+            }
+            // Products in flight end before the tensor memory is given back (bounded, as every wait).
+            tc_commit(&ctl.drain);
+            mbar_wait_bounded(&ctl.drain, 0, kAttnWaitNs);
+        }
+        __syncwarp();
+    } else if (warp == Shape::kLoadWarp) {
+        // ---------------------------------------------------------------------------- loads
+        // A lane for each box: the tokens of one page within a block, up to 128 of them.
+        constexpr int kSlots = k8 ? kRaw : kRing;
+        uint64_t* filled = k8 ? ctl.raw_full : ctl.full;
+        uint64_t* freed = k8 ? ctl.raw_empty : ctl.empty;
+        const int box = min(a.c.page_size, kBlockKeys), boxes = kBlockKeys / box;
+        int64_t tile = 0;
+        auto page_of = [&](int64_t t) {  // the page of token t
+            int id = 0;
+            if (lane < boxes && t < a.a.prefix_len) {
+                id = a.a.prefix_pages[t >> a.page_shift];
+                if (id < 0 || id >= a.c.n_pages) {
+                    *(volatile int*)&ctl.bad = 1;
+                    id = 0;
+                }
+            }
+            return id;
+        };
+        int64_t item = u0 / p.nblk, token = (u0 - item * p.nblk) * kBlockKeys;
+        int page = page_of(token + lane * box);
+        for (int64_t v = u0; v < u1 && alive; ++v) {
+            const int head = (int)(item / p.n_tiles);
+            const int64_t left = a.a.prefix_len - token;
+            const int live = (int)min((int64_t)boxes, (left + box - 1) / box);
+            const int row = (int)((token + lane * box) & (a.c.page_size - 1));
+            token += kBlockKeys;
+            if (token >= a.a.prefix_len) token = 0, ++item;
+            const int next = v + 1 < u1 ? page_of(token + lane * box) : 0;
+            for (int kv = 0; kv < 2 && alive; ++kv, ++tile) {
+                const int slot = (int)(tile % kSlots);
+                if (tile >= kSlots) alive = wait_all(&freed[slot], (uint32_t)(tile / kSlots - 1) & 1);
+                if (!alive) break;
+                unsigned char* dst = k8 ? raw_ring + slot * Shape::kRawBytes : ring + slot * Shape::kTileBytes;
+                if (lane == 0) mbar_arrive_expect_tx(&filled[slot], (uint32_t)(live * box) * (k8 ? D + 2 : 2 * D));
+                __syncwarp();
+                if (lane < live) {
+                    if (k8) {
+                        const int64_t at = (((int64_t)page * a.c.n_heads + head) << a.page_shift) + row;
+                        bulk_g2s(dst + lane * box * D, static_cast<const char*>(kv ? a.c.v : a.c.k) + at * D, (uint32_t)(box * D), &filled[slot]);
+                        bulk_g2s(dst + 128 * D + lane * box * 2, static_cast<const char*>(kv ? a.c.v_scale : a.c.k_scale) + at * 2,
+                                 (uint32_t)(box * 2), &filled[slot]);
+                    } else {
+                        for (int cb = 0; cb < D / 64; ++cb)
+                            tma_load4(dst + cb * (128 * 128) + lane * box * 128, kv ? &vmap : &kmap, cb * 64, row, head, page, &filled[slot]);
+                    }
+                }
+                if (!k8 && kv && left < kBlockKeys) {
+                    // Rows past the prefix hold anything (0 * NaN is NaN): zero them once the copy has landed.
+                    alive = wait_all(&filled[slot], (uint32_t)(tile / kSlots) & 1);
+                    if (!alive) {
+                        ++tile;
+                        break;
+                    }
+                    for (int i = lane; i < (kBlockKeys - (int)left) * (D / 8); i += 32)
+                        *reinterpret_cast<uint4*>(dst + tile_byte((int)left + i / (D / 8), i % (D / 8))) = make_uint4(0u, 0u, 0u, 0u);
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ctl.tail);
+                }
+            }
+            page = next;
+        }
+        // Copies in flight land before the CTA leaves: the last fill of every slot.
+        for (int i = 0; i < kSlots; ++i) {
+            const int64_t last = tile - 1 - i;
+            if (last >= 0) mbar_wait_bounded(&filled[last % kSlots], (uint32_t)(last / kSlots) & 1, kAttnWaitNs);
+        }
+    } else {
+        // ---------------------------------------------------------------------------- 8-bit codes to float16
+        constexpr int kPieces = D / 16;                // 16-byte pieces of a code row
+        constexpr int kRowsPerStep = 128 / kPieces;    // rows that the 128 threads convert at a time
+        const int t = (int)threadIdx.x - Shape::kConvertWarp * 32, cw = t >> 5;
+        const int piece = t % kPieces, sub = t / kPieces;
+        // The eight lanes of a 128-byte code row fill both column blocks; the upper four write their halves the
+        // other way round, so that the eight 16-byte stores of a phase hit different banks.
+        const bool swap = piece >= 4;
+        // A barrier of the four warps that also tells whether `ok` holds in all of them.
+        auto all_of_four_warps = [](bool ok) {
+            int r;
+            asm volatile(
+                "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\t"
+                "barrier.cta.red.and.pred q, 1, 128, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+                : "=r"(r)
+                : "r"((int)ok)
+                : "memory");
+            return r != 0;
+        };
+        int64_t token = (u0 - u0 / p.nblk * p.nblk) * kBlockKeys;
+        const int64_t tiles = 2 * (u1 - u0);
+        for (int64_t tile = 0; tile < tiles; ++tile) {
+            const int par = (int)(tile & 1);  // keys, values
+            const int rs = (int)(tile % kRaw), slot = (int)(tile % kRing);
+            const int left = (int)min((int64_t)kBlockKeys, a.a.prefix_len - token);
+            if (par) {
+                token += kBlockKeys;
+                if (token >= a.a.prefix_len) token = 0;
+            }
+            const unsigned char* raw = raw_ring + rs * Shape::kRawBytes;
+            if (alive) alive = wait_all(&ctl.raw_full[rs], (uint32_t)(tile / kRaw) & 1);
+            // The tile's unit, a power of two no larger than the largest scale and more than half of it (1 if
+            // there is none), and each token's factor.
+            const float s = alive && t < left ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(raw + 128 * D)[t]) : 0.f;
+            float most = s;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+            if (lane == 0) ctl.warp_max[par][cw] = most;
+            if (!(alive = all_of_four_warps(alive))) break;  // the four warps go on or give up together
+            const float4 mx = *reinterpret_cast<const float4*>(ctl.warp_max[par]);
+            most = fmaxf(fmaxf(mx.x, mx.y), fmaxf(mx.z, mx.w));
+            const int e = most > 0.f ? max(-126, min((int)(__float_as_uint(most) >> 23) - 127, 126)) : 0;
+            ctl.factor[par][t] = __float2half_rn(s * __uint_as_float((uint32_t)(127 - e) << 23));
+            all_of_four_warps(true);
+            if (tile >= kRing) alive = wait_all(&ctl.empty[slot], (uint32_t)(tile / kRing - 1) & 1);
+            if (!alive) continue;
+            const int block_slot = (int)((tile >> 1) % kScalars);
+            if (t == 0) {
+                if (par)
+                    ctl.value_exp[block_slot] = (float)e;
+                else
+                    ctl.key_unit[block_slot] = __uint_as_float((uint32_t)(127 + e) << 23);
+            }
+            if (par) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl.scalar_full[block_slot]);
+            }
+            unsigned char* dst = ring + slot * Shape::kTileBytes;
+#pragma unroll 4
+            for (int i = 0; i < kPieces; ++i) {
+                const int r = i * kRowsPerStep + sub;
+                uint4 x = *reinterpret_cast<const uint4*>(raw + r * D + piece * 16);
+                if (r >= left) x = make_uint4(0u, 0u, 0u, 0u);  // past the prefix: anything
+                const __half2 f = __half2half2(ctl.factor[par][r]);
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                uint32_t h[8];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    code_pairs<kFormat>(w[j], h[2 * j], h[2 * j + 1]);
+#pragma unroll
+                    for (int k = 2 * j; k < 2 * j + 2; ++k) {
+                        const __half2 y = __hmul2(*reinterpret_cast<__half2*>(&h[k]), f);
+                        h[k] = *reinterpret_cast<const uint32_t*>(&y);
+                    }
+                }
+                const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
+                *reinterpret_cast<uint4*>(dst + tile_byte(r, 2 * piece + (swap ? 1 : 0))) = swap ? hi : lo;
+                *reinterpret_cast<uint4*>(dst + tile_byte(r, 2 * piece + (swap ? 0 : 1))) = swap ? lo : hi;
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&ctl.full[slot]);
+                mbar_arrive(&ctl.raw_empty[rs]);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == Shape::kMmaWarp) tmem_free(tmem, Shape::kTmemCols);
+}
+
+}  // namespace tps

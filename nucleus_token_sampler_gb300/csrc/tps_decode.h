@@ -50,7 +50,8 @@ struct AttnPlan {
     int n_tiles;         // row tiles of one key head
     bool tensor;         // the tcgen05 kernel computes the shared part
     int suffix_tiles;    // 16-row tiles of one sequence's Tq G rows
-    int cluster;         // CTAs that share one sequence's own tokens
+    bool one_warp;       // each warp has a sequence (and head, tile) for itself
+    int cluster;         // else: CTAs that share one sequence's own tokens
     size_t off_ml, bytes;  // workspace: outputs first, then (maximum, sum)
 };
 
@@ -58,14 +59,17 @@ struct AttnArgs {
     tps_kv_cache c;
     tps_attention a;
     AttnPlan p;
-    int G;
+    int G, page_shift;
     float qk_scale;  // scale * log2(e)
-    float* part;     // [pieces, tile_rows, D]
+    float* part;     // [pieces][D / 4][tile_rows][4]: a warp's rows lie side by side
     float2* ml;      // [pieces, tile_rows]: maximum in base-2 units, sum (negative: a bad page id)
 };
 
 // The shared part, then the own tokens and the join.
 cudaError_t launch_attn_prefix_rows(const AttnArgs& a, cudaStream_t stream);
+cudaError_t launch_attn_prefix_bf16(const AttnArgs& a, cudaStream_t stream);
+cudaError_t launch_attn_prefix_fp8(const AttnArgs& a, cudaStream_t stream);
+cudaError_t launch_attn_prefix_int8(const AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_attn_suffix(const AttnArgs& a, bool after_prefix, cudaStream_t stream);
 
 }  // namespace tps
