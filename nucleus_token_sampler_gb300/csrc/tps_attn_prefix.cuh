@@ -20,7 +20,8 @@
 //                             TMEM over them, where they are the first operand of the second product
 //   the next warp             issues every product
 //   one warp                  loads tiles: bf16 by TMA into place, 8-bit codes by bulk copies
-//   8-bit: four warps         convert code tiles to float16 ones
+//   8-bit: one warp           brings the tokens' scales to a tile's unit
+//   8-bit: eight warps        convert code tiles to float16 ones
 // Shared memory: the query tiles and a ring of 128-token tiles (keys, values, keys, ...), in the 128-byte
 // swizzle, and a ring of code tiles; TMEM: scores and outputs of each tile.  Every wait is bounded: a wait that runs
 // out makes all roles leave, and the pieces say so.
@@ -38,26 +39,30 @@
 namespace tps {
 
 constexpr int kBlockKeys = 128;
-constexpr int kRaw = 4;             // tiles of 8-bit codes in shared memory
-constexpr int kScalars = 4;         // blocks whose scale factors are kept
+constexpr int kScalars = 8;         // blocks whose scale factors are kept
 
 template <int D, int kFormat, int kTiles> struct PrefixShape {
     static constexpr bool k8 = kFormat != TPS_KV_BF16;
-    static constexpr int kMmaWarp = 4 * kTiles, kLoadWarp = kMmaWarp + 1, kConvertWarp = kMmaWarp + 2;
-    static constexpr int kThreads = (kConvertWarp + (k8 ? 4 : 0)) * 32;
+    static constexpr int kMmaWarp = 4 * kTiles, kLoadWarp = kMmaWarp + 1, kScaleWarp = kMmaWarp + 2;
+    static constexpr int kConvertWarp = kMmaWarp + 4, kConvertWarps = 8;
+    static constexpr int kThreads = (kConvertWarp + (k8 ? kConvertWarps : 0)) * 32;
+    // Registers where the roles share them out (640 threads at 96 at launch): 2 x 144 + 3 x 64 = 5 x 96.
+    static constexpr bool kSplitRegs = k8 && kTiles == 2;
+    static constexpr int kRegsSoftmax = 144, kRegsOthers = 64;
+    static_assert(2 * kRegsSoftmax + 3 * kRegsOthers <= 5 * 96, "no more than the launch gave");
     static constexpr int kTileBytes = 128 * D * 2;         // a query, key or value tile
     static constexpr int kRing = k8 && D == 128 && kTiles == 2 ? 3 : 4;  // key and value tiles in shared memory
+    static constexpr int kRaw = D == 128 ? 3 : 4;          // tiles of 8-bit codes
     static constexpr int kRawBytes = 128 * D + 128 * 2;    // codes and scales of a tile
     static constexpr int kTmemCols = kTiles == 2 ? 512 : 256;
     static constexpr int kScoreCol = 0, kOutCol = 128 * kTiles;  // tile m: scores at 128 m, outputs at kOutCol + D m
     struct Control {
         uint64_t q_full, full[kRing], empty[kRing], s_full[kTiles], p_full[kTiles], o_full[kTiles], tail, drain;
-        uint64_t raw_full[kRaw], raw_empty[kRaw], scalar_full[kScalars];
+        uint64_t raw_full[kRaw], factor_full[kRaw], raw_empty[kRaw], scalar_full[kScalars];
         uint32_t tmem;
         int abort, bad;
         float key_unit[kScalars], value_exp[kScalars];
-        alignas(16) float warp_max[2][4];  // read as a float4
-        __half factor[2][128];  // [parity of the tile][token]
+        alignas(16) __half factor[kRaw][128];  // of the tokens of a code tile
     };
     static constexpr size_t kSmem =
         (size_t)(kTiles + kRing) * kTileBytes + (k8 ? (size_t)kRaw * kRawBytes : 0) + sizeof(Control) + 1024;
@@ -96,7 +101,7 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
     using Shape = PrefixShape<D, kFormat, kTiles>;
     using Control = typename Shape::Control;
     constexpr bool k8 = Shape::k8;
-    constexpr int kRing = Shape::kRing;
+    constexpr int kRing = Shape::kRing, kRaw = Shape::kRaw;
     extern __shared__ unsigned char raw_smem[];
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~(uintptr_t)1023);
     unsigned char* q_tile = smem;
@@ -110,10 +115,14 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
 
     if (threadIdx.x == 0) {
         mbar_init(&ctl.q_full, 128 * kTiles);
-        for (int i = 0; i < kRing; ++i) mbar_init(&ctl.full[i], k8 ? 4 : 1), mbar_init(&ctl.empty[i], 1);
+        for (int i = 0; i < kRing; ++i) mbar_init(&ctl.full[i], k8 ? Shape::kConvertWarps : 1), mbar_init(&ctl.empty[i], 1);
         for (int i = 0; i < kTiles; ++i) mbar_init(&ctl.s_full[i], 1), mbar_init(&ctl.p_full[i], 128), mbar_init(&ctl.o_full[i], 1);
-        for (int i = 0; i < kScalars; ++i) mbar_init(&ctl.scalar_full[i], 4);
-        for (int i = 0; i < kRaw; ++i) mbar_init(&ctl.raw_full[i], 1), mbar_init(&ctl.raw_empty[i], 4);
+        for (int i = 0; i < kScalars; ++i) mbar_init(&ctl.scalar_full[i], 1);
+        for (int i = 0; i < kRaw; ++i) {
+            mbar_init(&ctl.raw_full[i], 1);
+            mbar_init(&ctl.factor_full[i], 1);
+            mbar_init(&ctl.raw_empty[i], Shape::kConvertWarps);
+        }
         mbar_init(&ctl.tail, 1);
         mbar_init(&ctl.drain, 1);
         ctl.abort = 0;
@@ -132,9 +141,8 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         if (mbar_try_wait(bar, parity)) return true;
         const uint64_t t0 = globaltimer_ns();
-        for (uint32_t i = 1;; ++i) {  // no suspend hint: a hand-over every few hundred nanoseconds wants a quick wake-up
-            if (mbar_try_wait(bar, parity)) return true;
-            if ((i & 15u) != 0) continue;
+        for (;;) {
+            if (mbar_try_wait(bar, parity, 20000u)) return true;  // suspended, not spinning
             if (*abort_flag) return false;
             if (globaltimer_ns() - t0 > kAttnWaitNs) {
                 *abort_flag = 1;
@@ -145,6 +153,13 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
     // The same for a whole warp, whose lanes go on or give up together.
     auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait(bar, parity)) != 0; };
     bool alive = true;
+
+    if constexpr (Shape::kSplitRegs) {
+        if (warp < 4 * kTiles)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Shape::kRegsSoftmax));
+        else
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Shape::kRegsOthers));
+    }
 
     if (warp < 4 * kTiles) {
         // ---------------------------------------------------------------------------- softmax
@@ -222,61 +237,67 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
                     inv = exp2_fast(-add);
                 }
                 const int64_t left = a.a.prefix_len - (v - item * p.nblk) * kBlockKeys;
-                float2 part = make_float2(0.f, 0.f);
-                auto chunk = [&](float (&s)[32], int ch) {
+                float2 total = make_float2(0.f, 0.f);
+                // Scores past the prefix become -inf.
+                auto mask = [&](float (&s)[32], int ch) {
                     if (left < ch * 32 + 32) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             if (ch * 32 + i >= left) s[i] = neg;
                     }
-                    float top = fmaxf(s[0], s[1]);
+                };
+                auto largest = [&](const float (&s)[32]) {
+                    float t = s[0];
 #pragma unroll
-                    for (int i = 2; i < 32; i += 2) top = fmaxf(fmaxf(top, s[i]), s[i + 1]);
-                    top = fmaf(top, c, add);
-                    if (__any_sync(0xFFFFFFFFu, top > ref + kSlack)) {
-                        // raise the references that need it: scale the sum, the output and this block's weights
-                        const float to = top > ref + kSlack ? ceilf(top) : ref;
-                        const float f = to == ref ? 1.f : exp2_fast(ref - to);
-                        ref = to;
-                        sum *= f;
-                        part.x *= f, part.y *= f;
-                        if (v > u) {
+                    for (int i = 1; i < 32; ++i) t = fmaxf(t, s[i]);
+                    return t;
+                };
+                // Raise the references that need it: scale the sum, the output and the weights of chunks 0 .. done - 1.
+                auto raise = [&](float top, int done) {
+                    const float to = top > ref ? ceilf(top) : ref;
+                    const float f = to == ref ? 1.f : exp2_fast(ref - to);
+                    ref = to;
+                    sum *= f;
+                    total.x *= f, total.y *= f;
+                    if (v > u) {
 #pragma unroll 1
-                            for (int i = 0; i < D; i += 16) {
-                                uint32_t o[16];
-                                tmem_ld16(o_addr + i, o);
-                                tmem_wait_ld(o);
+                        for (int i = 0; i < D; i += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(o_addr + i, o);
+                            tmem_wait_ld(o);
 #pragma unroll
-                                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                                tmem_st16(o_addr + i, o);
-                            }
-                        }
-#pragma unroll 1
-                        for (int i = 0; i < ch; ++i) {
-                            uint32_t w[16];
-                            tmem_wait_st();
-                            tmem_ld16(s_addr + i * 16, w);
-                            tmem_wait_ld(w);
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                if (k8) {
-                                    const __half2 h = __hmul2(*reinterpret_cast<__half2*>(&w[j]), __float2half2_rn(f));
-                                    w[j] = *reinterpret_cast<const uint32_t*>(&h);
-                                } else {
-                                    const __nv_bfloat162 h = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&w[j]), __float2bfloat162_rn(f));
-                                    w[j] = *reinterpret_cast<const uint32_t*>(&h);
-                                }
-                            }
-                            tmem_st16(s_addr + i * 16, w);
+                            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                            tmem_st16(o_addr + i, o);
                         }
                     }
-                    const float b = add - (ref == neg ? 0.f : ref) + (k8 ? kLift : 0.f);
+#pragma unroll 1
+                    for (int i = 0; i < done; ++i) {
+                        uint32_t w[16];
+                        tmem_wait_st();
+                        tmem_ld16(s_addr + i * 16, w);
+                        tmem_wait_ld(w);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            if (k8) {
+                                const __half2 h = __hmul2(*reinterpret_cast<__half2*>(&w[j]), __float2half2_rn(f));
+                                w[j] = *reinterpret_cast<const uint32_t*>(&h);
+                            } else {
+                                const __nv_bfloat162 h = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&w[j]), __float2bfloat162_rn(f));
+                                w[j] = *reinterpret_cast<const uint32_t*>(&h);
+                            }
+                        }
+                        tmem_st16(s_addr + i * 16, w);
+                    }
+                };
+                // Weights of 32 scores, to columns [16 ch, 16 ch + 16), whose scores have been read; their sum.
+                auto weigh = [&](const float (&s)[32], int ch, float b) {
+                    float2 part[2];
                     uint32_t w[16];
 #pragma unroll
                     for (int i = 0; i < 32; i += 2) {
                         float2 x = fma2(make_float2(s[i], s[i + 1]), make_float2(c, c), make_float2(b, b));
                         x.x = exp2_fast(x.x), x.y = exp2_fast(x.y);
-                        part = add2(part, x);
+                        part[(i >> 1) & 1] = i < 4 ? x : add2(part[(i >> 1) & 1], x);
                         if (k8) {
                             const __half2 h = __floats2half2_rn(x.x, x.y);
                             w[i / 2] = *reinterpret_cast<const uint32_t*>(&h);
@@ -285,21 +306,31 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
                         }
                     }
                     tmem_st16(s_addr + ch * 16, w);
+                    return add2(part[0], part[1]);
                 };
-                // 32 scores at a time, the next ones on their way meanwhile.  The weights of a chunk go over
-                // scores that have been read: chunk ch's over columns [16 ch, 16 ch + 16).
-                float sa[32], sb[32];
-                tmem_ld32(s_addr, sa);
-#pragma unroll 1
+                // 64 scores at a time, first weighed against the reference as it stands: a weight above 2^kSlack
+                // (times the lift) shows in their sum, so the usual step looks for no maximum at all.
+                constexpr float kMost = k8 ? 32768.f : 256.f;  // 2^(kSlack + kLift), 2^kSlack
+#pragma unroll
                 for (int ch = 0; ch < 4; ch += 2) {
+                    float sa[32], sb[32];
+                    tmem_ld32(s_addr + ch * 32, sa);
+                    tmem_ld32(s_addr + ch * 32 + 32, sb);
                     tmem_wait_ld(sa);
-                    tmem_ld32(s_addr + (ch + 1) * 32, sb);
-                    chunk(sa, ch);
                     tmem_wait_ld(sb);
-                    if (ch == 0) tmem_ld32(s_addr + 64, sa);
-                    chunk(sb, ch + 1);
+                    mask(sa, ch);
+                    mask(sb, ch + 1);
+                    float b = add - (ref == neg ? 0.f : ref) + (k8 ? kLift : 0.f);
+                    float2 x = add2(weigh(sa, ch, b), weigh(sb, ch + 1, b));
+                    if (__any_sync(0xFFFFFFFFu, !(x.x + x.y <= kMost) || ref == neg)) {
+                        raise(fmaf(fmaxf(largest(sa), largest(sb)), c, add), ch);
+                        b = add - (ref == neg ? 0.f : ref) + (k8 ? kLift : 0.f);
+                        tmem_wait_st();
+                        x = add2(weigh(sa, ch, b), weigh(sb, ch + 1, b));
+                    }
+                    total = add2(total, x);
                 }
-                sum = fmaf(part.x + part.y, inv, sum);
+                sum = fmaf(total.x + total.y, inv, sum);
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(&ctl.p_full[m]);
@@ -333,65 +364,78 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
             }
     } else if (warp == Shape::kMmaWarp) {
         // ---------------------------------------------------------------------------- products
-        if (lane == 0) {
-            constexpr uint32_t kScoreDesc = mma_desc(128, 128, !k8, false), kOutDesc = mma_desc(128, D, !k8, true);
-            const uint32_t q_addr = smem_u32(q_tile), ring_addr = smem_u32(ring);
-            uint32_t q_phase = 0, p_phase = 0, tail_phase = 0;
-            int64_t tile = 0;  // tiles consumed from the ring
-            auto scores = [&](int m, int slot) {
+        // The whole warp walks along and one lane issues: a hand-over costs a few instructions, and the
+        // descriptors are constants added to three bases.
+        constexpr uint32_t kScoreDesc = mma_desc(128, 128, !k8, false), kOutDesc = mma_desc(128, D, !k8, true);
+        const uint64_t q_desc = smem_desc(smem_u32(q_tile), 16), k_desc = smem_desc(smem_u32(ring), 16);
+        const uint64_t v_desc = smem_desc(smem_u32(ring), 128 * 128);
+        const bool leader = elect_one();
+        uint32_t q_phase = 0, p_phase = 0, tail_phase = 0;
+        uint32_t tile_slot = 0, tile_phase = 0;  // the ring's next tile
+        auto take = [&]() {                      // wait for it; its slot
+            alive = wait_all(&ctl.full[tile_slot], tile_phase);
+            const uint32_t slot = tile_slot;
+            if (++tile_slot == kRing) tile_slot = 0, tile_phase ^= 1;
+            return slot;
+        };
+        auto scores = [&](int m, uint32_t slot) {
+            if (leader) {
+                const uint64_t qd = q_desc + (uint64_t)(m * (Shape::kTileBytes >> 4)), kd = k_desc + (uint64_t)(slot * (Shape::kTileBytes >> 4));
 #pragma unroll
                 for (int s = 0; s < D / 16; ++s) {
-                    const uint32_t off = (uint32_t)((s >> 2) * (128 * 128) + (s & 3) * 32);
-                    mma_ss(tmem + Shape::kScoreCol + 128 * m, smem_desc(q_addr + m * Shape::kTileBytes + off, 16),
-                           smem_desc(ring_addr + slot * Shape::kTileBytes + off, 16), kScoreDesc, s > 0);
+                    const uint64_t off = (uint64_t)(((s >> 2) * (128 * 128) + (s & 3) * 32) >> 4);
+                    mma_ss(tmem + Shape::kScoreCol + 128 * m, qd + off, kd + off, kScoreDesc, s > 0);
                 }
                 tc_commit(&ctl.s_full[m]);
-            };
-            for (int64_t u = u0; u < u1 && alive;) {
-                const int64_t item = u / p.nblk, end = min(u1, (item + 1) * p.nblk);
-                if (!(alive = wait(&ctl.q_full, q_phase++ & 1))) break;
-                int kslot = (int)(tile % kRing);
-                if (!(alive = wait(&ctl.full[kslot], (uint32_t)(tile / kRing) & 1))) break;
-                ++tile;
-                tc_fence_after();
-                for (int m = 0; m < kTiles; ++m) scores(m, kslot);
-                tc_commit(&ctl.empty[kslot]);
-                for (int64_t v = u; v < end && alive; ++v) {
-                    const int vslot = (int)(tile % kRing);
-                    if (!(alive = wait(&ctl.full[vslot], (uint32_t)(tile / kRing) & 1))) break;
-                    ++tile;
-                    if (!k8 && a.a.prefix_len < (v - item * p.nblk + 1) * kBlockKeys)  // its rows past the prefix are zeroed
-                        if (!(alive = wait(&ctl.tail, tail_phase++ & 1))) break;
-                    for (int m = 0; m < kTiles; ++m) {
-                        if (!(alive = wait(&ctl.p_full[m], p_phase & 1))) break;
-                        tc_fence_after();
+            }
+        };
+        for (int64_t u = u0; u < u1 && alive;) {
+            const int64_t item = u / p.nblk, end = min(u1, (item + 1) * p.nblk);
+            if (!(alive = wait_all(&ctl.q_full, q_phase++ & 1))) break;
+            uint32_t kslot = take();
+            if (!alive) break;
+            tc_fence_after();
+#pragma unroll
+            for (int m = 0; m < kTiles; ++m) scores(m, kslot);
+            if (leader) tc_commit(&ctl.empty[kslot]);
+            for (int64_t v = u; v < end && alive; ++v) {
+                const uint32_t vslot = take();
+                if (!alive) break;
+                if (!k8 && a.a.prefix_len < (v - item * p.nblk + 1) * kBlockKeys)  // its rows past the prefix are zeroed
+                    if (!(alive = wait_all(&ctl.tail, tail_phase++ & 1))) break;
+#pragma unroll
+                for (int m = 0; m < kTiles; ++m) {
+                    if (!(alive = wait_all(&ctl.p_full[m], p_phase & 1))) break;
+                    tc_fence_after();
+                    if (leader) {
+                        const uint64_t vd = v_desc + (uint64_t)(vslot * (Shape::kTileBytes >> 4));
 #pragma unroll
                         for (int s = 0; s < kBlockKeys / 16; ++s)
-                            mma_ts(tmem + Shape::kOutCol + D * m, tmem + Shape::kScoreCol + 128 * m + s * 8,
-                                   smem_desc(ring_addr + vslot * Shape::kTileBytes + s * 2048, 128 * 128), kOutDesc, v > u || s > 0);
-                        if (v + 1 == end) {
-                            tc_commit(&ctl.o_full[m]);
-                        } else {
-                            if (m == 0) {
-                                kslot = (int)(tile % kRing);
-                                if (!(alive = wait(&ctl.full[kslot], (uint32_t)(tile / kRing) & 1))) break;
-                                ++tile;
-                                tc_fence_after();
-                            }
-                            scores(m, kslot);
-                        }
+                            mma_ts(tmem + Shape::kOutCol + D * m, tmem + Shape::kScoreCol + 128 * m + s * 8, vd + (uint64_t)(s * (2048 >> 4)),
+                                   kOutDesc, s > 0 || v > u);
+                        if (v + 1 == end) tc_commit(&ctl.o_full[m]);
                     }
-                    if (!alive) break;
-                    ++p_phase;
+                    if (v + 1 < end) {
+                        if (m == 0) {
+                            kslot = take();
+                            if (!alive) break;
+                            tc_fence_after();
+                        }
+                        scores(m, kslot);
+                    }
+                }
+                if (!alive) break;
+                ++p_phase;
+                if (leader) {
                     tc_commit(&ctl.empty[vslot]);
                     if (v + 1 < end) tc_commit(&ctl.empty[kslot]);
                 }
-                u = end;
             }
-            // Products in flight end before the tensor memory is given back (bounded, as every wait).
-            tc_commit(&ctl.drain);
-            mbar_wait_bounded(&ctl.drain, 0, kAttnWaitNs);
+            u = end;
         }
+        // Products in flight end before the tensor memory is given back (bounded, as every wait).
+        if (leader) tc_commit(&ctl.drain);
+        mbar_wait_bounded(&ctl.drain, 0, kAttnWaitNs);
         __syncwarp();
     } else if (warp == Shape::kLoadWarp) {
         // ---------------------------------------------------------------------------- loads
@@ -461,79 +505,93 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
             const int64_t last = tile - 1 - i;
             if (last >= 0) mbar_wait_bounded(&filled[last % kSlots], (uint32_t)(last / kSlots) & 1, kAttnWaitNs);
         }
-    } else {
+    } else if (k8 && warp < Shape::kConvertWarp) {
+        // ---------------------------------------------------------------------------- scales
+        // A tile's unit is a power of two no larger than its largest scale and more than half of it (1 if
+        // there is none); a token's factor is its scale in that unit.  One warp for every tile in turn: a
+        // barrier's phase may only be waited for by a role that sees each of its phases.
+        const int64_t tiles = warp == Shape::kScaleWarp ? 2 * (u1 - u0) : 0;
+        int64_t token = (u0 - u0 / p.nblk * p.nblk) * kBlockKeys;
+        for (int64_t tile = 0; tile < tiles; ++tile) {
+            const int rs = (int)(tile % kRaw), slot = (int)((tile >> 1) % kScalars);
+            const bool values = tile & 1;
+            const int64_t left = a.a.prefix_len - token;
+            if (values) token = left <= kBlockKeys ? 0 : token + kBlockKeys;
+            if (!(alive = wait_all(&ctl.raw_full[rs], (uint32_t)(tile / kRaw) & 1))) break;
+            const uint2 w = *reinterpret_cast<const uint2*>(raw_ring + rs * Shape::kRawBytes + 128 * D + lane * 8);
+            float s[4] = {__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
+                          __uint_as_float(w.y & 0xFFFF0000u)};
+            float most = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (lane * 4 + i >= left) s[i] = 0.f;  // past the prefix: anything
+                most = fmaxf(most, s[i]);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+            const int e = most > 0.f ? max(-126, min((int)(__float_as_uint(most) >> 23) - 127, 126)) : 0;
+            const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+            const __half2 lo = __floats2half2_rn(s[0] * inv, s[1] * inv), hi = __floats2half2_rn(s[2] * inv, s[3] * inv);
+            *reinterpret_cast<uint2*>(&ctl.factor[rs][lane * 4]) =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+            if (lane == 0) {
+                if (values)
+                    ctl.value_exp[slot] = (float)e;
+                else
+                    ctl.key_unit[slot] = __uint_as_float((uint32_t)(127 + e) << 23);
+            }
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&ctl.factor_full[rs]);
+                if (values) mbar_arrive(&ctl.scalar_full[slot]);
+            }
+        }
+    } else if (k8) {
         // ---------------------------------------------------------------------------- 8-bit codes to float16
-        constexpr int kPieces = D / 16;                // 16-byte pieces of a code row
-        constexpr int kRowsPerStep = 128 / kPieces;    // rows that the 128 threads convert at a time
-        const int t = (int)threadIdx.x - Shape::kConvertWarp * 32, cw = t >> 5;
+        constexpr int kPieces = D / 16;                           // 16-byte pieces of a code row
+        constexpr int kThreadsConv = Shape::kConvertWarps * 32;
+        constexpr int kSteps = 128 * kPieces / kThreadsConv, kRowsPerStep = kThreadsConv / kPieces;
+        const int t = (int)threadIdx.x - Shape::kConvertWarp * 32;
         const int piece = t % kPieces, sub = t / kPieces;
         // The eight lanes of a 128-byte code row fill both column blocks; the upper four write their halves the
         // other way round, so that the eight 16-byte stores of a phase hit different banks.
         const bool swap = piece >= 4;
-        // A barrier of the four warps that also tells whether `ok` holds in all of them.
-        auto all_of_four_warps = [](bool ok) {
-            int r;
-            asm volatile(
-                "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\t"
-                "barrier.cta.red.and.pred q, 1, 128, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
-                : "=r"(r)
-                : "r"((int)ok)
-                : "memory");
-            return r != 0;
-        };
         int64_t token = (u0 - u0 / p.nblk * p.nblk) * kBlockKeys;
         const int64_t tiles = 2 * (u1 - u0);
-        for (int64_t tile = 0; tile < tiles; ++tile) {
-            const int par = (int)(tile & 1);  // keys, values
-            const int rs = (int)(tile % kRaw), slot = (int)(tile % kRing);
-            const int left = (int)min((int64_t)kBlockKeys, a.a.prefix_len - token);
-            if (par) {
-                token += kBlockKeys;
-                if (token >= a.a.prefix_len) token = 0;
-            }
+        int rs = 0, slot = 0;
+        uint32_t raw_phase = 0, phase = 1;  // of the code tiles; of the tiles' last use (none yet)
+        for (int64_t tile = 0; tile < tiles && alive; ++tile) {
+            const int64_t left = a.a.prefix_len - token;
+            if (tile & 1) token = left <= kBlockKeys ? 0 : token + kBlockKeys;
             const unsigned char* raw = raw_ring + rs * Shape::kRawBytes;
-            if (alive) alive = wait_all(&ctl.raw_full[rs], (uint32_t)(tile / kRaw) & 1);
-            // The tile's unit, a power of two no larger than the largest scale and more than half of it (1 if
-            // there is none), and each token's factor.
-            const float s = alive && t < left ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(raw + 128 * D)[t]) : 0.f;
-            float most = s;
+            if (!(alive = wait_all(&ctl.factor_full[rs], raw_phase))) break;  // and with it the codes
+            if (!(alive = wait_all(&ctl.raw_full[rs], raw_phase))) break;
+            uint4 x[kSteps];
+            __half2 f[kSteps];
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
-            if (lane == 0) ctl.warp_max[par][cw] = most;
-            if (!(alive = all_of_four_warps(alive))) break;  // the four warps go on or give up together
-            const float4 mx = *reinterpret_cast<const float4*>(ctl.warp_max[par]);
-            most = fmaxf(fmaxf(mx.x, mx.y), fmaxf(mx.z, mx.w));
-            const int e = most > 0.f ? max(-126, min((int)(__float_as_uint(most) >> 23) - 127, 126)) : 0;
-            ctl.factor[par][t] = __float2half_rn(s * __uint_as_float((uint32_t)(127 - e) << 23));
-            all_of_four_warps(true);
-            if (tile >= kRing) alive = wait_all(&ctl.empty[slot], (uint32_t)(tile / kRing - 1) & 1);
-            if (!alive) continue;
-            const int block_slot = (int)((tile >> 1) % kScalars);
-            if (t == 0) {
-                if (par)
-                    ctl.value_exp[block_slot] = (float)e;
-                else
-                    ctl.key_unit[block_slot] = __uint_as_float((uint32_t)(127 + e) << 23);
-            }
-            if (par) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl.scalar_full[block_slot]);
-            }
-            unsigned char* dst = ring + slot * Shape::kTileBytes;
-#pragma unroll 4
-            for (int i = 0; i < kPieces; ++i) {
+            for (int i = 0; i < kSteps; ++i) {
                 const int r = i * kRowsPerStep + sub;
-                uint4 x = *reinterpret_cast<const uint4*>(raw + r * D + piece * 16);
-                if (r >= left) x = make_uint4(0u, 0u, 0u, 0u);  // past the prefix: anything
-                const __half2 f = __half2half2(ctl.factor[par][r]);
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                x[i] = *reinterpret_cast<const uint4*>(raw + r * D + piece * 16);
+                f[i] = __half2half2(ctl.factor[rs][r]);
+            }
+            if (left < kBlockKeys) {  // past the prefix: anything
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i)
+                    if (i * kRowsPerStep + sub >= left) x[i] = make_uint4(0u, 0u, 0u, 0u);
+            }
+            if (!(alive = wait_all(&ctl.empty[slot], phase))) break;
+            unsigned char* dst = ring + slot * Shape::kTileBytes;
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                const int r = i * kRowsPerStep + sub;
+                const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
                 uint32_t h[8];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     code_pairs<kFormat>(w[j], h[2 * j], h[2 * j + 1]);
 #pragma unroll
                     for (int k = 2 * j; k < 2 * j + 2; ++k) {
-                        const __half2 y = __hmul2(*reinterpret_cast<__half2*>(&h[k]), f);
+                        const __half2 y = __hmul2(*reinterpret_cast<__half2*>(&h[k]), f[i]);
                         h[k] = *reinterpret_cast<const uint32_t*>(&y);
                     }
                 }
@@ -547,6 +605,8 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
                 mbar_arrive(&ctl.full[slot]);
                 mbar_arrive(&ctl.raw_empty[rs]);
             }
+            if (++rs == kRaw) rs = 0, raw_phase ^= 1;
+            if (++slot == kRing) slot = 0, phase ^= 1;
         }
     }
     tc_fence_before();
