@@ -40,6 +40,12 @@ constexpr int kRowsBlock = 64;
 constexpr int64_t kTensorRows = 33;
 // Sequences (times heads and row tiles) per SM from which each warp takes one for itself.
 constexpr int64_t kOneWarpItems = 8;
+// Tokens (times triples of sequence, key head and row tile) up to which each sequence walks over the prefix
+// itself: one launch instead of two, and nothing to join, for reading the prefix again from the L2 cache.
+constexpr int64_t kAloneTokens = 65536, kAloneTensorTokens = 32768;
+// Tokens of one sequence (at most) from which the own tokens are cut evenly over the SMs, for up to
+// kLinePairs sequences times row tiles.
+constexpr int64_t kLineTokens = 2048, kLinePairs = 1024;
 
 int plan_attention(const tps_kv_cache& c, const tps_attention& a, int sms, tps::AttnPlan* out)
 {
@@ -48,25 +54,46 @@ int plan_attention(const tps_kv_cache& c, const tps_attention& a, int sms, tps::
     const int64_t own_rows = (int64_t)a.q_len * G;
     if (own_rows > (1 << 24) || a.B > (int64_t(1) << 31) / (own_rows * c.n_heads)) return TPS_ERR_ARG;
     p.R = a.B * own_rows;
-    p.suffix_tiles = (int)((own_rows + 15) / 16);
-    p.tensor = p.R >= kTensorRows;
-    p.tile_rows = !p.tensor ? 16 : (p.R <= 128 ? 128 : 256);
-    p.block_keys = p.tensor ? 128 : kRowsBlock;
-    p.n_tiles = (int)((p.R + p.tile_rows - 1) / p.tile_rows);
-    p.nblk = (a.prefix_len + p.block_keys - 1) / p.block_keys;
-    p.items = (int64_t)p.n_tiles * c.n_heads;
-    p.units = p.items * p.nblk;
-    p.ctas = std::min<int64_t>(p.units, (int64_t)sms * (p.tensor ? 1 : kRowsCtasPerSm));
-    p.pieces = p.units ? p.ctas + p.items : 0;
-    // Several CTAs share one sequence's own tokens where there are few sequences and many tokens.
-    const int64_t alone = a.B * c.n_heads * p.suffix_tiles;
-    const int64_t tokens = a.table_width * c.page_size;
+    p.suffix_rows = own_rows <= 8 ? 8 : 16;
+    p.suffix_tiles = (int)((own_rows + p.suffix_rows - 1) / p.suffix_rows);
+    const int64_t alone = a.B * c.n_heads * p.suffix_tiles;  // (sequence, key head, tile) triples
+    p.shared = a.prefix_len > 0 && a.B > 1 && alone > (p.R >= kTensorRows ? kAloneTensorTokens : kAloneTokens) / a.prefix_len;
+    if (p.shared) {
+        p.tensor = p.R >= kTensorRows;
+        p.tile_rows = p.tensor ? (p.R <= 128 ? 128 : 256) : (p.R <= 8 ? 8 : 16);
+        p.block_keys = p.tensor ? 128 : kRowsBlock;
+        const int64_t n_tiles = (p.R + p.tile_rows - 1) / p.tile_rows, items = n_tiles * c.n_heads;
+        p.nblk = (int)((a.prefix_len + p.block_keys - 1) / p.block_keys);
+        if (items > INT32_MAX / p.nblk) return TPS_ERR_ARG;
+        p.n_tiles = (int)n_tiles;
+        p.items = (int)items;
+        p.units = p.items * p.nblk;
+        // No more CTAs than the longest share needs: fewer pieces to join, and SMs left for the own tokens.
+        const int most = sms * (p.tensor ? 1 : kRowsCtasPerSm);
+        p.share = (int)(((int64_t)p.units + most - 1) / most);
+        p.ctas = (int)(((int64_t)p.units + p.share - 1) / p.share);
+        p.pieces = (int64_t)p.ctas + p.items;
+    }
+    // Several CTAs share one sequence's tokens where there are few sequences and many tokens, as long as
+    // all of them are resident at once (by the kernel's registers and shared memory).
+    const int64_t resident = (int64_t)sms * (p.suffix_rows == 8 && c.format != TPS_KV_BF16 ? 4 : 3);
+    const int64_t tokens = a.table_width * c.page_size + (p.shared ? 0 : a.prefix_len);
     p.one_warp = alone >= kOneWarpItems * (int64_t)sms;
+    p.line = !p.one_warp && a.B * p.suffix_tiles <= kLinePairs && tokens >= kLineTokens;
     p.cluster = 1;
-    while (!p.one_warp && p.cluster < 8 && alone * p.cluster < 2 * (int64_t)sms && tokens >= (int64_t)p.cluster * 512) p.cluster *= 2;
+    while (!p.one_warp && !p.line && p.cluster < 8 && alone * p.cluster * 2 <= resident && tokens >= (int64_t)p.cluster * 256)
+        p.cluster *= 2;
     if (alone * p.cluster > INT32_MAX - 4) return TPS_ERR_ARG;
     p.off_ml = (size_t)p.pieces * p.tile_rows * c.head_dim * sizeof(float);
     p.bytes = p.off_ml + (size_t)p.pieces * p.tile_rows * sizeof(float2);
+    if (p.line) {
+        p.line_ctas = 3 * (int64_t)sms;  // as many as are resident
+        p.line_pieces = p.line_ctas + alone;
+        p.off_line_part = (p.bytes + 255) / 256 * 256;
+        p.off_line_ml = p.off_line_part + (size_t)p.line_pieces * p.suffix_rows * c.head_dim * sizeof(float);
+        p.off_line = (p.off_line_ml + (size_t)p.line_pieces * p.suffix_rows * sizeof(float2) + 255) / 256 * 256;
+        p.bytes = p.off_line + (size_t)(a.B * p.suffix_tiles + 1) * sizeof(int64_t);
+    }
     *out = p;
     return TPS_OK;
 }
@@ -193,6 +220,9 @@ int tps_prefix_attention(const tps_kv_cache* cache, const tps_attention* args, v
     }
     a.part = reinterpret_cast<float*>(ws);
     a.ml = reinterpret_cast<float2*>(ws + a.p.off_ml);
+    a.line_part = reinterpret_cast<float*>(ws + a.p.off_line_part);
+    a.line_ml = reinterpret_cast<float2*>(ws + a.p.off_line_ml);
+    a.line = reinterpret_cast<int64_t*>(ws + a.p.off_line);
     if (a.p.units) {
         if (!a.p.tensor)
             e = tps::launch_attn_prefix_rows(a, st);
@@ -201,7 +231,8 @@ int tps_prefix_attention(const tps_kv_cache* cache, const tps_attention* args, v
                 : cache->format == TPS_KV_FP8 ? tps::launch_attn_prefix_fp8(a, st)
                                               : tps::launch_attn_prefix_int8(a, st);
     }
-    if (e == cudaSuccess) e = tps::launch_attn_suffix(a, a.p.units > 0, st);
+    if (e == cudaSuccess)
+        e = a.p.line ? tps::launch_attn_line(a, a.p.units > 0, st) : tps::launch_attn_suffix(a, a.p.units > 0, st);
     if (a.p.bytes && !args->workspace) {
         const cudaError_t ef = cudaFreeAsync(ws, st);
         if (e == cudaSuccess) e = ef;

@@ -62,6 +62,7 @@ template <int D, int kFormat, int kTiles> struct PrefixShape {
         uint32_t tmem;
         int abort, bad;
         float key_unit[kScalars], value_exp[kScalars];
+        alignas(16) __nv_bfloat16 key_scale[kFormat == TPS_KV_INT8 ? kScalars : 1][128];  // int8: of the block's tokens
         alignas(16) __half factor[kRaw][128];  // of the tokens of a code tile
     };
     static constexpr size_t kSmem =
@@ -94,6 +95,48 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b)
     return d;
 }
 
+// A CTA's way along the line of blocks, item by item.
+struct Way {
+    int item, head, tile, block, left;  // tile: row tile of the head; block: of the item; left: blocks of the CTA from here on
+    __device__ __forceinline__ explicit Way(const AttnPlan& p)
+    {
+        const int u0 = (int)blockIdx.x * p.share;
+        left = min(p.share, p.units - u0);
+        item = u0 / p.nblk;
+        block = u0 - item * p.nblk;
+        head = item / p.n_tiles;
+        tile = item - head * p.n_tiles;
+    }
+    __device__ __forceinline__ int blocks(const AttnPlan& p) const { return min(left, p.nblk - block); }  // of this item
+    __device__ __forceinline__ void next(const AttnPlan& p)
+    {
+        left -= blocks(p);
+        block = 0;
+        ++item;
+        if (++tile == p.n_tiles) tile = 0, ++head;
+    }
+    __device__ __forceinline__ void step(const AttnPlan& p)  // one block on
+    {
+        --left;
+        if (++block == p.nblk) {
+            block = 0;
+            ++item;
+            if (++tile == p.n_tiles) tile = 0, ++head;
+        }
+    }
+};
+
+// A place in a ring of barriers: which one, and the parity of its present phase.
+template <int kSlots> struct Turn {
+    int slot = 0;
+    uint32_t parity;
+    __device__ __forceinline__ explicit Turn(uint32_t parity_) : parity(parity_) {}
+    __device__ __forceinline__ void next()
+    {
+        if (++slot == kSlots) slot = 0, parity ^= 1;
+    }
+};
+
 template <int D, int kFormat, int kTiles>
 __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
     attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap)
@@ -111,10 +154,10 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
 
     const AttnPlan& p = a.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t u0 = (int64_t)blockIdx.x * p.units / p.ctas, u1 = ((int64_t)blockIdx.x + 1) * p.units / p.ctas;
+    const int prefix = (int)a.a.prefix_len;
 
     if (threadIdx.x == 0) {
-        mbar_init(&ctl.q_full, 128 * kTiles);
+        mbar_init(&ctl.q_full, 4 * kTiles);
         for (int i = 0; i < kRing; ++i) mbar_init(&ctl.full[i], k8 ? Shape::kConvertWarps : 1), mbar_init(&ctl.empty[i], 1);
         for (int i = 0; i < kTiles; ++i) mbar_init(&ctl.s_full[i], 1), mbar_init(&ctl.p_full[i], 128), mbar_init(&ctl.o_full[i], 1);
         for (int i = 0; i < kScalars; ++i) mbar_init(&ctl.scalar_full[i], 1);
@@ -153,7 +196,6 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
     // The same for a whole warp, whose lanes go on or give up together.
     auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait(bar, parity)) != 0; };
     bool alive = true;
-
     if constexpr (Shape::kSplitRegs) {
         if (warp < 4 * kTiles)
             asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Shape::kRegsSoftmax));
@@ -169,77 +211,102 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
         const uint32_t s_addr = tmem + lanes + Shape::kScoreCol + 128 * m, o_addr = tmem + lanes + Shape::kOutCol + D * m;
         const float neg = -__int_as_float(0x7F800000);
         unsigned char* my_q = q_tile + m * Shape::kTileBytes;
-        uint32_t s_phase = 0, o_phase = 0;
-        int64_t block = 0;  // blocks this CTA has passed
-        const bool flip = a.qk_scale < 0.f;
+        uint32_t s_parity = 0, o_parity = 0;
+        Turn<kScalars> scalar(0);
+        const uint32_t sign = a.qk_scale < 0.f ? 0x80008000u : 0u;
         const float unit = fmaxf(fabsf(a.qk_scale), 1e-30f);  // never 0: a masked score times it stays -inf
-        for (int64_t u = u0; u < u1 && alive;) {
-            const int64_t item = u / p.nblk, end = min(u1, (item + 1) * p.nblk);
-            const int head = (int)(item / p.n_tiles);
-            const int64_t row = (item - (int64_t)head * p.n_tiles) * (128 * kTiles) + in_tile;
-            // the query row, as it is (bf16) or brought into float16's range
+        Way way(p);
+        for (; way.left > 0 && alive; way.next(p)) {
+            // The warp's 32 query rows, D / 8 lanes to a row: as they are (bf16) or brought into float16's range.
             float row_unit = unit;
             {
-                uint4 w[D / 8];
-                if (row < p.R) {
-                    const int64_t bt = row / a.G;
-                    const uint4* src = reinterpret_cast<const uint4*>(
-                        static_cast<const __nv_bfloat16*>(a.a.q) + (bt * a.a.n_q_heads + (int64_t)head * a.G + (row - bt * a.G)) * D);
-#pragma unroll
-                    for (int c = 0; c < D / 8; ++c) w[c] = src[c];
-                } else {
-#pragma unroll
-                    for (int c = 0; c < D / 8; ++c) w[c] = make_uint4(0u, 0u, 0u, 0u);
+                constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes of a row, rows at a time
+                const int piece = lane % kLanes, sub = lane / kLanes;
+                const int64_t first = (int64_t)way.tile * (128 * kTiles) + warp * 32;
+                int64_t bt = first + sub;
+                int gi = 0;  // row = bt G + gi
+                if (a.G > 1) {
+                    bt = first < 0x7FFFFFFF ? (uint32_t)(first + sub) / (uint32_t)a.G : (first + sub) / a.G;
+                    gi = (int)(first + sub - bt * a.G);
                 }
-                const uint32_t sign = flip ? 0x80008000u : 0u;
-                float f = 1.f;
-                if (k8) {
-                    float amax = 0.f;
+                const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.a.q) + (int64_t)way.head * a.G * D + piece * 8;
 #pragma unroll
-                    for (int c = 0; c < D / 8; ++c) {
-                        const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+                for (int half = 0; half < 2; ++half) {  // sixteen rows' loads on the way at once
+                    constexpr int kSteps = 16 / kRows;
+                    uint4 w[kSteps];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float lo = fabsf(__uint_as_float(x[i] << 16)), hi = fabsf(__uint_as_float(x[i] & 0xFFFF0000u));
-                            amax = lo < -neg ? fmaxf(amax, lo) : amax;
-                            amax = hi < -neg ? fmaxf(amax, hi) : amax;
-                        }
+                    for (int i = 0; i < kSteps; ++i) {
+                        const int r = half * 16 + i * kRows + sub;
+                        w[i] = first + r < p.R ? *reinterpret_cast<const uint4*>(q + (bt * a.a.n_q_heads + gi) * D) : make_uint4(0u, 0u, 0u, 0u);
+                        gi += kRows;
+                        while (gi >= a.G) gi -= a.G, ++bt;
                     }
-                    f = f16_row_scale(amax);
-                    row_unit = unit / f;
-                }
 #pragma unroll
-                for (int c = 0; c < D / 8; ++c) {
-                    uint32_t x[4] = {w[c].x ^ sign, w[c].y ^ sign, w[c].z ^ sign, w[c].w ^ sign};
-                    if (k8) {
+                    for (int i = 0; i < kSteps; ++i) {
+                        const int r = half * 16 + i * kRows + sub;
+                        uint32_t x[4] = {w[i].x ^ sign, w[i].y ^ sign, w[i].z ^ sign, w[i].w ^ sign};
+                        if (k8) {
+                            float amax = 0.f;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const __half2 h = __floats2half2_rn(__uint_as_float(x[i] << 16) * f, __uint_as_float(x[i] & 0xFFFF0000u) * f);
-                            x[i] = *reinterpret_cast<const uint32_t*>(&h);
+                            for (int k = 0; k < 4; ++k) {
+                                const float lo = fabsf(__uint_as_float(x[k] << 16)), hi = fabsf(__uint_as_float(x[k] & 0xFFFF0000u));
+                                amax = lo < -neg ? fmaxf(amax, lo) : amax;
+                                amax = hi < -neg ? fmaxf(amax, hi) : amax;
+                            }
+#pragma unroll
+                            for (int o = kLanes / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+                            const float f = f16_row_scale(amax);
+                            // lane r of the warp answers for row r
+#pragma unroll
+                            for (int k = 0; k < kRows; ++k) {
+                                const float other = __shfl_sync(0xFFFFFFFFu, f, k * kLanes);
+                                if (lane == half * 16 + i * kRows + k) row_unit = unit / other;
+                            }
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const __half2 h = __floats2half2_rn(__uint_as_float(x[k] << 16) * f, __uint_as_float(x[k] & 0xFFFF0000u) * f);
+                                x[k] = *reinterpret_cast<const uint32_t*>(&h);
+                            }
                         }
+                        *reinterpret_cast<uint4*>(my_q + tile_byte((warp & 3) * 32 + r, piece)) = make_uint4(x[0], x[1], x[2], x[3]);
                     }
-                    *reinterpret_cast<uint4*>(my_q + tile_byte(in_tile & 127, c)) = make_uint4(x[0], x[1], x[2], x[3]);
                 }
                 fence_proxy_async();
-                mbar_arrive(&ctl.q_full);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl.q_full);
             }
             float ref = neg, sum = 0.f;
-            for (int64_t v = u; v < end; ++v, ++block) {
-                if (!(alive = wait_all(&ctl.s_full[m], s_phase & 1))) break;
-                ++s_phase;
+            const int blocks = way.blocks(p);
+            for (int v = 0; v < blocks; ++v) {
+                if (!(alive = wait_all(&ctl.s_full[m], s_parity))) break;
+                s_parity ^= 1;
                 tc_fence_after();
                 float c = row_unit, add = 0.f, inv = 1.f;
+                const int scales = scalar.slot;
                 if (k8) {
-                    const int slot = (int)(block % kScalars);
-                    if (!(alive = wait_all(&ctl.scalar_full[slot], (uint32_t)(block / kScalars) & 1))) break;
-                    c *= ctl.key_unit[slot];
-                    add = ctl.value_exp[slot];
+                    if (!(alive = wait_all(&ctl.scalar_full[scalar.slot], scalar.parity))) break;
+                    c *= ctl.key_unit[scalar.slot];
+                    add = ctl.value_exp[scalar.slot];
                     inv = exp2_fast(-add);
+                    scalar.next();
                 }
-                const int64_t left = a.a.prefix_len - (v - item * p.nblk) * kBlockKeys;
+                const int left = prefix - (way.block + v) * kBlockKeys;
                 float2 total = make_float2(0.f, 0.f);
-                // Scores past the prefix become -inf.
-                auto mask = [&](float (&s)[32], int ch) {
+                // int8: a score's key scale (the codes are in the tile as they are).  Scores past the prefix become -inf.
+                auto ready = [&](float (&s)[32], int ch) {
+                    if constexpr (kFormat == TPS_KV_INT8) {
+                        const uint4* f = reinterpret_cast<const uint4*>(ctl.key_scale[scales] + ch * 32);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint4 x = f[i];
+                            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                s[8 * i + 2 * k] *= __uint_as_float(w[k] << 16);
+                                s[8 * i + 2 * k + 1] *= __uint_as_float(w[k] & 0xFFFF0000u);
+                            }
+                        }
+                    }
                     if (left < ch * 32 + 32) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
@@ -259,7 +326,7 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
                     ref = to;
                     sum *= f;
                     total.x *= f, total.y *= f;
-                    if (v > u) {
+                    if (v > 0) {
 #pragma unroll 1
                         for (int i = 0; i < D; i += 16) {
                             uint32_t o[16];
@@ -318,8 +385,8 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
                     tmem_ld32(s_addr + ch * 32 + 32, sb);
                     tmem_wait_ld(sa);
                     tmem_wait_ld(sb);
-                    mask(sa, ch);
-                    mask(sb, ch + 1);
+                    ready(sa, ch);
+                    ready(sb, ch + 1);
                     float b = add - (ref == neg ? 0.f : ref) + (k8 ? kLift : 0.f);
                     float2 x = add2(weigh(sa, ch, b), weigh(sb, ch + 1, b));
                     if (__any_sync(0xFFFFFFFFu, !(x.x + x.y <= kMost) || ref == neg)) {
@@ -335,10 +402,9 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
                 tc_fence_before();
                 mbar_arrive(&ctl.p_full[m]);
             }
-            if (alive) alive = wait_all(&ctl.o_full[m], o_phase & 1);
-            ++o_phase;
-            const int64_t piece = blockIdx.x + item;
-            const int64_t at = piece * p.tile_rows + in_tile;
+            if (alive) alive = wait_all(&ctl.o_full[m], o_parity);
+            o_parity ^= 1;
+            const int64_t piece = (int64_t)blockIdx.x + way.item;
             if (alive) {
                 tc_fence_after();
                 float4* dst = reinterpret_cast<float4*>(a.part + piece * p.tile_rows * D) + in_tile;
@@ -349,19 +415,15 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
                     tmem_wait_ld(o);
 #pragma unroll
                     for (int j = 0; j < 32; j += 4)
-                        dst[(int64_t)((i + j) / 4) * p.tile_rows] = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                        dst[(i + j) / 4 * p.tile_rows] = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
                 }
                 tc_fence_before();
             }
-            a.ml[at] = make_float2(ref, !alive ? kPieceTimeout : (*(volatile int*)&ctl.bad ? kPieceBadPage : sum));
-            u = end;
+            a.ml[piece * p.tile_rows + in_tile] = make_float2(ref, !alive ? kPieceTimeout : (*(volatile int*)&ctl.bad ? kPieceBadPage : sum));
         }
         if (!alive)  // the pieces of the items that were not reached
-            for (int64_t u = u0; u < u1;) {
-                const int64_t item = u / p.nblk;
-                a.ml[(blockIdx.x + item) * p.tile_rows + in_tile] = make_float2(neg, kPieceTimeout);
-                u = min(u1, (item + 1) * p.nblk);
-            }
+            for (Way rest(p); rest.left > 0; rest.next(p))
+                a.ml[((int64_t)blockIdx.x + rest.item) * p.tile_rows + in_tile] = make_float2(neg, kPieceTimeout);
     } else if (warp == Shape::kMmaWarp) {
         // ---------------------------------------------------------------------------- products
         // The whole warp walks along and one lane issues: a hand-over costs a few instructions, and the
@@ -370,15 +432,15 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
         const uint64_t q_desc = smem_desc(smem_u32(q_tile), 16), k_desc = smem_desc(smem_u32(ring), 16);
         const uint64_t v_desc = smem_desc(smem_u32(ring), 128 * 128);
         const bool leader = elect_one();
-        uint32_t q_phase = 0, p_phase = 0, tail_phase = 0;
-        uint32_t tile_slot = 0, tile_phase = 0;  // the ring's next tile
-        auto take = [&]() {                      // wait for it; its slot
-            alive = wait_all(&ctl.full[tile_slot], tile_phase);
-            const uint32_t slot = tile_slot;
-            if (++tile_slot == kRing) tile_slot = 0, tile_phase ^= 1;
+        uint32_t q_parity = 0, p_parity = 0, tail_parity = 0;
+        Turn<kRing> turn(0);
+        auto take = [&]() {  // wait for the ring's next tile; its slot
+            alive = wait_all(&ctl.full[turn.slot], turn.parity);
+            const int slot = turn.slot;
+            turn.next();
             return slot;
         };
-        auto scores = [&](int m, uint32_t slot) {
+        auto scores = [&](int m, int slot) {
             if (leader) {
                 const uint64_t qd = q_desc + (uint64_t)(m * (Shape::kTileBytes >> 4)), kd = k_desc + (uint64_t)(slot * (Shape::kTileBytes >> 4));
 #pragma unroll
@@ -389,33 +451,37 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
                 tc_commit(&ctl.s_full[m]);
             }
         };
-        for (int64_t u = u0; u < u1 && alive;) {
-            const int64_t item = u / p.nblk, end = min(u1, (item + 1) * p.nblk);
-            if (!(alive = wait_all(&ctl.q_full, q_phase++ & 1))) break;
-            uint32_t kslot = take();
+        Way way(p);
+        for (; way.left > 0 && alive; way.next(p)) {
+            const int blocks = way.blocks(p);
+            if (!(alive = wait_all(&ctl.q_full, q_parity))) break;
+            q_parity ^= 1;
+            int kslot = take();
             if (!alive) break;
             tc_fence_after();
 #pragma unroll
             for (int m = 0; m < kTiles; ++m) scores(m, kslot);
             if (leader) tc_commit(&ctl.empty[kslot]);
-            for (int64_t v = u; v < end && alive; ++v) {
-                const uint32_t vslot = take();
+            for (int v = 0; v < blocks && alive; ++v) {
+                const int vslot = take();
                 if (!alive) break;
-                if (!k8 && a.a.prefix_len < (v - item * p.nblk + 1) * kBlockKeys)  // its rows past the prefix are zeroed
-                    if (!(alive = wait_all(&ctl.tail, tail_phase++ & 1))) break;
+                if (!k8 && prefix < (way.block + v + 1) * kBlockKeys) {  // its rows past the prefix are zeroed
+                    if (!(alive = wait_all(&ctl.tail, tail_parity))) break;
+                    tail_parity ^= 1;
+                }
 #pragma unroll
                 for (int m = 0; m < kTiles; ++m) {
-                    if (!(alive = wait_all(&ctl.p_full[m], p_phase & 1))) break;
+                    if (!(alive = wait_all(&ctl.p_full[m], p_parity))) break;
                     tc_fence_after();
                     if (leader) {
                         const uint64_t vd = v_desc + (uint64_t)(vslot * (Shape::kTileBytes >> 4));
 #pragma unroll
                         for (int s = 0; s < kBlockKeys / 16; ++s)
                             mma_ts(tmem + Shape::kOutCol + D * m, tmem + Shape::kScoreCol + 128 * m + s * 8, vd + (uint64_t)(s * (2048 >> 4)),
-                                   kOutDesc, s > 0 || v > u);
-                        if (v + 1 == end) tc_commit(&ctl.o_full[m]);
+                                   kOutDesc, s > 0 || v > 0);
+                        if (v + 1 == blocks) tc_commit(&ctl.o_full[m]);
                     }
-                    if (v + 1 < end) {
+                    if (v + 1 < blocks) {
                         if (m == 0) {
                             kslot = take();
                             if (!alive) break;
@@ -425,13 +491,12 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
                     }
                 }
                 if (!alive) break;
-                ++p_phase;
+                p_parity ^= 1;
                 if (leader) {
                     tc_commit(&ctl.empty[vslot]);
-                    if (v + 1 < end) tc_commit(&ctl.empty[kslot]);
+                    if (v + 1 < blocks) tc_commit(&ctl.empty[kslot]);
                 }
             }
-            u = end;
         }
         // Products in flight end before the tensor memory is given back (bounded, as every wait).
         if (leader) tc_commit(&ctl.drain);
@@ -444,109 +509,107 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
         uint64_t* filled = k8 ? ctl.raw_full : ctl.full;
         uint64_t* freed = k8 ? ctl.raw_empty : ctl.empty;
         const int box = min(a.c.page_size, kBlockKeys), boxes = kBlockKeys / box;
-        int64_t tile = 0;
-        auto page_of = [&](int64_t t) {  // the page of token t
-            int id = 0;
-            if (lane < boxes && t < a.a.prefix_len) {
-                id = a.a.prefix_pages[t >> a.page_shift];
-                if (id < 0 || id >= a.c.n_pages) {
-                    *(volatile int*)&ctl.bad = 1;
-                    id = 0;
-                }
+        auto page_of = [&](int token) { return lane < boxes && token < prefix ? a.a.prefix_pages[token >> a.page_shift] : 0; };
+        Way way(p);
+        int page = page_of(way.block * kBlockKeys + lane * box);
+        Turn<kSlots> turn(1);  // a slot's first fill waits for nothing: the phase before its first
+        int fills = 0;
+        while (way.left > 0 && alive) {
+            const int head = way.head, token = way.block * kBlockKeys, left = prefix - token;
+            const int live = min(boxes, (left + box - 1) / box);
+            const int row = (token + lane * box) & (a.c.page_size - 1);
+            int id = page;
+            if (id < 0 || id >= a.c.n_pages) {
+                *(volatile int*)&ctl.bad = 1;
+                id = 0;
             }
-            return id;
-        };
-        int64_t item = u0 / p.nblk, token = (u0 - item * p.nblk) * kBlockKeys;
-        int page = page_of(token + lane * box);
-        for (int64_t v = u0; v < u1 && alive; ++v) {
-            const int head = (int)(item / p.n_tiles);
-            const int64_t left = a.a.prefix_len - token;
-            const int live = (int)min((int64_t)boxes, (left + box - 1) / box);
-            const int row = (int)((token + lane * box) & (a.c.page_size - 1));
-            token += kBlockKeys;
-            if (token >= a.a.prefix_len) token = 0, ++item;
-            const int next = v + 1 < u1 ? page_of(token + lane * box) : 0;
-            for (int kv = 0; kv < 2 && alive; ++kv, ++tile) {
-                const int slot = (int)(tile % kSlots);
-                if (tile >= kSlots) alive = wait_all(&freed[slot], (uint32_t)(tile / kSlots - 1) & 1);
-                if (!alive) break;
-                unsigned char* dst = k8 ? raw_ring + slot * Shape::kRawBytes : ring + slot * Shape::kTileBytes;
-                if (lane == 0) mbar_arrive_expect_tx(&filled[slot], (uint32_t)(live * box) * (k8 ? D + 2 : 2 * D));
+            way.step(p);
+            if (way.left > 0) page = page_of(way.block * kBlockKeys + lane * box);  // the next block's, not looked at before it is needed
+            for (int kv = 0; kv < 2; ++kv) {
+                if (!(alive = wait_all(&freed[turn.slot], turn.parity))) break;
+                unsigned char* dst = k8 ? raw_ring + turn.slot * Shape::kRawBytes : ring + turn.slot * Shape::kTileBytes;
+                uint64_t* bar = &filled[turn.slot];
+                if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(live * box) * (k8 ? D + 2 : 2 * D));
                 __syncwarp();
                 if (lane < live) {
                     if (k8) {
-                        const int64_t at = (((int64_t)page * a.c.n_heads + head) << a.page_shift) + row;
-                        bulk_g2s(dst + lane * box * D, static_cast<const char*>(kv ? a.c.v : a.c.k) + at * D, (uint32_t)(box * D), &filled[slot]);
+                        const int64_t at = (((int64_t)id * a.c.n_heads + head) << a.page_shift) + row;
+                        bulk_g2s(dst + lane * box * D, static_cast<const char*>(kv ? a.c.v : a.c.k) + at * D, (uint32_t)(box * D), bar);
                         bulk_g2s(dst + 128 * D + lane * box * 2, static_cast<const char*>(kv ? a.c.v_scale : a.c.k_scale) + at * 2,
-                                 (uint32_t)(box * 2), &filled[slot]);
+                                 (uint32_t)(box * 2), bar);
                     } else {
                         for (int cb = 0; cb < D / 64; ++cb)
-                            tma_load4(dst + cb * (128 * 128) + lane * box * 128, kv ? &vmap : &kmap, cb * 64, row, head, page, &filled[slot]);
+                            tma_load4(dst + cb * (128 * 128) + lane * box * 128, kv ? &vmap : &kmap, cb * 64, row, head, id, bar);
                     }
                 }
+                const uint32_t parity = turn.parity ^ 1;  // of this fill
+                turn.next();
+                ++fills;
                 if (!k8 && kv && left < kBlockKeys) {
                     // Rows past the prefix hold anything (0 * NaN is NaN): zero them once the copy has landed.
-                    alive = wait_all(&filled[slot], (uint32_t)(tile / kSlots) & 1);
-                    if (!alive) {
-                        ++tile;
-                        break;
-                    }
-                    for (int i = lane; i < (kBlockKeys - (int)left) * (D / 8); i += 32)
-                        *reinterpret_cast<uint4*>(dst + tile_byte((int)left + i / (D / 8), i % (D / 8))) = make_uint4(0u, 0u, 0u, 0u);
+                    if (!(alive = wait_all(bar, parity))) break;
+                    for (int i = lane; i < (kBlockKeys - left) * (D / 8); i += 32)
+                        *reinterpret_cast<uint4*>(dst + tile_byte(left + i / (D / 8), i % (D / 8))) = make_uint4(0u, 0u, 0u, 0u);
                     fence_proxy_async();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&ctl.tail);
                 }
             }
-            page = next;
         }
         // Copies in flight land before the CTA leaves: the last fill of every slot.
-        for (int i = 0; i < kSlots; ++i) {
-            const int64_t last = tile - 1 - i;
-            if (last >= 0) mbar_wait_bounded(&filled[last % kSlots], (uint32_t)(last / kSlots) & 1, kAttnWaitNs);
-        }
-    } else if (k8 && warp < Shape::kConvertWarp) {
+        for (int i = 1; i <= min(fills, kSlots); ++i)
+            mbar_wait_bounded(&filled[(fills - i) % kSlots], (uint32_t)((fills - i) / kSlots) & 1, kAttnWaitNs);
+    } else if (k8 && warp == Shape::kScaleWarp) {
         // ---------------------------------------------------------------------------- scales
         // A tile's unit is a power of two no larger than its largest scale and more than half of it (1 if
-        // there is none); a token's factor is its scale in that unit.  One warp for every tile in turn: a
+        // there is none); a token's factor is its scale in that unit.  The keys of int8 stay codes, and the scores
+        // take their scales: a score is the exponent of a weight, and code times scale (7 bits by 8) rounded to
+        // float16's 11 would cost it more than a weight's own rounding does.  One warp for every tile in turn: a
         // barrier's phase may only be waited for by a role that sees each of its phases.
-        const int64_t tiles = warp == Shape::kScaleWarp ? 2 * (u1 - u0) : 0;
-        int64_t token = (u0 - u0 / p.nblk * p.nblk) * kBlockKeys;
-        for (int64_t tile = 0; tile < tiles; ++tile) {
-            const int rs = (int)(tile % kRaw), slot = (int)((tile >> 1) % kScalars);
-            const bool values = tile & 1;
-            const int64_t left = a.a.prefix_len - token;
-            if (values) token = left <= kBlockKeys ? 0 : token + kBlockKeys;
-            if (!(alive = wait_all(&ctl.raw_full[rs], (uint32_t)(tile / kRaw) & 1))) break;
-            const uint2 w = *reinterpret_cast<const uint2*>(raw_ring + rs * Shape::kRawBytes + 128 * D + lane * 8);
-            float s[4] = {__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
-                          __uint_as_float(w.y & 0xFFFF0000u)};
-            float most = 0.f;
+        Way way(p);
+        Turn<kRaw> raw_turn(0);
+        Turn<kScalars> scalar(0);
+        for (; way.left > 0 && alive; way.step(p), scalar.next()) {
+            const int left = prefix - way.block * kBlockKeys;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (lane * 4 + i >= left) s[i] = 0.f;  // past the prefix: anything
-                most = fmaxf(most, s[i]);
-            }
+            for (int kv = 0; kv < 2; ++kv, raw_turn.next()) {
+                const int rs = raw_turn.slot;
+                if (!(alive = wait_all(&ctl.raw_full[rs], raw_turn.parity))) break;
+                uint2 w = *reinterpret_cast<const uint2*>(raw_ring + rs * Shape::kRawBytes + 128 * D + lane * 8);
+                if (left < kBlockKeys) {  // past the prefix: anything
+                    const int in = left - lane * 4;
+                    w.x = in >= 2 ? w.x : (in == 1 ? w.x & 0xFFFFu : 0u);
+                    w.y = in >= 4 ? w.y : (in == 3 ? w.y & 0xFFFFu : 0u);
+                }
+                if (kFormat == TPS_KV_INT8 && !kv) {
+                    *reinterpret_cast<uint2*>(&ctl.key_scale[scalar.slot][lane * 4]) = w;
+                    if (lane == 0) ctl.key_unit[scalar.slot] = 1.f;
+                } else {
+                    const float s[4] = {__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
+                                        __uint_as_float(w.y & 0xFFFF0000u)};
+                    float most = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
-            const int e = most > 0.f ? max(-126, min((int)(__float_as_uint(most) >> 23) - 127, 126)) : 0;
-            const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-            const __half2 lo = __floats2half2_rn(s[0] * inv, s[1] * inv), hi = __floats2half2_rn(s[2] * inv, s[3] * inv);
-            *reinterpret_cast<uint2*>(&ctl.factor[rs][lane * 4]) =
-                make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-            if (lane == 0) {
-                if (values)
-                    ctl.value_exp[slot] = (float)e;
-                else
-                    ctl.key_unit[slot] = __uint_as_float((uint32_t)(127 + e) << 23);
-            }
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&ctl.factor_full[rs]);
-                if (values) mbar_arrive(&ctl.scalar_full[slot]);
+                    for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+                    const int e = most > 0.f ? max(-126, min((int)(__float_as_uint(most) >> 23) - 127, 126)) : 0;
+                    const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+                    const __half2 lo = __floats2half2_rn(s[0] * inv, s[1] * inv), hi = __floats2half2_rn(s[2] * inv, s[3] * inv);
+                    *reinterpret_cast<uint2*>(&ctl.factor[rs][lane * 4]) =
+                        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+                    if (lane == 0) {
+                        if (kv)
+                            ctl.value_exp[scalar.slot] = (float)e;
+                        else
+                            ctl.key_unit[scalar.slot] = __uint_as_float((uint32_t)(127 + e) << 23);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&ctl.factor_full[rs]);
+                    if (kv) mbar_arrive(&ctl.scalar_full[scalar.slot]);
+                }
             }
         }
-    } else if (k8) {
+    } else if (k8 && warp >= Shape::kConvertWarp) {
         // ---------------------------------------------------------------------------- 8-bit codes to float16
         constexpr int kPieces = D / 16;                           // 16-byte pieces of a code row
         constexpr int kThreadsConv = Shape::kConvertWarps * 32;
@@ -556,57 +619,57 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
         // The eight lanes of a 128-byte code row fill both column blocks; the upper four write their halves the
         // other way round, so that the eight 16-byte stores of a phase hit different banks.
         const bool swap = piece >= 4;
-        int64_t token = (u0 - u0 / p.nblk * p.nblk) * kBlockKeys;
-        const int64_t tiles = 2 * (u1 - u0);
-        int rs = 0, slot = 0;
-        uint32_t raw_phase = 0, phase = 1;  // of the code tiles; of the tiles' last use (none yet)
-        for (int64_t tile = 0; tile < tiles && alive; ++tile) {
-            const int64_t left = a.a.prefix_len - token;
-            if (tile & 1) token = left <= kBlockKeys ? 0 : token + kBlockKeys;
-            const unsigned char* raw = raw_ring + rs * Shape::kRawBytes;
-            if (!(alive = wait_all(&ctl.factor_full[rs], raw_phase))) break;  // and with it the codes
-            if (!(alive = wait_all(&ctl.raw_full[rs], raw_phase))) break;
-            uint4 x[kSteps];
-            __half2 f[kSteps];
+        Way way(p);
+        Turn<kRaw> raw_turn(0);
+        Turn<kRing> turn(1);
+        for (; way.left > 0 && alive; way.step(p)) {
+            const int left = prefix - way.block * kBlockKeys;
+#pragma unroll 1
+            for (int kv = 0; kv < 2; ++kv, raw_turn.next(), turn.next()) {
+                const int rs = raw_turn.slot;
+                const unsigned char* raw = raw_ring + rs * Shape::kRawBytes;
+                if (!(alive = wait_all(&ctl.factor_full[rs], raw_turn.parity))) break;
+                if (!(alive = wait_all(&ctl.raw_full[rs], raw_turn.parity))) break;
+                uint4 x[kSteps];
+                __half2 f[kSteps];
 #pragma unroll
-            for (int i = 0; i < kSteps; ++i) {
-                const int r = i * kRowsPerStep + sub;
-                x[i] = *reinterpret_cast<const uint4*>(raw + r * D + piece * 16);
-                f[i] = __half2half2(ctl.factor[rs][r]);
-            }
-            if (left < kBlockKeys) {  // past the prefix: anything
-#pragma unroll
-                for (int i = 0; i < kSteps; ++i)
-                    if (i * kRowsPerStep + sub >= left) x[i] = make_uint4(0u, 0u, 0u, 0u);
-            }
-            if (!(alive = wait_all(&ctl.empty[slot], phase))) break;
-            unsigned char* dst = ring + slot * Shape::kTileBytes;
-#pragma unroll
-            for (int i = 0; i < kSteps; ++i) {
-                const int r = i * kRowsPerStep + sub;
-                const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-                uint32_t h[8];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    code_pairs<kFormat>(w[j], h[2 * j], h[2 * j + 1]);
-#pragma unroll
-                    for (int k = 2 * j; k < 2 * j + 2; ++k) {
-                        const __half2 y = __hmul2(*reinterpret_cast<__half2*>(&h[k]), f[i]);
-                        h[k] = *reinterpret_cast<const uint32_t*>(&y);
-                    }
+                for (int i = 0; i < kSteps; ++i) {
+                    const int r = i * kRowsPerStep + sub;
+                    x[i] = *reinterpret_cast<const uint4*>(raw + r * D + piece * 16);
+                    f[i] = kFormat == TPS_KV_INT8 && !kv ? __float2half2_rn(1.f) : __half2half2(ctl.factor[rs][r]);
                 }
-                const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-                *reinterpret_cast<uint4*>(dst + tile_byte(r, 2 * piece + (swap ? 1 : 0))) = swap ? hi : lo;
-                *reinterpret_cast<uint4*>(dst + tile_byte(r, 2 * piece + (swap ? 0 : 1))) = swap ? lo : hi;
+                if (left < kBlockKeys) {  // past the prefix: anything
+#pragma unroll
+                    for (int i = 0; i < kSteps; ++i)
+                        if (i * kRowsPerStep + sub >= left) x[i] = make_uint4(0u, 0u, 0u, 0u);
+                }
+                if (!(alive = wait_all(&ctl.empty[turn.slot], turn.parity))) break;
+                unsigned char* dst = ring + turn.slot * Shape::kTileBytes;
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i) {
+                    const int r = i * kRowsPerStep + sub;
+                    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                    uint32_t h[8];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        code_pairs<kFormat>(w[j], h[2 * j], h[2 * j + 1]);
+#pragma unroll
+                        for (int k = 2 * j; k < 2 * j + 2; ++k) {
+                            const __half2 y = __hmul2(*reinterpret_cast<__half2*>(&h[k]), f[i]);
+                            h[k] = *reinterpret_cast<const uint32_t*>(&y);
+                        }
+                    }
+                    const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
+                    *reinterpret_cast<uint4*>(dst + tile_byte(r, 2 * piece + (swap ? 1 : 0))) = swap ? hi : lo;
+                    *reinterpret_cast<uint4*>(dst + tile_byte(r, 2 * piece + (swap ? 0 : 1))) = swap ? lo : hi;
+                }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&ctl.full[turn.slot]);
+                    mbar_arrive(&ctl.raw_empty[rs]);
+                }
             }
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&ctl.full[slot]);
-                mbar_arrive(&ctl.raw_empty[rs]);
-            }
-            if (++rs == kRaw) rs = 0, raw_phase ^= 1;
-            if (++slot == kRing) slot = 0, phase ^= 1;
         }
     }
     tc_fence_before();

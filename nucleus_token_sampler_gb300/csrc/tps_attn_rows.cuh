@@ -14,11 +14,14 @@
 //
 // What bounds it: the bytes of the keys and values, and the latency of a short sequence's few steps.  Each
 // warp has a ring of its own in shared memory that bulk copies fill 16 tokens at a time, and works without
-// the others: no barrier but its own.  A lane reads 16 bytes of a key row and 16 of a value row at a time;
-// the product q.k is the same for any order of the D components, so they serve as its fragments of
-// consecutive k-steps of mma.sync m16n8k16 as they lie (the query fragments are loaded in the same order),
-// and the columns of the output are renumbered so that a lane's bytes of a value row are one column each
-// of consecutive tiles.  mma.sync rather than tcgen05: the 16 rows fill an eighth of a tcgen05 tile.
+// the others: no barrier but its own.  The products are taken transposed, K Q^T and V^T P^T, with the
+// tokens (and then the D components) as the 16 rows of mma.sync m16n8k16 and the query rows as its 8
+// columns: the 4 to 8 query heads of a key head fill an 8-wide tile where they would leave a 16-wide one
+// half empty, in matrix instructions, in exponentials and in registers.  The product q.k is the same for any
+// order of the D components, so a lane's 16 bytes of a key row serve as its fragments of consecutive
+// k-steps as they lie (the query fragments are loaded in the same order); a lane's 16 bytes of a value row
+// become rows g and g + 8 of consecutive tiles.  mma.sync rather than tcgen05: 8 or 16 rows fill a
+// sixteenth or an eighth of a tcgen05 tile.
 #pragma once
 
 #include <cstdint>
@@ -49,16 +52,25 @@ __device__ __forceinline__ float log2_fast(float x)
     return y;
 }
 
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, bool half)
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1, bool half)
 {
     if (half)
         asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
     else
         asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The transpose of an 8 x 8 matrix of 16-bit numbers held as a fragment.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x)
+{
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 
 // Two codes to float16 (the low half first).  fp8: the two bytes of `w`'s low half.  int8: bytes that
@@ -95,8 +107,7 @@ __device__ __forceinline__ void code_pairs(uint32_t w, uint32_t& p01, uint32_t& 
 // 0 marks a slot that was never written and counts as the smallest scale.
 __device__ __forceinline__ float floor_scale(float s) { return s > 0.f || s != s ? s : 0x1p-40f; }
 
-// Query rows of a warp: row i of the 16 is query row row0 + i of the tile's `rows`.
-// Fragments hold 4 consecutive components from kstep_base(s, quad) on for k-step s.
+// Components of a head that a lane holds for k-step s: 4 consecutive ones from here on.
 template <int kFormat>
 __device__ __forceinline__ int kstep_base(int s, int quad)
 {
@@ -113,60 +124,76 @@ __device__ __forceinline__ float f16_row_scale(float a)
     return __uint_as_float((uint32_t)min(max(127 - e, 1), 254) << 23);  // brings it to [1, 2)
 }
 
-template <int D, int kFormat> struct RowState {
+// A warp's work on 8 N query rows.  Lane (g, quad) = (lane / 4, lane % 4) holds, of rows 8 n + 2 quad + e, the
+// reference and its part of the sum, and the output's components g D/8 + 2 t + h in o[n][t][2 h + e].
+template <int D, int N> struct RowState {
     static constexpr int kSteps = D / 16;   // k-steps of q.k
-    static constexpr int kTiles = D / 8;    // 8-column tiles of the output
-    uint32_t q[kSteps][4];
-    float o[kTiles][4];
-    float m[2], l[2];  // rows g and g + 8: reference (agreed on by the quad) and this lane's part of the sum
-    float unscale[2];  // what the row's float16 scaling has to be undone by, times scale log2(e)
+    static constexpr int kTiles = D / 16;   // 16-component tiles of the output
+    uint32_t q[N][kSteps][2];               // row 8 n + g
+    float o[N][kTiles][4];
+    float m[N][2], l[N][2];
+    float unscale[N][2];  // scale log2(e), over the power of two of the row's float16 form
 };
 
-// Load the fragments of the 16 query rows at `q` (row stride in elements; rows past `rows` are zero).
-template <int D, int kFormat, typename RowPtr>
-__device__ __forceinline__ void load_query(RowState<D, kFormat>& st, int rows, float qk_scale, RowPtr row_ptr)
+// Ask for the query rows (those from `rows` on are zero); ready_query makes them what the products take.
+template <int D, int kFormat, int N, typename RowPtr>
+__device__ __forceinline__ void load_query(RowState<D, N>& st, int rows, RowPtr row_ptr)
 {
     const int lane = threadIdx.x & 31, g = lane >> 2, quad = lane & 3;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const int row = g + 8 * r;
-        float amax = 0.f;
+    for (int n = 0; n < N; ++n) {
+        const int row = 8 * n + g;
 #pragma unroll
         for (int s = 0; s < D / 16; ++s) {
             uint2 w = make_uint2(0u, 0u);
             if (row < rows) w = *reinterpret_cast<const uint2*>(row_ptr(row) + kstep_base<kFormat>(s, quad));
-            st.q[s][r] = w.x;
-            st.q[s][2 + r] = w.y;
-            if (kFormat != TPS_KV_BF16) {
+            st.q[n][s][0] = w.x;
+            st.q[n][s][1] = w.y;
+        }
+    }
+}
+template <int D, int kFormat, int N>
+__device__ __forceinline__ void ready_query(RowState<D, N>& st, float qk_scale)
+{
+    const int quad = threadIdx.x & 3;
+    const float inf = __int_as_float(0x7F800000);
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        float amax = 0.f, f = 1.f;
+        if (kFormat != TPS_KV_BF16) {
+#pragma unroll
+            for (int s = 0; s < D / 16; ++s) {
+                const uint2 w = make_uint2(st.q[n][s][0], st.q[n][s][1]);
                 const float x[4] = {__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u),
                                     __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u)};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) amax = fabsf(x[i]) < __int_as_float(0x7F800000) ? fmaxf(amax, fabsf(x[i])) : amax;
+                for (int i = 0; i < 4; ++i) amax = fabsf(x[i]) < inf ? fmaxf(amax, fabsf(x[i])) : amax;
             }
         }
-        st.unscale[r] = qk_scale;
         if (kFormat != TPS_KV_BF16) {
             amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-            const float f = f16_row_scale(amax);
-            st.unscale[r] = qk_scale / f;
+            f = f16_row_scale(amax);
 #pragma unroll
-            for (int s = 0; s < D / 16; ++s) {
+            for (int s = 0; s < D / 16; ++s)
 #pragma unroll
-                for (int i = 0; i < 4; i += 2) {
-                    const uint32_t w = st.q[s][i + r];
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t w = st.q[n][s][i];
                     const __half2 h = __floats2half2_rn(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xFFFF0000u) * f);
-                    st.q[s][i + r] = *reinterpret_cast<const uint32_t*>(&h);
+                    st.q[n][s][i] = *reinterpret_cast<const uint32_t*>(&h);
                 }
-            }
         }
-        st.m[r] = -__int_as_float(0x7F800000);
-        st.l[r] = 0.f;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {  // lane 4 r holds row r's factor
+            st.unscale[n][e] = kFormat != TPS_KV_BF16 ? qk_scale / __shfl_sync(0xFFFFFFFFu, f, (2 * quad + e) * 4) : qk_scale;
+            st.m[n][e] = -inf;
+            st.l[n][e] = 0.f;
+        }
+#pragma unroll
+        for (int t = 0; t < D / 16; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) st.o[n][t][i] = 0.f;
     }
-#pragma unroll
-    for (int t = 0; t < D / 8; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) st.o[t][i] = 0.f;
 }
 
 // A warp's ring of 16-token chunks in shared memory: keys, values and, for 8-bit formats, their scales.
@@ -176,8 +203,8 @@ template <int D, int kFormat> struct Chunk {
     static constexpr int kRowBytes = k8 ? D : 2 * D;
     static constexpr int kValues = 16 * kRowBytes, kKeyScales = 32 * kRowBytes, kValueScales = kKeyScales + (k8 ? 32 : 0);
     static constexpr int kBytes = kValueScales + (k8 ? 32 : 0);
-    // 12 to 16 KB for each warp: with 12 warps on an SM more bytes are on the way than the memory's latency asks for
-    static constexpr int kStages = (k8 ? 4 : 2) * (D == 64 ? 2 : 1);
+    // 12 to 16 KB for each warp: with 12 to 16 warps on an SM more bytes are on the way than the latency asks for
+    static constexpr int kStages = (k8 ? 3 : 2) * (D == 64 ? 2 : 1);
     static constexpr int kRing = (kStages * kBytes + 127) / 128 * 128;
 };
 
@@ -188,32 +215,36 @@ template <int D, int kFormat> struct RowsShared {
     int bad;  // 1: a bad page or length, 2: a wait ran out
 };
 
-// Where the tokens lie: `pages` lists the pages of one head's tokens in order.
-struct PageList {
-    const int32_t* pages;
-    int64_t n_pages;
-    int shift, head, heads;
-    // First row of the 16-token chunk that starts at token t (a multiple of 16), or -1 for a bad page.
-    __device__ __forceinline__ int64_t row(int t) const
-    {
-        const int p = pages[t >> shift];
-        return (p < 0 || p >= n_pages) ? -1 : (((int64_t)p * heads + head) << shift) + (t & ((1 << shift) - 1));
-    }
-};
-
-// A warp's walk over the 16-token chunks first, first + step, ... below `last` tokens.
+// A warp's walk over the 16-token chunks first, first + step, ... below `last` tokens; `pages` lists the pages
+// of one head's tokens in order.
 template <int D, int kFormat> struct Walk {
     using C = Chunk<D, kFormat>;
     const tps_kv_cache& c;
-    const PageList& list;
+    int shift, head;
     unsigned char* ring;
     uint64_t* full;
+    const int32_t* pages;
     uint32_t fills;  // copies into the ring so far, over the life of the kernel (parity of the barriers)
+    int first, step, last, ahead;  // `ahead`: the next chunk to ask for
+    int page;                      // its page, read one request early and not looked at before the next one
+    int fault;                     // 1: a page that is not the cache's
 
-    // Ask for the chunk at `row` (its first cache row): one lane for each of the copies.
-    __device__ __forceinline__ void request(int64_t row)
+    // The page of the chunk at `first`, if the list reaches as far as `tokens`: may be called before the number of
+    // tokens is known, so that this read does not wait for that one.
+    __device__ __forceinline__ void look(const int32_t* pages_, int first_, int64_t tokens)
+    {
+        pages = pages_;
+        page = first_ < tokens ? pages[first_ >> shift] : 0;
+    }
+    // Ask for the next chunk: one lane for each of its copies.
+    __device__ __forceinline__ void request()
     {
         const int lane = threadIdx.x & 31, stage = (int)(fills % C::kStages);
+        int id = page;
+        if (id < 0 || id >= c.n_pages) fault = 1, id = 0;
+        const int64_t row = (((int64_t)id * c.n_heads + head) << shift) + (ahead & ((1 << shift) - 1));
+        ahead += step;
+        if (ahead < last) page = pages[ahead >> shift];
         unsigned char* dst = ring + stage * C::kBytes;
         if (lane == 0) mbar_arrive_expect_tx(&full[stage], C::kBytes);
         __syncwarp();
@@ -223,38 +254,37 @@ template <int D, int kFormat> struct Walk {
         if (C::k8 && lane == 3) bulk_g2s(dst + C::kValueScales, static_cast<const char*>(c.v_scale) + row * 2, 32, &full[stage]);
         ++fills;
     }
+    // Begin, after look(): the first chunks are on their way when this returns (the ring holds nothing still used).
+    __device__ __forceinline__ void start(int first_, int step_, int last_)
+    {
+        first = ahead = first_, step = step_, last = last_;
+#pragma unroll
+        for (int i = 0; i < C::kStages; ++i)
+            if (ahead < last) request();
+    }
 };
 
-// Attend to the chunks first, first + step, ... below `last` tokens; the warp's rows g and g + 8 see the tokens
-// below lim[0], lim[1].  Returns 0, or 1 after a page that is not the cache's, 2 after a wait that ran out.
-template <int D, int kFormat>
-__device__ __forceinline__ int attend(RowState<D, kFormat>& st, Walk<D, kFormat>& walk, int first, int step, int last,
-                                      const int (&lim)[2])
+// Attend to the chunks of a walk that has been started; row 8 n + 2 quad + e sees the tokens below
+// lim[n][e].  Returns 0, or 1 after a page that is not the cache's, 2 after a wait that ran out.
+template <int D, int kFormat, int N>
+__device__ __forceinline__ int attend(RowState<D, N>& st, Walk<D, kFormat>& walk, const int (&lim)[N][2])
 {
     using C = Chunk<D, kFormat>;
     constexpr bool k8 = C::k8;
     constexpr int kKeyLoads = C::kRowBytes / 64;  // 16-byte pieces of one key row held by its quad's lane
     constexpr int kValWords = C::kRowBytes / 32;  // words of one value row held by a lane
-    constexpr int kCols = D / 8;                  // columns of a value row held by a lane
+    constexpr int kTiles = D / 16;
     const int lane = threadIdx.x & 31, g = lane >> 2, quad = lane & 3;
     const float neg = -__int_as_float(0x7F800000);
-    if (first >= last) return 0;
-
-    int fault = 0;
-    // `ahead` is the next chunk to ask for; its page number is read one request early.
-    int ahead = first;
-    int64_t row = walk.list.row(first);
-    auto request = [&]() {
-        if (row < 0) fault = 1, row = 0;
-        walk.request(row);
-        ahead += step;
-        if (ahead < last) row = walk.list.row(ahead);
-    };
-    uint32_t at = walk.fills;  // the fill that is used next
+    const int last = walk.last;
+    if (walk.first >= last) return walk.fault;
+    int all_see = last;  // tokens that every row sees
 #pragma unroll
-    for (int i = 0; i < C::kStages; ++i)
-        if (ahead < last) request();
-    for (int t0 = first; t0 < last; t0 += step, ++at) {
+    for (int n = 0; n < N; ++n) all_see = min(all_see, min(lim[n][0], lim[n][1]));
+    all_see = (int)__reduce_min_sync(0xFFFFFFFFu, (uint32_t)all_see);
+    const uint32_t chunks = (uint32_t)((last - walk.first + walk.step - 1) / walk.step);
+    uint32_t at = walk.fills - min(chunks, (uint32_t)C::kStages);  // the fill that is used next
+    for (int t0 = walk.first; t0 < last; t0 += walk.step, ++at) {
         const int stage = (int)(at % C::kStages);
         if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&walk.full[stage], (at / C::kStages) & 1, kAttnWaitNs))) {
             for (; at != walk.fills; ++at)  // what is on the way lands before the warp goes on (bounded again)
@@ -262,26 +292,6 @@ __device__ __forceinline__ int attend(RowState<D, kFormat>& st, Walk<D, kFormat>
             return 2;
         }
         const unsigned char* buf = walk.ring + stage * C::kBytes;
-        const bool partial = t0 + 16 > last;
-        float z[2][4] = {};
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int j = 0; j < kKeyLoads; ++j) {
-                const uint4 x = *reinterpret_cast<const uint4*>(buf + (n * 8 + g) * C::kRowBytes + j * 64 + quad * 16);
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                if (k8) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t b0, b1;
-                        code_pairs<kFormat>(w[i], b0, b1);
-                        mma16816(z[n], st.q[j * 4 + i], b0, b1, true);
-                    }
-                } else {
-                    mma16816(z[n], st.q[j * 2 % (D / 16)], w[0], w[1], false);
-                    mma16816(z[n], st.q[(j * 2 + 1) % (D / 16)], w[2], w[3], false);
-                }
-            }
         uint32_t vreg[4][kValWords];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -298,147 +308,186 @@ __device__ __forceinline__ int attend(RowState<D, kFormat>& st, Walk<D, kFormat>
                     vreg[i][(j + 3) % kValWords] = w.w;
                 }
             }
-            if (partial && t0 + tok >= last) {  // rows past the end hold anything, and 0 * NaN is NaN
+        }
+        // tokens g (0, 1) and g + 8 (2, 3), rows 2 quad + {0, 1}; every other k-step in a chain of its own
+        float z[N][4] = {}, z_odd[N][4] = {};
 #pragma unroll
-                for (int j = 0; j < kValWords; ++j) vreg[i][j] = 0u;
+        for (int j = 0; j < kKeyLoads; ++j) {
+            const uint4 x = *reinterpret_cast<const uint4*>(buf + g * C::kRowBytes + j * 64 + quad * 16);
+            const uint4 y = *reinterpret_cast<const uint4*>(buf + (g + 8) * C::kRowBytes + j * 64 + quad * 16);
+            const uint32_t wx[4] = {x.x, x.y, x.z, x.w}, wy[4] = {y.x, y.y, y.z, y.w};
+            if (k8) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t x0, x1, y0, y1;
+                    code_pairs<kFormat>(wx[i], x0, x1);
+                    code_pairs<kFormat>(wy[i], y0, y1);
+#pragma unroll
+                    for (int n = 0; n < N; ++n) mma16816(i & 1 ? z_odd[n] : z[n], x0, y0, x1, y1, st.q[n][j * 4 + i][0], st.q[n][j * 4 + i][1], true);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int n = 0; n < N; ++n)
+                        mma16816(i & 1 ? z_odd[n] : z[n], wx[2 * i], wy[2 * i], wx[2 * i + 1], wy[2 * i + 1], st.q[n][(j * 2 + i) % (D / 16)][0],
+                                 st.q[n][(j * 2 + i) % (D / 16)][1], false);
             }
         }
-        // Scores in base-2 units, with the value's scale folded in; columns n * 8 + quad * 2 + {0, 1}.
-        float inv_s[2][2];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            uint32_t ks = 0, vs = 0;
-            if (k8) {
-                ks = *reinterpret_cast<const uint32_t*>(buf + C::kKeyScales + n * 16 + quad * 4);
-                vs = *reinterpret_cast<const uint32_t*>(buf + C::kValueScales + n * 16 + quad * 4);
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) z[n][i] += z_odd[n][i];
+        // Scores in base-2 units, with the value's scale folded in.
+        float add[2] = {0.f, 0.f}, inv_s[2] = {1.f, 1.f};
+        if (k8) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t ks = *reinterpret_cast<const uint16_t*>(buf + C::kKeyScales + (g + 8 * h) * 2);
+                const uint32_t vs = *reinterpret_cast<const uint16_t*>(buf + C::kValueScales + (g + 8 * h) * 2);
+                const float kf = floor_scale(__uint_as_float(ks << 16)), s = floor_scale(__uint_as_float(vs << 16));
+                add[h] = log2_fast(s);
+                inv_s[h] = s == s ? __fdividef(1.f, s) : 1.f;  // NaN reaches the weight through `add` where it is seen
+#pragma unroll
+                for (int n = 0; n < N; ++n) z[n][2 * h] *= kf, z[n][2 * h + 1] *= kf;
             }
+        }
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float kf = 1.f, add = 0.f;
-                if (k8) {
-                    kf = floor_scale(__uint_as_float(e ? ks & 0xFFFF0000u : ks << 16));
-                    const float s = floor_scale(__uint_as_float(e ? vs & 0xFFFF0000u : vs << 16));
-                    add = log2_fast(s);
-                    inv_s[n][e] = s == s ? __fdividef(1.f, s) : 1.f;  // NaN reaches the weight through `add` where it is seen
-                }
-                const int tok = t0 + n * 8 + quad * 2 + e;
+        for (int n = 0; n < N; ++n)
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    float& x = z[n][r * 2 + e];
-                    x = k8 ? fmaf(x * kf, st.unscale[r], add) : x * st.unscale[r];
-                    if (tok >= lim[r]) x = neg;
-                }
+            for (int i = 0; i < 4; ++i) z[n][i] = fmaf(z[n][i], st.unscale[n][i & 1], add[i >> 1]);
+        if (t0 + 16 > all_see) {
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (t0 + g + 8 * (i >> 1) >= lim[n][i & 1]) z[n][i] = neg;
+            if (t0 + 16 > last) {  // rows past the end hold anything, and 0 * NaN is NaN
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (t0 + (i >> 1) * 8 + quad * 2 + (i & 1) >= last) {
+#pragma unroll
+                        for (int j = 0; j < kValWords; ++j) vreg[i][j] = 0u;
+                    }
             }
         }
         __syncwarp();  // every lane has read the stage
-        if (ahead < last) request();
+        if (walk.ahead < last) walk.request();
         // Raise the references where a score exceeds them by more than the slack (or is the first one).
-        const float top0 = fmaxf(fmaxf(z[0][0], z[0][1]), fmaxf(z[1][0], z[1][1]));
-        const float top1 = fmaxf(fmaxf(z[0][2], z[0][3]), fmaxf(z[1][2], z[1][3]));
-        if (__any_sync(0xFFFFFFFFu, top0 > st.m[0] + kSlack || top1 > st.m[1] + kSlack)) {
-            const float top[2] = {top0, top1};
-            float f[2];
+        bool over = false;
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                float t = fmaxf(top[r], __shfl_xor_sync(0xFFFFFFFFu, top[r], 1));
-                t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 2));
-                const float m = t > st.m[r] + kSlack ? t : st.m[r];
-                f[r] = m == st.m[r] ? 1.f : exp2_fast(st.m[r] - m);
-                st.m[r] = m;
-                st.l[r] *= f[r];
-            }
+        for (int n = 0; n < N; ++n)
 #pragma unroll
-            for (int t = 0; t < D / 8; ++t) {
-                st.o[t][0] *= f[0], st.o[t][1] *= f[0];
-                st.o[t][2] *= f[1], st.o[t][3] *= f[1];
+            for (int e = 0; e < 2; ++e) over = over || fmaxf(z[n][e], z[n][2 + e]) > st.m[n][e] + kSlack;
+        if (__any_sync(0xFFFFFFFFu, over)) {
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                float f[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float t = fmaxf(z[n][e], z[n][2 + e]);
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, o));
+                    const float m = t > st.m[n][e] + kSlack ? t : st.m[n][e];
+                    f[e] = m == st.m[n][e] ? 1.f : exp2_fast(st.m[n][e] - m);
+                    st.m[n][e] = m;
+                    st.l[n][e] *= f[e];
+                }
+#pragma unroll
+                for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) st.o[n][t][i] *= f[i & 1];
             }
         }
-        uint32_t p[4];
+        uint32_t p[N][2];
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < N; ++n) {
+            float w[4];
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const float ref = st.m[r] == neg ? 0.f : st.m[r];  // nothing seen yet: every weight is 0
-                const float w0 = exp2_fast(z[n][r * 2] - ref + (k8 ? kLift : 0.f));
-                const float w1 = exp2_fast(z[n][r * 2 + 1] - ref + (k8 ? kLift : 0.f));
-                if (k8) {
-                    st.l[r] = fmaf(w0, inv_s[n][0], fmaf(w1, inv_s[n][1], st.l[r]));
-                    const __half2 h = __floats2half2_rn(w0, w1);
-                    p[n * 2 + r] = *reinterpret_cast<const uint32_t*>(&h);
-                } else {
-                    st.l[r] += w0 + w1;
-                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(p[n * 2 + r]) : "f"(w1), "f"(w0));
-                }
+            for (int i = 0; i < 4; ++i) {
+                const float m = st.m[n][i & 1];  // -inf: nothing seen yet, every weight is 0
+                w[i] = exp2_fast(z[n][i] - (m == neg ? 0.f : m) + (k8 ? kLift : 0.f));
+                st.l[n][i & 1] = k8 ? fmaf(w[i], inv_s[i >> 1], st.l[n][i & 1]) : st.l[n][i & 1] + w[i];
             }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t x;
+                if (k8) {
+                    const __half2 y = __floats2half2_rn(w[2 * h], w[2 * h + 1]);
+                    x = *reinterpret_cast<const uint32_t*>(&y);
+                } else {
+                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(x) : "f"(w[2 * h + 1]), "f"(w[2 * h]));
+                }
+                p[n][h] = transpose8(x);  // tokens 8 h + 2 quad + {0, 1} of row g
+            }
+        }
 #pragma unroll
         for (int w = 0; w < kValWords; ++w) {
             if (k8) {
-                // bytes of tokens (0, 1) and (2, 3) side by side: columns 4w .. 4w + 3
+                // bytes of tokens (0, 1) and (2, 3) side by side: components 4w .. 4w + 3, two tiles
                 uint32_t a = vreg[0][w], b = vreg[1][w], cc = vreg[2][w], d = vreg[3][w];
                 if (kFormat == TPS_KV_INT8) a ^= 0x80808080u, b ^= 0x80808080u, cc ^= 0x80808080u, d ^= 0x80808080u;
-                const uint32_t ab01 = __byte_perm(a, b, 0x5140u), ab23 = __byte_perm(a, b, 0x7362u);
-                const uint32_t cd01 = __byte_perm(cc, d, 0x5140u), cd23 = __byte_perm(cc, d, 0x7362u);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t x = i < 2 ? ab01 : ab23, y = i < 2 ? cd01 : cd23;
-                    uint32_t b0, b1;
+                for (int half = 0; half < 2; ++half) {
+                    const uint32_t ab = __byte_perm(a, b, half ? 0x7362u : 0x5140u), cd = __byte_perm(cc, d, half ? 0x7362u : 0x5140u);
+                    uint32_t a0, a1, a2, a3;
                     if (kFormat == TPS_KV_FP8) {
-                        b0 = fp8_pair((i & 1) ? x >> 16 : x);
-                        b1 = fp8_pair((i & 1) ? y >> 16 : y);
+                        a0 = fp8_pair(ab), a1 = fp8_pair(ab >> 16), a2 = fp8_pair(cd), a3 = fp8_pair(cd >> 16);
                     } else {
-                        b0 = int8_pair(x, (i & 1) ? 0x4342u : 0x4140u);
-                        b1 = int8_pair(y, (i & 1) ? 0x4342u : 0x4140u);
+                        a0 = int8_pair(ab, 0x4140u), a1 = int8_pair(ab, 0x4342u);
+                        a2 = int8_pair(cd, 0x4140u), a3 = int8_pair(cd, 0x4342u);
                     }
-                    mma16816(st.o[(w * 4 + i) % kCols], p, b0, b1, true);
+#pragma unroll
+                    for (int n = 0; n < N; ++n)
+                        mma16816(st.o[n][(w * 2 + half) % kTiles], a0, a1, a2, a3, p[n][0], p[n][1], true);
                 }
             } else {
-                mma16816(st.o[(w * 2) % kCols], p, __byte_perm(vreg[0][w], vreg[1][w], 0x5410u),
-                         __byte_perm(vreg[2][w], vreg[3][w], 0x5410u), false);
-                mma16816(st.o[(w * 2 + 1) % kCols], p, __byte_perm(vreg[0][w], vreg[1][w], 0x7632u),
-                         __byte_perm(vreg[2][w], vreg[3][w], 0x7632u), false);
+                const uint32_t a0 = __byte_perm(vreg[0][w], vreg[1][w], 0x5410u), a1 = __byte_perm(vreg[0][w], vreg[1][w], 0x7632u);
+                const uint32_t a2 = __byte_perm(vreg[2][w], vreg[3][w], 0x5410u), a3 = __byte_perm(vreg[2][w], vreg[3][w], 0x7632u);
+#pragma unroll
+                for (int n = 0; n < N; ++n) mma16816(st.o[n][w % kTiles], a0, a1, a2, a3, p[n][0], p[n][1], false);
             }
         }
     }
-    return fault;
+    return walk.fault;
 }
 
 // This lane's part of the sums becomes the row's.
-template <int D, int kFormat>
-__device__ __forceinline__ void finish_sums(RowState<D, kFormat>& st)
+template <int D, int N>
+__device__ __forceinline__ void finish_sums(RowState<D, N>& st)
 {
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        st.l[r] += __shfl_xor_sync(0xFFFFFFFFu, st.l[r], 1);
-        st.l[r] += __shfl_xor_sync(0xFFFFFFFFu, st.l[r], 2);
-    }
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) st.l[n][e] += __shfl_xor_sync(0xFFFFFFFFu, st.l[n][e], o);
 }
 
-// Put a warp's first `rows` rows into its part of shared memory in natural column order (a lane's columns are
-// (2 quad + e) D/8 + tile).
-template <int D, int kFormat>
-__device__ __forceinline__ void store_rows(RowsShared<D, kFormat>& sm, RowState<D, kFormat>& st, int rows)
+// Put a warp's first `rows` rows into its part of shared memory.
+template <int D, int kFormat, int N>
+__device__ __forceinline__ void store_rows(RowsShared<D, kFormat>& sm, RowState<D, N>& st, int rows)
 {
     static_assert(sizeof(sm.ring[0]) >= 16 * D * sizeof(float), "the ring holds 16 rows of output");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, quad = lane & 3;
     float* o = reinterpret_cast<float*>(sm.ring[warp]);
     finish_sums(st);
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const int row = g + 8 * r;
-        if (row >= rows) continue;
-        if (quad == 0) {
-            sm.m[warp][row] = st.m[r];
-            sm.l[warp][row] = st.l[r];
-        }
+    for (int n = 0; n < N; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            float* dst = o + row * D + (quad * 2 + e) * (D / 8);
+            const int row = 8 * n + 2 * quad + e;
+            if (row >= rows) continue;
+            if (g == 0) {
+                sm.m[warp][row] = st.m[n][e];
+                sm.l[warp][row] = st.l[n][e];
+            }
+            float* dst = o + row * D + g * (D / 8);
 #pragma unroll
-            for (int t = 0; t < D / 8; t += 4)
-                *reinterpret_cast<float4*>(dst + t) = make_float4(st.o[t][r * 2 + e], st.o[t + 1][r * 2 + e],
-                                                                  st.o[t + 2][r * 2 + e], st.o[t + 3][r * 2 + e]);
+            for (int t = 0; t < D / 16; t += 2)
+                *reinterpret_cast<float4*>(dst + 2 * t) =
+                    make_float4(st.o[n][t][e], st.o[n][t][2 + e], st.o[n][t + 1][e], st.o[n][t + 1][2 + e]);
         }
-    }
 }
 
 template <int D, int kFormat>
@@ -472,61 +521,72 @@ struct Joined {
     }
 };
 
-// The shared prefix, 16 rows at a time: CTA c's part of the line of blocks (AttnPlan).
-template <int D, int kFormat>
-__global__ void __launch_bounds__(kRowsThreads, 3) attn_prefix_rows_kernel(const AttnArgs a)
+// The join of the CTA's warps becomes piece `piece` (their rows are in shared memory, after a barrier).
+template <int D, int kFormat, int N>
+__device__ __forceinline__ void write_piece(const RowsShared<D, kFormat>& sm, float* part, float2* ml, int64_t piece)
 {
+    constexpr int kRows = 8 * N;
+    float* po = part + piece * kRows * D;
+    for (int i = threadIdx.x; i < kRows * D / 4; i += kRowsThreads) {
+        const int r = i % kRows, col = i / kRows * 4;
+        Joined j{sm.m[0][r], 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+#pragma unroll
+        for (int w = 1; w < kRowsWarps; ++w) j.top = fmax_nan(j.top, sm.m[w][r]);
+#pragma unroll
+        for (int w = 0; w < kRowsWarps; ++w)
+            j.add(sm.m[w][r], *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(sm.ring[w]) + r * D + col), sm.l[w][r]);
+        *reinterpret_cast<float4*>(po + (col / 4 * kRows + r) * 4) = j.acc;
+        if (col == 0) ml[piece * kRows + r] = make_float2(j.top, sm.bad == 2 ? kPieceTimeout : (sm.bad ? kPieceBadPage : j.l));
+    }
+}
+
+// The shared prefix, 8 N rows at a time: CTA c's part of the line of blocks (AttnPlan).
+template <int D, int kFormat, int N>
+__global__ void __launch_bounds__(kRowsThreads, N == 1 ? 4 : 3) attn_prefix_rows_kernel(const AttnArgs a)
+{
+    constexpr int kRows = 8 * N;
     extern __shared__ __align__(128) unsigned char raw[];
     RowsShared<D, kFormat>& sm = *reinterpret_cast<RowsShared<D, kFormat>*>(raw);
     const AttnPlan& p = a.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t u0 = (int64_t)blockIdx.x * p.units / p.ctas, u1 = ((int64_t)blockIdx.x + 1) * p.units / p.ctas;
+    const int u0 = (int)blockIdx.x * p.share, u1 = min(p.share, p.units - u0) + u0;
     init_rings(sm);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    PageList list{a.a.prefix_pages, a.c.n_pages, a.page_shift, 0, a.c.n_heads};
-    Walk<D, kFormat> walk{a.c, list, sm.ring[warp], sm.full[warp], 0u};
-    for (int64_t u = u0; u < u1;) {
-        const int64_t item = u / p.nblk;
-        const int64_t end = min(u1, (item + 1) * p.nblk);
-        const int head = (int)(item / p.n_tiles);
-        const int64_t r0 = (item - (int64_t)head * p.n_tiles) * 16;
-        const int rows = (int)min((int64_t)16, p.R - r0);
-        const int t0 = (int)(u - item * p.nblk) * p.block_keys;
-        const int t1 = (int)min(a.a.prefix_len, (end - item * p.nblk) * (int64_t)p.block_keys);
-        RowState<D, kFormat> st;
-        load_query<D, kFormat>(st, rows, a.qk_scale, [&](int r) {
+    Walk<D, kFormat> walk{a.c, a.page_shift, 0, sm.ring[warp], sm.full[warp]};
+    for (int u = u0; u < u1;) {
+        const int item = u / p.nblk;
+        const int end = min(u1 - item * p.nblk, p.nblk) + item * p.nblk;
+        const int head = item / p.n_tiles;
+        const int64_t r0 = (int64_t)(item - head * p.n_tiles) * kRows;
+        const int rows = (int)min((int64_t)kRows, p.R - r0);
+        const int t0 = (u - item * p.nblk) * p.block_keys;
+        const int t1 = (int)min(a.a.prefix_len, (int64_t)(end - item * p.nblk) * p.block_keys);
+        walk.head = head;
+        walk.look(a.a.prefix_pages, t0 + warp * 16, t1);
+        RowState<D, N> st;
+        load_query<D, kFormat, N>(st, rows, [&](int r) {
             const int64_t row = r0 + r, bt = row / a.G;
             return static_cast<const __nv_bfloat16*>(a.a.q) + (bt * a.a.n_q_heads + (int64_t)head * a.G + (row - bt * a.G)) * D;
         });
-        list.head = head;
-        const int lim[2] = {t1, t1};
-        const int fault = attend<D, kFormat>(st, walk, t0 + warp * 16, kRowsWarps * 16, t1, lim);
-        store_rows<D, kFormat>(sm, st, 16);
+        walk.start(t0 + warp * 16, kRowsWarps * 16, t1);
+        ready_query<D, kFormat, N>(st, a.qk_scale);
+        int lim[N][2];
+#pragma unroll
+        for (int n = 0; n < N; ++n) lim[n][0] = lim[n][1] = t1;
+        const int fault = attend<D, kFormat, N>(st, walk, lim);
+        store_rows<D, kFormat, N>(sm, st, kRows);
         if (fault && lane == 0) atomicMax(&sm.bad, fault);
         __syncthreads();
-        const int64_t piece = blockIdx.x + item;
-        float* po = a.part + piece * 16 * D;
-        for (int i = threadIdx.x; i < 16 * D / 4; i += kRowsThreads) {
-            const int r = i & 15, col = (i >> 4) * 4;
-            Joined j{sm.m[0][r], 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-#pragma unroll
-            for (int w = 1; w < kRowsWarps; ++w) j.top = fmax_nan(j.top, sm.m[w][r]);
-#pragma unroll
-            for (int w = 0; w < kRowsWarps; ++w)
-                j.add(sm.m[w][r], *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(sm.ring[w]) + r * D + col), sm.l[w][r]);
-            *reinterpret_cast<float4*>(po + (col / 4 * 16 + r) * 4) = j.acc;
-            if (col == 0) a.ml[piece * 16 + r] = make_float2(j.top, sm.bad == 2 ? kPieceTimeout : (sm.bad ? kPieceBadPage : j.l));
-        }
+        write_piece<D, kFormat, N>(sm, a.part, a.ml, (int64_t)blockIdx.x + item);
         __syncthreads();
         // The rings held output: order those accesses before the next copies into them.
         fence_proxy_async();
-        if (sm.bad == 2) {  // give up: every later piece says so (uniform: nothing writes it here)
-            for (u = end; u < u1; u = min(u1, (u / p.nblk + 1) * p.nblk))
-                if (threadIdx.x < 16) a.ml[(blockIdx.x + u / p.nblk) * 16 + threadIdx.x] = make_float2(0.f, kPieceTimeout);
-            break;
-        }
         u = end;
+        if (sm.bad == 2) break;  // a wait ran out (uniform: nothing writes it here)
     }
+    if (sm.bad == 2 && threadIdx.x < kRows)  // then every piece says so
+        for (int item = u0 / p.nblk; item <= (u1 - 1) / p.nblk; ++item)
+            a.ml[((int64_t)blockIdx.x + item) * kRows + threadIdx.x] = make_float2(0.f, kPieceTimeout);
 }
 
 // The pieces of the shared prefix that hold a row's item: piece `first` on, `count` of them.
@@ -536,9 +596,8 @@ struct Pieces {
 };
 __device__ __forceinline__ Pieces pieces_of(const AttnPlan& p, int64_t item)
 {
-    if (p.nblk == 0) return Pieces{0, 0};
-    const int64_t c0 = ((item * p.nblk + 1) * p.ctas - 1) / p.units, c1 = ((item + 1) * p.nblk * p.ctas - 1) / p.units;
-    return Pieces{c0 + item, (int)(c1 - c0 + 1)};
+    const int first = (int)item * p.nblk, c0 = first / p.share, c1 = (first + p.nblk - 1) / p.share;
+    return Pieces{c0 + item, c1 - c0 + 1};
 }
 
 // 1 / sum as the output takes it: 0 where no token was seen, NaN where something was bad.
@@ -546,6 +605,95 @@ __device__ __forceinline__ float inverse_sum(float l, bool bad)
 {
     if (bad) return __int_as_float(0x7FC00000);
     return l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+}
+
+// The join of many parts of a few rows by a CTA.  The parts' (maximum, sum) come in parallel, 64 at a time; a
+// warp for each row turns them into weights in shared memory; then every thread adds up its float4 columns
+// with twelve loads on the way at once.
+constexpr int kJoinChunk = 64, kFlight = 12;
+template <int kRows> struct JoinShared {
+    float2 ml[kRows][kJoinChunk];  // then (weight, -)
+    float scale[kRows], top[kRows], l[kRows];
+    int state[kRows];  // 1: a bad page, 2: a wait that ran out
+};
+
+// kMost: most float4 of output for each thread.  ml(row, part) and value(row, part, column) fetch a part's;
+// output i of the CTA's rows * columns is column `column(i)` of row i / columns.
+template <int kRows, int kMost, typename Ml, typename Value, typename Column>
+__device__ __forceinline__ void join_parts(JoinShared<kRows>& sm, int rows, int columns, int parts, float4 (&acc)[kMost], Ml ml, Value value,
+                                           Column column)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const float neg = -__int_as_float(0x7F800000);
+#pragma unroll
+    for (int k = 0; k < kMost; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (threadIdx.x < kRows) sm.top[threadIdx.x] = neg, sm.l[threadIdx.x] = 0.f, sm.state[threadIdx.x] = 0;
+    for (int c0 = 0; c0 < parts; c0 += kJoinChunk) {
+        const int n = min(parts - c0, kJoinChunk);
+        __syncthreads();
+        for (int i = threadIdx.x; i < rows * kJoinChunk; i += kRowsThreads) {
+            const int r = i / kJoinChunk, j = i % kJoinChunk;
+            sm.ml[r][j] = j < n ? ml(r, c0 + j) : make_float2(neg, 0.f);
+        }
+        __syncthreads();
+        for (int r = warp; r < rows; r += kRowsWarps) {
+            float2 x[kJoinChunk / 32];
+            float top = sm.top[r];
+            const float was = top;
+#pragma unroll
+            for (int k = 0; k < kJoinChunk / 32; ++k) {
+                x[k] = sm.ml[r][lane + 32 * k];
+                top = fmax_nan(top, x[k].x);
+            }
+            top = warp_max_nan(top);
+            float l = 0.f;
+            int state = 0;
+#pragma unroll
+            for (int k = 0; k < kJoinChunk / 32; ++k) {
+                const float w = join_weight(x[k].x, top);
+                state = max(state, x[k].y < 0.f ? (x[k].y == kPieceTimeout ? 2 : 1) : 0);
+                l = fmaf(w, x[k].y, l);
+                sm.ml[r][lane + 32 * k].x = w;
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+            state = (int)warp_max_u32((uint32_t)state);
+            if (lane == 0) {
+                const float f = join_weight(was, top);
+                sm.scale[r] = f;
+                sm.top[r] = top;
+                sm.l[r] = fmaf(sm.l[r], f, l);
+                sm.state[r] = max(sm.state[r], state);
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kMost; ++k) {
+            const int i = threadIdx.x + k * kRowsThreads;
+            if (i >= rows * columns) break;
+            const int r = i / columns, col = column(i);
+            const float f = sm.scale[r];
+            float4 y = acc[k];
+            y.x *= f, y.y *= f, y.z *= f, y.w *= f;
+            for (int j = 0; j < n; j += kFlight) {
+                float4 x[kFlight];
+                float w[kFlight];
+#pragma unroll
+                for (int t = 0; t < kFlight; ++t) {  // past the end: the last part again, with weight 0
+                    x[t] = value(r, c0 + min(j + t, n - 1), col);
+                    w[t] = j + t < n ? sm.ml[r][j + t].x : 0.f;
+                }
+#pragma unroll
+                for (int t = 0; t < kFlight; ++t)
+                    if (j + t < n) {
+                        y.x = fmaf(w[t], x[t].x, y.x), y.y = fmaf(w[t], x[t].y, y.y);
+                        y.z = fmaf(w[t], x[t].z, y.z), y.w = fmaf(w[t], x[t].w, y.w);
+                    }
+            }
+            acc[k] = y;
+        }
+    }
+    __syncthreads();
 }
 
 template <int kFormat>
@@ -559,12 +707,15 @@ __device__ __forceinline__ float log_sum(float top, float l, bool bad)
 // One sequence's own tokens for one key head, then the join with the pieces of the shared prefix, the
 // division by the sum and the output.  With many sequences each warp has one for itself, and joins in
 // registers; else the four warps of a CTA, or of a cluster of CTAs, take its chunks in turn and join
-// through (distributed) shared memory.
-template <int D, int kFormat, bool kOneWarp>
-__global__ void __launch_bounds__(kRowsThreads, 3) attn_suffix_kernel(const AttnArgs a)
+// through (distributed) shared memory.  A small call has no pieces: every sequence walks over the prefix
+// itself (AttnPlan::shared).
+template <int D, int kFormat, int N, bool kOneWarp>
+__global__ void __launch_bounds__(kRowsThreads, N == 1 ? 4 : 3) attn_suffix_kernel(const AttnArgs a)
 {
+    constexpr int kRows = 8 * N;
     extern __shared__ __align__(128) unsigned char raw[];
     RowsShared<D, kFormat>& sm = *reinterpret_cast<RowsShared<D, kFormat>*>(raw);
+    JoinShared<kRows>& js = *reinterpret_cast<JoinShared<kRows>*>(raw + (sizeof(sm) + 15) / 16 * 16);  // not there where kOneWarp
     const AttnPlan& p = a.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, quad = lane & 3;
     const int ncl = kOneWarp ? 1 : p.cluster, rank = kOneWarp ? 0 : (int)(blockIdx.x % ncl);
@@ -575,93 +726,125 @@ __global__ void __launch_bounds__(kRowsThreads, 3) attn_suffix_kernel(const Attn
     const int64_t b = bh / (uint32_t)a.c.n_heads;
     const int head = (int)(bh - (uint32_t)b * a.c.n_heads);
     if (kOneWarp && b >= a.a.B) return;  // the last CTA's spare warps
-    const int Tq = a.a.q_len, G = a.G, r0 = tile * 16, rows = min(16, Tq * G - r0);
+    const int Tq = a.a.q_len, G = a.G, r0 = tile * kRows, rows = min(kRows, Tq * G - r0);
     const int len = a.a.suffix_len[b];
     const bool fits = len >= 0 && len <= a.a.table_width << a.page_shift;
     // Row r of the sequence is query r / G, head r % G of the group: own tokens that it sees.
     auto seen = [&](int r) {
-        const int n = len - Tq + 1 + min(r, Tq * G - 1) / G;
+        const int n = len - Tq + 1 + (Tq == 1 ? 0 : min(r, Tq * G - 1) / G);
         return fits && n > 0 ? n : 0;
     };
     auto out_row = [&](int r) {
-        const int t = (r0 + r) / G;
+        const int t = Tq == 1 ? 0 : (r0 + r) / G;
         return (b * Tq + t) * a.a.n_q_heads + (int64_t)head * G + (r0 + r - t * G);
     };
-    RowState<D, kFormat> st;
-    load_query<D, kFormat>(st, rows, a.qk_scale, [&](int r) { return static_cast<const __nv_bfloat16*>(a.a.q) + out_row(r) * D; });
-    const PageList list{a.a.page_table + b * a.a.table_ld, a.c.n_pages, a.page_shift, head, a.c.n_heads};
-    Walk<D, kFormat> walk{a.c, list, sm.ring[warp], sm.full[warp], 0u};
-    const int lim[2] = {seen(r0 + g), seen(r0 + g + 8)};
-    const int last = seen(r0 + rows - 1);
-    const int fault = attend<D, kFormat>(st, walk, kOneWarp ? 0 : (rank * kRowsWarps + warp) * 16, kOneWarp ? 16 : ncl * kRowsWarps * 16,
-                                         last, lim);
+    const int first = kOneWarp ? 0 : (rank * kRowsWarps + warp) * 16, step = kOneWarp ? 16 : ncl * kRowsWarps * 16;
+    const bool own_prefix = !p.shared && a.a.prefix_len;
+    const int32_t* own_pages = a.a.page_table + b * a.a.table_ld;
+    const int64_t capacity = a.a.table_width << a.page_shift;
+    Walk<D, kFormat> walk{a.c, a.page_shift, head, sm.ring[warp], sm.full[warp]};
+    walk.look(own_prefix ? a.a.prefix_pages : own_pages, first, own_prefix ? a.a.prefix_len : capacity);
+    RowState<D, N> st;
+    load_query<D, kFormat, N>(st, rows, [&](int r) { return static_cast<const __nv_bfloat16*>(a.a.q) + out_row(r) * D; });
+    walk.start(first, step, own_prefix ? (int)a.a.prefix_len : seen(r0 + rows - 1));
+    ready_query<D, kFormat, N>(st, a.qk_scale);
+    int lim[N][2];
+    int fault = 0;
+    if (own_prefix) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) lim[n][0] = lim[n][1] = (int)a.a.prefix_len;
+        const int own_first = own_pages && first < capacity ? own_pages[first >> a.page_shift] : 0;  // on its way meanwhile
+        fault = attend<D, kFormat, N>(st, walk, lim);
+        walk.pages = own_pages, walk.page = own_first;
+        walk.start(first, step, fault == 2 ? 0 : seen(r0 + rows - 1));
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) lim[n][e] = seen(r0 + 8 * n + 2 * quad + e);
+    fault = max(fault, attend<D, kFormat, N>(st, walk, lim));
     const float neg = -__int_as_float(0x7F800000);
     const int64_t row0 = b * Tq * G + r0;  // the tile's first row among the key head's R
 
     if (kOneWarp) {
         finish_sums(st);
         asm volatile("griddepcontrol.wait;" ::: "memory");  // the pieces of the shared prefix
-        const Pieces pc = pieces_of(p, (int64_t)head * p.n_tiles + row0 / p.tile_rows);
-        const int in0 = (int)(row0 % p.tile_rows);
+        Pieces pc{0, 0}, pc_next{0, 0};
+        int in0 = 0;
+        if (p.shared) {
+            const int64_t item = (int64_t)head * p.n_tiles + row0 / p.tile_rows;
+            in0 = (int)(row0 % p.tile_rows);
+            pc = pieces_of(p, item);
+            if (in0 + rows > p.tile_rows) pc_next = pieces_of(p, item + 1);  // a prefix tile ends inside these rows
+        }
         bool any_bad = false, any_late = fault == 2;
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int row = g + 8 * r;
-            if (row >= rows) continue;
-            // A tile of the prefix may end inside these rows: its next one is the next item.
-            Pieces mine = pc;
-            int in_tile = in0 + row;
-            if (in_tile >= p.tile_rows) in_tile -= p.tile_rows, mine = pieces_of(p, (int64_t)head * p.n_tiles + row0 / p.tile_rows + 1);
-            const float2* ml = a.ml + mine.first * p.tile_rows + in_tile;
-            float top = st.m[r];
-#pragma unroll 4
-            for (int j = 0; j < mine.count; ++j) top = fmax_nan(top, ml[(int64_t)j * p.tile_rows].x);
-            const float f0 = join_weight(st.m[r], top);
-            float l = st.l[r] * f0;
-            bool bad = fault || !fits, late = fault == 2;
-#pragma unroll
-            for (int t = 0; t < D / 8; ++t) st.o[t][2 * r] *= f0, st.o[t][2 * r + 1] *= f0;
-            const float4* part = reinterpret_cast<const float4*>(a.part) + mine.first * p.tile_rows * (D / 4) + in_tile;
-#pragma unroll 2
-            for (int j = 0; j < mine.count; ++j) {
-                const float2 x = ml[(int64_t)j * p.tile_rows];
-                const float f = join_weight(x.x, top);
-                bad = bad || x.y < 0.f;
-                late = late || x.y == kPieceTimeout;
-                l = fmaf(f, x.y, l);
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-#pragma unroll
-                    for (int t = 0; t < D / 8; t += 4) {
-                        const float4 y = part[((int64_t)j * (D / 4) + ((quad * 2 + e) * (D / 8) + t) / 4) * p.tile_rows];
-                        st.o[t][2 * r + e] = fmaf(f, y.x, st.o[t][2 * r + e]);
-                        st.o[t + 1][2 * r + e] = fmaf(f, y.y, st.o[t + 1][2 * r + e]);
-                        st.o[t + 2][2 * r + e] = fmaf(f, y.z, st.o[t + 2][2 * r + e]);
-                        st.o[t + 3][2 * r + e] = fmaf(f, y.w, st.o[t + 3][2 * r + e]);
-                    }
-            }
-            const float inv = inverse_sum(l, bad);
-            const int64_t orow = out_row(row);
+        for (int n = 0; n < N; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
+                const int row = 8 * n + 2 * quad + e;
+                if (row >= rows) continue;
+                int in_tile = in0 + row;
+                Pieces mine = pc;
+                if (in_tile >= p.tile_rows) in_tile -= p.tile_rows, mine = pc_next;
+                const float2* ml = a.ml + mine.first * p.tile_rows + in_tile;
+                float top = st.m[n][e];
+                for (int j = 0; j < mine.count; j += 4) {  // four at a time, past the end the last one again
+                    float m[4];
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) m[t] = ml[(int64_t)min(j + t, mine.count - 1) * p.tile_rows].x;
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) top = fmax_nan(top, m[t]);
+                }
+                const float f0 = join_weight(st.m[n][e], top);
+                float l = st.l[n][e] * f0;
+                bool bad = fault || !fits, late = fault == 2;
+                float acc[D / 8];
+#pragma unroll
+                for (int t = 0; t < D / 16; ++t) acc[2 * t] = st.o[n][t][e] * f0, acc[2 * t + 1] = st.o[n][t][2 + e] * f0;
+                const float4* part = reinterpret_cast<const float4*>(a.part) + (mine.first * (D / 4) + g * (D / 32)) * p.tile_rows + in_tile;
+                for (int j = 0; j < mine.count; j += 2) {  // two at a time, past the end with weight 0
+                    const int next = min(j + 1, mine.count - 1);
+                    const float2 x[2] = {ml[(int64_t)j * p.tile_rows], ml[(int64_t)next * p.tile_rows]};
+                    float4 y[2][D / 32];
+#pragma unroll
+                    for (int t = 0; t < D / 32; ++t) {
+                        y[0][t] = part[((int64_t)j * (D / 4) + t) * p.tile_rows];
+                        y[1][t] = part[((int64_t)next * (D / 4) + t) * p.tile_rows];
+                    }
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        if (k && j + 1 >= mine.count) break;
+                        const float f = join_weight(x[k].x, top);
+                        bad = bad || x[k].y < 0.f;
+                        late = late || x[k].y == kPieceTimeout;
+                        l = fmaf(f, x[k].y, l);
+#pragma unroll
+                        for (int t = 0; t < D / 32; ++t) {
+                            acc[4 * t] = fmaf(f, y[k][t].x, acc[4 * t]), acc[4 * t + 1] = fmaf(f, y[k][t].y, acc[4 * t + 1]);
+                            acc[4 * t + 2] = fmaf(f, y[k][t].z, acc[4 * t + 2]), acc[4 * t + 3] = fmaf(f, y[k][t].w, acc[4 * t + 3]);
+                        }
+                    }
+                }
+                const float inv = inverse_sum(l, bad);
+                const int64_t orow = out_row(row);
                 uint32_t w[D / 16];
 #pragma unroll
-                for (int t = 0; t < D / 8; t += 2)
-                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[t / 2]) : "f"(st.o[t + 1][2 * r + e] * inv), "f"(st.o[t][2 * r + e] * inv));
-                uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.a.out) + orow * D + (quad * 2 + e) * (D / 8));
+                for (int t = 0; t < D / 16; ++t)
+                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[t]) : "f"(acc[2 * t + 1] * inv), "f"(acc[2 * t] * inv));
+                uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.a.out) + orow * D + g * (D / 8));
 #pragma unroll
                 for (int i = 0; i < D / 64; ++i) dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                if (g == 0 && a.a.out_lse) a.a.out_lse[orow] = log_sum<kFormat>(top, l, bad);
+                any_bad = any_bad || bad;
+                any_late = any_late || late;
             }
-            if (quad == 0 && a.a.out_lse) a.a.out_lse[orow] = log_sum<kFormat>(top, l, bad);
-            any_bad = any_bad || bad;
-            any_late = any_late || late;
-        }
         any_bad = __any_sync(0xFFFFFFFFu, any_bad);
         any_late = __any_sync(0xFFFFFFFFu, any_late);
         if (lane == 0 && head == 0 && tile == p.suffix_tiles - 1 && a.a.out_status)
             a.a.out_status[b] = any_late ? TPS_ROW_TIMEOUT : (any_bad ? TPS_ROW_BAD_PARAM : TPS_ROW_OK);
     } else {
-        store_rows<D, kFormat>(sm, st, rows);
+        store_rows<D, kFormat, N>(sm, st, rows);
         if (lane == 0 && (fault || !fits)) atomicMax(&sm.bad, max(fault, 1));
         if (ncl > 1) {
             cluster_arrive();
@@ -670,7 +853,7 @@ __global__ void __launch_bounds__(kRowsThreads, 3) attn_suffix_kernel(const Attn
             __syncthreads();
         }
         asm volatile("griddepcontrol.wait;" ::: "memory");
-        // Rank k joins every ncl-th group of four columns, from all CTAs' shared memory.
+        // Every rank joins a D / ncl columns wide strip, from all CTAs' shared memory and from the pieces.
         const uint32_t base = smem_u32(raw);
         auto peer = [&](const void* x, int who) {
             const uint32_t addr = base + (uint32_t)(static_cast<const unsigned char*>(x) - raw);
@@ -689,52 +872,262 @@ __global__ void __launch_bounds__(kRowsThreads, 3) attn_suffix_kernel(const Attn
                          : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(addr));
             return x;
         };
+        Pieces pc{0, 0}, pc_next{0, 0};
+        int in0 = 0;
+        if (p.shared) {
+            const int64_t item = (int64_t)head * p.n_tiles + row0 / p.tile_rows;
+            in0 = (int)(row0 % p.tile_rows);
+            pc = pieces_of(p, item);
+            if (in0 + rows > p.tile_rows) pc_next = pieces_of(p, item + 1);  // a prefix tile ends inside these rows
+        }
+        const int own = ncl * kRowsWarps, columns = D / 4 / ncl;
+        auto piece_of = [&](int r, int j) {  // row r's piece j - own, and its row of the tile there (-1: it has no such piece)
+            const bool wraps = in0 + r >= p.tile_rows;
+            const Pieces& mine = wraps ? pc_next : pc;
+            return make_longlong2(mine.first + (j - own), j - own < mine.count ? in0 + r - (wraps ? p.tile_rows : 0) : -1);
+        };
+        float4 acc[kRows * D / 4 / kRowsThreads];
+        join_parts(
+            js, rows, columns, own + max(pc.count, pc_next.count), acc,
+            [&](int r, int j) {
+                if (j < own) return make_float2(ld1(peer(&sm.m[j % kRowsWarps][r], j / kRowsWarps)), ld1(peer(&sm.l[j % kRowsWarps][r], j / kRowsWarps)));
+                const longlong2 at = piece_of(r, j);
+                return at.y < 0 ? make_float2(neg, 0.f) : a.ml[at.x * p.tile_rows + at.y];
+            },
+            [&](int r, int j, int col) {
+                if (j < own) return ld4(peer(reinterpret_cast<const float*>(sm.ring[j % kRowsWarps]) + r * D + col * 4, j / kRowsWarps));
+                const longlong2 at = piece_of(r, j);
+                if (at.y < 0) return make_float4(0.f, 0.f, 0.f, 0.f);
+                return reinterpret_cast<const float4*>(a.part)[(at.x * (D / 4) + col) * p.tile_rows + at.y];
+            },
+            [&](int i) { return rank * columns + i % columns; });
         int own_bad = 0;
         for (int k = 0; k < ncl; ++k) {
             int x;
             asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(x) : "r"(peer(&sm.bad, k)));
             own_bad = max(own_bad, x);
         }
-        for (int i = threadIdx.x * ncl + rank; i < rows * (D / 4); i += kRowsThreads * ncl) {
-            const int r = i / (D / 4), col = i % (D / 4) * 4;
-            const int64_t row = row0 + r;
-            const Pieces mine = pieces_of(p, (int64_t)head * p.n_tiles + row / p.tile_rows);
-            const int in_tile = (int)(row % p.tile_rows);
-            const float2* ml = a.ml + mine.first * p.tile_rows + in_tile;
-            Joined j{neg, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-            for (int k = 0; k < ncl; ++k)
 #pragma unroll
-                for (int w = 0; w < kRowsWarps; ++w) j.top = fmax_nan(j.top, ld1(peer(&sm.m[w][r], k)));
-#pragma unroll 4
-            for (int n = 0; n < mine.count; ++n) j.top = fmax_nan(j.top, ml[(int64_t)n * p.tile_rows].x);
-            for (int k = 0; k < ncl; ++k)
-#pragma unroll
-                for (int w = 0; w < kRowsWarps; ++w)
-                    j.add(ld1(peer(&sm.m[w][r], k)), ld4(peer(reinterpret_cast<const float*>(sm.ring[w]) + r * D + col, k)),
-                          ld1(peer(&sm.l[w][r], k)));
-            bool bad = own_bad != 0, late = own_bad == 2;
-            const float4* part = reinterpret_cast<const float4*>(a.part) + (mine.first * (D / 4) + col / 4) * p.tile_rows + in_tile;
-#pragma unroll 8
-            for (int n = 0; n < mine.count; ++n) {
-                const float2 x = ml[(int64_t)n * p.tile_rows];
-                bad = bad || x.y < 0.f;
-                late = late || x.y == kPieceTimeout;
-                j.add(x.x, part[(int64_t)n * (D / 4) * p.tile_rows], x.y);
-            }
-            const float inv = inverse_sum(j.l, bad);
+        for (int k = 0; k < kRows * D / 4 / kRowsThreads; ++k) {
+            const int i = threadIdx.x + k * kRowsThreads;
+            if (i >= rows * columns) break;
+            const int r = i / columns, col = rank * columns + i % columns;
+            const int state = max(js.state[r], own_bad);
+            const float inv = inverse_sum(js.l[r], state != 0);
             const int64_t orow = out_row(r);
             uint2 w;
-            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.x) : "f"(j.acc.y * inv), "f"(j.acc.x * inv));
-            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(j.acc.w * inv), "f"(j.acc.z * inv));
-            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.a.out) + orow * D + col) = w;
-            if (col == 0 && a.a.out_lse) a.a.out_lse[orow] = log_sum<kFormat>(j.top, j.l, bad);
-            if (i == 0 && head == 0 && tile == p.suffix_tiles - 1 && a.a.out_status)
-                a.a.out_status[b] = late ? TPS_ROW_TIMEOUT : (bad ? TPS_ROW_BAD_PARAM : TPS_ROW_OK);
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.x) : "f"(acc[k].y * inv), "f"(acc[k].x * inv));
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(acc[k].w * inv), "f"(acc[k].z * inv));
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.a.out) + orow * D + col * 4) = w;
+            if (col == 0 && a.a.out_lse) a.a.out_lse[orow] = log_sum<kFormat>(js.top[r], js.l[r], state != 0);
+            if (i == 0 && rank == 0 && head == 0 && tile == p.suffix_tiles - 1 && a.a.out_status)
+                a.a.out_status[b] = state == 2 ? TPS_ROW_TIMEOUT : (state ? TPS_ROW_BAD_PARAM : TPS_ROW_OK);
         }
         if (ncl > 1) {  // no CTA may leave while others read its shared memory
             cluster_arrive();
             cluster_wait();
         }
+    }
+}
+
+// ---------------------------------------------------------------------------------------------
+// Few sequences with many tokens of their own: their lengths differ, so the tokens are cut evenly instead.
+// The 64-token blocks of all (sequence, row tile, key head) items form one line, whose length only the
+// device knows: every CTA adds up the sequences' blocks, then takes its share of the line and leaves a
+// piece for each item it meets, as for the prefix; a last kernel joins the pieces.  Where the prefix is
+// not shared, its blocks come first in each item.
+// ---------------------------------------------------------------------------------------------
+constexpr int kLineMax = 1024;  // (sequence, row tile) pairs that a CTA adds up
+constexpr int kLineBlock = kRowsWarps * 16;
+
+// Tokens of its own that the last row of a tile sees (0 where the length is bad), and whether it is not.
+struct OwnTokens {
+    int seen;
+    bool fits;
+};
+__device__ __forceinline__ OwnTokens own_tokens(const AttnArgs& a, int64_t b, int row)
+{
+    const int len = a.a.suffix_len[b], Tq = a.a.q_len;
+    const bool fits = len >= 0 && len <= a.a.table_width << a.page_shift;
+    const int n = len - Tq + 1 + (Tq == 1 ? 0 : min(row, Tq * a.G - 1) / a.G);
+    return OwnTokens{fits && n > 0 ? n : 0, fits};
+}
+
+template <int D, int kFormat, int N>
+__global__ void __launch_bounds__(kRowsThreads, N == 1 ? 4 : 3) attn_line_kernel(const AttnArgs a)
+{
+    constexpr int kRows = 8 * N;
+    extern __shared__ __align__(128) unsigned char raw[];
+    RowsShared<D, kFormat>& sm = *reinterpret_cast<RowsShared<D, kFormat>*>(raw);
+    int64_t* before = reinterpret_cast<int64_t*>(raw + (sizeof(sm) + 15) / 16 * 16);  // blocks of the pairs before each one
+    int64_t* warp_sum = before + kLineMax + 1;
+    const AttnPlan& p = a.p;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = lane & 3;
+    const int heads = a.c.n_heads, pairs = (int)(a.a.B * p.suffix_tiles), Tq = a.a.q_len, G = a.G;
+    init_rings(sm);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int shared_len = p.shared ? 0 : (int)a.a.prefix_len, shared_blocks = (shared_len + kLineBlock - 1) / kLineBlock;
+
+    // Exclusive sums over the pairs: 8 consecutive ones for each thread.
+    constexpr int kEach = kLineMax / kRowsThreads;
+    int64_t mine[kEach], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int bt = threadIdx.x * kEach + i;
+        mine[i] = sum;
+        if (bt < pairs) {
+            const int b = bt / p.suffix_tiles, tile = bt - b * p.suffix_tiles;
+            sum += shared_blocks + (own_tokens(a, b, min(Tq * G, (tile + 1) * kRows) - 1).seen + kLineBlock - 1) / kLineBlock;
+        }
+    }
+    int64_t upto = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+        if (lane >= o) upto += x;
+    }
+    if (lane == 31) warp_sum[warp] = upto;
+    __syncthreads();
+    int64_t base = upto - sum;
+    for (int w = 0; w < warp; ++w) base += warp_sum[w];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) before[threadIdx.x * kEach + i] = base + mine[i];
+    if (threadIdx.x == kRowsThreads - 1) before[kLineMax] = base + sum;
+    __syncthreads();
+    const int64_t total = before[kLineMax] * heads;
+    if (blockIdx.x == 0)  // the join reads them
+        for (int i = threadIdx.x; i <= pairs; i += kRowsThreads) a.line[i] = i == pairs ? before[kLineMax] : before[i];
+
+    Walk<D, kFormat> walk{a.c, a.page_shift, 0, sm.ring[warp], sm.full[warp]};
+    const int64_t share = (total + p.line_ctas - 1) / p.line_ctas, u0 = blockIdx.x * share, u1 = min(u0 + share, total);
+    bool gave_up = false;
+    for (int64_t u = u0; u < u1;) {
+        // The pair whose blocks, once for each head, hold block u of the line.
+        int lo = 0, hi = pairs - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (before[mid] * heads <= u)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        const int bt = lo, b = bt / p.suffix_tiles, tile = bt - b * p.suffix_tiles;
+        const int64_t blocks = (bt + 1 < pairs ? before[bt + 1] : before[kLineMax]) - before[bt];
+        const int head = (int)((u - before[bt] * heads) / blocks);
+        const int64_t start = before[bt] * heads + head * blocks, end = min(u1, start + blocks);
+        const int r0 = tile * kRows, rows = min(kRows, Tq * G - r0);
+        const int first = (int)(u - start), past = (int)(end - start);  // blocks of the item
+        if (!gave_up) {
+            // Its blocks of the prefix (where each sequence walks over it itself), then its own.
+            const int p0 = min(first, shared_blocks) * kLineBlock, p1 = min(min(past, shared_blocks) * kLineBlock, shared_len);
+            const int seen = own_tokens(a, b, r0 + rows - 1).seen;
+            const int t0 = max(first - shared_blocks, 0) * kLineBlock, t1 = min(max(past - shared_blocks, 0) * kLineBlock, seen);
+            const int32_t* own_pages = a.a.page_table + b * a.a.table_ld;
+            walk.head = head;
+            walk.look(p0 < p1 ? a.a.prefix_pages : own_pages, (p0 < p1 ? p0 : t0) + warp * 16, p0 < p1 ? p1 : t1);
+            RowState<D, N> st;
+            load_query<D, kFormat, N>(st, rows, [&](int r) {
+                const int t = Tq == 1 ? 0 : (r0 + r) / G;
+                return static_cast<const __nv_bfloat16*>(a.a.q) +
+                       (((int64_t)b * Tq + t) * a.a.n_q_heads + (int64_t)head * G + (r0 + r - t * G)) * D;
+            });
+            walk.start((p0 < p1 ? p0 : t0) + warp * 16, kRowsWarps * 16, p0 < p1 ? p1 : t1);
+            ready_query<D, kFormat, N>(st, a.qk_scale);
+            int lim[N][2];
+            int fault = 0;
+            if (p0 < p1) {
+#pragma unroll
+                for (int n = 0; n < N; ++n) lim[n][0] = lim[n][1] = p1;
+                fault = attend<D, kFormat, N>(st, walk, lim);
+                walk.look(own_pages, t0 + warp * 16, t1);
+                walk.start(t0 + warp * 16, kRowsWarps * 16, fault == 2 ? 0 : t1);
+            }
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) lim[n][e] = min(t1, own_tokens(a, b, r0 + 8 * n + 2 * quad + e).seen);
+            fault = max(fault, attend<D, kFormat, N>(st, walk, lim));
+            store_rows<D, kFormat, N>(sm, st, kRows);
+            if (fault && lane == 0) atomicMax(&sm.bad, fault);
+        }
+        __syncthreads();
+        gave_up = sm.bad == 2;
+        write_piece<D, kFormat, N>(sm, a.line_part, a.line_ml, blockIdx.x + (int64_t)bt * heads + head);
+        __syncthreads();
+        if (threadIdx.x == 0 && !gave_up) sm.bad = 0;  // a bad page is this item's alone
+        walk.fault = 0;
+        fence_proxy_async();  // the rings held output: those accesses come before the next copies into them
+        __syncthreads();
+        u = end;
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // this grid ends after the prefix's, so the join need wait for this one only
+}
+
+template <int D, int kFormat>
+__global__ void __launch_bounds__(kRowsThreads) attn_join_kernel(const AttnArgs a)
+{
+    __shared__ JoinShared<16> js;
+    const AttnPlan& p = a.p;
+    const int heads = a.c.n_heads, Tq = a.a.q_len, G = a.G;
+    const uint32_t bt = blockIdx.x / (uint32_t)heads;
+    const int head = (int)(blockIdx.x - bt * heads);
+    const int64_t b = bt / (uint32_t)p.suffix_tiles;
+    const int tile = (int)(bt - (uint32_t)b * p.suffix_tiles);
+    const int r0 = tile * p.suffix_rows, rows = min(p.suffix_rows, Tq * G - r0);
+    const int64_t row0 = b * Tq * G + r0;
+    const bool fits = own_tokens(a, b, 0).fits;
+    Pieces pc{0, 0}, pc_next{0, 0}, own{0, 0};
+    int in0 = 0;
+    if (p.shared) {
+        const int64_t item = (int64_t)head * p.n_tiles + row0 / p.tile_rows;
+        in0 = (int)(row0 % p.tile_rows);
+        pc = pieces_of(p, item);
+        if (in0 + rows > p.tile_rows) pc_next = pieces_of(p, item + 1);  // a prefix tile ends inside these rows
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t total = a.line[a.a.B * p.suffix_tiles] * heads, before = a.line[bt], blocks = a.line[bt + 1] - before;
+    if (blocks) {
+        const int64_t start = before * heads + head * blocks;
+        const int64_t share = (total + p.line_ctas - 1) / p.line_ctas, c0 = start / share, c1 = (start + blocks - 1) / share;
+        own = Pieces{c0 + (int64_t)bt * heads + head, (int)(c1 - c0 + 1)};
+    }
+    const float neg = -__int_as_float(0x7F800000);
+    auto piece_of = [&](int r, int j) {  // row r's piece j of the prefix, and its row of the tile there (-1: it has no such piece)
+        const bool wraps = in0 + r >= p.tile_rows;
+        const Pieces& mine = wraps ? pc_next : pc;
+        return make_longlong2(mine.first + j, j < mine.count ? in0 + r - (wraps ? p.tile_rows : 0) : -1);
+    };
+    constexpr int kMost = 16 * (D / 4) / kRowsThreads;
+    float4 acc[kMost];
+    join_parts(
+        js, rows, D / 4, own.count + max(pc.count, pc_next.count), acc,
+        [&](int r, int j) {
+            if (j < own.count) return a.line_ml[(own.first + j) * p.suffix_rows + r];
+            const longlong2 at = piece_of(r, j - own.count);
+            return at.y < 0 ? make_float2(neg, 0.f) : a.ml[at.x * p.tile_rows + at.y];
+        },
+        [&](int r, int j, int col) {
+            if (j < own.count) return reinterpret_cast<const float4*>(a.line_part)[((own.first + j) * (D / 4) + col) * p.suffix_rows + r];
+            const longlong2 at = piece_of(r, j - own.count);
+            if (at.y < 0) return make_float4(0.f, 0.f, 0.f, 0.f);
+            return reinterpret_cast<const float4*>(a.part)[(at.x * (D / 4) + col) * p.tile_rows + at.y];
+        },
+        [&](int i) { return i % (D / 4); });
+#pragma unroll
+    for (int k = 0; k < kMost; ++k) {
+        const int i = threadIdx.x + k * kRowsThreads;
+        if (i >= rows * (D / 4)) break;
+        const int r = i / (D / 4), col = i % (D / 4), state = max(js.state[r], fits ? 0 : 1);
+        const float inv = inverse_sum(js.l[r], state != 0);
+        const int t = (r0 + r) / G;
+        const int64_t orow = (b * Tq + t) * a.a.n_q_heads + (int64_t)head * G + (r0 + r - t * G);
+        uint2 w;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.x) : "f"(acc[k].y * inv), "f"(acc[k].x * inv));
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(acc[k].w * inv), "f"(acc[k].z * inv));
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.a.out) + orow * D + col * 4) = w;
+        if (col == 0 && a.a.out_lse) a.a.out_lse[orow] = log_sum<kFormat>(js.top[r], js.l[r], state != 0);
+        if (i == 0 && head == 0 && tile == p.suffix_tiles - 1 && a.a.out_status)
+            a.a.out_status[b] = state == 2 ? TPS_ROW_TIMEOUT : (state ? TPS_ROW_BAD_PARAM : TPS_ROW_OK);
     }
 }
 

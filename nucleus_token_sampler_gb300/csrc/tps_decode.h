@@ -38,21 +38,26 @@ cudaError_t launch_kv_read(const KvReadArgs& a, bool bf16, int sms, cudaStream_t
 
 // The work of one prefix-attention call.  The shared part is cut along items and tokens: an item is one
 // key head and `tile_rows` of its R = B Tq G query rows; its prefix is nblk blocks of `block_keys`
-// tokens.  The items' blocks form one line of `units` blocks, of which CTA c of `ctas` takes
-// [c units / ctas, (c + 1) units / ctas): every CTA gets the same number of blocks (give or take one)
-// whatever the number of items.  A CTA's part of an item leaves one piece in the workspace, the
+// tokens.  The items' blocks form one line of `units` blocks, of which each CTA takes `share` consecutive ones
+// (the last CTA what is left).  A CTA's part of an item leaves one piece in the workspace, the
 // unnormalised output of its rows with their maximum and sum; piece c + item is CTA c's of that item
 // (going along the line either number grows, so no two share one).
 struct AttnPlan {
     int64_t R;           // query rows of one key head
-    int64_t items, nblk, units, ctas, pieces;
+    int items, nblk, units, share, ctas;
+    int64_t pieces;
     int tile_rows, block_keys;
     int n_tiles;         // row tiles of one key head
+    bool shared;         // the prefix is computed once, into pieces (else by each sequence for itself)
     bool tensor;         // the tcgen05 kernel computes the shared part
-    int suffix_tiles;    // 16-row tiles of one sequence's Tq G rows
+    int suffix_rows;     // rows of a tile of one sequence's Tq G rows: 8 or 16
+    int suffix_tiles;
     bool one_warp;       // each warp has a sequence (and head, tile) for itself
     int cluster;         // else: CTAs that share one sequence's own tokens
-    size_t off_ml, bytes;  // workspace: outputs first, then (maximum, sum)
+    bool line;           // or: the own tokens are cut evenly over `line_ctas` CTAs, which leave pieces too
+    int64_t line_ctas, line_pieces;
+    // workspace: outputs of the prefix's pieces, their (maximum, sum); the same of the line's; its sums
+    size_t off_ml, off_line_part, off_line_ml, off_line, bytes;
 };
 
 struct AttnArgs {
@@ -63,6 +68,9 @@ struct AttnArgs {
     float qk_scale;  // scale * log2(e)
     float* part;     // [pieces][D / 4][tile_rows][4]: a warp's rows lie side by side
     float2* ml;      // [pieces, tile_rows]: maximum in base-2 units, sum (negative: a bad page id)
+    float* line_part;
+    float2* line_ml;
+    int64_t* line;   // [B * suffix_tiles + 1] blocks before each (sequence, tile) pair
 };
 
 // The shared part, then the own tokens and the join.
@@ -71,5 +79,6 @@ cudaError_t launch_attn_prefix_bf16(const AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_attn_prefix_fp8(const AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_attn_prefix_int8(const AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_attn_suffix(const AttnArgs& a, bool after_prefix, cudaStream_t stream);
+cudaError_t launch_attn_line(const AttnArgs& a, bool after_prefix, cudaStream_t stream);
 
 }  // namespace tps

@@ -1,4 +1,4 @@
-// The 16-row attention kernels for each head size and cache format, and their launches.
+// The 8- and 16-row attention kernels for each head size and cache format, and their launches.
 #include "tps_attn_rows.cuh"
 
 #include <atomic>
@@ -21,29 +21,36 @@ cudaError_t allow_smem(Kernel k, size_t bytes, std::atomic<uint64_t>& allowed)
     return e;
 }
 
-template <int D, int kFormat>
-cudaError_t prefix_rows(const AttnArgs& a, cudaStream_t stream)
+template <int D, int kFormat, int N>
+cudaError_t prefix_rows_shape(const AttnArgs& a, cudaStream_t stream)
 {
     static std::atomic<uint64_t> allowed{0};
-    auto k = attn_prefix_rows_kernel<D, kFormat>;
+    auto k = attn_prefix_rows_kernel<D, kFormat, N>;
     const cudaError_t e = allow_smem(k, sizeof(RowsShared<D, kFormat>), allowed);
     if (e != cudaSuccess) return e;
     k<<<(unsigned)a.p.ctas, kRowsThreads, sizeof(RowsShared<D, kFormat>), stream>>>(a);
     return cudaGetLastError();
 }
 
-template <int D, int kFormat, bool kOneWarp>
+template <int D, int kFormat>
+cudaError_t prefix_rows(const AttnArgs& a, cudaStream_t stream)
+{
+    return a.p.tile_rows == 8 ? prefix_rows_shape<D, kFormat, 1>(a, stream) : prefix_rows_shape<D, kFormat, 2>(a, stream);
+}
+
+template <int D, int kFormat, int N, bool kOneWarp>
 cudaError_t suffix_shape(const AttnArgs& a, bool after_prefix, cudaStream_t stream)
 {
     static std::atomic<uint64_t> allowed{0};
-    auto k = attn_suffix_kernel<D, kFormat, kOneWarp>;
-    const cudaError_t e = allow_smem(k, sizeof(RowsShared<D, kFormat>), allowed);
+    auto k = attn_suffix_kernel<D, kFormat, N, kOneWarp>;
+    const size_t smem = (sizeof(RowsShared<D, kFormat>) + 15) / 16 * 16 + (kOneWarp ? 0 : sizeof(JoinShared<8 * N>));
+    const cudaError_t e = allow_smem(k, smem, allowed);
     if (e != cudaSuccess) return e;
     const int64_t items = a.a.B * a.c.n_heads * a.p.suffix_tiles;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(kOneWarp ? (items + kRowsWarps - 1) / kRowsWarps : items * a.p.cluster), 1, 1);
     cfg.blockDim = dim3(kRowsThreads, 1, 1);
-    cfg.dynamicSmemBytes = sizeof(RowsShared<D, kFormat>);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     int n = 0;
@@ -67,30 +74,90 @@ cudaError_t suffix_shape(const AttnArgs& a, bool after_prefix, cudaStream_t stre
 template <int D, int kFormat>
 cudaError_t suffix(const AttnArgs& a, bool after_prefix, cudaStream_t stream)
 {
-    return a.p.one_warp ? suffix_shape<D, kFormat, true>(a, after_prefix, stream)
-                        : suffix_shape<D, kFormat, false>(a, after_prefix, stream);
+    if (a.p.suffix_rows == 8)
+        return a.p.one_warp ? suffix_shape<D, kFormat, 1, true>(a, after_prefix, stream)
+                            : suffix_shape<D, kFormat, 1, false>(a, after_prefix, stream);
+    return a.p.one_warp ? suffix_shape<D, kFormat, 2, true>(a, after_prefix, stream)
+                        : suffix_shape<D, kFormat, 2, false>(a, after_prefix, stream);
+}
+
+cudaLaunchAttribute dependent()
+{
+    cudaLaunchAttribute at = {};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    return at;
+}
+
+template <int D, int kFormat, int N>
+cudaError_t line_shape(const AttnArgs& a, bool after_prefix, cudaStream_t stream)
+{
+    static std::atomic<uint64_t> allowed{0};
+    auto k = attn_line_kernel<D, kFormat, N>;
+    const size_t smem = (sizeof(RowsShared<D, kFormat>) + 15) / 16 * 16 + (kLineMax + 1 + kRowsWarps) * sizeof(int64_t);
+    cudaError_t e = allow_smem(k, smem, allowed);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute at = dependent();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)a.p.line_ctas, 1, 1);
+    cfg.blockDim = dim3(kRowsThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &at;
+    cfg.numAttrs = after_prefix ? 1 : 0;
+    e = cudaLaunchKernelEx(&cfg, k, a);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3((unsigned)(a.a.B * a.p.suffix_tiles * a.c.n_heads), 1, 1);
+    cfg.dynamicSmemBytes = 0;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_join_kernel<D, kFormat>, a);
+}
+
+template <int D, int kFormat>
+cudaError_t line(const AttnArgs& a, bool after_prefix, cudaStream_t stream)
+{
+    return a.p.suffix_rows == 8 ? line_shape<D, kFormat, 1>(a, after_prefix, stream) : line_shape<D, kFormat, 2>(a, after_prefix, stream);
+}
+
+enum class Part { kPrefix, kOwn, kLine };
+
+template <int D, int kFormat>
+cudaError_t part_of(Part part, const AttnArgs& a, bool after_prefix, cudaStream_t stream)
+{
+    switch (part) {
+    case Part::kPrefix: return prefix_rows<D, kFormat>(a, stream);
+    case Part::kOwn: return suffix<D, kFormat>(a, after_prefix, stream);
+    default: return line<D, kFormat>(a, after_prefix, stream);
+    }
 }
 
 template <int D>
-cudaError_t by_format(const AttnArgs& a, bool own, bool after_prefix, cudaStream_t stream)
+cudaError_t by_format(Part part, const AttnArgs& a, bool after_prefix, cudaStream_t stream)
 {
     switch (a.c.format) {
-    case TPS_KV_BF16: return own ? suffix<D, TPS_KV_BF16>(a, after_prefix, stream) : prefix_rows<D, TPS_KV_BF16>(a, stream);
-    case TPS_KV_FP8: return own ? suffix<D, TPS_KV_FP8>(a, after_prefix, stream) : prefix_rows<D, TPS_KV_FP8>(a, stream);
-    default: return own ? suffix<D, TPS_KV_INT8>(a, after_prefix, stream) : prefix_rows<D, TPS_KV_INT8>(a, stream);
+    case TPS_KV_BF16: return part_of<D, TPS_KV_BF16>(part, a, after_prefix, stream);
+    case TPS_KV_FP8: return part_of<D, TPS_KV_FP8>(part, a, after_prefix, stream);
+    default: return part_of<D, TPS_KV_INT8>(part, a, after_prefix, stream);
     }
+}
+
+cudaError_t launch(Part part, const AttnArgs& a, bool after_prefix, cudaStream_t stream)
+{
+    return a.c.head_dim == 64 ? by_format<64>(part, a, after_prefix, stream) : by_format<128>(part, a, after_prefix, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_prefix_rows(const AttnArgs& a, cudaStream_t stream)
-{
-    return a.c.head_dim == 64 ? by_format<64>(a, false, false, stream) : by_format<128>(a, false, false, stream);
-}
+cudaError_t launch_attn_prefix_rows(const AttnArgs& a, cudaStream_t stream) { return launch(Part::kPrefix, a, false, stream); }
 
 cudaError_t launch_attn_suffix(const AttnArgs& a, bool after_prefix, cudaStream_t stream)
 {
-    return a.c.head_dim == 64 ? by_format<64>(a, true, after_prefix, stream) : by_format<128>(a, true, after_prefix, stream);
+    return launch(Part::kOwn, a, after_prefix, stream);
+}
+
+cudaError_t launch_attn_line(const AttnArgs& a, bool after_prefix, cudaStream_t stream)
+{
+    return launch(Part::kLine, a, after_prefix, stream);
 }
 
 }  // namespace tps

@@ -5,6 +5,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import struct
 
 import torch
 
@@ -46,54 +47,74 @@ def declare(lib):
     lib.tps_prefix_attention_workspace.argtypes = [_P, _P]
 
 
-_SAME = contextlib.nullcontext()
+# A call's arguments are packed as the structures above lie in memory (native sizes and alignment):
+# several times faster than filling a ctypes structure field by field.
+# ("0q" pads the end to their alignment.)
+_NORM_LAYOUT, _ATTENTION_LAYOUT = struct.Struct("@4P8q5P2q6if0q"), struct.Struct("@8P5q2if0q")
+assert _NORM_LAYOUT.size == ctypes.sizeof(_NormRope) and _ATTENTION_LAYOUT.size == ctypes.sizeof(_Attention)
+_pack_norm, _pack_attention = _NORM_LAYOUT.pack, _ATTENTION_LAYOUT.pack
+
+_Tensor = torch.Tensor
+_empty = torch.empty  # with a device object: Tensor.new_empty and device strings take twice as long
+_fns = None
 
 
-def _on(dev, stream):
-    """The context a call allocates and launches in, and the raw stream.  A call on the current device
-    and stream, the usual one, enters nothing: the two context managers cost several microseconds."""
+def _bound():
+    """The entry points, once the library is loaded."""
+    global _fns
+    if _fns is None:
+        from . import load
+        lib = load()
+        _fns = (lib.tps_qk_norm_rope, lib.tps_kv_write, lib.tps_kv_read, lib.tps_prefix_attention,
+                lib.tps_prefix_attention_workspace)
+    return _fns
+
+
+def _run(device_index, stream, call, *args):
+    """``call(raw stream, *args)`` on the given stream or the current one.  A call on the current device
+    and stream, the usual one, enters no context: the two managers cost several microseconds."""
     if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(dev.index)
-        return (_SAME if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)), raw
-    both = contextlib.ExitStack()
-    both.enter_context(torch.cuda.device(dev))
-    both.enter_context(torch.cuda.stream(stream))
-    return both, stream.cuda_stream
+        raw = torch._C._cuda_getCurrentRawStream(device_index)
+        if device_index == torch._C._cuda_getDevice():
+            return call(raw, *args)
+        with torch.cuda.device(device_index):
+            return call(raw, *args)
+    with torch.cuda.device(device_index), torch.cuda.stream(stream):
+        return call(stream.cuda_stream, *args)
 
 
-def _lib():
-    from . import load
-    return load()
-
-
-def _check(rc, name):
-    if rc != 0:
-        from . import _ERRORS
-        lib = _lib()
-        extra = f" (cudaError {lib.tps_last_cuda_error()})" if rc == 5 else ""
-        raise RuntimeError(f"{name} failed: {_ERRORS.get(rc, rc)}{extra}")
+def _fail(rc, name):
+    from . import _ERRORS, load
+    extra = f" (cudaError {load().tps_last_cuda_error()})" if rc == 5 else ""
+    raise RuntimeError(f"{name} failed: {_ERRORS.get(rc, rc)}{extra}")
 
 
 def _code(dt):
-    from . import _dtype_code
-    return _dtype_code(dt)
+    if dt is torch.bfloat16:
+        return 1
+    if dt is torch.float32:
+        return 0
+    raise TypeError(f"values must be float32 or bfloat16, got {dt}")
 
 
-def _index(t, name, shape, dtype, dev, dense=True):
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != dev or tuple(t.shape) != shape or (
-            dense and not t.is_contiguous()):
-        raise ValueError(f"{name} must be a{' contiguous' if dense else ''} {dtype} tensor of shape {shape} on {dev}")
+def _dense(t, name, shape, dtype, device_index):
+    """The address of a contiguous tensor of this shape, type and device."""
+    if not isinstance(t, _Tensor) or t.dtype is not dtype or t.shape != shape or t.get_device() != device_index or (
+            not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{device_index}")
     return t.data_ptr()
 
 
-def _heads(t, name, dev=None, dtype=None):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+def _heads(t, name, device_index=None, dtype=None):
+    """Token and head strides of a [T, heads, head_dim] CUDA tensor."""
+    if not isinstance(t, _Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
-    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+    st = t.stride()
+    if len(st) != 3 or (st[2] != 1 and t.shape[2] > 1):
         raise ValueError(f"{name} must be [T, heads, head_dim] with unit stride along head_dim")
-    if dev is not None and (t.device != dev or t.dtype != dtype):
-        raise ValueError(f"{name} must be a {dtype} tensor on {dev}")
-    return t
+    if dtype is not None and (t.dtype is not dtype or t.get_device() != device_index):
+        raise ValueError(f"{name} must be a {dtype} tensor on cuda:{device_index}")
+    return st
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, positions, cos_sin, *, eps: float = 1e-6, interleaved: bool = False,
@@ -109,37 +130,42 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, cos_sin, *, eps: float = 1
     (2i, 2i + 1) rather than (i, i + R/2).  ``out``: a (q, k) pair to write to (the inputs themselves to
     work in place), else new tensors.  ``status``: an int32 [T] tensor that gets 3 for a token whose
     position is not in the table (its outputs are NaN), else 0.  Returns (q, k)."""
-    _heads(q, "q")
-    dev, dt = q.device, q.dtype
-    _heads(k, "k", dev, dt)
+    qs = _heads(q, "q")
+    dev, dt = q.get_device(), q.dtype
+    ks = _heads(k, "k", dev, dt)
     T, Hq, D = q.shape
-    Hk = k.shape[1]
-    if k.shape[0] != T or k.shape[2] != D:
+    Tk, Hk, Dk = k.shape
+    if Tk != T or Dk != D:
         raise ValueError("q and k must hold the same tokens and head size")
-    if not isinstance(cos_sin, torch.Tensor) or cos_sin.dim() != 2:
+    if not isinstance(cos_sin, _Tensor) or cos_sin.dim() != 2:
         raise ValueError("cos_sin must be a float32 [positions, R] tensor")
     n_pos, R = cos_sin.shape
     if R % 2 or R > D:
         raise ValueError("cos_sin must hold an even number of columns, at most the head size")
-    code = _code(dt)
-    ctx, raw = _on(dev, stream)
-    with ctx:
-        if out is None:
-            oq, ok = q.new_empty((T, Hq, D)), k.new_empty((T, Hk, D))
-        else:
-            oq, ok = _heads(out[0], "out[0]", dev, dt), _heads(out[1], "out[1]", dev, dt)
-            if oq.shape != q.shape or ok.shape != k.shape:
-                raise ValueError("out must have the shapes of q and k")
-        a = _NormRope(q.data_ptr(), k.data_ptr(), oq.data_ptr(), ok.data_ptr(), q.stride(0), q.stride(1), k.stride(0),
-                      k.stride(1), oq.stride(0), oq.stride(1), ok.stride(0), ok.stride(1),
-                      None if q_weight is None else _index(q_weight, "q_weight", (D,), torch.float32, dev),
-                      None if k_weight is None else _index(k_weight, "k_weight", (D,), torch.float32, dev),
-                      _index(positions, "positions", (T,), torch.int32, dev),
-                      _index(cos_sin, "cos_sin", (n_pos, R), torch.float32, dev),
-                      None if status is None else _index(status, "status", (T,), torch.int32, dev),
-                      T, n_pos, Hq, Hk, D, R, bool(interleaved), code, eps)
-        rc = _lib().tps_qk_norm_rope(ctypes.byref(a), raw)
-    _check(rc, "tps_qk_norm_rope")
+    if out is not None:
+        oqs, oks = _heads(out[0], "out[0]", dev, dt), _heads(out[1], "out[1]", dev, dt)
+        if out[0].shape != q.shape or out[1].shape != k.shape:
+            raise ValueError("out must have the shapes of q and k")
+    else:
+        oqs, oks = (Hq * D, D), (Hk * D, D)
+    tail = (qs[0], qs[1], ks[0], ks[1], oqs[0], oqs[1], oks[0], oks[1],
+            0 if q_weight is None else _dense(q_weight, "q_weight", (D,), torch.float32, dev),
+            0 if k_weight is None else _dense(k_weight, "k_weight", (D,), torch.float32, dev),
+            _dense(positions, "positions", (T,), torch.int32, dev),
+            _dense(cos_sin, "cos_sin", (n_pos, R), torch.float32, dev),
+            0 if status is None else _dense(status, "status", (T,), torch.int32, dev),
+            T, n_pos, Hq, Hk, D, R, 1 if interleaved else 0, _code(dt), eps)
+    return _run(dev, stream, _norm, q, k, out, tail)
+
+
+def _norm(raw, q, k, out, tail):
+    if out is None:
+        dt, dev = q.dtype, q.device
+        out = _empty(q.shape, dtype=dt, device=dev), _empty(k.shape, dtype=dt, device=dev)
+    oq, ok = out
+    rc = _bound()[0](_pack_norm(q.data_ptr(), k.data_ptr(), oq.data_ptr(), ok.data_ptr(), *tail), raw)
+    if rc:
+        _fail(rc, "tps_qk_norm_rope")
     return oq, ok
 
 
@@ -164,19 +190,21 @@ class KVCache:
             raise ValueError("head_dim must be a multiple of 16, at most 512")
         if pages < 1 or heads < 1:
             raise ValueError("a cache holds at least one page and one head")
-        _index(k, "k", (pages, heads, page, D), k.dtype, k.device)
-        _index(v, "v", (pages, heads, page, D), k.dtype, k.device)
+        dev = k.get_device()
+        _dense(k, "k", (pages, heads, page, D), k.dtype, dev)
+        _dense(v, "v", (pages, heads, page, D), k.dtype, dev)
         for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
             if self.format == "bf16":
                 if t is not None:
                     raise ValueError(f"{name}: a bfloat16 cache has no scales")
             else:
-                _index(t, name, (pages, heads, page), torch.bfloat16, k.device)
+                _dense(t, name, (pages, heads, page), torch.bfloat16, dev)
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.n_pages, self.n_heads, self.page_size, self.head_dim = pages, heads, page, D
         self.device = k.device
         ptr = lambda t: None if t is None else t.data_ptr()
-        self._c = _Cache(ptr(k), ptr(v), ptr(k_scale), ptr(v_scale), pages, heads, page, D, self.FORMATS[self.format][0])
+        self._index = dev
+        self._bytes = bytes(_Cache(ptr(k), ptr(v), ptr(k_scale), ptr(v_scale), pages, heads, page, D, self.FORMATS[self.format][0]))
 
     @classmethod
     def empty(cls, n_pages: int, n_heads: int, page_size: int, head_dim: int, format: str = "fp8", device="cuda"):
@@ -195,39 +223,45 @@ def kv_write(cache: KVCache, k, v, slots, *, stream=None) -> None:
     """Store T tokens: ``k``, ``v`` [T, heads, head_dim] (float32 or bfloat16, token and head strides
     free) at the slots ``slots`` ([T] int64).  8-bit caches get codes and a scale per (token, head); a
     slot outside the cache is skipped (-1 pads).  Slots of one call must differ from one another."""
-    _heads(k, "k", cache.device, k.dtype)
-    _heads(v, "v", cache.device, k.dtype)
+    dev = cache._index
+    dt = k.dtype
+    ks, vs = _heads(k, "k", dev, dt), _heads(v, "v", dev, dt)
     T = k.shape[0]
     if k.shape != (T, cache.n_heads, cache.head_dim) or v.shape != k.shape:
         raise ValueError(f"k and v must be [T, {cache.n_heads}, {cache.head_dim}]")
-    at = _index(slots, "slots", (T,), torch.int64, cache.device)
-    ctx, raw = _on(cache.device, stream)
-    with ctx:
-        rc = _lib().tps_kv_write(ctypes.byref(cache._c), k.data_ptr(), v.data_ptr(), _code(k.dtype), T, k.stride(0),
-                                 k.stride(1), v.stride(0), v.stride(1), at, raw)
-    _check(rc, "tps_kv_write")
+    _run(dev, stream, _write, (cache._bytes, k.data_ptr(), v.data_ptr(), _code(dt), T, ks[0], ks[1], vs[0], vs[1],
+                               _dense(slots, "slots", (T,), torch.int64, dev)))
+
+
+def _write(raw, args):
+    rc = _bound()[1](*args, raw)
+    if rc:
+        _fail(rc, "tps_kv_write")
 
 
 def kv_read(cache: KVCache, slots, *, dtype=torch.bfloat16, out=None, stream=None):
     """The stored values of the slots ``slots`` ([T] int64) as (k, v), [T, heads, head_dim] of ``dtype``
     (float32 or bfloat16); a slot outside the cache reads as zeros.  ``out``: a (k, v) pair to write to."""
-    dev = cache.device
-    if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
+    dev = cache._index
+    if not isinstance(slots, _Tensor) or slots.dim() != 1:
         raise ValueError("slots must be an int64 [T] tensor")
     T = slots.shape[0]
-    at = _index(slots, "slots", (T,), torch.int64, dev)
+    at = _dense(slots, "slots", (T,), torch.int64, dev)
     shape = (T, cache.n_heads, cache.head_dim)
-    code = _code(dtype)
-    ctx, raw = _on(dev, stream)
-    with ctx:
-        if out is None:
-            k, v = torch.empty(shape, dtype=dtype, device=dev), torch.empty(shape, dtype=dtype, device=dev)
-        else:
-            k, v = out
-            _index(k, "out[0]", shape, dtype, dev)
-            _index(v, "out[1]", shape, dtype, dev)
-        rc = _lib().tps_kv_read(ctypes.byref(cache._c), at, T, k.data_ptr(), v.data_ptr(), code, raw)
-    _check(rc, "tps_kv_read")
+    if out is not None:
+        _dense(out[0], "out[0]", shape, dtype, dev)
+        _dense(out[1], "out[1]", shape, dtype, dev)
+    return _run(dev, stream, _read, cache, at, shape, dtype, _code(dtype), out)
+
+
+def _read(raw, cache, at, shape, dtype, code, out):
+    if out is None:
+        dev = cache.device
+        out = _empty(shape, dtype=dtype, device=dev), _empty(shape, dtype=dtype, device=dev)
+    k, v = out
+    rc = _bound()[2](cache._bytes, at, shape[0], k.data_ptr(), v.data_ptr(), code, raw)
+    if rc:
+        _fail(rc, "tps_kv_read")
     return k, v
 
 
@@ -246,53 +280,55 @@ def prefix_attention(q, cache: KVCache, prefix_pages, prefix_len: int, page_tabl
     sequence with a page outside the cache or a length outside its table (its outputs are NaN), else 0.
     ``workspace``: a uint8 tensor of at least ``prefix_attention_workspace(...)`` bytes to use instead of
     the library's memory pool."""
-    if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dtype != torch.bfloat16 or q.dim() not in (3, 4) or (
+    if not isinstance(q, _Tensor) or not q.is_cuda or q.dtype is not torch.bfloat16 or q.dim() not in (3, 4) or (
             not q.is_contiguous()):
         raise ValueError("q must be a contiguous bfloat16 CUDA tensor [B, heads, D] or [B, tokens, heads, D]")
-    dev = q.device
-    B, D = q.shape[0], q.shape[-1]
-    if dev != cache.device or D != cache.head_dim:
+    dev, shape = q.get_device(), q.shape
+    B, Hq, D = shape[0], shape[-2], shape[-1]
+    if dev != cache._index or D != cache.head_dim:
         raise ValueError(f"q must have head size {cache.head_dim} and be on {cache.device}")
     if D not in (64, 128):
         raise ValueError("prefix_attention takes head sizes 64 and 128")
-    Hq = q.shape[-2]
     if Hq % cache.n_heads:
         raise ValueError(f"the query heads must be a multiple of the cache's {cache.n_heads} heads")
     prefix_len = int(prefix_len)
-    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2 or (
-            page_table.shape[1] > 1 and page_table.stride(1) != 1):
-        raise ValueError("page_table must be an int32 [B, W] tensor with unit stride along W")
+    if not isinstance(page_table, _Tensor) or page_table.dim() != 2 or page_table.shape[0] != B or (
+            page_table.dtype is not torch.int32 or page_table.get_device() != dev):
+        raise ValueError(f"page_table must be an int32 [{B}, W] tensor on {cache.device}")
     W = page_table.shape[1]
-    if not isinstance(prefix_pages, torch.Tensor) or prefix_pages.dim() != 1 or prefix_len < 0 or (
+    ts = page_table.stride()
+    if W > 1 and ts[1] != 1:
+        raise ValueError("page_table must have unit stride along W")
+    if not isinstance(prefix_pages, _Tensor) or prefix_pages.dim() != 1 or prefix_len < 0 or (
             prefix_pages.shape[0] * cache.page_size < prefix_len):
         raise ValueError("prefix_pages must be an int32 [n] tensor whose pages hold prefix_len tokens")
-    ctx, raw = _on(dev, stream)
-    with ctx:
-        if out is None:
-            out = torch.empty_like(q)
-        else:
-            _index(out, "out", tuple(q.shape), torch.bfloat16, dev)
-        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev) if want_lse else None
-        a = _Attention(q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
-                       _index(prefix_pages, "prefix_pages", tuple(prefix_pages.shape), torch.int32, dev),
-                       _index(page_table, "page_table", (B, W), torch.int32, dev, dense=False),
-                       _index(suffix_len, "suffix_len", (B,), torch.int32, dev),
-                       None if status is None else _index(status, "status", (B,), torch.int32, dev),
-                       None if workspace is None else workspace.data_ptr(),
-                       0 if workspace is None else workspace.numel() * workspace.element_size(),
-                       B, prefix_len, W, page_table.stride(0) if B > 1 else W, q.shape[1] if q.dim() == 4 else 1, Hq,
-                       D ** -0.5 if scale is None else scale)
-        rc = _lib().tps_prefix_attention(ctypes.byref(cache._c), ctypes.byref(a), raw)
-    _check(rc, "tps_prefix_attention")
+    if out is not None:
+        _dense(out, "out", shape, torch.bfloat16, dev)
+    tail = (_dense(prefix_pages, "prefix_pages", prefix_pages.shape, torch.int32, dev), page_table.data_ptr(),
+            _dense(suffix_len, "suffix_len", (B,), torch.int32, dev),
+            0 if status is None else _dense(status, "status", (B,), torch.int32, dev),
+            0 if workspace is None else workspace.data_ptr(),
+            0 if workspace is None else workspace.numel() * workspace.element_size(),
+            B, prefix_len, W, ts[0] if B > 1 else W, shape[1] if len(shape) == 4 else 1, Hq,
+            D ** -0.5 if scale is None else scale)
+    return _run(dev, stream, _attend, q, cache, out, want_lse, tail)
+
+
+def _attend(raw, q, cache, out, want_lse, tail):
+    if out is None:
+        out = _empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    lse = _empty(q.shape[:-1], dtype=torch.float32, device=q.device) if want_lse else None
+    rc = _bound()[3](cache._bytes, _pack_attention(q.data_ptr(), out.data_ptr(), lse.data_ptr() if want_lse else 0, *tail), raw)
+    if rc:
+        _fail(rc, "tps_prefix_attention")
     return (out, lse) if want_lse else out
 
 
 def prefix_attention_workspace(q_shape, cache: KVCache, prefix_len: int, table_width: int) -> int:
     """Bytes of workspace ``prefix_attention`` needs for a query of this shape."""
     B, Hq = q_shape[0], q_shape[-2]
-    a = _Attention(None, None, None, None, None, None, None, None, 0, B, int(prefix_len), table_width, table_width,
-                   q_shape[1] if len(q_shape) == 4 else 1, Hq, 1.0)
-    n = _lib().tps_prefix_attention_workspace(ctypes.byref(cache._c), ctypes.byref(a))
+    n = _bound()[4](cache._bytes, _pack_attention(0, 0, 0, 0, 0, 0, 0, 0, 0, B, int(prefix_len), table_width, table_width,
+                                                  q_shape[1] if len(q_shape) == 4 else 1, Hq, 1.0))
     if n < 0:
         raise ValueError("arguments that prefix_attention would refuse")
     return n

@@ -268,6 +268,13 @@ SHAPES = [  # B, Tq, Hq, Hkv, D, prefix, own lengths, page
     (2, 1, 8, 2, 128, 100, [4000, 1], 16),          # a long own part: several CTAs for each sequence
     (1, 40, 6, 1, 64, 200, [40], 16),               # 240 rows of one sequence
     (257, 1, 4, 1, 64, 130, [1, 2, 3], 16),
+    (6, 1, 8, 2, 64, 6000, [0, 2500, 100], 32),     # long own parts cut evenly, the prefix shared by 24 rows
+    (3, 5, 16, 2, 128, 17000, [5, 2600, 700], 64),  # three row tiles for each sequence, 120 rows
+    (12, 1, 32, 4, 128, 900, [0, 3000, 64, 65], 16),
+    (5, 1, 4, 4, 64, 0, [0, 0, 4097, 0, 0], 256),
+    (2, 1, 8, 8, 128, 2500, [0], 64),               # the prefix walked over by each sequence, nothing of their own
+    (30, 1, 4, 2, 64, 100, [5, 0, 17], 16),
+    (9, 7, 6, 2, 64, 50, [7, 20], 16),              # 21 rows for each sequence and key head
 ]
 
 
