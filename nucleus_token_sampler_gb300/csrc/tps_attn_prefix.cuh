@@ -85,6 +85,15 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
     return d;
 }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
 __device__ __forceinline__ float2 add2(float2 a, float2 b)
 {
     float2 d;
@@ -302,8 +311,9 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
                             const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
-                                s[8 * i + 2 * k] *= __uint_as_float(w[k] << 16);
-                                s[8 * i + 2 * k + 1] *= __uint_as_float(w[k] & 0xFFFF0000u);
+                                const float2 y = mul2(make_float2(s[8 * i + 2 * k], s[8 * i + 2 * k + 1]),
+                                                      make_float2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u)));
+                                s[8 * i + 2 * k] = y.x, s[8 * i + 2 * k + 1] = y.y;
                             }
                         }
                     }

@@ -18,24 +18,35 @@ int log2_of(int n)
 
 // Lanes of a vector (a power of two holding head_dim / 16) and CTAs for n vectors.
 int lanes_of(const tps_kv_cache& c) { return 1 << log2_of(c.head_dim / 16); }
-unsigned grid_of(int64_t n, int L, int sms)
+unsigned grid_of(int64_t n, int L, int flight, int sms)
 {
-    const int64_t per = kKvThreads / L;
-    return (unsigned)std::min<int64_t>((n + per - 1) / per, (int64_t)sms * 8);
+    const int64_t per = kKvThreads / L, one = (n + per - 1) / per;
+    // A call too small for two CTAs on every SM takes one vector for each group of lanes, so that they spread
+    // over more SMs.
+    return (unsigned)std::min<int64_t>(one <= 2 * (int64_t)sms ? one : (one + flight - 1) / flight, (int64_t)sms * 16);
+}
+
+template <typename T, bool kWide>
+void write_format(const KvWriteArgs& a, unsigned grid, int L, int shift, cudaStream_t stream)
+{
+    switch (a.c.format) {
+    case TPS_KV_BF16: kv_write_kernel<T, TPS_KV_BF16, kWide><<<grid, kKvThreads, 0, stream>>>(a, L, shift); break;
+    case TPS_KV_FP8: kv_write_kernel<T, TPS_KV_FP8, kWide><<<grid, kKvThreads, 0, stream>>>(a, L, shift); break;
+    default: kv_write_kernel<T, TPS_KV_INT8, kWide><<<grid, kKvThreads, 0, stream>>>(a, L, shift); break;
+    }
 }
 
 template <typename T>
 cudaError_t write_type(const KvWriteArgs& a, int sms, cudaStream_t stream)
 {
     const int L = lanes_of(a.c), shift = log2_of(a.c.page_size), es = sizeof(T);
-    const unsigned grid = grid_of(a.T * 2 * a.c.n_heads, L, sms);
+    const unsigned grid = grid_of(a.T * 2 * a.c.n_heads, L, sizeof(T) == 2 ? kKvFlight : kKvFlight / 2, sms);
     const bool wide = ((reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v) | (uintptr_t)(a.k_ld * es) |
                         (uintptr_t)(a.k_hd * es) | (uintptr_t)(a.v_ld * es) | (uintptr_t)(a.v_hd * es)) & 15) == 0;
-    switch (a.c.format) {
-    case TPS_KV_BF16: kv_write_kernel<T, TPS_KV_BF16><<<grid, kKvThreads, 0, stream>>>(a, L, shift, wide); break;
-    case TPS_KV_FP8: kv_write_kernel<T, TPS_KV_FP8><<<grid, kKvThreads, 0, stream>>>(a, L, shift, wide); break;
-    default: kv_write_kernel<T, TPS_KV_INT8><<<grid, kKvThreads, 0, stream>>>(a, L, shift, wide); break;
-    }
+    if (wide)
+        write_format<T, true>(a, grid, L, shift, stream);
+    else
+        write_format<T, false>(a, grid, L, shift, stream);
     return cudaGetLastError();
 }
 
@@ -43,7 +54,7 @@ template <typename T>
 cudaError_t read_type(const KvReadArgs& a, int sms, cudaStream_t stream)
 {
     const int L = lanes_of(a.c), shift = log2_of(a.c.page_size);
-    const unsigned grid = grid_of(a.T * 2 * a.c.n_heads, L, sms);
+    const unsigned grid = grid_of(a.T * 2 * a.c.n_heads, L, kKvFlight, sms);
     switch (a.c.format) {
     case TPS_KV_BF16: kv_read_kernel<T, TPS_KV_BF16><<<grid, kKvThreads, 0, stream>>>(a, L, shift); break;
     case TPS_KV_FP8: kv_read_kernel<T, TPS_KV_FP8><<<grid, kKvThreads, 0, stream>>>(a, L, shift); break;

@@ -7,20 +7,36 @@ namespace tps {
 
 namespace {
 
+constexpr int kNormResident = 1024;  // threads of an SM that the launch fills
+
 bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-template <typename T, int L>
-cudaError_t launch_units(const tps_norm_rope& a, int threads, cudaStream_t stream)
+template <typename T, int L, int kWalks>
+cudaError_t launch_walks(const tps_norm_rope& a, unsigned grid, int threads, cudaStream_t stream)
 {
     if (a.interleaved)
-        norm_rope_kernel<T, L, true><<<(unsigned)a.T, threads, 0, stream>>>(a);
+        norm_rope_kernel<T, L, true, kWalks><<<grid, threads, 0, stream>>>(a);
     else
-        norm_rope_kernel<T, L, false><<<(unsigned)a.T, threads, 0, stream>>>(a);
+        norm_rope_kernel<T, L, false, kWalks><<<grid, threads, 0, stream>>>(a);
     return cudaGetLastError();
 }
 
+template <typename T, int L>
+cudaError_t launch_units(const tps_norm_rope& a, int sms, cudaStream_t stream)
+{
+    // Few tokens: a CTA for each, all of its heads at once as far as 256 threads reach.  Many: two heads for
+    // each group of lanes, and no more CTAs than are resident, each walking over its tokens.
+    const int H = a.n_q_heads + a.n_k_heads;
+    const bool two = a.T > 4 * sms && H > 1;
+    const int want = two ? (H + 1) / 2 : H;                                  // groups
+    const int most = kNormMaxThreads / L, walks = (want + most - 1) / most;  // rounds over the heads
+    const int threads = std::min(kNormMaxThreads, ((want + walks - 1) / walks * L + 31) / 32 * 32);
+    const unsigned grid = (unsigned)std::min<int64_t>(a.T, (int64_t)sms * (kNormResident / threads));
+    return two ? launch_walks<T, L, 2>(a, grid, threads, stream) : launch_walks<T, L, 1>(a, grid, threads, stream);
+}
+
 template <typename T>
-cudaError_t launch_type(const tps_norm_rope& a, cudaStream_t stream)
+cudaError_t launch_type(const tps_norm_rope& a, int sms, cudaStream_t stream)
 {
     constexpr int N = Pack<T>::kN;
     const int H = a.n_q_heads + a.n_k_heads, units = a.head_dim / (2 * N);
@@ -36,24 +52,21 @@ cudaError_t launch_type(const tps_norm_rope& a, cudaStream_t stream)
     }
     int L = 1;
     while (L < units) L *= 2;
-    // As few walks over the heads as 256 threads allow, and no more threads than those walks fill.
-    const int walks = (H * L + kNormMaxThreads - 1) / kNormMaxThreads;
-    const int threads = std::min(kNormMaxThreads, ((H + walks - 1) / walks * L + 31) / 32 * 32);
     switch (L) {
-    case 1: return launch_units<T, 1>(a, threads, stream);
-    case 2: return launch_units<T, 2>(a, threads, stream);
-    case 4: return launch_units<T, 4>(a, threads, stream);
-    case 8: return launch_units<T, 8>(a, threads, stream);
-    case 16: return launch_units<T, 16>(a, threads, stream);
-    default: return launch_units<T, 32>(a, threads, stream);
+    case 1: return launch_units<T, 1>(a, sms, stream);
+    case 2: return launch_units<T, 2>(a, sms, stream);
+    case 4: return launch_units<T, 4>(a, sms, stream);
+    case 8: return launch_units<T, 8>(a, sms, stream);
+    case 16: return launch_units<T, 16>(a, sms, stream);
+    default: return launch_units<T, 32>(a, sms, stream);
     }
 }
 
 }  // namespace
 
-cudaError_t launch_norm_rope(const tps_norm_rope& a, int, cudaStream_t stream)
+cudaError_t launch_norm_rope(const tps_norm_rope& a, int sms, cudaStream_t stream)
 {
-    return a.dtype == TPS_BF16 ? launch_type<__nv_bfloat16>(a, stream) : launch_type<float>(a, stream);
+    return a.dtype == TPS_BF16 ? launch_type<__nv_bfloat16>(a, sms, stream) : launch_type<float>(a, sms, stream);
 }
 
 }  // namespace tps

@@ -4,7 +4,7 @@
 // element read and written: memory alone bounds it, and for a decode step's few tokens the latency of
 // one read and one write.
 //
-// One CTA per token.  A group of L lanes (a power of two) holds one head; a lane's unit is a pair of
+// CTAs walk over the tokens.  A group of L lanes (a power of two) holds one head; a lane's unit is a pair of
 // 16-byte vectors whose elements rotate with each other, so a rotation needs no other lane: for
 // halves the vectors at u and rot/2 + u, for adjacent pairs two neighbours.  The cosines and sines of a
 // lane's unit are the same for every head, so each lane loads them once per token and walks over the
@@ -62,12 +62,11 @@ __device__ __forceinline__ void load_floats(const float* p, float (&x)[N])
     }
 }
 
-template <typename T, int L, bool kInterleaved>
+template <typename T, int L, bool kInterleaved, int kWalks>
 __global__ void __launch_bounds__(kNormMaxThreads) norm_rope_kernel(const tps_norm_rope a)
 {
     constexpr int N = Pack<T>::kN;
-    const int64_t tok = blockIdx.x;
-    const int u = threadIdx.x % L, groups = blockDim.x / L;
+    const int u = threadIdx.x % L, groups = blockDim.x / L, group = threadIdx.x / L;
     const int rot = a.rot_dim, half = rot / 2, D = a.head_dim;
     const int units = D / (2 * N), turning = rot / (2 * N);
     const bool live = u < units, turn = u < turning;
@@ -79,74 +78,99 @@ __global__ void __launch_bounds__(kNormMaxThreads) norm_rope_kernel(const tps_no
         ia = rot + (u - turning) * 2 * N;
         ib = ia + N;
     }
-    const int pos = a.positions[tok];
-    const bool known = pos >= 0 && (int64_t)pos < a.n_positions;
-    if (threadIdx.x == 0 && a.out_status) a.out_status[tok] = known ? TPS_ROW_OK : TPS_ROW_BAD_PARAM;
-    const float nan = __int_as_float(0x7FC00000);
-    // halves: element j of the two vectors turns by angle u N + j; adjacent: elements 2j, 2j + 1 of the
-    // pair of vectors by angle u N + j.  Either way the unit uses angles [u N, u N + N).
-    float c[N], s[N];
-    if (turn && known) {
-        load_floats<N>(a.cos_sin + (int64_t)pos * rot + u * N, c);
-        load_floats<N>(a.cos_sin + (int64_t)pos * rot + half + u * N, s);
-    } else {
-#pragma unroll
-        for (int j = 0; j < N; ++j) c[j] = known ? 1.f : nan, s[j] = known ? 0.f : nan;
-    }
     const int H = a.n_q_heads + a.n_k_heads;
-    const float inv_d = 1.f / (float)D;
-    for (int h0 = 0; h0 < H; h0 += groups) {
-        const int h = h0 + threadIdx.x / L;
-        const bool on = live && h < H;
-        const bool is_q = h < a.n_q_heads;
-        const int hh = is_q ? h : h - a.n_q_heads;
-        const T* src = is_q ? static_cast<const T*>(a.q) + tok * a.q_ld + hh * a.q_hd
-                            : static_cast<const T*>(a.k) + tok * a.k_ld + hh * a.k_hd;
-        float x[N] = {}, y[N] = {};
-        if (on) {
-            Pack<T>::load(src + ia, x);
-            Pack<T>::load(src + ib, y);
+    const float inv_d = 1.f / (float)D, nan = __int_as_float(0x7FC00000);
+    // kWalks heads of each group at a time; the next ones (the next token's after a token's last) are asked for
+    // before the present ones are worked on.
+    uint4 xa[kWalks], xb[kWalks];
+    auto ask = [&](int64_t tok, int h0) {
+#pragma unroll
+        for (int k = 0; k < kWalks; ++k) {
+            const int h = h0 + k * groups + group;
+            const bool is_q = h < a.n_q_heads, on = live && h < H && tok < a.T;
+            const int hh = is_q ? h : h - a.n_q_heads;
+            const T* src = is_q ? static_cast<const T*>(a.q) + tok * a.q_ld + hh * a.q_hd
+                                : static_cast<const T*>(a.k) + tok * a.k_ld + hh * a.k_hd;
+            xa[k] = on ? *reinterpret_cast<const uint4*>(src + ia) : make_uint4(0u, 0u, 0u, 0u);
+            xb[k] = on ? *reinterpret_cast<const uint4*>(src + ib) : make_uint4(0u, 0u, 0u, 0u);
         }
-        float ss = 0.f;
-#pragma unroll
-        for (int j = 0; j < N; ++j) ss = fmaf(x[j], x[j], fmaf(y[j], y[j], ss));
-#pragma unroll
-        for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-        if (!on) continue;
-        const float r = rsqrtf(fmaf(ss, inv_d, a.eps));
-        const float* w = is_q ? a.q_weight : a.k_weight;
-        if (w) {
-            float wa[N], wb[N];
-            load_floats<N>(w + ia, wa);
-            load_floats<N>(w + ib, wb);
-#pragma unroll
-            for (int j = 0; j < N; ++j) x[j] *= r * wa[j], y[j] *= r * wb[j];
+    };
+    int64_t tok = blockIdx.x;
+    int pos = a.positions[tok];
+    ask(tok, 0);
+    for (; tok < a.T; tok += gridDim.x) {
+        const int64_t next_tok = tok + gridDim.x;
+        const bool known = pos >= 0 && (int64_t)pos < a.n_positions;
+        if (threadIdx.x == 0 && a.out_status) a.out_status[tok] = known ? TPS_ROW_OK : TPS_ROW_BAD_PARAM;
+        // halves: element j of the two vectors turns by angle u N + j; adjacent: elements 2j, 2j + 1 of the
+        // pair of vectors by angle u N + j.  Either way the unit uses angles [u N, u N + N).
+        float c[N], s[N];
+        if (turn && known) {
+            load_floats<N>(a.cos_sin + (int64_t)pos * rot + u * N, c);
+            load_floats<N>(a.cos_sin + (int64_t)pos * rot + half + u * N, s);
         } else {
 #pragma unroll
-            for (int j = 0; j < N; ++j) x[j] *= r, y[j] *= r;
+            for (int j = 0; j < N; ++j) c[j] = known ? 1.f : nan, s[j] = known ? 0.f : nan;
         }
-        if (kInterleaved && turn) {
+        if (next_tok < a.T) pos = a.positions[next_tok];
+        for (int h0 = 0; h0 < H; h0 += groups * kWalks) {
+            uint4 va[kWalks], vb[kWalks];
 #pragma unroll
-            for (int j = 0; j < N; j += 2) {  // pairs inside each vector
-                const float x0 = x[j], y0 = y[j];
-                const int k = j / 2, m = N / 2 + j / 2;
-                x[j] = x0 * c[k] - x[j + 1] * s[k];
-                x[j + 1] = x[j + 1] * c[k] + x0 * s[k];
-                y[j] = y0 * c[m] - y[j + 1] * s[m];
-                y[j + 1] = y[j + 1] * c[m] + y0 * s[m];
-            }
-        } else {  // components that do not turn have cosine 1 and sine 0
+            for (int k = 0; k < kWalks; ++k) va[k] = xa[k], vb[k] = xb[k];
+            if (h0 + groups * kWalks < H)
+                ask(tok, h0 + groups * kWalks);
+            else
+                ask(next_tok, 0);
 #pragma unroll
-            for (int j = 0; j < N; ++j) {
-                const float x0 = x[j];
-                x[j] = x0 * c[j] - y[j] * s[j];
-                y[j] = y[j] * c[j] + x0 * s[j];
+            for (int k = 0; k < kWalks; ++k) {
+                const int h = h0 + k * groups + group;
+                const bool is_q = h < a.n_q_heads;
+                const int hh = is_q ? h : h - a.n_q_heads;
+                float x[N], y[N];
+                Elem<T>::unpack(va[k], x);
+                Elem<T>::unpack(vb[k], y);
+                float ss = 0.f;
+#pragma unroll
+                for (int j = 0; j < N; ++j) ss = fmaf(x[j], x[j], fmaf(y[j], y[j], ss));
+#pragma unroll
+                for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+                if (!live || h >= H) continue;
+                const float r = rsqrtf(fmaf(ss, inv_d, a.eps));
+                const float* w = is_q ? a.q_weight : a.k_weight;
+                if (w) {
+                    float wa[N], wb[N];
+                    load_floats<N>(w + ia, wa);
+                    load_floats<N>(w + ib, wb);
+#pragma unroll
+                    for (int j = 0; j < N; ++j) x[j] *= r * wa[j], y[j] *= r * wb[j];
+                } else {
+#pragma unroll
+                    for (int j = 0; j < N; ++j) x[j] *= r, y[j] *= r;
+                }
+                if (kInterleaved && turn) {
+#pragma unroll
+                    for (int j = 0; j < N; j += 2) {  // pairs inside each vector
+                        const float x0 = x[j], y0 = y[j];
+                        const int i = j / 2, m = N / 2 + j / 2;
+                        x[j] = x0 * c[i] - x[j + 1] * s[i];
+                        x[j + 1] = x[j + 1] * c[i] + x0 * s[i];
+                        y[j] = y0 * c[m] - y[j + 1] * s[m];
+                        y[j + 1] = y[j + 1] * c[m] + y0 * s[m];
+                    }
+                } else {  // components that do not turn have cosine 1 and sine 0
+#pragma unroll
+                    for (int j = 0; j < N; ++j) {
+                        const float x0 = x[j];
+                        x[j] = x0 * c[j] - y[j] * s[j];
+                        y[j] = y[j] * c[j] + x0 * s[j];
+                    }
+                }
+                T* dst = is_q ? static_cast<T*>(a.out_q) + tok * a.oq_ld + hh * a.oq_hd
+                              : static_cast<T*>(a.out_k) + tok * a.ok_ld + hh * a.ok_hd;
+                Pack<T>::store(dst + ia, x);
+                Pack<T>::store(dst + ib, y);
             }
         }
-        T* dst = is_q ? static_cast<T*>(a.out_q) + tok * a.oq_ld + hh * a.oq_hd
-                      : static_cast<T*>(a.out_k) + tok * a.ok_ld + hh * a.ok_hd;
-        Pack<T>::store(dst + ia, x);
-        Pack<T>::store(dst + ib, y);
     }
 }
 
