@@ -8,8 +8,12 @@ built for another machine, the calls raise.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
+import shutil
 import subprocess
+import sysconfig
 import threading
 
 import torch
@@ -41,6 +45,10 @@ ROW_STATUS = {0: "ok", 1: "nan", 2: "all_masked", 3: "bad_param", 4: "timeout"}
 _ERRORS = {1: "invalid argument", 2: "unknown dtype", 3: "vocabulary too large", 4: "misaligned pointer",
            5: "CUDA runtime error", 6: "more scratch than the fixed array of tps_sample_noalloc holds, or than the workspace given"}
 
+# The native part of the tensor binding: a CPython module compiled against the installed PyTorch.
+_BINDING = os.path.join(_HERE, "_tps_torch.so")
+_BINDING_SOURCE = os.path.join(_CSRC, "tps_torch.cpp")
+
 _lock = threading.Lock()
 _lib = None
 
@@ -49,36 +57,74 @@ def library_path() -> str:
     return _LIB
 
 
-def _stale() -> bool:
-    if not os.path.exists(_LIB):
+def _older(target, deps) -> bool:
+    if not os.path.exists(target):
         return True
-    t = os.path.getmtime(_LIB)
-    deps = [os.path.join(_CSRC, f) for f in _SOURCES + _HEADERS] + [os.path.join(_INCLUDE, "tps.h")]
+    t = os.path.getmtime(target)
     return any(os.path.getmtime(p) > t for p in deps)
 
 
+def _stale() -> bool:
+    return _older(_LIB, [os.path.join(_CSRC, f) for f in _SOURCES + _HEADERS] + [os.path.join(_INCLUDE, "tps.h")])
+
+
+def _binding_stale() -> bool:
+    # newer than the PyTorch it is compiled against, too
+    return _older(_BINDING, [_BINDING_SOURCE, os.path.join(_INCLUDE, "tps.h"), torch.version.__file__])
+
+
+def _binding_command(out):
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"))),
+                        "include")
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], cuda]
+    return (["g++", "-O2", "-std=c++17", "-shared", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"]
+            + [f"-I{p}" for p in inc] + ["-o", out, _BINDING_SOURCE, f"-L{os.path.join(root, 'lib')}"]
+            + ["-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"])
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile ``libtps.so`` for sm_103a with nvcc: the translation units in parallel, then one link."""
-    if not force and not _stale():
+    """Compile ``libtps.so`` for sm_103a with nvcc (the translation units in parallel, then one link) and,
+    beside them, the native part of the tensor binding."""
+    lib, binding = force or _stale(), force or _binding_stale()
+    if not (lib or binding):
         return _LIB
     objdir = os.path.join(_HERE, "_build", f"obj{os.getpid()}")
     os.makedirs(objdir, exist_ok=True)
     objs, procs = [], []
-    for f in _SOURCES:
+    made = os.path.join(objdir, "binding.so")
+    if binding:
+        procs.append(("tps_torch.cpp", subprocess.Popen(_binding_command(made))))
+    for f in _SOURCES if lib else []:
         o = os.path.join(objdir, f.replace(".cu", ".o"))
         cmd = _NVCC + (["-Xptxas=-v"] if verbose else []) + ["-c", "-o", o, os.path.join(_CSRC, f)]
         procs.append((f, subprocess.Popen(cmd)))
         objs.append(o)
     failed = [f for f, p in procs if p.wait() != 0]
     if failed:
-        raise RuntimeError(f"nvcc failed on {', '.join(failed)}")
-    tmp = _LIB + f".tmp{os.getpid()}"
-    subprocess.run(_NVCC + ["-shared", "-o", tmp] + objs, check=True)
-    os.replace(tmp, _LIB)
+        raise RuntimeError(f"compilation failed: {', '.join(failed)}")
+    if lib:
+        tmp = _LIB + f".tmp{os.getpid()}"
+        subprocess.run(_NVCC + ["-shared", "-o", tmp] + objs, check=True)
+        os.replace(tmp, _LIB)
+    if binding:
+        os.replace(made, _BINDING)
     for o in objs:
         os.remove(o)
     os.rmdir(objdir)
     return _LIB
+
+
+def load_binding():
+    """The native part of the tensor binding (built first if it is missing or older than its sources)."""
+    with _lock:
+        build()
+        loader = importlib.machinery.ExtensionFileLoader("_tps_torch", _BINDING)
+        spec = importlib.util.spec_from_loader("_tps_torch", loader)
+        module = importlib.util.module_from_spec(spec)
+        loader.exec_module(module)
+        return module
 
 
 def load():

@@ -1,11 +1,12 @@
 """The decode-step operators in front of the sampler: per-head norm and rotation, the paged key/value
 cache and the attention of a batch that shares a long prefix.  Like the rest of the binding these
-functions only check tensors and hand pointers and the CUDA stream to the C ABI (``include/tps.h``)."""
+functions only check tensors and hand pointers and the CUDA stream to the C ABI (``include/tps.h``); the
+checking is native code too (``csrc/tps_torch.cpp``), because in Python it takes longer than a decode step's
+kernels."""
 from __future__ import annotations
 
 import contextlib
 import ctypes
-import struct
 
 import torch
 
@@ -47,40 +48,21 @@ def declare(lib):
     lib.tps_prefix_attention_workspace.argtypes = [_P, _P]
 
 
-# A call's arguments are packed as the structures above lie in memory (native sizes and alignment):
-# several times faster than filling a ctypes structure field by field.
-# ("0q" pads the end to their alignment.)
-_NORM_LAYOUT, _ATTENTION_LAYOUT = struct.Struct("@4P8q5P2q6if0q"), struct.Struct("@8P5q2if0q")
-assert _NORM_LAYOUT.size == ctypes.sizeof(_NormRope) and _ATTENTION_LAYOUT.size == ctypes.sizeof(_Attention)
-_pack_norm, _pack_attention = _NORM_LAYOUT.pack, _ATTENTION_LAYOUT.pack
-
 _Tensor = torch.Tensor
-_empty = torch.empty  # with a device object: Tensor.new_empty and device strings take twice as long
-_fns = None
+_ops = None
 
 
-def _bound():
-    """The entry points, once the library is loaded."""
-    global _fns
-    if _fns is None:
-        from . import load
+def _torch_ops():
+    """The native module that checks tensors and calls the library (csrc/tps_torch.cpp), loaded with it."""
+    global _ops
+    if _ops is None:
+        from . import load, load_binding
         lib = load()
-        _fns = (lib.tps_qk_norm_rope, lib.tps_kv_write, lib.tps_kv_read, lib.tps_prefix_attention,
-                lib.tps_prefix_attention_workspace)
-    return _fns
-
-
-def _run(device_index, stream, call, *args):
-    """``call(raw stream, *args)`` on the given stream or the current one.  A call on the current device
-    and stream, the usual one, enters no context: the two managers cost several microseconds."""
-    if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(device_index)
-        if device_index == torch._C._cuda_getDevice():
-            return call(raw, *args)
-        with torch.cuda.device(device_index):
-            return call(raw, *args)
-    with torch.cuda.device(device_index), torch.cuda.stream(stream):
-        return call(stream.cuda_stream, *args)
+        _ops = load_binding()
+        address = lambda f: ctypes.cast(f, ctypes.c_void_p).value
+        _ops.bind(address(lib.tps_qk_norm_rope), address(lib.tps_kv_write), address(lib.tps_kv_read),
+                  address(lib.tps_prefix_attention), _fail, torch.OutOfMemoryError)
+    return _ops
 
 
 def _fail(rc, name):
@@ -89,32 +71,23 @@ def _fail(rc, name):
     raise RuntimeError(f"{name} failed: {_ERRORS.get(rc, rc)}{extra}")
 
 
-def _code(dt):
-    if dt is torch.bfloat16:
-        return 1
-    if dt is torch.float32:
-        return 0
-    raise TypeError(f"values must be float32 or bfloat16, got {dt}")
+def _on(stream, device):
+    """Run on `stream`: what the call allocates and launches there goes there."""
+    both = contextlib.ExitStack()
+    both.enter_context(torch.cuda.device(device))
+    both.enter_context(torch.cuda.stream(stream))
+    return both
 
 
-def _dense(t, name, shape, dtype, device_index):
-    """The address of a contiguous tensor of this shape, type and device."""
-    if not isinstance(t, _Tensor) or t.dtype is not dtype or t.shape != shape or t.get_device() != device_index or (
-            not t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{device_index}")
-    return t.data_ptr()
+def _cache(cache):
+    if not isinstance(cache, KVCache):
+        raise ValueError("cache must be a KVCache")
+    return cache
 
 
-def _heads(t, name, device_index=None, dtype=None):
-    """Token and head strides of a [T, heads, head_dim] CUDA tensor."""
-    if not isinstance(t, _Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
-    st = t.stride()
-    if len(st) != 3 or (st[2] != 1 and t.shape[2] > 1):
-        raise ValueError(f"{name} must be [T, heads, head_dim] with unit stride along head_dim")
-    if dtype is not None and (t.dtype is not dtype or t.get_device() != device_index):
-        raise ValueError(f"{name} must be a {dtype} tensor on cuda:{device_index}")
-    return st
+def _dense(t, name, shape, dtype, device):
+    if not isinstance(t, _Tensor) or t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, positions, cos_sin, *, eps: float = 1e-6, interleaved: bool = False,
@@ -130,43 +103,11 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, cos_sin, *, eps: float = 1
     (2i, 2i + 1) rather than (i, i + R/2).  ``out``: a (q, k) pair to write to (the inputs themselves to
     work in place), else new tensors.  ``status``: an int32 [T] tensor that gets 3 for a token whose
     position is not in the table (its outputs are NaN), else 0.  Returns (q, k)."""
-    qs = _heads(q, "q")
-    dev, dt = q.get_device(), q.dtype
-    ks = _heads(k, "k", dev, dt)
-    T, Hq, D = q.shape
-    Tk, Hk, Dk = k.shape
-    if Tk != T or Dk != D:
-        raise ValueError("q and k must hold the same tokens and head size")
-    if not isinstance(cos_sin, _Tensor) or cos_sin.dim() != 2:
-        raise ValueError("cos_sin must be a float32 [positions, R] tensor")
-    n_pos, R = cos_sin.shape
-    if R % 2 or R > D:
-        raise ValueError("cos_sin must hold an even number of columns, at most the head size")
-    if out is not None:
-        oqs, oks = _heads(out[0], "out[0]", dev, dt), _heads(out[1], "out[1]", dev, dt)
-        if out[0].shape != q.shape or out[1].shape != k.shape:
-            raise ValueError("out must have the shapes of q and k")
-    else:
-        oqs, oks = (Hq * D, D), (Hk * D, D)
-    tail = (qs[0], qs[1], ks[0], ks[1], oqs[0], oqs[1], oks[0], oks[1],
-            0 if q_weight is None else _dense(q_weight, "q_weight", (D,), torch.float32, dev),
-            0 if k_weight is None else _dense(k_weight, "k_weight", (D,), torch.float32, dev),
-            _dense(positions, "positions", (T,), torch.int32, dev),
-            _dense(cos_sin, "cos_sin", (n_pos, R), torch.float32, dev),
-            0 if status is None else _dense(status, "status", (T,), torch.int32, dev),
-            T, n_pos, Hq, Hk, D, R, 1 if interleaved else 0, _code(dt), eps)
-    return _run(dev, stream, _norm, q, k, out, tail)
-
-
-def _norm(raw, q, k, out, tail):
-    if out is None:
-        dt, dev = q.dtype, q.device
-        out = _empty(q.shape, dtype=dt, device=dev), _empty(k.shape, dtype=dt, device=dev)
-    oq, ok = out
-    rc = _bound()[0](_pack_norm(q.data_ptr(), k.data_ptr(), oq.data_ptr(), ok.data_ptr(), *tail), raw)
-    if rc:
-        _fail(rc, "tps_qk_norm_rope")
-    return oq, ok
+    ops = _ops or _torch_ops()
+    if stream is not None:
+        with _on(stream, q.device):
+            return ops.norm(q, k, q_weight, k_weight, positions, cos_sin, eps, interleaved, out, status)
+    return ops.norm(q, k, q_weight, k_weight, positions, cos_sin, eps, interleaved, out, status)
 
 
 class KVCache:
@@ -190,7 +131,7 @@ class KVCache:
             raise ValueError("head_dim must be a multiple of 16, at most 512")
         if pages < 1 or heads < 1:
             raise ValueError("a cache holds at least one page and one head")
-        dev = k.get_device()
+        dev = k.device
         _dense(k, "k", (pages, heads, page, D), k.dtype, dev)
         _dense(v, "v", (pages, heads, page, D), k.dtype, dev)
         for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
@@ -203,7 +144,7 @@ class KVCache:
         self.n_pages, self.n_heads, self.page_size, self.head_dim = pages, heads, page, D
         self.device = k.device
         ptr = lambda t: None if t is None else t.data_ptr()
-        self._index = dev
+        self._index = dev.index
         self._bytes = bytes(_Cache(ptr(k), ptr(v), ptr(k_scale), ptr(v_scale), pages, heads, page, D, self.FORMATS[self.format][0]))
 
     @classmethod
@@ -223,46 +164,29 @@ def kv_write(cache: KVCache, k, v, slots, *, stream=None) -> None:
     """Store T tokens: ``k``, ``v`` [T, heads, head_dim] (float32 or bfloat16, token and head strides
     free) at the slots ``slots`` ([T] int64).  8-bit caches get codes and a scale per (token, head); a
     slot outside the cache is skipped (-1 pads).  Slots of one call must differ from one another."""
-    dev = cache._index
-    dt = k.dtype
-    ks, vs = _heads(k, "k", dev, dt), _heads(v, "v", dev, dt)
-    T = k.shape[0]
-    if k.shape != (T, cache.n_heads, cache.head_dim) or v.shape != k.shape:
-        raise ValueError(f"k and v must be [T, {cache.n_heads}, {cache.head_dim}]")
-    _run(dev, stream, _write, (cache._bytes, k.data_ptr(), v.data_ptr(), _code(dt), T, ks[0], ks[1], vs[0], vs[1],
-                               _dense(slots, "slots", (T,), torch.int64, dev)))
-
-
-def _write(raw, args):
-    rc = _bound()[1](*args, raw)
-    if rc:
-        _fail(rc, "tps_kv_write")
+    c = _cache(cache)
+    ops = _ops or _torch_ops()
+    if stream is not None:
+        with _on(stream, c.device):
+            return ops.write(c._bytes, c._index, k, v, slots)
+    return ops.write(c._bytes, c._index, k, v, slots)
 
 
 def kv_read(cache: KVCache, slots, *, dtype=torch.bfloat16, out=None, stream=None):
     """The stored values of the slots ``slots`` ([T] int64) as (k, v), [T, heads, head_dim] of ``dtype``
     (float32 or bfloat16); a slot outside the cache reads as zeros.  ``out``: a (k, v) pair to write to."""
-    dev = cache._index
-    if not isinstance(slots, _Tensor) or slots.dim() != 1:
-        raise ValueError("slots must be an int64 [T] tensor")
-    T = slots.shape[0]
-    at = _dense(slots, "slots", (T,), torch.int64, dev)
-    shape = (T, cache.n_heads, cache.head_dim)
-    if out is not None:
-        _dense(out[0], "out[0]", shape, dtype, dev)
-        _dense(out[1], "out[1]", shape, dtype, dev)
-    return _run(dev, stream, _read, cache, at, shape, dtype, _code(dtype), out)
-
-
-def _read(raw, cache, at, shape, dtype, code, out):
-    if out is None:
-        dev = cache.device
-        out = _empty(shape, dtype=dtype, device=dev), _empty(shape, dtype=dtype, device=dev)
-    k, v = out
-    rc = _bound()[2](cache._bytes, at, shape[0], k.data_ptr(), v.data_ptr(), code, raw)
-    if rc:
-        _fail(rc, "tps_kv_read")
-    return k, v
+    c = _cache(cache)
+    ops = _ops or _torch_ops()
+    if dtype is torch.bfloat16:
+        code = 1
+    elif dtype is torch.float32:
+        code = 0
+    else:
+        raise TypeError(f"values are read as float32 or bfloat16, not {dtype}")
+    if stream is not None:
+        with _on(stream, c.device):
+            return ops.read(c._bytes, c._index, slots, code, out)
+    return ops.read(c._bytes, c._index, slots, code, out)
 
 
 def prefix_attention(q, cache: KVCache, prefix_pages, prefix_len: int, page_table, suffix_len, *, scale=None,
@@ -280,55 +204,23 @@ def prefix_attention(q, cache: KVCache, prefix_pages, prefix_len: int, page_tabl
     sequence with a page outside the cache or a length outside its table (its outputs are NaN), else 0.
     ``workspace``: a uint8 tensor of at least ``prefix_attention_workspace(...)`` bytes to use instead of
     the library's memory pool."""
-    if not isinstance(q, _Tensor) or not q.is_cuda or q.dtype is not torch.bfloat16 or q.dim() not in (3, 4) or (
-            not q.is_contiguous()):
-        raise ValueError("q must be a contiguous bfloat16 CUDA tensor [B, heads, D] or [B, tokens, heads, D]")
-    dev, shape = q.get_device(), q.shape
-    B, Hq, D = shape[0], shape[-2], shape[-1]
-    if dev != cache._index or D != cache.head_dim:
-        raise ValueError(f"q must have head size {cache.head_dim} and be on {cache.device}")
-    if D not in (64, 128):
-        raise ValueError("prefix_attention takes head sizes 64 and 128")
-    if Hq % cache.n_heads:
-        raise ValueError(f"the query heads must be a multiple of the cache's {cache.n_heads} heads")
-    prefix_len = int(prefix_len)
-    if not isinstance(page_table, _Tensor) or page_table.dim() != 2 or page_table.shape[0] != B or (
-            page_table.dtype is not torch.int32 or page_table.get_device() != dev):
-        raise ValueError(f"page_table must be an int32 [{B}, W] tensor on {cache.device}")
-    W = page_table.shape[1]
-    ts = page_table.stride()
-    if W > 1 and ts[1] != 1:
-        raise ValueError("page_table must have unit stride along W")
-    if not isinstance(prefix_pages, _Tensor) or prefix_pages.dim() != 1 or prefix_len < 0 or (
-            prefix_pages.shape[0] * cache.page_size < prefix_len):
-        raise ValueError("prefix_pages must be an int32 [n] tensor whose pages hold prefix_len tokens")
-    if out is not None:
-        _dense(out, "out", shape, torch.bfloat16, dev)
-    tail = (_dense(prefix_pages, "prefix_pages", prefix_pages.shape, torch.int32, dev), page_table.data_ptr(),
-            _dense(suffix_len, "suffix_len", (B,), torch.int32, dev),
-            0 if status is None else _dense(status, "status", (B,), torch.int32, dev),
-            0 if workspace is None else workspace.data_ptr(),
-            0 if workspace is None else workspace.numel() * workspace.element_size(),
-            B, prefix_len, W, ts[0] if B > 1 else W, shape[1] if len(shape) == 4 else 1, Hq,
-            D ** -0.5 if scale is None else scale)
-    return _run(dev, stream, _attend, q, cache, out, want_lse, tail)
-
-
-def _attend(raw, q, cache, out, want_lse, tail):
-    if out is None:
-        out = _empty(q.shape, dtype=torch.bfloat16, device=q.device)
-    lse = _empty(q.shape[:-1], dtype=torch.float32, device=q.device) if want_lse else None
-    rc = _bound()[3](cache._bytes, _pack_attention(q.data_ptr(), out.data_ptr(), lse.data_ptr() if want_lse else 0, *tail), raw)
-    if rc:
-        _fail(rc, "tps_prefix_attention")
-    return (out, lse) if want_lse else out
+    c = _cache(cache)
+    ops = _ops or _torch_ops()
+    if stream is not None:
+        with _on(stream, c.device):
+            return ops.attention(q, c._bytes, c._index, prefix_pages, prefix_len, page_table, suffix_len, scale, want_lse,
+                                 out, status, workspace)
+    return ops.attention(q, c._bytes, c._index, prefix_pages, prefix_len, page_table, suffix_len, scale, want_lse, out, status,
+                         workspace)
 
 
 def prefix_attention_workspace(q_shape, cache: KVCache, prefix_len: int, table_width: int) -> int:
     """Bytes of workspace ``prefix_attention`` needs for a query of this shape."""
     B, Hq = q_shape[0], q_shape[-2]
-    n = _bound()[4](cache._bytes, _pack_attention(0, 0, 0, 0, 0, 0, 0, 0, 0, B, int(prefix_len), table_width, table_width,
-                                                  q_shape[1] if len(q_shape) == 4 else 1, Hq, 1.0))
+    from . import load
+    a = _Attention(B=B, prefix_len=int(prefix_len), table_width=table_width, table_ld=table_width,
+                   q_len=q_shape[1] if len(q_shape) == 4 else 1, n_q_heads=Hq, scale=1.0)
+    n = load().tps_prefix_attention_workspace(_cache(cache)._bytes, ctypes.byref(a))
     if n < 0:
         raise ValueError("arguments that prefix_attention would refuse")
     return n
