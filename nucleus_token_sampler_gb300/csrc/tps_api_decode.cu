@@ -91,8 +91,7 @@ int plan_attention(const tps_kv_cache& c, const tps_attention& a, int sms, tps::
         p.line_pieces = p.line_ctas + alone;
         p.off_line_part = (p.bytes + 255) / 256 * 256;
         p.off_line_ml = p.off_line_part + (size_t)p.line_pieces * p.suffix_rows * c.head_dim * sizeof(float);
-        p.off_line = (p.off_line_ml + (size_t)p.line_pieces * p.suffix_rows * sizeof(float2) + 255) / 256 * 256;
-        p.bytes = p.off_line + (size_t)(a.B * p.suffix_tiles + 1) * sizeof(int64_t);
+        p.bytes = p.off_line_ml + (size_t)p.line_pieces * p.suffix_rows * sizeof(float2);
     }
     *out = p;
     return TPS_OK;
@@ -222,7 +221,6 @@ int tps_prefix_attention(const tps_kv_cache* cache, const tps_attention* args, v
     a.ml = reinterpret_cast<float2*>(ws + a.p.off_ml);
     a.line_part = reinterpret_cast<float*>(ws + a.p.off_line_part);
     a.line_ml = reinterpret_cast<float2*>(ws + a.p.off_line_ml);
-    a.line = reinterpret_cast<int64_t*>(ws + a.p.off_line);
     if (a.p.units) {
         if (!a.p.tensor)
             e = tps::launch_attn_prefix_rows(a, st);

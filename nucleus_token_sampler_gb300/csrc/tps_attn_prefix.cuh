@@ -229,57 +229,71 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
             // The warp's 32 query rows, D / 8 lanes to a row: as they are (bf16) or brought into float16's range.
             float row_unit = unit;
             {
-                constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes of a row, rows at a time
+                constexpr int kLanes = D / 8, kRows = 32 / kLanes, kSteps = 32 / kRows;  // lanes of a row, rows at a time
                 const int piece = lane % kLanes, sub = lane / kLanes;
-                const int64_t first = (int64_t)way.tile * (128 * kTiles) + warp * 32;
-                int64_t bt = first + sub;
-                int gi = 0;  // row = bt G + gi
-                if (a.G > 1) {
-                    bt = first < 0x7FFFFFFF ? (uint32_t)(first + sub) / (uint32_t)a.G : (first + sub) / a.G;
-                    gi = (int)(first + sub - bt * a.G);
+                const int64_t first = (int64_t)way.tile * (128 * kTiles) + warp * 32 + sub, row_elems = (int64_t)a.a.n_q_heads * D;
+                // row = bt G + gi lies at bt * row_elems + (head G + gi) D; kRows rows on without a division
+                const int64_t bt = first <= 0x7FFFFFFF ? (uint32_t)first / (uint32_t)a.G : first / a.G;
+                int gi = (int)(first - bt * a.G);
+                const int wraps = kRows / a.G, rem = kRows - wraps * a.G;
+                const __nv_bfloat16* src =
+                    static_cast<const __nv_bfloat16*>(a.a.q) + bt * row_elems + ((int64_t)way.head * a.G + gi) * D + piece * 8;
+                // All on their way at once, straight to their places; loops and not unrolled code, whose instructions
+                // would be fetched for this one use.
+                auto place = [&](int i) { return my_q + tile_byte((warp & 3) * 32 + i * kRows + sub, piece); };
+#pragma unroll 2
+                for (int i = 0; i < kSteps; ++i) {
+                    const bool in = first + i * kRows < p.R;  // else zeros
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(place(i))),
+                                 "l"(in ? static_cast<const void*>(src) : a.a.q), "r"(in ? 16 : 0)
+                                 : "memory");
+                    const bool over = gi + rem >= a.G;
+                    src += (wraps + over) * row_elems + (rem - (over ? a.G : 0)) * D;
+                    gi += rem - (over ? a.G : 0);
                 }
-                const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.a.q) + (int64_t)way.head * a.G * D + piece * 8;
+                asm volatile("cp.async.wait_all;" ::: "memory");  // each lane goes on with what it copied itself
+                float row_f = 1.f;                                // of this lane's row, row `lane` of the warp
+                if (k8 || sign) {
+                    constexpr int kAtOnce = 4;
+#pragma unroll 1
+                    for (int i0 = 0; i0 < kSteps; i0 += kAtOnce) {
+                        uint32_t x[kAtOnce][4], most[kAtOnce];
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {  // sixteen rows' loads on the way at once
-                    constexpr int kSteps = 16 / kRows;
-                    uint4 w[kSteps];
-#pragma unroll
-                    for (int i = 0; i < kSteps; ++i) {
-                        const int r = half * 16 + i * kRows + sub;
-                        w[i] = first + r < p.R ? *reinterpret_cast<const uint4*>(q + (bt * a.a.n_q_heads + gi) * D) : make_uint4(0u, 0u, 0u, 0u);
-                        gi += kRows;
-                        while (gi >= a.G) gi -= a.G, ++bt;
-                    }
-#pragma unroll
-                    for (int i = 0; i < kSteps; ++i) {
-                        const int r = half * 16 + i * kRows + sub;
-                        uint32_t x[4] = {w[i].x ^ sign, w[i].y ^ sign, w[i].z ^ sign, w[i].w ^ sign};
-                        if (k8) {
-                            float amax = 0.f;
+                        for (int i = 0; i < kAtOnce; ++i) {
+                            const uint4 w = *reinterpret_cast<const uint4*>(place(i0 + i));
+                            x[i][0] = w.x ^ sign, x[i][1] = w.y ^ sign, x[i][2] = w.z ^ sign, x[i][3] = w.w ^ sign;
+                            // magnitudes order like their bits (a NaN or an infinity leaves the row as it is)
+                            most[i] = 0;
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
-                                const float lo = fabsf(__uint_as_float(x[k] << 16)), hi = fabsf(__uint_as_float(x[k] & 0xFFFF0000u));
-                                amax = lo < -neg ? fmaxf(amax, lo) : amax;
-                                amax = hi < -neg ? fmaxf(amax, hi) : amax;
-                            }
-#pragma unroll
-                            for (int o = kLanes / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-                            const float f = f16_row_scale(amax);
-                            // lane r of the warp answers for row r
-#pragma unroll
-                            for (int k = 0; k < kRows; ++k) {
-                                const float other = __shfl_sync(0xFFFFFFFFu, f, k * kLanes);
-                                if (lane == half * 16 + i * kRows + k) row_unit = unit / other;
-                            }
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const __half2 h = __floats2half2_rn(__uint_as_float(x[k] << 16) * f, __uint_as_float(x[k] & 0xFFFF0000u) * f);
-                                x[k] = *reinterpret_cast<const uint32_t*>(&h);
+                                most[i] = max(most[i], x[i][k] & 0x7FFF0000u);
+                                most[i] = max(most[i], x[i][k] << 16 & 0x7FFF0000u);
                             }
                         }
-                        *reinterpret_cast<uint4*>(my_q + tile_byte((warp & 3) * 32 + r, piece)) = make_uint4(x[0], x[1], x[2], x[3]);
+                        if (k8) {
+#pragma unroll
+                            for (int o = kLanes / 2; o > 0; o >>= 1)
+#pragma unroll
+                                for (int i = 0; i < kAtOnce; ++i) most[i] = max(most[i], __shfl_xor_sync(0xFFFFFFFFu, most[i], o));
+#pragma unroll
+                            for (int i = 0; i < kAtOnce; ++i) {
+                                const float f = f16_row_scale(__uint_as_float(most[i]));
+                                const float other = __shfl_sync(0xFFFFFFFFu, f, (lane % kRows) * kLanes);  // row i kRows + lane % kRows
+                                if (lane / kRows == i0 + i) row_f = other;
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    const __half2 h =
+                                        __floats2half2_rn(__uint_as_float(x[i][k] << 16) * f, __uint_as_float(x[i][k] & 0xFFFF0000u) * f);
+                                    x[i][k] = *reinterpret_cast<const uint32_t*>(&h);
+                                }
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < kAtOnce; ++i)
+                            *reinterpret_cast<uint4*>(place(i0 + i)) = make_uint4(x[i][0], x[i][1], x[i][2], x[i][3]);
                     }
                 }
+                row_unit = unit / row_f;
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl.q_full);

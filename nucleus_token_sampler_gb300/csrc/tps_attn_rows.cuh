@@ -120,8 +120,9 @@ __device__ __forceinline__ int kstep_base(int s, int quad)
 __device__ __forceinline__ float f16_row_scale(float a)
 {
     const int e = (int)((__float_as_uint(a) >> 23) & 0xFF) - 127;
-    if (e >= 128 || a == 0.f || (e <= 14 && e >= -2)) return 1.f;
-    return __uint_as_float((uint32_t)min(max(127 - e, 1), 254) << 23);  // brings it to [1, 2)
+    const bool usual = (e >= -2 && e <= 14) || e >= 128 || a == 0.f;
+    const uint32_t f = (uint32_t)min(max(127 - e, 1), 254) << 23;  // brings it to [1, 2)
+    return __uint_as_float(usual ? 0x3F800000u : f);
 }
 
 // A warp's work on 8 N query rows.  Lane (g, quad) = (lane / 4, lane % 4) holds, of rows 8 n + 2 quad + e, the
@@ -953,22 +954,15 @@ __device__ __forceinline__ OwnTokens own_tokens(const AttnArgs& a, int64_t b, in
     return OwnTokens{fits && n > 0 ? n : 0, fits};
 }
 
-template <int D, int kFormat, int N>
-__global__ void __launch_bounds__(kRowsThreads, N == 1 ? 4 : 3) attn_line_kernel(const AttnArgs a)
+// Blocks of the pairs before each one, before[pairs] and on: all of them.  8 consecutive pairs for each thread.
+struct LineSums {
+    int64_t before[kLineMax + 1], warp_sum[kRowsWarps];
+};
+__device__ __forceinline__ void line_sums(LineSums& sm, const AttnArgs& a, int tile_rows)
 {
-    constexpr int kRows = 8 * N;
-    extern __shared__ __align__(128) unsigned char raw[];
-    RowsShared<D, kFormat>& sm = *reinterpret_cast<RowsShared<D, kFormat>*>(raw);
-    int64_t* before = reinterpret_cast<int64_t*>(raw + (sizeof(sm) + 15) / 16 * 16);  // blocks of the pairs before each one
-    int64_t* warp_sum = before + kLineMax + 1;
-    const AttnPlan& p = a.p;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = lane & 3;
-    const int heads = a.c.n_heads, pairs = (int)(a.a.B * p.suffix_tiles), Tq = a.a.q_len, G = a.G;
-    init_rings(sm);
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int shared_len = p.shared ? 0 : (int)a.a.prefix_len, shared_blocks = (shared_len + kLineBlock - 1) / kLineBlock;
-
-    // Exclusive sums over the pairs: 8 consecutive ones for each thread.
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int pairs = (int)(a.a.B * a.p.suffix_tiles), rows = a.a.q_len * a.G;
+    const int shared_blocks = a.p.shared ? 0 : ((int)a.a.prefix_len + kLineBlock - 1) / kLineBlock;
     constexpr int kEach = kLineMax / kRowsThreads;
     int64_t mine[kEach], sum = 0;
 #pragma unroll
@@ -976,8 +970,8 @@ __global__ void __launch_bounds__(kRowsThreads, N == 1 ? 4 : 3) attn_line_kernel
         const int bt = threadIdx.x * kEach + i;
         mine[i] = sum;
         if (bt < pairs) {
-            const int b = bt / p.suffix_tiles, tile = bt - b * p.suffix_tiles;
-            sum += shared_blocks + (own_tokens(a, b, min(Tq * G, (tile + 1) * kRows) - 1).seen + kLineBlock - 1) / kLineBlock;
+            const int b = bt / a.p.suffix_tiles, tile = bt - b * a.p.suffix_tiles;
+            sum += shared_blocks + (own_tokens(a, b, min(rows, (tile + 1) * tile_rows) - 1).seen + kLineBlock - 1) / kLineBlock;
         }
     }
     int64_t upto = sum;
@@ -986,17 +980,32 @@ __global__ void __launch_bounds__(kRowsThreads, N == 1 ? 4 : 3) attn_line_kernel
         const int64_t x = __shfl_up_sync(0xFFFFFFFFu, upto, o);
         if (lane >= o) upto += x;
     }
-    if (lane == 31) warp_sum[warp] = upto;
+    if (lane == 31) sm.warp_sum[warp] = upto;
     __syncthreads();
     int64_t base = upto - sum;
-    for (int w = 0; w < warp; ++w) base += warp_sum[w];
+    for (int w = 0; w < warp; ++w) base += sm.warp_sum[w];
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) before[threadIdx.x * kEach + i] = base + mine[i];
-    if (threadIdx.x == kRowsThreads - 1) before[kLineMax] = base + sum;
+    for (int i = 0; i < kEach; ++i) sm.before[threadIdx.x * kEach + i] = base + mine[i];
+    if (threadIdx.x == kRowsThreads - 1) sm.before[kLineMax] = base + sum;
     __syncthreads();
+}
+
+template <int D, int kFormat, int N>
+__global__ void __launch_bounds__(kRowsThreads, N == 1 ? 4 : 3) attn_line_kernel(const AttnArgs a)
+{
+    constexpr int kRows = 8 * N;
+    extern __shared__ __align__(128) unsigned char raw[];
+    RowsShared<D, kFormat>& sm = *reinterpret_cast<RowsShared<D, kFormat>*>(raw);
+    LineSums& sums = *reinterpret_cast<LineSums*>(raw + (sizeof(sm) + 15) / 16 * 16);
+    const AttnPlan& p = a.p;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = lane & 3;
+    const int heads = a.c.n_heads, pairs = (int)(a.a.B * p.suffix_tiles), Tq = a.a.q_len, G = a.G;
+    init_rings(sm);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int shared_len = p.shared ? 0 : (int)a.a.prefix_len, shared_blocks = (shared_len + kLineBlock - 1) / kLineBlock;
+    line_sums(sums, a, kRows);
+    const int64_t* before = sums.before;
     const int64_t total = before[kLineMax] * heads;
-    if (blockIdx.x == 0)  // the join reads them
-        for (int i = threadIdx.x; i <= pairs; i += kRowsThreads) a.line[i] = i == pairs ? before[kLineMax] : before[i];
 
     Walk<D, kFormat> walk{a.c, a.page_shift, 0, sm.ring[warp], sm.full[warp]};
     const int64_t share = (total + p.line_ctas - 1) / p.line_ctas, u0 = blockIdx.x * share, u1 = min(u0 + share, total);
@@ -1063,10 +1072,13 @@ __global__ void __launch_bounds__(kRowsThreads, N == 1 ? 4 : 3) attn_line_kernel
     asm volatile("griddepcontrol.wait;" ::: "memory");  // this grid ends after the prefix's, so the join need wait for this one only
 }
 
+// The join: a CTA for each item and strip of 32 columns.
+constexpr int kStrip = 32;
 template <int D, int kFormat>
 __global__ void __launch_bounds__(kRowsThreads) attn_join_kernel(const AttnArgs a)
 {
     __shared__ JoinShared<16> js;
+    __shared__ LineSums sums;
     const AttnPlan& p = a.p;
     const int heads = a.c.n_heads, Tq = a.a.q_len, G = a.G;
     const uint32_t bt = blockIdx.x / (uint32_t)heads;
@@ -1084,23 +1096,25 @@ __global__ void __launch_bounds__(kRowsThreads) attn_join_kernel(const AttnArgs 
         pc = pieces_of(p, item);
         if (in0 + rows > p.tile_rows) pc_next = pieces_of(p, item + 1);  // a prefix tile ends inside these rows
     }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int64_t total = a.line[a.a.B * p.suffix_tiles] * heads, before = a.line[bt], blocks = a.line[bt + 1] - before;
+    line_sums(sums, a, p.suffix_rows);  // while the line is still at work
+    const int64_t total = sums.before[kLineMax] * heads, before = sums.before[bt];
+    const int64_t blocks = ((int64_t)bt + 1 < a.a.B * p.suffix_tiles ? sums.before[bt + 1] : sums.before[kLineMax]) - before;
     if (blocks) {
         const int64_t start = before * heads + head * blocks;
         const int64_t share = (total + p.line_ctas - 1) / p.line_ctas, c0 = start / share, c1 = (start + blocks - 1) / share;
         own = Pieces{c0 + (int64_t)bt * heads + head, (int)(c1 - c0 + 1)};
     }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const float neg = -__int_as_float(0x7F800000);
     auto piece_of = [&](int r, int j) {  // row r's piece j of the prefix, and its row of the tile there (-1: it has no such piece)
         const bool wraps = in0 + r >= p.tile_rows;
         const Pieces& mine = wraps ? pc_next : pc;
         return make_longlong2(mine.first + j, j < mine.count ? in0 + r - (wraps ? p.tile_rows : 0) : -1);
     };
-    constexpr int kMost = 16 * (D / 4) / kRowsThreads;
+    constexpr int kMost = 16 * (kStrip / 4) / kRowsThreads, kColumns = kStrip / 4;
     float4 acc[kMost];
     join_parts(
-        js, rows, D / 4, own.count + max(pc.count, pc_next.count), acc,
+        js, rows, kColumns, own.count + max(pc.count, pc_next.count), acc,
         [&](int r, int j) {
             if (j < own.count) return a.line_ml[(own.first + j) * p.suffix_rows + r];
             const longlong2 at = piece_of(r, j - own.count);
@@ -1112,12 +1126,12 @@ __global__ void __launch_bounds__(kRowsThreads) attn_join_kernel(const AttnArgs 
             if (at.y < 0) return make_float4(0.f, 0.f, 0.f, 0.f);
             return reinterpret_cast<const float4*>(a.part)[(at.x * (D / 4) + col) * p.tile_rows + at.y];
         },
-        [&](int i) { return i % (D / 4); });
+        [&](int i) { return (int)blockIdx.y * kColumns + i % kColumns; });
 #pragma unroll
     for (int k = 0; k < kMost; ++k) {
         const int i = threadIdx.x + k * kRowsThreads;
-        if (i >= rows * (D / 4)) break;
-        const int r = i / (D / 4), col = i % (D / 4), state = max(js.state[r], fits ? 0 : 1);
+        if (i >= rows * kColumns) break;
+        const int r = i / kColumns, col = (int)blockIdx.y * kColumns + i % kColumns, state = max(js.state[r], fits ? 0 : 1);
         const float inv = inverse_sum(js.l[r], state != 0);
         const int t = (r0 + r) / G;
         const int64_t orow = (b * Tq + t) * a.a.n_q_heads + (int64_t)head * G + (r0 + r - t * G);
@@ -1126,7 +1140,7 @@ __global__ void __launch_bounds__(kRowsThreads) attn_join_kernel(const AttnArgs 
         asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(acc[k].w * inv), "f"(acc[k].z * inv));
         *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.a.out) + orow * D + col * 4) = w;
         if (col == 0 && a.a.out_lse) a.a.out_lse[orow] = log_sum<kFormat>(js.top[r], js.l[r], state != 0);
-        if (i == 0 && head == 0 && tile == p.suffix_tiles - 1 && a.a.out_status)
+        if (i == 0 && col == 0 && head == 0 && tile == p.suffix_tiles - 1 && a.a.out_status)
             a.a.out_status[b] = state == 2 ? TPS_ROW_TIMEOUT : (state ? TPS_ROW_BAD_PARAM : TPS_ROW_OK);
     }
 }

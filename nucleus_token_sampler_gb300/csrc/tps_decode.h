@@ -56,8 +56,8 @@ struct AttnPlan {
     int cluster;         // else: CTAs that share one sequence's own tokens
     bool line;           // or: the own tokens are cut evenly over `line_ctas` CTAs, which leave pieces too
     int64_t line_ctas, line_pieces;
-    // workspace: outputs of the prefix's pieces, their (maximum, sum); the same of the line's; its sums
-    size_t off_ml, off_line_part, off_line_ml, off_line, bytes;
+    // workspace: outputs of the prefix's pieces, their (maximum, sum); the same of the line's
+    size_t off_ml, off_line_part, off_line_ml, bytes;
 };
 
 struct AttnArgs {
@@ -70,7 +70,6 @@ struct AttnArgs {
     float2* ml;      // [pieces, tile_rows]: maximum in base-2 units, sum (negative: a bad page id)
     float* line_part;
     float2* line_ml;
-    int64_t* line;   // [B * suffix_tiles + 1] blocks before each (sequence, tile) pair
 };
 
 // The shared part, then the own tokens and the join.

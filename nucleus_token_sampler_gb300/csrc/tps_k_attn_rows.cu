@@ -94,7 +94,7 @@ cudaError_t line_shape(const AttnArgs& a, bool after_prefix, cudaStream_t stream
 {
     static std::atomic<uint64_t> allowed{0};
     auto k = attn_line_kernel<D, kFormat, N>;
-    const size_t smem = (sizeof(RowsShared<D, kFormat>) + 15) / 16 * 16 + (kLineMax + 1 + kRowsWarps) * sizeof(int64_t);
+    const size_t smem = (sizeof(RowsShared<D, kFormat>) + 15) / 16 * 16 + sizeof(LineSums);
     cudaError_t e = allow_smem(k, smem, allowed);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute at = dependent();
@@ -107,7 +107,7 @@ cudaError_t line_shape(const AttnArgs& a, bool after_prefix, cudaStream_t stream
     cfg.numAttrs = after_prefix ? 1 : 0;
     e = cudaLaunchKernelEx(&cfg, k, a);
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3((unsigned)(a.a.B * a.p.suffix_tiles * a.c.n_heads), 1, 1);
+    cfg.gridDim = dim3((unsigned)(a.a.B * a.p.suffix_tiles * a.c.n_heads), D / kStrip, 1);
     cfg.dynamicSmemBytes = 0;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, attn_join_kernel<D, kFormat>, a);
