@@ -608,39 +608,69 @@ __device__ __forceinline__ float inverse_sum(float l, bool bad)
     return l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
 }
 
-// The join of many parts of a few rows by a CTA.  The parts' (maximum, sum) come in parallel, 64 at a time; a
-// warp for each row turns them into weights in shared memory; then every thread adds up its float4 columns
-// with twelve loads on the way at once.
-constexpr int kJoinChunk = 64, kFlight = 12;
+// The join of many parts of a few rows by a CTA, a group of parts after the other.  The parts' (maximum, sum)
+// come in parallel, 64 at a time; a warp for each row turns them into weights in shared memory; then every
+// thread adds up its float4 columns with sixteen loads on the way at once.  The loops are short on purpose:
+// this code runs once for a CTA, and instructions that are fetched for one use cost more than they do.
+constexpr int kJoinChunk = 64, kFlight = 16;
 template <int kRows> struct JoinShared {
     float2 ml[kRows][kJoinChunk];  // then (weight, -)
     float scale[kRows], top[kRows], l[kRows];
     int state[kRows];  // 1: a bad page, 2: a wait that ran out
+    __device__ __forceinline__ void clear()
+    {
+        if (threadIdx.x < kRows) {
+            top[threadIdx.x] = -__int_as_float(0x7F800000);
+            l[threadIdx.x] = 0.f;
+            state[threadIdx.x] = 0;
+        }
+    }
 };
 
-// kMost: most float4 of output for each thread.  ml(row, part) and value(row, part, column) fetch a part's;
-// output i of the CTA's rows * columns is column `column(i)` of row i / columns.
-template <int kRows, int kMost, typename Ml, typename Value, typename Column>
-__device__ __forceinline__ void join_parts(JoinShared<kRows>& sm, int rows, int columns, int parts, float4 (&acc)[kMost], Ml ml, Value value,
-                                           Column column)
+// Parts of one row (and column) that lie a constant distance apart in memory.
+struct FarRow {
+    const float2* at;
+    int64_t stride;
+    int count;
+    __device__ __forceinline__ float2 operator()(int j) const { return at[j * stride]; }
+};
+struct FarCell {
+    const float4* at;
+    int64_t stride;
+    int count;
+    __device__ __forceinline__ float4 operator()(int j) const { return at[j * stride]; }
+};
+
+// Add a group of `parts` parts (at most, of any row) to the join.  row(r): the (maximum, sum) of row r's parts;
+// cell(r, column): their values; both with the row's count.  Output i of the rows * columns is column
+// `column(i)` of row i / columns.  kMost: outputs of a thread, at most.
+template <int kRows, int kMost, typename Row, typename Cell, typename Column>
+__device__ __forceinline__ void join_parts(JoinShared<kRows>& sm, int rows, int columns, int parts, float4 (&acc)[kMost], Row row,
+                                           Cell cell, Column column)
 {
+    constexpr int kPerRow = kRowsThreads / kRows;  // threads that fetch a row's (maximum, sum)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const float neg = -__int_as_float(0x7F800000);
-#pragma unroll
-    for (int k = 0; k < kMost; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (threadIdx.x < kRows) sm.top[threadIdx.x] = neg, sm.l[threadIdx.x] = 0.f, sm.state[threadIdx.x] = 0;
     for (int c0 = 0; c0 < parts; c0 += kJoinChunk) {
-        const int n = min(parts - c0, kJoinChunk);
         __syncthreads();
-        for (int i = threadIdx.x; i < rows * kJoinChunk; i += kRowsThreads) {
-            const int r = i / kJoinChunk, j = i % kJoinChunk;
-            sm.ml[r][j] = j < n ? ml(r, c0 + j) : make_float2(neg, 0.f);
+        if (threadIdx.x / kPerRow < rows) {
+            const int r = threadIdx.x / kPerRow;
+            const auto ml = row(r);
+            float2 x[kJoinChunk / kPerRow];
+#pragma unroll
+            for (int k = 0; k < kJoinChunk / kPerRow; ++k) {
+                const int j = c0 + threadIdx.x % kPerRow + k * kPerRow;
+                x[k] = j < ml.count ? ml(j) : make_float2(neg, 0.f);
+            }
+#pragma unroll
+            for (int k = 0; k < kJoinChunk / kPerRow; ++k) sm.ml[r][threadIdx.x % kPerRow + k * kPerRow] = x[k];
         }
         __syncthreads();
+#pragma unroll 1
         for (int r = warp; r < rows; r += kRowsWarps) {
             float2 x[kJoinChunk / 32];
-            float top = sm.top[r];
-            const float was = top;
+            const float was = sm.top[r];
+            float top = was;
 #pragma unroll
             for (int k = 0; k < kJoinChunk / 32; ++k) {
                 x[k] = sm.ml[r][lane + 32 * k];
@@ -672,30 +702,56 @@ __device__ __forceinline__ void join_parts(JoinShared<kRows>& sm, int rows, int 
         for (int k = 0; k < kMost; ++k) {
             const int i = threadIdx.x + k * kRowsThreads;
             if (i >= rows * columns) break;
-            const int r = i / columns, col = column(i);
+            const int r = i / columns;
+            const auto value = cell(r, column(i));
+            const int n = min(value.count - c0, kJoinChunk);
             const float f = sm.scale[r];
-            float4 y = acc[k];
-            y.x *= f, y.y *= f, y.z *= f, y.w *= f;
+            float4 y = make_float4(acc[k].x * f, acc[k].y * f, acc[k].z * f, acc[k].w * f);
+#pragma unroll 1
             for (int j = 0; j < n; j += kFlight) {
                 float4 x[kFlight];
-                float w[kFlight];
 #pragma unroll
-                for (int t = 0; t < kFlight; ++t) {  // past the end: the last part again, with weight 0
-                    x[t] = value(r, c0 + min(j + t, n - 1), col);
-                    w[t] = j + t < n ? sm.ml[r][j + t].x : 0.f;
-                }
+                for (int t = 0; t < kFlight; ++t) x[t] = value(c0 + min(j + t, n - 1));  // past the end: the last one again
 #pragma unroll
-                for (int t = 0; t < kFlight; ++t)
+                for (int t = 0; t < kFlight; ++t) {
+                    const float w = j + t < n ? sm.ml[r][j + t].x : 0.f;
                     if (j + t < n) {
-                        y.x = fmaf(w[t], x[t].x, y.x), y.y = fmaf(w[t], x[t].y, y.y);
-                        y.z = fmaf(w[t], x[t].z, y.z), y.w = fmaf(w[t], x[t].w, y.w);
+                        y.x = fmaf(w, x[t].x, y.x), y.y = fmaf(w, x[t].y, y.y);
+                        y.z = fmaf(w, x[t].z, y.z), y.w = fmaf(w, x[t].w, y.w);
                     }
+                }
             }
             acc[k] = y;
         }
     }
-    __syncthreads();
 }
+
+// The prefix's pieces for the rows of one tile of a sequence: a tile of the prefix may end inside them.
+struct PrefixPieces {
+    Pieces mine, next;
+    int in0, tile_rows;
+    __device__ __forceinline__ PrefixPieces(const AttnPlan& p, int head, int64_t row0, int rows)
+        : mine{0, 0}, next{0, 0}, in0(0), tile_rows(p.tile_rows)
+    {
+        if (!p.shared) return;
+        const int t = row0 <= 0x7FFFFFFF ? (int)((uint32_t)row0 / (uint32_t)p.tile_rows) : (int)(row0 / p.tile_rows);
+        in0 = (int)(row0 - (int64_t)t * p.tile_rows);
+        mine = pieces_of(p, head * p.n_tiles + t);
+        if (in0 + rows > p.tile_rows) next = pieces_of(p, head * p.n_tiles + t + 1);
+    }
+    __device__ __forceinline__ int most() const { return max(mine.count, next.count); }
+    __device__ __forceinline__ const Pieces& of(int r) const { return in0 + r >= tile_rows ? next : mine; }
+    __device__ __forceinline__ int in_tile(int r) const { return in0 + r >= tile_rows ? in0 + r - tile_rows : in0 + r; }
+    __device__ __forceinline__ FarRow row(const AttnArgs& a, int r) const
+    {
+        return FarRow{a.ml + of(r).first * tile_rows + in_tile(r), tile_rows, of(r).count};
+    }
+    __device__ __forceinline__ FarCell cell(const AttnArgs& a, int D, int r, int col) const
+    {
+        return FarCell{reinterpret_cast<const float4*>(a.part) + (of(r).first * (D / 4) + col) * tile_rows + in_tile(r),
+                       (int64_t)(D / 4) * tile_rows, of(r).count};
+    }
+};
 
 template <int kFormat>
 __device__ __forceinline__ float log_sum(float top, float l, bool bad)
@@ -770,14 +826,7 @@ __global__ void __launch_bounds__(kRowsThreads, N == 1 ? 4 : 3) attn_suffix_kern
     if (kOneWarp) {
         finish_sums(st);
         asm volatile("griddepcontrol.wait;" ::: "memory");  // the pieces of the shared prefix
-        Pieces pc{0, 0}, pc_next{0, 0};
-        int in0 = 0;
-        if (p.shared) {
-            const int64_t item = (int64_t)head * p.n_tiles + row0 / p.tile_rows;
-            in0 = (int)(row0 % p.tile_rows);
-            pc = pieces_of(p, item);
-            if (in0 + rows > p.tile_rows) pc_next = pieces_of(p, item + 1);  // a prefix tile ends inside these rows
-        }
+        const PrefixPieces pieces(p, head, row0, rows);
         bool any_bad = false, any_late = fault == 2;
 #pragma unroll
         for (int n = 0; n < N; ++n)
@@ -785,9 +834,8 @@ __global__ void __launch_bounds__(kRowsThreads, N == 1 ? 4 : 3) attn_suffix_kern
             for (int e = 0; e < 2; ++e) {
                 const int row = 8 * n + 2 * quad + e;
                 if (row >= rows) continue;
-                int in_tile = in0 + row;
-                Pieces mine = pc;
-                if (in_tile >= p.tile_rows) in_tile -= p.tile_rows, mine = pc_next;
+                const Pieces mine = pieces.of(row);
+                const int in_tile = pieces.in_tile(row);
                 const float2* ml = a.ml + mine.first * p.tile_rows + in_tile;
                 float top = st.m[n][e];
                 for (int j = 0; j < mine.count; j += 4) {  // four at a time, past the end the last one again
@@ -862,46 +910,47 @@ __global__ void __launch_bounds__(kRowsThreads, N == 1 ? 4 : 3) attn_suffix_kern
             asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(out) : "r"(addr), "r"(who));
             return out;
         };
-        auto ld1 = [](uint32_t addr) {
-            float x;
-            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(addr));
-            return x;
-        };
-        auto ld4 = [](uint32_t addr) {
-            float4 x;
-            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                         : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(addr));
-            return x;
-        };
-        Pieces pc{0, 0}, pc_next{0, 0};
-        int in0 = 0;
-        if (p.shared) {
-            const int64_t item = (int64_t)head * p.n_tiles + row0 / p.tile_rows;
-            in0 = (int)(row0 % p.tile_rows);
-            pc = pieces_of(p, item);
-            if (in0 + rows > p.tile_rows) pc_next = pieces_of(p, item + 1);  // a prefix tile ends inside these rows
-        }
+        const PrefixPieces pieces(p, head, row0, rows);
         const int own = ncl * kRowsWarps, columns = D / 4 / ncl;
-        auto piece_of = [&](int r, int j) {  // row r's piece j - own, and its row of the tile there (-1: it has no such piece)
-            const bool wraps = in0 + r >= p.tile_rows;
-            const Pieces& mine = wraps ? pc_next : pc;
-            return make_longlong2(mine.first + (j - own), j - own < mine.count ? in0 + r - (wraps ? p.tile_rows : 0) : -1);
+        struct NearRow {
+            uint32_t m, l;  // of this CTA's warp 0
+            int count;
+            __device__ __forceinline__ float2 operator()(int j) const
+            {
+                float2 x;
+                uint32_t at_m, at_l;
+                asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at_m) : "r"(m + (j % kRowsWarps) * 64u), "r"(j / kRowsWarps));
+                asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at_l) : "r"(l + (j % kRowsWarps) * 64u), "r"(j / kRowsWarps));
+                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x.x) : "r"(at_m));
+                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x.y) : "r"(at_l));
+                return x;
+            }
         };
-        float4 acc[kRows * D / 4 / kRowsThreads];
+        struct NearCell {
+            uint32_t o;
+            int count;
+            __device__ __forceinline__ float4 operator()(int j) const
+            {
+                float4 x;
+                uint32_t at;
+                asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(o + (j % kRowsWarps) * (uint32_t)sizeof(sm.ring[0])), "r"(j / kRowsWarps));
+                asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(at));
+                return x;
+            }
+        };
+        static_assert(sizeof(sm.m[0]) == 64 && sizeof(sm.l[0]) == 64, "a warp's sixteen rows");
+        constexpr int kMost = (kRows * D / 4 + kRowsThreads - 1) / kRowsThreads;
+        float4 acc[kMost];
+#pragma unroll
+        for (int k = 0; k < kMost; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        js.clear();
+        auto column = [&](int i) { return rank * columns + i % columns; };
         join_parts(
-            js, rows, columns, own + max(pc.count, pc_next.count), acc,
-            [&](int r, int j) {
-                if (j < own) return make_float2(ld1(peer(&sm.m[j % kRowsWarps][r], j / kRowsWarps)), ld1(peer(&sm.l[j % kRowsWarps][r], j / kRowsWarps)));
-                const longlong2 at = piece_of(r, j);
-                return at.y < 0 ? make_float2(neg, 0.f) : a.ml[at.x * p.tile_rows + at.y];
-            },
-            [&](int r, int j, int col) {
-                if (j < own) return ld4(peer(reinterpret_cast<const float*>(sm.ring[j % kRowsWarps]) + r * D + col * 4, j / kRowsWarps));
-                const longlong2 at = piece_of(r, j);
-                if (at.y < 0) return make_float4(0.f, 0.f, 0.f, 0.f);
-                return reinterpret_cast<const float4*>(a.part)[(at.x * (D / 4) + col) * p.tile_rows + at.y];
-            },
-            [&](int i) { return rank * columns + i % columns; });
+            js, rows, columns, own, acc, [&](int r) { return NearRow{smem_u32(&sm.m[0][r]), smem_u32(&sm.l[0][r]), own}; },
+            [&](int r, int col) { return NearCell{smem_u32(sm.ring[0]) + (uint32_t)(r * D + col * 4) * 4u, own}; }, column);
+        join_parts(
+            js, rows, columns, pieces.most(), acc, [&](int r) { return pieces.row(a, r); },
+            [&](int r, int col) { return pieces.cell(a, D, r, col); }, column);
         int own_bad = 0;
         for (int k = 0; k < ncl; ++k) {
             int x;
@@ -909,10 +958,10 @@ __global__ void __launch_bounds__(kRowsThreads, N == 1 ? 4 : 3) attn_suffix_kern
             own_bad = max(own_bad, x);
         }
 #pragma unroll
-        for (int k = 0; k < kRows * D / 4 / kRowsThreads; ++k) {
+        for (int k = 0; k < kMost; ++k) {
             const int i = threadIdx.x + k * kRowsThreads;
             if (i >= rows * columns) break;
-            const int r = i / columns, col = rank * columns + i % columns;
+            const int r = i / columns, col = column(i);
             const int state = max(js.state[r], own_bad);
             const float inv = inverse_sum(js.l[r], state != 0);
             const int64_t orow = out_row(r);
@@ -1088,14 +1137,8 @@ __global__ void __launch_bounds__(kRowsThreads) attn_join_kernel(const AttnArgs 
     const int r0 = tile * p.suffix_rows, rows = min(p.suffix_rows, Tq * G - r0);
     const int64_t row0 = b * Tq * G + r0;
     const bool fits = own_tokens(a, b, 0).fits;
-    Pieces pc{0, 0}, pc_next{0, 0}, own{0, 0};
-    int in0 = 0;
-    if (p.shared) {
-        const int64_t item = (int64_t)head * p.n_tiles + row0 / p.tile_rows;
-        in0 = (int)(row0 % p.tile_rows);
-        pc = pieces_of(p, item);
-        if (in0 + rows > p.tile_rows) pc_next = pieces_of(p, item + 1);  // a prefix tile ends inside these rows
-    }
+    Pieces own{0, 0};
+    const PrefixPieces pieces(p, head, row0, rows);
     line_sums(sums, a, p.suffix_rows);  // while the line is still at work
     const int64_t total = sums.before[kLineMax] * heads, before = sums.before[bt];
     const int64_t blocks = ((int64_t)bt + 1 < a.a.B * p.suffix_tiles ? sums.before[bt + 1] : sums.before[kLineMax]) - before;
@@ -1105,33 +1148,29 @@ __global__ void __launch_bounds__(kRowsThreads) attn_join_kernel(const AttnArgs 
         own = Pieces{c0 + (int64_t)bt * heads + head, (int)(c1 - c0 + 1)};
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const float neg = -__int_as_float(0x7F800000);
-    auto piece_of = [&](int r, int j) {  // row r's piece j of the prefix, and its row of the tile there (-1: it has no such piece)
-        const bool wraps = in0 + r >= p.tile_rows;
-        const Pieces& mine = wraps ? pc_next : pc;
-        return make_longlong2(mine.first + j, j < mine.count ? in0 + r - (wraps ? p.tile_rows : 0) : -1);
-    };
     constexpr int kMost = 16 * (kStrip / 4) / kRowsThreads, kColumns = kStrip / 4;
     float4 acc[kMost];
+#pragma unroll
+    for (int k = 0; k < kMost; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    js.clear();
+    auto column = [&](int i) { return (int)blockIdx.y * kColumns + i % kColumns; };
     join_parts(
-        js, rows, kColumns, own.count + max(pc.count, pc_next.count), acc,
-        [&](int r, int j) {
-            if (j < own.count) return a.line_ml[(own.first + j) * p.suffix_rows + r];
-            const longlong2 at = piece_of(r, j - own.count);
-            return at.y < 0 ? make_float2(neg, 0.f) : a.ml[at.x * p.tile_rows + at.y];
+        js, rows, kColumns, own.count, acc,
+        [&](int r) { return FarRow{a.line_ml + own.first * p.suffix_rows + r, p.suffix_rows, own.count}; },
+        [&](int r, int col) {
+            return FarCell{reinterpret_cast<const float4*>(a.line_part) + (own.first * (D / 4) + col) * p.suffix_rows + r,
+                           (int64_t)(D / 4) * p.suffix_rows, own.count};
         },
-        [&](int r, int j, int col) {
-            if (j < own.count) return reinterpret_cast<const float4*>(a.line_part)[((own.first + j) * (D / 4) + col) * p.suffix_rows + r];
-            const longlong2 at = piece_of(r, j - own.count);
-            if (at.y < 0) return make_float4(0.f, 0.f, 0.f, 0.f);
-            return reinterpret_cast<const float4*>(a.part)[(at.x * (D / 4) + col) * p.tile_rows + at.y];
-        },
-        [&](int i) { return (int)blockIdx.y * kColumns + i % kColumns; });
+        column);
+    join_parts(
+        js, rows, kColumns, pieces.most(), acc, [&](int r) { return pieces.row(a, r); },
+        [&](int r, int col) { return pieces.cell(a, D, r, col); }, column);
+    __syncthreads();
 #pragma unroll
     for (int k = 0; k < kMost; ++k) {
         const int i = threadIdx.x + k * kRowsThreads;
         if (i >= rows * kColumns) break;
-        const int r = i / kColumns, col = (int)blockIdx.y * kColumns + i % kColumns, state = max(js.state[r], fits ? 0 : 1);
+        const int r = i / kColumns, col = column(i), state = max(js.state[r], fits ? 0 : 1);
         const float inv = inverse_sum(js.l[r], state != 0);
         const int t = (r0 + r) / G;
         const int64_t orow = (b * Tq + t) * a.a.n_q_heads + (int64_t)head * G + (r0 + r - t * G);
