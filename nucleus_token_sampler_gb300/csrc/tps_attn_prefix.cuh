@@ -639,10 +639,11 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
         constexpr int kThreadsConv = Shape::kConvertWarps * 32;
         constexpr int kSteps = 128 * kPieces / kThreadsConv, kRowsPerStep = kThreadsConv / kPieces;
         const int t = (int)threadIdx.x - Shape::kConvertWarp * 32;
-        const int piece = t % kPieces, sub = t / kPieces;
-        // The eight lanes of a 128-byte code row fill both column blocks; the upper four write their halves the
-        // other way round, so that the eight 16-byte stores of a phase hit different banks.
-        const bool swap = piece >= 4;
+        // Eight lanes at a time read 16 bytes each and write two 16-byte chunks each.  At D = 128 they are the first half
+        // of one code row and the second half of the next: then both the reads and, by the swizzle, the writes of
+        // the eight hit different banks.
+        const int piece = kPieces == 8 ? (t & 3) + 4 * ((t >> 2 ^ t >> 3) & 1) : t % kPieces;
+        const int sub = kPieces == 8 ? (t >> 5) * 4 + (t >> 4 & 1) * 2 + (t >> 2 & 1) : t / kPieces;
         Way way(p);
         Turn<kRaw> raw_turn(0);
         Turn<kRing> turn(1);
@@ -683,9 +684,8 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
                             h[k] = *reinterpret_cast<const uint32_t*>(&y);
                         }
                     }
-                    const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-                    *reinterpret_cast<uint4*>(dst + tile_byte(r, 2 * piece + (swap ? 1 : 0))) = swap ? hi : lo;
-                    *reinterpret_cast<uint4*>(dst + tile_byte(r, 2 * piece + (swap ? 0 : 1))) = swap ? lo : hi;
+                    *reinterpret_cast<uint4*>(dst + tile_byte(r, 2 * piece)) = make_uint4(h[0], h[1], h[2], h[3]);
+                    *reinterpret_cast<uint4*>(dst + tile_byte(r, 2 * piece + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
                 }
                 fence_proxy_async();
                 __syncwarp();
