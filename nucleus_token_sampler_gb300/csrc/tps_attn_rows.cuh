@@ -608,33 +608,32 @@ __device__ __forceinline__ float inverse_sum(float l, bool bad)
     return l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
 }
 
-// The join of many parts of a few rows by a CTA, a group of parts after the other.  The parts' (maximum, sum)
-// come in parallel, 64 at a time; a warp for each row turns them into weights in shared memory; then every
-// thread adds up its float4 columns with sixteen loads on the way at once.  The loops are short on purpose:
-// this code runs once for a CTA, and instructions that are fetched for one use cost more than they do.
-constexpr int kJoinChunk = 64, kFlight = 16;
+// The join of many parts of a few rows by a CTA.  The parts' (maximum, sum) come in parallel, 64 at a time; a warp
+// for each row turns them into weights in shared memory; then every thread adds up its float4 columns with many loads
+// on the way at once, the first sixteen since before the weights were known.  The loops are short on purpose: this
+// code runs once for a CTA, and instructions that are fetched for one use cost more than they do.
+constexpr int kJoinChunk = 64, kFlight = 16, kNearFlight = 8;
 template <int kRows> struct JoinShared {
     float2 ml[kRows][kJoinChunk];  // then (weight, -)
     float scale[kRows], top[kRows], l[kRows];
     int state[kRows];  // 1: a bad page, 2: a wait that ran out
-    __device__ __forceinline__ void clear()
-    {
-        if (threadIdx.x < kRows) {
-            top[threadIdx.x] = -__int_as_float(0x7F800000);
-            l[threadIdx.x] = 0.f;
-            state[threadIdx.x] = 0;
-        }
-    }
+};
+
+struct NoPart {
+    static constexpr int count = 0;
+    __device__ __forceinline__ NoPart operator()(int) const { return *this; }
+    __device__ __forceinline__ operator float2() const { return make_float2(0.f, 0.f); }
+    __device__ __forceinline__ operator float4() const { return make_float4(0.f, 0.f, 0.f, 0.f); }
 };
 
 // Parts of one row (and column) that lie a constant distance apart in memory.
-struct FarRow {
+struct PartRow {
     const float2* at;
     int64_t stride;
     int count;
     __device__ __forceinline__ float2 operator()(int j) const { return at[j * stride]; }
 };
-struct FarCell {
+struct PartCell {
     const float4* at;
     int64_t stride;
     int count;
@@ -652,30 +651,54 @@ struct JoinOut {
     __device__ __forceinline__ bool in(int i) const { return row(i) < rows; }
 };
 
-// Add a group of `parts` parts (at most, of any row) to the join.  row(r): the (maximum, sum) of row r's parts;
-// cell(r, column): their values; both with the row's count.  kMost: outputs of a thread, at most.
-template <int kRows, int kMost, typename Row, typename Cell>
-__device__ __forceinline__ void join_parts(JoinShared<kRows>& sm, const JoinOut& out, int parts, float4 (&acc)[kMost], Row row,
-                                           Cell cell)
+// Join two groups of parts, at most n_near and n_far of any row.  row(r): the (maximum, sum) of row r's parts of the
+// group; cell(r, column): their values; both with the row's count.  kMost: outputs of a thread, at most.
+template <int kRows, int kMost, typename NearRow, typename NearCell, typename FarRow, typename FarCell>
+__device__ __forceinline__ void join_parts(JoinShared<kRows>& sm, const JoinOut& out, float4 (&acc)[kMost], int n_near, NearRow near_row,
+                                           NearCell near_cell, int n_far, FarRow far_row, FarCell far_cell)
 {
-    const int rows = out.rows;
-    constexpr int kPerRow = kRowsThreads / kRows;  // threads that fetch a row's (maximum, sum)
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kPerRow = kRowsThreads / kRows, kEach = kJoinChunk / kPerRow;  // threads that fetch a row's (maximum, sum), of each
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rows = out.rows;
     const float neg = -__int_as_float(0x7F800000);
-    for (int c0 = 0; c0 < parts; c0 += kJoinChunk) {
+    if (threadIdx.x < kRows) {
+        sm.top[threadIdx.x] = neg;
+        sm.l[threadIdx.x] = 0.f;
+        sm.state[threadIdx.x] = 0;
+    }
+#pragma unroll
+    for (int k = 0; k < kMost; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c0 = 0; c0 < n_near + n_far; c0 += kJoinChunk) {
         __syncthreads();
+        const int far0 = max(c0 - n_near, 0);  // the chunk's first far part
+        float2 ml[kEach];
         if (threadIdx.x / kPerRow < rows) {
             const int r = threadIdx.x / kPerRow;
-            const auto ml = row(r);
-            float2 x[kJoinChunk / kPerRow];
+            const auto near = near_row(r);
+            const auto far = far_row(r);
 #pragma unroll
-            for (int k = 0; k < kJoinChunk / kPerRow; ++k) {
+            for (int k = 0; k < kEach; ++k) {
                 const int j = c0 + threadIdx.x % kPerRow + k * kPerRow;
-                x[k] = j < ml.count ? ml(j) : make_float2(neg, 0.f);
+                ml[k] = make_float2(neg, 0.f);
+                if (j < n_near) {
+                    if (j < near.count) ml[k] = near(j);
+                } else if (j - n_near < far.count) {
+                    ml[k] = far(j - n_near);
+                }
             }
-#pragma unroll
-            for (int k = 0; k < kJoinChunk / kPerRow; ++k) sm.ml[r][threadIdx.x % kPerRow + k * kPerRow] = x[k];
         }
+        float4 x[kFlight];
+        auto fetch = [&](const auto& value, int j, int n) {
+#pragma unroll
+            for (int t = 0; t < kFlight; ++t) x[t] = value(min(j + t, n - 1));  // past the end: the last one again
+        };
+        if (out.in(threadIdx.x)) {
+            const auto value = far_cell(out.row(threadIdx.x), out.column(threadIdx.x));
+            const int n = min(value.count, c0 + kJoinChunk - n_near);
+            if (far0 < n) fetch(value, far0, n);
+        }
+        if (threadIdx.x / kPerRow < rows)
+#pragma unroll
+            for (int k = 0; k < kEach; ++k) sm.ml[threadIdx.x / kPerRow][threadIdx.x % kPerRow + k * kPerRow] = ml[k];
         __syncthreads();
 #pragma unroll 1
         for (int r = warp; r < rows; r += kRowsWarps) {
@@ -714,27 +737,36 @@ __device__ __forceinline__ void join_parts(JoinShared<kRows>& sm, const JoinOut&
             const int i = threadIdx.x + k * kRowsThreads;
             if (!out.in(i)) continue;
             const int r = out.row(i);
-            const auto value = cell(r, out.column(i));
-            const int n = min(value.count - c0, kJoinChunk);
             const float f = sm.scale[r];
             float4 y = make_float4(acc[k].x * f, acc[k].y * f, acc[k].z * f, acc[k].w * f);
+            auto add = [&](float w, const float4& v) {
+                y.x = fmaf(w, v.x, y.x), y.y = fmaf(w, v.y, y.y);
+                y.z = fmaf(w, v.z, y.z), y.w = fmaf(w, v.w, y.w);
+            };
+            const auto near = near_cell(r, out.column(i));
+            const int near_n = min(near.count, c0 + kJoinChunk);
 #pragma unroll 1
-            for (int j = 0; j < n; j += kFlight) {
-                float4 x[kFlight];
+            for (int j = c0; j < near_n; j += kNearFlight) {
+                float4 v[kNearFlight];
 #pragma unroll
-                for (int t = 0; t < kFlight; ++t) x[t] = value(c0 + min(j + t, n - 1));  // past the end: the last one again
+                for (int t = 0; t < kNearFlight; ++t) v[t] = near(min(j + t, near_n - 1));
 #pragma unroll
-                for (int t = 0; t < kFlight; ++t) {
-                    const float w = j + t < n ? sm.ml[r][j + t].x : 0.f;
-                    if (j + t < n) {
-                        y.x = fmaf(w, x[t].x, y.x), y.y = fmaf(w, x[t].y, y.y);
-                        y.z = fmaf(w, x[t].z, y.z), y.w = fmaf(w, x[t].w, y.w);
-                    }
-                }
+                for (int t = 0; t < kNearFlight; ++t)
+                    if (j + t < near_n) add(sm.ml[r][j + t - c0].x, v[t]);
+            }
+            const auto far = far_cell(r, out.column(i));
+            const int n = min(far.count, c0 + kJoinChunk - n_near);
+#pragma unroll 1
+            for (int j = far0; j < n; j += kFlight) {
+                if (k > 0 || j > far0) fetch(far, j, n);
+#pragma unroll
+                for (int t = 0; t < kFlight; ++t)
+                    if (j + t < n) add(sm.ml[r][j + t + n_near - c0].x, x[t]);
             }
             acc[k] = y;
         }
     }
+    __syncthreads();
 }
 
 // The prefix's pieces for the rows of one tile of a sequence: a tile of the prefix may end inside them.
@@ -753,13 +785,13 @@ struct PrefixPieces {
     __device__ __forceinline__ int most() const { return max(mine.count, next.count); }
     __device__ __forceinline__ const Pieces& of(int r) const { return in0 + r >= tile_rows ? next : mine; }
     __device__ __forceinline__ int in_tile(int r) const { return in0 + r >= tile_rows ? in0 + r - tile_rows : in0 + r; }
-    __device__ __forceinline__ FarRow row(const AttnArgs& a, int r) const
+    __device__ __forceinline__ PartRow row(const AttnArgs& a, int r) const
     {
-        return FarRow{a.ml + of(r).first * tile_rows + in_tile(r), tile_rows, of(r).count};
+        return PartRow{a.ml + of(r).first * tile_rows + in_tile(r), tile_rows, of(r).count};
     }
-    __device__ __forceinline__ FarCell cell(const AttnArgs& a, int D, int r, int col) const
+    __device__ __forceinline__ PartCell cell(const AttnArgs& a, int D, int r, int col) const
     {
-        return FarCell{reinterpret_cast<const float4*>(a.part) + (of(r).first * (D / 4) + col) * tile_rows + in_tile(r),
+        return PartCell{reinterpret_cast<const float4*>(a.part) + (of(r).first * (D / 4) + col) * tile_rows + in_tile(r),
                        (int64_t)(D / 4) * tile_rows, of(r).count};
     }
 };
@@ -912,7 +944,6 @@ __global__ void __launch_bounds__(kRowsThreads, N == 1 ? 4 : 3) attn_suffix_kern
         } else {
             __syncthreads();
         }
-        asm volatile("griddepcontrol.wait;" ::: "memory");
         // Every rank joins a D / ncl columns wide strip, from all CTAs' shared memory and from the pieces.
         const uint32_t base = smem_u32(raw);
         auto peer = [&](const void* x, int who) {
@@ -953,21 +984,18 @@ __global__ void __launch_bounds__(kRowsThreads, N == 1 ? 4 : 3) attn_suffix_kern
         static_assert(sizeof(sm.m[0]) == 64 && sizeof(sm.l[0]) == 64, "a warp's sixteen rows");
         constexpr int kMost = (kRows * D / 4 + kRowsThreads - 1) / kRowsThreads;
         float4 acc[kMost];
-#pragma unroll
-        for (int k = 0; k < kMost; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        js.clear();
-        join_parts(
-            js, out, own, acc, [&](int r) { return NearRow{smem_u32(&sm.m[0][r]), smem_u32(&sm.l[0][r]), own}; },
-            [&](int r, int col) { return NearCell{smem_u32(sm.ring[0]) + (uint32_t)(r * D + col * 4) * 4u, own}; });
-        join_parts(
-            js, out, pieces.most(), acc, [&](int r) { return pieces.row(a, r); },
-            [&](int r, int col) { return pieces.cell(a, D, r, col); });
         int own_bad = 0;
-        for (int k = 0; k < ncl; ++k) {
-            int x;
-            asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(x) : "r"(peer(&sm.bad, k)));
-            own_bad = max(own_bad, x);
-        }
+        if (lane < ncl) asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(own_bad) : "r"(peer(&sm.bad, lane)));
+        own_bad = (int)warp_max_u32((uint32_t)own_bad);
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        auto own_row = [&](int r) { return NearRow{smem_u32(&sm.m[0][r]), smem_u32(&sm.l[0][r]), own}; };
+        auto own_cell = [&](int r, int col) { return NearCell{smem_u32(sm.ring[0]) + (uint32_t)(r * D + col * 4) * 4u, own}; };
+        if (p.shared)
+            join_parts(
+                js, out, acc, own, own_row, own_cell, pieces.most(), [&](int r) { return pieces.row(a, r); },
+                [&](int r, int col) { return pieces.cell(a, D, r, col); });
+        else  // the loads in the wider of the two ways
+            join_parts(js, out, acc, 0, [](int) { return NoPart{}; }, [](int, int) { return NoPart{}; }, own, own_row, own_cell);
 #pragma unroll
         for (int k = 0; k < kMost; ++k) {
             const int i = threadIdx.x + k * kRowsThreads;
@@ -1161,21 +1189,15 @@ __global__ void __launch_bounds__(kRowsThreads) attn_join_kernel(const AttnArgs 
     asm volatile("griddepcontrol.wait;" ::: "memory");
     constexpr int kMost = 16 * (kStrip / 4) / kRowsThreads, kColumns = kStrip / 4;
     float4 acc[kMost];
-#pragma unroll
-    for (int k = 0; k < kMost; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    js.clear();
     const JoinOut out{rows, (int)blockIdx.y * kColumns, kColumns, 2};
     join_parts(
-        js, out, own.count, acc,
-        [&](int r) { return FarRow{a.line_ml + own.first * p.suffix_rows + r, p.suffix_rows, own.count}; },
+        js, out, acc, pieces.most(), [&](int r) { return pieces.row(a, r); },
+        [&](int r, int col) { return pieces.cell(a, D, r, col); }, own.count,
+        [&](int r) { return PartRow{a.line_ml + own.first * p.suffix_rows + r, p.suffix_rows, own.count}; },
         [&](int r, int col) {
-            return FarCell{reinterpret_cast<const float4*>(a.line_part) + (own.first * (D / 4) + col) * p.suffix_rows + r,
-                           (int64_t)(D / 4) * p.suffix_rows, own.count};
+            return PartCell{reinterpret_cast<const float4*>(a.line_part) + (own.first * (D / 4) + col) * p.suffix_rows + r,
+                            (int64_t)(D / 4) * p.suffix_rows, own.count};
         });
-    join_parts(
-        js, out, pieces.most(), acc, [&](int r) { return pieces.row(a, r); },
-        [&](int r, int col) { return pieces.cell(a, D, r, col); });
-    __syncthreads();
 #pragma unroll
     for (int k = 0; k < kMost; ++k) {
         const int i = threadIdx.x + k * kRowsThreads;
