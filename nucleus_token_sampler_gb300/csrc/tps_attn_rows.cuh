@@ -372,7 +372,10 @@ __device__ __forceinline__ int attend(RowState<D, N>& st, Walk<D, kFormat>& walk
                     }
             }
         }
-        __syncwarp();  // every lane has read the stage
+        // Every lane has read the stage, values included, before a copy may write there: to the compiler the copy's
+        // writes are no stores, so without the fence it may move the loads of the values past the request.
+        fence_proxy_async();
+        __syncwarp();
         if (walk.ahead < last) walk.request();
         // Raise the references where a score exceeds them by more than the slack (or is the first one).
         bool over = false;

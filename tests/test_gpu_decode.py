@@ -421,3 +421,18 @@ def test_no_prefix_equals_all_prefix():
     kv = plain.values(c)
     _check_attention((a, la), q, kv, pp, 500, table, n, 128 ** -0.5, "bf16")
     _check_attention((b, lb), q, kv, pp[:0], 0, pp.view(1, -1), m, 128 ** -0.5, "bf16")
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "int8"])
+@pytest.mark.parametrize("B,Hq,Hkv,D,prefix,lens", [
+    (12, 32, 4, 128, 900, [0, 3000, 64, 65]),   # the prefix walked over by each sequence, long rings
+    (16, 32, 4, 128, 2048, [1000, 3000]), (48, 8, 2, 64, 700, [500]), (400, 32, 8, 128, 300, [150, 20])])
+def test_attention_repeats_itself(fmt, B, Hq, Hkv, D, prefix, lens):
+    """Bit for bit, over many runs: copies into a ring never overtake the reads of what they replace."""
+    c, q, pp, table, n = _case(_gen(77), B, 1, Hq, Hkv, D, prefix, lens, 16, fmt)
+    want, lse = tps.prefix_attention(q, c, pp, prefix, table, n, want_lse=True)
+    differ = torch.zeros((), dtype=torch.int64, device=DEV)
+    for _ in range(300):
+        got, again = tps.prefix_attention(q, c, pp, prefix, table, n, want_lse=True)
+        differ += (got != want).sum() + (again != lse).sum()
+    assert int(differ) == 0
