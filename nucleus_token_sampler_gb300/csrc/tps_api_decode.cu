@@ -33,19 +33,21 @@ int check_cache(const tps_kv_cache* c, bool pointers)
     return TPS_OK;
 }
 
-// CTAs of the 16-row prefix kernel per SM, and the tokens of its blocks (one step of its four warps).
-constexpr int kRowsCtasPerSm = 2;
-constexpr int kRowsBlock = 64;
-// Query rows of one key head from which the tcgen05 kernel computes the shared part.
-constexpr int64_t kTensorRows = 33;
-// Sequences (times heads and row tiles) per SM from which each warp takes one for itself.
-constexpr int64_t kOneWarpItems = 8;
 // Tokens (times triples of sequence, key head and row tile) up to which each sequence walks over the prefix
 // itself: one launch instead of two, and nothing to join, for reading the prefix again from the L2 cache.
-constexpr int64_t kAloneTokens = 65536, kAloneTensorTokens = 32768;
-// Tokens of one sequence (at most) from which the own tokens are cut evenly over the SMs, for up to
-// kLinePairs sequences times row tiles.
-constexpr int64_t kLineTokens = 2048, kLinePairs = 1024;
+// With 8 key heads of 128, alone / shared, us: bfloat16 8 x 500 9.2 / 9.7, 5 x 1,000 11.0 / 10.0, 8 x 1,000 11.1 /
+// 10.1, 2 x 2,000 14.7 / 10.5, 8 x 2,000 21.3 / 12.8; fp8 (whose shared part converts its codes) 5 x 1,000 10.9 /
+// 13.3, 8 x 1,000 12.3 / 13.3, 8 x 2,000 20.6 / 16.0, 5 x 2,000 16.8 / 14.7, 2 x 4,000 16.3 / 15.9.
+constexpr int64_t kAloneBf16 = 24576, kAlone8 = 49152;
+// Sequences (times heads and row tiles) per SM from which each warp takes one for itself, and where they hold few
+// tokens.  4 warps of a CTA / one warp each, on a prefix of 4,000, bfloat16, us: 768 items of up to 60 tokens 30.3 /
+// 28.8, of 300 38.3 / 46.8; 1,024 items 36.4 / 29.1 and 45.6 / 48.5; 1,216 items 44.9 / 32.2 and 54.2 / 51.4.
+constexpr int64_t kOneWarpItems = 8, kOneWarpShort = 5, kShortTokens = 128;
+// Tokens of one sequence (at most) from which the own tokens are cut evenly over the SMs, for up to kLinePairs
+// sequences times row tiles.  Clusters / even cuts, 16 sequences with 8 key heads of 128, us: bfloat16 2,000 tokens
+// 36.7 / 38.0, 4,000 58.6 / 49.8; fp8 4,000 41.3 / 44.2, 9,000 69.2 / 59.6; 48 sequences: bfloat16 4,000 107 / 113,
+// 8,000 196 / 171; fp8 4,000 106 / 99.
+constexpr int64_t kLineTokens = 4096, kLinePairs = 1024;
 
 int plan_attention(const tps_kv_cache& c, const tps_attention& a, int sms, tps::AttnPlan* out)
 {
@@ -57,20 +59,17 @@ int plan_attention(const tps_kv_cache& c, const tps_attention& a, int sms, tps::
     p.suffix_rows = own_rows <= 8 ? 8 : 16;
     p.suffix_tiles = (int)((own_rows + p.suffix_rows - 1) / p.suffix_rows);
     const int64_t alone = a.B * c.n_heads * p.suffix_tiles;  // (sequence, key head, tile) triples
-    p.shared = a.prefix_len > 0 && a.B > 1 && alone > (p.R >= kTensorRows ? kAloneTensorTokens : kAloneTokens) / a.prefix_len;
+    p.shared = a.prefix_len > 0 && a.B > 1 && alone > (c.format == TPS_KV_BF16 ? kAloneBf16 : kAlone8) / a.prefix_len;
     if (p.shared) {
-        p.tensor = p.R >= kTensorRows;
-        p.tile_rows = p.tensor ? (p.R <= 128 ? 128 : 256) : (p.R <= 8 ? 8 : 16);
-        p.block_keys = p.tensor ? 128 : kRowsBlock;
+        p.tile_rows = p.R <= 128 ? 128 : 256;
         const int64_t n_tiles = (p.R + p.tile_rows - 1) / p.tile_rows, items = n_tiles * c.n_heads;
-        p.nblk = (int)((a.prefix_len + p.block_keys - 1) / p.block_keys);
+        p.nblk = (int)((a.prefix_len + tps::kBlockKeys - 1) / tps::kBlockKeys);
         if (items > INT32_MAX / p.nblk) return TPS_ERR_ARG;
         p.n_tiles = (int)n_tiles;
         p.items = (int)items;
         p.units = p.items * p.nblk;
         // No more CTAs than the longest share needs: fewer pieces to join, and SMs left for the own tokens.
-        const int most = sms * (p.tensor ? 1 : kRowsCtasPerSm);
-        p.share = (int)(((int64_t)p.units + most - 1) / most);
+        p.share = (int)(((int64_t)p.units + sms - 1) / sms);
         p.ctas = (int)(((int64_t)p.units + p.share - 1) / p.share);
         p.pieces = (int64_t)p.ctas + p.items;
     }
@@ -78,7 +77,7 @@ int plan_attention(const tps_kv_cache& c, const tps_attention& a, int sms, tps::
     // all of them are resident at once (by the kernel's registers and shared memory).
     const int64_t resident = (int64_t)sms * (p.suffix_rows == 8 && c.format != TPS_KV_BF16 ? 4 : 3);
     const int64_t tokens = a.table_width * c.page_size + (p.shared ? 0 : a.prefix_len);
-    p.one_warp = alone >= kOneWarpItems * (int64_t)sms;
+    p.one_warp = alone >= (tokens <= kShortTokens ? kOneWarpShort : kOneWarpItems) * sms;
     p.line = !p.one_warp && a.B * p.suffix_tiles <= kLinePairs && tokens >= kLineTokens;
     p.cluster = 1;
     while (!p.one_warp && !p.line && p.cluster < 8 && alone * p.cluster * 2 <= resident && tokens >= (int64_t)p.cluster * 256)
@@ -222,15 +221,11 @@ int tps_prefix_attention(const tps_kv_cache* cache, const tps_attention* args, v
     a.line_part = reinterpret_cast<float*>(ws + a.p.off_line_part);
     a.line_ml = reinterpret_cast<float2*>(ws + a.p.off_line_ml);
     if (a.p.units) {
-        if (!a.p.tensor)
-            e = tps::launch_attn_prefix_rows(a, st);
-        else
-            e = cache->format == TPS_KV_BF16  ? tps::launch_attn_prefix_bf16(a, st)
-                : cache->format == TPS_KV_FP8 ? tps::launch_attn_prefix_fp8(a, st)
-                                              : tps::launch_attn_prefix_int8(a, st);
+        e = cache->format == TPS_KV_BF16  ? tps::launch_attn_prefix_bf16(a, st)
+            : cache->format == TPS_KV_FP8 ? tps::launch_attn_prefix_fp8(a, st)
+                                          : tps::launch_attn_prefix_int8(a, st);
     }
-    if (e == cudaSuccess)
-        e = a.p.line ? tps::launch_attn_line(a, a.p.units > 0, st) : tps::launch_attn_suffix(a, a.p.units > 0, st);
+    if (e == cudaSuccess) e = tps::launch_attn_own(a, a.p.units > 0, st);
     if (a.p.bytes && !args->workspace) {
         const cudaError_t ef = cudaFreeAsync(ws, st);
         if (e == cudaSuccess) e = ef;

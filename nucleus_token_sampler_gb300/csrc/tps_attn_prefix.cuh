@@ -38,7 +38,6 @@
 
 namespace tps {
 
-constexpr int kBlockKeys = 128;
 constexpr int kScalars = 8;         // blocks whose scale factors are kept
 
 template <int D, int kFormat, int kTiles> struct PrefixShape {

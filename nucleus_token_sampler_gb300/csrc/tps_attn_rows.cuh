@@ -1,6 +1,5 @@
 // tps_attn_rows.cuh -- attention of up to 16 query rows per warp over paged keys and values, and the
-// join of its parts: every sequence's own tokens, and the shared prefix where the batch has too few
-// rows for the tcgen05 kernel.
+// join of its parts: every sequence's own tokens, and the prefix of a call too small to share its work.
 //
 // Mathematics.  With z_j = scale log2(e) q.k_j, one pass over the tokens holds a reference m, the sum
 // l = sum 2^(z_j - m) and the output o = sum 2^(z_j - m) v_j in float32; m is raised (and l, o scaled)
@@ -542,55 +541,6 @@ __device__ __forceinline__ void write_piece(const RowsShared<D, kFormat>& sm, fl
         *reinterpret_cast<float4*>(po + (col / 4 * kRows + r) * 4) = j.acc;
         if (col == 0) ml[piece * kRows + r] = make_float2(j.top, sm.bad == 2 ? kPieceTimeout : (sm.bad ? kPieceBadPage : j.l));
     }
-}
-
-// The shared prefix, 8 N rows at a time: CTA c's part of the line of blocks (AttnPlan).
-template <int D, int kFormat, int N>
-__global__ void __launch_bounds__(kRowsThreads, N == 1 ? 4 : 3) attn_prefix_rows_kernel(const AttnArgs a)
-{
-    constexpr int kRows = 8 * N;
-    extern __shared__ __align__(128) unsigned char raw[];
-    RowsShared<D, kFormat>& sm = *reinterpret_cast<RowsShared<D, kFormat>*>(raw);
-    const AttnPlan& p = a.p;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int u0 = (int)blockIdx.x * p.share, u1 = min(p.share, p.units - u0) + u0;
-    init_rings(sm);
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    Walk<D, kFormat> walk{a.c, a.page_shift, 0, sm.ring[warp], sm.full[warp]};
-    for (int u = u0; u < u1;) {
-        const int item = u / p.nblk;
-        const int end = min(u1 - item * p.nblk, p.nblk) + item * p.nblk;
-        const int head = item / p.n_tiles;
-        const int64_t r0 = (int64_t)(item - head * p.n_tiles) * kRows;
-        const int rows = (int)min((int64_t)kRows, p.R - r0);
-        const int t0 = (u - item * p.nblk) * p.block_keys;
-        const int t1 = (int)min(a.a.prefix_len, (int64_t)(end - item * p.nblk) * p.block_keys);
-        walk.head = head;
-        walk.look(a.a.prefix_pages, t0 + warp * 16, t1);
-        RowState<D, N> st;
-        load_query<D, kFormat, N>(st, rows, [&](int r) {
-            const int64_t row = r0 + r, bt = row / a.G;
-            return static_cast<const __nv_bfloat16*>(a.a.q) + (bt * a.a.n_q_heads + (int64_t)head * a.G + (row - bt * a.G)) * D;
-        });
-        walk.start(t0 + warp * 16, kRowsWarps * 16, t1);
-        ready_query<D, kFormat, N>(st, a.qk_scale);
-        int lim[N][2];
-#pragma unroll
-        for (int n = 0; n < N; ++n) lim[n][0] = lim[n][1] = t1;
-        const int fault = attend<D, kFormat, N>(st, walk, lim);
-        store_rows<D, kFormat, N>(sm, st, kRows);
-        if (fault && lane == 0) atomicMax(&sm.bad, fault);
-        __syncthreads();
-        write_piece<D, kFormat, N>(sm, a.part, a.ml, (int64_t)blockIdx.x + item);
-        __syncthreads();
-        // The rings held output: order those accesses before the next copies into them.
-        fence_proxy_async();
-        u = end;
-        if (sm.bad == 2) break;  // a wait ran out (uniform: nothing writes it here)
-    }
-    if (sm.bad == 2 && threadIdx.x < kRows)  // then every piece says so
-        for (int item = u0 / p.nblk; item <= (u1 - 1) / p.nblk; ++item)
-            a.ml[((int64_t)blockIdx.x + item) * kRows + threadIdx.x] = make_float2(0.f, kPieceTimeout);
 }
 
 // The pieces of the shared prefix that hold a row's item: piece `first` on, `count` of them.

@@ -37,19 +37,19 @@ struct KvReadArgs {
 cudaError_t launch_kv_read(const KvReadArgs& a, bool bf16, int sms, cudaStream_t stream);
 
 // The work of one prefix-attention call.  The shared part is cut along items and tokens: an item is one
-// key head and `tile_rows` of its R = B Tq G query rows; its prefix is nblk blocks of `block_keys`
+// key head and `tile_rows` of its R = B Tq G query rows; its prefix is nblk blocks of kBlockKeys
 // tokens.  The items' blocks form one line of `units` blocks, of which each CTA takes `share` consecutive ones
 // (the last CTA what is left).  A CTA's part of an item leaves one piece in the workspace, the
 // unnormalised output of its rows with their maximum and sum; piece c + item is CTA c's of that item
 // (going along the line either number grows, so no two share one).
+constexpr int kBlockKeys = 128;
 struct AttnPlan {
     int64_t R;           // query rows of one key head
     int items, nblk, units, share, ctas;
     int64_t pieces;
-    int tile_rows, block_keys;
+    int tile_rows;
     int n_tiles;         // row tiles of one key head
     bool shared;         // the prefix is computed once, into pieces (else by each sequence for itself)
-    bool tensor;         // the tcgen05 kernel computes the shared part
     int suffix_rows;     // rows of a tile of one sequence's Tq G rows: 8 or 16
     int suffix_tiles;
     bool one_warp;       // each warp has a sequence (and head, tile) for itself
@@ -73,11 +73,9 @@ struct AttnArgs {
 };
 
 // The shared part, then the own tokens and the join.
-cudaError_t launch_attn_prefix_rows(const AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_attn_prefix_bf16(const AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_attn_prefix_fp8(const AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_attn_prefix_int8(const AttnArgs& a, cudaStream_t stream);
-cudaError_t launch_attn_suffix(const AttnArgs& a, bool after_prefix, cudaStream_t stream);
-cudaError_t launch_attn_line(const AttnArgs& a, bool after_prefix, cudaStream_t stream);
+cudaError_t launch_attn_own(const AttnArgs& a, bool after_prefix, cudaStream_t stream);
 
 }  // namespace tps

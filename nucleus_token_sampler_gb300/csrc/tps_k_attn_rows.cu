@@ -21,23 +21,6 @@ cudaError_t allow_smem(Kernel k, size_t bytes, std::atomic<uint64_t>& allowed)
     return e;
 }
 
-template <int D, int kFormat, int N>
-cudaError_t prefix_rows_shape(const AttnArgs& a, cudaStream_t stream)
-{
-    static std::atomic<uint64_t> allowed{0};
-    auto k = attn_prefix_rows_kernel<D, kFormat, N>;
-    const cudaError_t e = allow_smem(k, sizeof(RowsShared<D, kFormat>), allowed);
-    if (e != cudaSuccess) return e;
-    k<<<(unsigned)a.p.ctas, kRowsThreads, sizeof(RowsShared<D, kFormat>), stream>>>(a);
-    return cudaGetLastError();
-}
-
-template <int D, int kFormat>
-cudaError_t prefix_rows(const AttnArgs& a, cudaStream_t stream)
-{
-    return a.p.tile_rows == 8 ? prefix_rows_shape<D, kFormat, 1>(a, stream) : prefix_rows_shape<D, kFormat, 2>(a, stream);
-}
-
 template <int D, int kFormat, int N, bool kOneWarp>
 cudaError_t suffix_shape(const AttnArgs& a, bool after_prefix, cudaStream_t stream)
 {
@@ -119,45 +102,27 @@ cudaError_t line(const AttnArgs& a, bool after_prefix, cudaStream_t stream)
     return a.p.suffix_rows == 8 ? line_shape<D, kFormat, 1>(a, after_prefix, stream) : line_shape<D, kFormat, 2>(a, after_prefix, stream);
 }
 
-enum class Part { kPrefix, kOwn, kLine };
-
 template <int D, int kFormat>
-cudaError_t part_of(Part part, const AttnArgs& a, bool after_prefix, cudaStream_t stream)
+cudaError_t own(const AttnArgs& a, bool after_prefix, cudaStream_t stream)
 {
-    switch (part) {
-    case Part::kPrefix: return prefix_rows<D, kFormat>(a, stream);
-    case Part::kOwn: return suffix<D, kFormat>(a, after_prefix, stream);
-    default: return line<D, kFormat>(a, after_prefix, stream);
-    }
+    return a.p.line ? line<D, kFormat>(a, after_prefix, stream) : suffix<D, kFormat>(a, after_prefix, stream);
 }
 
 template <int D>
-cudaError_t by_format(Part part, const AttnArgs& a, bool after_prefix, cudaStream_t stream)
+cudaError_t by_format(const AttnArgs& a, bool after_prefix, cudaStream_t stream)
 {
     switch (a.c.format) {
-    case TPS_KV_BF16: return part_of<D, TPS_KV_BF16>(part, a, after_prefix, stream);
-    case TPS_KV_FP8: return part_of<D, TPS_KV_FP8>(part, a, after_prefix, stream);
-    default: return part_of<D, TPS_KV_INT8>(part, a, after_prefix, stream);
+    case TPS_KV_BF16: return own<D, TPS_KV_BF16>(a, after_prefix, stream);
+    case TPS_KV_FP8: return own<D, TPS_KV_FP8>(a, after_prefix, stream);
+    default: return own<D, TPS_KV_INT8>(a, after_prefix, stream);
     }
-}
-
-cudaError_t launch(Part part, const AttnArgs& a, bool after_prefix, cudaStream_t stream)
-{
-    return a.c.head_dim == 64 ? by_format<64>(part, a, after_prefix, stream) : by_format<128>(part, a, after_prefix, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_prefix_rows(const AttnArgs& a, cudaStream_t stream) { return launch(Part::kPrefix, a, false, stream); }
-
-cudaError_t launch_attn_suffix(const AttnArgs& a, bool after_prefix, cudaStream_t stream)
+cudaError_t launch_attn_own(const AttnArgs& a, bool after_prefix, cudaStream_t stream)
 {
-    return launch(Part::kOwn, a, after_prefix, stream);
-}
-
-cudaError_t launch_attn_line(const AttnArgs& a, bool after_prefix, cudaStream_t stream)
-{
-    return launch(Part::kLine, a, after_prefix, stream);
+    return a.c.head_dim == 64 ? by_format<64>(a, after_prefix, stream) : by_format<128>(a, after_prefix, stream);
 }
 
 }  // namespace tps
