@@ -102,9 +102,9 @@ __device__ __forceinline__ void code_pairs(uint32_t w, uint32_t& p01, uint32_t& 
     }
 }
 
-// The value's scale and the factors a token's score and weight take from it.  A stored scale is never 0;
-// 0 marks a slot that was never written and counts as the smallest scale.
-__device__ __forceinline__ float floor_scale(float s) { return s > 0.f || s != s ? s : 0x1p-40f; }
+// A stored scale is at least 2^-40; what lies below (a slot never written, or what stands in rows past the end,
+// whose weight is 0) counts as that, so that 1 / s is finite.
+__device__ __forceinline__ float floor_scale(float s) { return s >= 0x1p-40f || s != s ? s : 0x1p-40f; }
 
 // Components of a head that a lane holds for k-step s: 4 consecutive ones from here on.
 template <int kFormat>

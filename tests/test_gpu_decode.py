@@ -436,3 +436,16 @@ def test_attention_repeats_itself(fmt, B, Hq, Hkv, D, prefix, lens):
         got, again = tps.prefix_attention(q, c, pp, prefix, table, n, want_lse=True)
         differ += (got != want).sum() + (again != lse).sum()
     assert int(differ) == 0
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "int8"])
+@pytest.mark.parametrize("B,prefix", [(3, 70), (60, 1500)])
+def test_attention_scales_past_the_end_may_be_tiny(fmt, B, prefix):
+    """1 / s overflows for a subnormal scale; in a row that is no token it must not reach the sum (0 * inf)."""
+    c, q, pp, table, n = _case(_gen(78), B, 1, 8, 2, 128, prefix, [3, 21], 16, fmt)
+    want, lse = tps.prefix_attention(q, c, pp, prefix, table, n, want_lse=True)
+    assert torch.isfinite(want).all() and torch.isfinite(lse).all()
+    for s in (c.k_scale, c.v_scale):
+        s[torch.isnan(s)] = 1e-39
+    got, again = tps.prefix_attention(q, c, pp, prefix, table, n, want_lse=True)
+    assert torch.equal(got, want) and torch.equal(again, lse)
