@@ -9,7 +9,8 @@
  * sampling with temperature" ('How to approach it': keep token i iff the mass of strictly more
  * probable tokens is below p; 'A strong answer': the greedy branch and per-request p).
  * An optional stage ahead of that chain, tps_apply_penalties, applies repetition, frequency and
- * presence penalties to the raw logits in place.
+ * presence penalties to the raw logits in place.  Further ahead stand the operators of a decode step whose
+ * batch shares a long prompt: tps_qk_norm_rope, tps_kv_write, tps_kv_read and tps_prefix_attention.
  *
  * Rules, per row (T = temperature[b], k = top_k[b], p = top_p[b], m = min_p[b]):
  *   - T <= 0: greedy; the token is the lowest index holding the largest logit.
@@ -33,7 +34,8 @@
  *     a few KB for 1,024 rows of 128,256 logits, at most about 2.5 MB for a split batch) from a
  *     stream-ordered memory pool the library creates once per device, and returns it on the call's
  *     stream; the pool keeps up to 64 MiB reserved between calls.  tps_sample_noalloc uses a fixed
- *     array instead; no other call allocates device memory;
+ *     array instead.  tps_prefix_attention takes its workspace from the same pool unless it is given one
+ *     (tps_prefix_attention_workspace says how much); no other call allocates device memory;
  *   - the library never synchronises the host, keeps no state between calls beyond that pool and
  *     a per-device cache of queried limits, and may be called from several host threads at once;
  *   - `stream` is a cudaStream_t (NULL = the legacy default stream); all work is enqueued on it;
@@ -424,7 +426,9 @@ typedef struct {
  * all share and their own tokens, both held in `cache` (head_dim 64 or 128).  The products with the
  * shared keys and values are computed once for the whole batch.  Products are accumulated and
  * softmax statistics held in float32; softmax weights are rounded to 16 bits for the second product
- * (bfloat16 for TPS_KV_BF16, float16 for 8-bit formats).  No result depends on another sequence's
+ * (bfloat16 for TPS_KV_BF16, float16 for 8-bit formats), and in the shared part so are int8 values.  Not
+ * accepted (TPS_ERR_ARG): more than 2^31 query rows, 2^24 rows of one sequence and key head, or 2^31 pairs of
+ * a block of 128 shared tokens and a tile of 128 or 256 rows.  No result depends on another sequence's
  * data, and cache rows past a sequence's length are never used, whatever they hold; a NaN or an infinity
  * in an own token's VALUE, though, also reaches those of the sequence's queries that causality hides the
  * token from (0 * NaN in the second product).

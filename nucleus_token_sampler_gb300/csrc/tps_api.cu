@@ -1,5 +1,5 @@
 // tps_api.cu -- the C ABI declared in include/tps.h: argument checks, kernel and launch-shape
-// choice, and the launches.  No host synchronisation, no state kept between calls beyond a
+// choice, and the launches, of the sampling calls.  No host synchronisation, no state kept between calls beyond a
 // per-device cache of queried limits.
 //
 // Two kernels sample the rows.  The cluster kernel (a thread-block cluster per row, the row held in
@@ -75,7 +75,7 @@ DeviceInfo g_dev[kMaxDevices];
 std::mutex g_mu;
 
 // The library's own stream-ordered memory pool per device, for the streaming kernel's per-call
-// scratch.  The device's default pool gives all unused memory back at every synchronisation, so the
+// scratch and the prefix attention's pieces (128 KB for each SM and row tile at most).  The device's default pool gives all unused memory back at every synchronisation, so the
 // first call after a cudaStreamSynchronize would map fresh memory on the host's critical path; this
 // pool keeps up to kPoolKeepBytes reserved instead (a call's scratch is a few KB for a batch of whole
 // rows and at most about 2.5 MB for a split batch).  Created once per device, with that device current, and kept until the

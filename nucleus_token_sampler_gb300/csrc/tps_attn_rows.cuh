@@ -20,7 +20,8 @@
 // order of the D components, so a lane's 16 bytes of a key row serve as its fragments of consecutive
 // k-steps as they lie (the query fragments are loaded in the same order); a lane's 16 bytes of a value row
 // become rows g and g + 8 of consecutive tiles.  mma.sync rather than tcgen05: 8 or 16 rows fill a
-// sixteenth or an eighth of a tcgen05 tile.
+// sixteenth or an eighth of a tcgen05 tile.  Measured: 16 sequences of up to 16,000 own tokens, 4 key heads of 128 in
+// bfloat16, 64 us with the prefix and the join (4.1 TB/s); 8 sequences on 1,000 shared tokens, one launch, 10.1 us.
 #pragma once
 
 #include <cstdint>
