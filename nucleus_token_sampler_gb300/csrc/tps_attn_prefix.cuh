@@ -61,7 +61,8 @@ template <int D, int kFormat, int kTiles> struct PrefixShape {
     static constexpr int kTmemCols = kTiles == 2 ? 512 : 256;
     static constexpr int kScoreCol = 0, kOutCol = 128 * kTiles;  // tile m: scores at 128 m, outputs at kOutCol + D m
     struct Control {
-        uint64_t q_full, full[kRing], empty[kRing], s_full[kTiles], p_full[kTiles], o_full[kTiles], tail, drain;
+        uint64_t q_full, full[kRing], empty[kRing], s_full[kTiles], p_full[kTiles], o_full[kTiles], drain;
+        uint64_t tail[kRing];  // bf16: the rows past the prefix of the value tile in this slot are zero
         uint64_t raw_full[kRaw], factor_full[kRaw], raw_empty[kRaw], scalar_full[kScalars];
         uint32_t tmem;
         int abort, bad;
@@ -171,7 +172,7 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
 
     if (threadIdx.x == 0) {
         mbar_init(&ctl.q_full, 4 * kTiles);
-        for (int i = 0; i < kRing; ++i) mbar_init(&ctl.full[i], k8 ? Shape::kConvertWarps : 1), mbar_init(&ctl.empty[i], 1);
+        for (int i = 0; i < kRing; ++i) mbar_init(&ctl.full[i], k8 ? Shape::kConvertWarps : 1), mbar_init(&ctl.empty[i], 1), mbar_init(&ctl.tail[i], 1);
         for (int i = 0; i < kTiles; ++i) mbar_init(&ctl.s_full[i], 1), mbar_init(&ctl.p_full[i], 128), mbar_init(&ctl.o_full[i], 1);
         for (int i = 0; i < kScalars; ++i) mbar_init(&ctl.scalar_full[i], 1);
         for (int i = 0; i < kRaw; ++i) {
@@ -179,7 +180,6 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
             mbar_init(&ctl.factor_full[i], 1);
             mbar_init(&ctl.raw_empty[i], Shape::kConvertWarps);
         }
-        mbar_init(&ctl.tail, 1);
         mbar_init(&ctl.drain, 1);
         ctl.abort = 0;
         ctl.bad = 0;
@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
         const uint64_t q_desc = smem_desc(smem_u32(q_tile), 16), k_desc = smem_desc(smem_u32(ring), 16);
         const uint64_t v_desc = smem_desc(smem_u32(ring), 128 * 128);
         const bool leader = elect_one();
-        uint32_t q_parity = 0, p_parity = 0, tail_parity = 0;
+        uint32_t q_parity = 0, p_parity = 0, tail_parity = 0;  // of the tail: a bit for each slot
         Turn<kRing> turn(0);
         auto take = [&]() {  // wait for the ring's next tile; its slot
             alive = wait_all(&ctl.full[turn.slot], turn.parity);
@@ -494,8 +494,8 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
                 const int vslot = take();
                 if (!alive) break;
                 if (!k8 && prefix < (way.block + v + 1) * kBlockKeys) {  // its rows past the prefix are zeroed
-                    if (!(alive = wait_all(&ctl.tail, tail_parity))) break;
-                    tail_parity ^= 1;
+                    if (!(alive = wait_all(&ctl.tail[vslot], tail_parity >> vslot & 1))) break;
+                    tail_parity ^= 1u << vslot;
                 }
 #pragma unroll
                 for (int m = 0; m < kTiles; ++m) {
@@ -571,16 +571,19 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
                     }
                 }
                 const uint32_t parity = turn.parity ^ 1;  // of this fill
+                const int slot = turn.slot;
                 turn.next();
                 ++fills;
                 if (!k8 && kv && left < kBlockKeys) {
-                    // Rows past the prefix hold anything (0 * NaN is NaN): zero them once the copy has landed.
+                    // Rows past the prefix hold anything (0 * NaN is NaN): zero them once the copy has landed.  Each slot has
+                    // a signal of its own: its next one comes after the slot was given back, so after this one's wait.  One
+                    // signal for all could complete two phases before the first was waited for, where items are one block long.
                     if (!(alive = wait_all(bar, parity))) break;
                     for (int i = lane; i < (kBlockKeys - left) * (D / 8); i += 32)
                         *reinterpret_cast<uint4*>(dst + tile_byte(left + i / (D / 8), i % (D / 8))) = make_uint4(0u, 0u, 0u, 0u);
                     fence_proxy_async();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&ctl.tail);
+                    if (lane == 0) mbar_arrive(&ctl.tail[slot]);
                 }
             }
         }

@@ -449,3 +449,18 @@ def test_attention_scales_past_the_end_may_be_tiny(fmt, B, prefix):
         s[torch.isnan(s)] = 1e-39
     got, again = tps.prefix_attention(q, c, pp, prefix, table, n, want_lse=True)
     assert torch.equal(got, want) and torch.equal(again, lse)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "int8"])
+@pytest.mark.parametrize("B,Tq,Hq,Hkv,D,prefix", [
+    (2100, 5, 64, 8, 64, 1), (512, 5, 64, 8, 128, 100), (512, 5, 64, 8, 64, 127), (1024, 1, 64, 8, 128, 100)])
+def test_attention_short_prefixes_with_several_items_a_cta(fmt, B, Tq, Hq, Hkv, D, prefix):
+    """Every item is one block that ends past the prefix, and each CTA has two or more of them, two in its ring at a time.  All outputs
+    are compared for the first and last sequences, whose rows lie in the first and last tiles, and some between."""
+    c, q, pp, table, n = _case(_gen(prefix), B, Tq, Hq, Hkv, D, prefix, [Tq, Tq + 3], 16, fmt, spare=20)
+    st = torch.full((B,), 9, dtype=torch.int32, device=DEV)
+    for _ in range(3):
+        out, lse = tps.prefix_attention(q, c, pp, prefix, table, n, want_lse=True, status=st)
+        assert (st == 0).all() and torch.isfinite(out).all() and torch.isfinite(lse).all()
+    some = torch.cat([torch.arange(8), torch.arange(B // 2 - 4, B // 2 + 4), torch.arange(B - 8, B)]).to(DEV)
+    _check_attention((out[some], lse[some]), q[some], plain.values(c), pp, prefix, table[some], n[some], D ** -0.5, fmt)
