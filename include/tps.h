@@ -426,8 +426,7 @@ typedef struct {
  * all share and their own tokens, both held in `cache` (head_dim 64 or 128).  The products with the
  * shared keys and values are computed once for the whole batch.  Products are accumulated and
  * softmax statistics held in float32; softmax weights are rounded to 16 bits for the second product
- * (bfloat16 for TPS_KV_BF16, float16 for 8-bit formats), and in the shared part so are int8 values
- * times their scales (each at most 2^-11 of sum p |v|; fp8 values are exact).  Not
+ * (bfloat16 for TPS_KV_BF16: at most 2^-8 of sum p |v|; float16 for 8-bit formats: at most 2^-11).  Not
  * accepted (TPS_ERR_ARG): more than 2^31 query rows, 2^24 rows of one sequence and key head, or 2^31 pairs of
  * a block of 128 shared tokens and a tile of 128 or 256 rows.  No result depends on another sequence's
  * data, and cache rows past a sequence's length are never used, whatever they hold; a NaN or an infinity

@@ -4,11 +4,11 @@
 // Mathematics.  As in tps_attn_rows.cuh: weights 2^(z - m) with a reference m per row that is raised only
 // when a score exceeds it by more than kSlack; m is a whole number here, so that raising it scales what
 // was already computed by an exact power of two.  8-bit formats become float16 on the way to the matrix
-// unit: for every block of 128 tokens the scales are taken relative to the block's largest, nk for keys
-// and nv for values (powers of two), so that code * scale / n is at most 448 (one rounding to 11
-// bits for int8, exact for fp8) whatever the magnitude of the cache's values.  The block's factors stay
-// scalars outside: z = (q.k') nk, and the weights take log2(nv) in their exponent (the row sum divides
-// by nv again).
+// unit.  For every block of 128 tokens the scales are taken in the block's unit, a power of two: nk for keys and
+// nv for values.  Codes of fp8 are multiplied by their scale in that unit.  Codes of int8 stay whole numbers (7 bits
+// times a scale's 8 would be rounded to float16's 11): the scores take the keys' scales, and a weight takes its
+// value's scale in float32, before its one rounding.  The block's units stay scalars outside: z = (q.k') nk, and the
+// weights take log2(nv) in their exponent (the row sum divides by nv again).
 //
 // What bounds it: with R of some hundreds, the matrix unit (512 clocks per 128 x 128 tile at D = 128) and
 // next to it the exponentials (one for each of its 16,384 weights) and the conversion of 8-bit codes; with
@@ -17,8 +17,8 @@
 // runs while the other's products do, and each block of keys and values is loaded and converted once
 // for 256 rows.  Measured with 8 key heads of 128: 1,024 x 4 rows on 16,384 tokens take 175 us in bfloat16 (1.57
 // PFLOP/s, the matrix unit 54% busy at half that length under a profiler) and 222 us in fp8 (1.24 PFLOP/s; the conversion
-// and the softmax share the issue slots); 48 x 25 rows of 64 on 20,011 tokens 95 us in int8 (0.52 PFLOP/s: half the
-// products for the same weights); 4 x 4 rows on 16,384 tokens 26 us with the join (2.6 TB/s).  A third score buffer, so that
+// and the softmax share the issue slots); 48 x 25 rows of 64 on 20,011 tokens 111 us in int8 (0.44 PFLOP/s: half the
+// products for the same weights; 95 us where the values' scales were rounded into the codes, which cost a second 2^-11); 4 x 4 rows on 16,384 tokens 26 us with the join (2.6 TB/s).  A third score buffer, so that
 // scores run ahead of the softmax, helped D = 64 (92.1 -> 88.8 us in bfloat16) and cost D = 128 more (125.5 ->
 // 132.9 us): each tile has one.  Roles:
 //   warps 0 .. 4 kTiles - 1   softmax, one thread per query row: scores from TMEM, weights back to
@@ -50,10 +50,11 @@ template <int D, int kFormat, int kTiles> struct PrefixShape {
     static constexpr int kMmaWarp = 4 * kTiles, kLoadWarp = kMmaWarp + 1, kScaleWarp = kMmaWarp + 2;
     static constexpr int kConvertWarp = kMmaWarp + 4, kConvertWarps = 8;
     static constexpr int kThreads = (kConvertWarp + (k8 ? kConvertWarps : 0)) * 32;
-    // Registers where the roles share them out (640 threads at 96 at launch): 2 x 144 + 3 x 64 = 5 x 96.
-    static constexpr bool kSplitRegs = k8 && kTiles == 2;
-    static constexpr int kRegsSoftmax = 144, kRegsOthers = 64;
-    static_assert(2 * kRegsSoftmax + 3 * kRegsOthers <= 5 * 96, "no more than the launch gave");
+    // Registers where the roles share them out: 640 threads at 96 at launch, 2 x 144 + 3 x 64 = 5 x 96, or 512 threads at
+    // 128, 200 + 3 x 104 = 4 x 128.
+    static constexpr bool kSplitRegs = kFormat == TPS_KV_INT8 || (k8 && kTiles == 2);
+    static constexpr int kRegsLaunch = kTiles == 2 ? 96 : 128, kRegsSoftmax = kTiles == 2 ? 144 : 200, kRegsOthers = kTiles == 2 ? 64 : 104;
+    static_assert(kTiles * kRegsSoftmax + 3 * kRegsOthers <= (kTiles + 3) * kRegsLaunch, "no more than the launch gave");
     static constexpr int kTileBytes = 128 * D * 2;         // a query, key or value tile
     static constexpr int kRing = k8 && D == 128 && kTiles == 2 ? 3 : 4;  // key and value tiles in shared memory
     static constexpr int kRaw = D == 128 ? 3 : 4;          // tiles of 8-bit codes
@@ -67,8 +68,9 @@ template <int D, int kFormat, int kTiles> struct PrefixShape {
         uint32_t tmem;
         int abort, bad;
         float key_unit[kScalars], value_exp[kScalars];
-        alignas(16) __nv_bfloat16 key_scale[kFormat == TPS_KV_INT8 ? kScalars : 1][128];  // int8: of the block's tokens
-        alignas(16) __half factor[kRaw][128];  // of the tokens of a code tile
+        // int8: of the block's tokens, the values' in the block's unit, at most 1
+        alignas(16) float key_scale[kFormat == TPS_KV_INT8 ? kScalars : 1][128], value_scale[kFormat == TPS_KV_INT8 ? kScalars : 1][128];
+        alignas(16) __half factor[kFormat == TPS_KV_FP8 ? kRaw : 1][128];  // fp8: of the tokens of a code tile
     };
     static constexpr size_t kSmem =
         (size_t)(kTiles + kRing) * kTileBytes + (k8 ? (size_t)kRaw * kRawBytes : 0) + sizeof(Control) + 1024;
@@ -322,17 +324,13 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
                 // int8: a score's key scale (the codes are in the tile as they are).  Scores past the prefix become -inf.
                 auto ready = [&](float (&s)[32], int ch) {
                     if constexpr (kFormat == TPS_KV_INT8) {
-                        const uint4* f = reinterpret_cast<const uint4*>(ctl.key_scale[scales] + ch * 32);
+                        const float4* f = reinterpret_cast<const float4*>(ctl.key_scale[scales] + ch * 32);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint4 x = f[i];
-                            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const float2 y = mul2(make_float2(s[8 * i + 2 * k], s[8 * i + 2 * k + 1]),
-                                                      make_float2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u)));
-                                s[8 * i + 2 * k] = y.x, s[8 * i + 2 * k + 1] = y.y;
-                            }
+                        for (int i = 0; i < 8; ++i) {
+                            const float4 x = f[i];
+                            const float2 y = mul2(make_float2(s[4 * i], s[4 * i + 1]), make_float2(x.x, x.y));
+                            const float2 z = mul2(make_float2(s[4 * i + 2], s[4 * i + 3]), make_float2(x.z, x.w));
+                            s[4 * i] = y.x, s[4 * i + 1] = y.y, s[4 * i + 2] = z.x, s[4 * i + 3] = z.y;
                         }
                     }
                     if (left < ch * 32 + 32) {
@@ -388,11 +386,16 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
                 auto weigh = [&](const float (&s)[32], int ch, float b) {
                     float2 part[2];
                     uint32_t w[16];
+                    float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                     for (int i = 0; i < 32; i += 2) {
                         float2 x = fma2(make_float2(s[i], s[i + 1]), make_float2(c, c), make_float2(b, b));
                         x.x = exp2_fast(x.x), x.y = exp2_fast(x.y);
                         part[(i >> 1) & 1] = i < 4 ? x : add2(part[(i >> 1) & 1], x);
+                        if constexpr (kFormat == TPS_KV_INT8) {  // the value's scale, after the sum and before the rounding
+                            if (i % 4 == 0) f = reinterpret_cast<const float4*>(ctl.value_scale[scales] + ch * 32)[i / 4];
+                            x = mul2(x, i % 4 == 0 ? make_float2(f.x, f.y) : make_float2(f.z, f.w));
+                        }
                         if (k8) {
                             const __half2 h = __floats2half2_rn(x.x, x.y);
                             w[i / 2] = *reinterpret_cast<const uint32_t*>(&h);
@@ -592,11 +595,10 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
             mbar_wait_bounded(&filled[(fills - i) % kSlots], (uint32_t)((fills - i) / kSlots) & 1, kAttnWaitNs);
     } else if (k8 && warp == Shape::kScaleWarp) {
         // ---------------------------------------------------------------------------- scales
-        // A tile's unit is a power of two no larger than its largest scale and more than half of it (1 if
-        // there is none); a token's factor is its scale in that unit.  The keys of int8 stay codes, and the scores
-        // take their scales: a score is the exponent of a weight, and code times scale (7 bits by 8) rounded to
-        // float16's 11 would cost it more than a weight's own rounding does.  One warp for every tile in turn: a
-        // barrier's phase may only be waited for by a role that sees each of its phases.
+        // A tile's unit is a power of two next to its largest scale, the one below for fp8 and the one above for int8,
+        // whose weights (up to 2^15) are multiplied by the scales; 1 if there is none.  fp8: a token's scale in that
+        // unit is the factor of its codes.  int8: the scores and the weights take the scales.  One warp for every tile in
+        // turn: a barrier's phase may only be waited for by a role that sees each of its phases.
         Way way(p);
         Turn<kRaw> raw_turn(0);
         Turn<kScalars> scalar(0);
@@ -612,20 +614,26 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
                     w.x = in >= 2 ? w.x : (in == 1 ? w.x & 0xFFFFu : 0u);
                     w.y = in >= 4 ? w.y : (in == 3 ? w.y & 0xFFFFu : 0u);
                 }
+                const float s[4] = {__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
+                                    __uint_as_float(w.y & 0xFFFF0000u)};
                 if (kFormat == TPS_KV_INT8 && !kv) {
-                    *reinterpret_cast<uint2*>(&ctl.key_scale[scalar.slot][lane * 4]) = w;
+                    *reinterpret_cast<float4*>(&ctl.key_scale[scalar.slot][lane * 4]) = make_float4(s[0], s[1], s[2], s[3]);
                     if (lane == 0) ctl.key_unit[scalar.slot] = 1.f;
                 } else {
-                    const float s[4] = {__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
-                                        __uint_as_float(w.y & 0xFFFF0000u)};
                     float most = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
-                    const int e = most > 0.f ? max(-126, min((int)(__float_as_uint(most) >> 23) - 127, 126)) : 0;
+                    const uint32_t up = kFormat == TPS_KV_INT8 ? 0x7FFFFFu : 0u;
+                    const int e = most > 0.f ? max(-126, min((int)((__float_as_uint(most) + up) >> 23) - 127, 126)) : 0;
                     const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-                    const __half2 lo = __floats2half2_rn(s[0] * inv, s[1] * inv), hi = __floats2half2_rn(s[2] * inv, s[3] * inv);
-                    *reinterpret_cast<uint2*>(&ctl.factor[rs][lane * 4]) =
-                        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+                    if constexpr (kFormat == TPS_KV_INT8) {
+                        *reinterpret_cast<float4*>(&ctl.value_scale[scalar.slot][lane * 4]) =
+                            make_float4(s[0] * inv, s[1] * inv, s[2] * inv, s[3] * inv);
+                    } else {
+                        const __half2 lo = __floats2half2_rn(s[0] * inv, s[1] * inv), hi = __floats2half2_rn(s[2] * inv, s[3] * inv);
+                        *reinterpret_cast<uint2*>(&ctl.factor[rs][lane * 4]) =
+                            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+                    }
                     if (lane == 0) {
                         if (kv)
                             ctl.value_exp[scalar.slot] = (float)e;
@@ -668,7 +676,7 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
                 for (int i = 0; i < kSteps; ++i) {
                     const int r = i * kRowsPerStep + sub;
                     x[i] = *reinterpret_cast<const uint4*>(raw + r * D + piece * 16);
-                    f[i] = kFormat == TPS_KV_INT8 && !kv ? __float2half2_rn(1.f) : __half2half2(ctl.factor[rs][r]);
+                    if constexpr (kFormat == TPS_KV_FP8) f[i] = __half2half2(ctl.factor[rs][r]);
                 }
                 if (left < kBlockKeys) {  // past the prefix: anything
 #pragma unroll
@@ -685,10 +693,12 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         code_pairs<kFormat>(w[j], h[2 * j], h[2 * j + 1]);
+                        if constexpr (kFormat == TPS_KV_FP8) {
 #pragma unroll
-                        for (int k = 2 * j; k < 2 * j + 2; ++k) {
-                            const __half2 y = __hmul2(*reinterpret_cast<__half2*>(&h[k]), f[i]);
-                            h[k] = *reinterpret_cast<const uint32_t*>(&y);
+                            for (int k = 2 * j; k < 2 * j + 2; ++k) {
+                                const __half2 y = __hmul2(*reinterpret_cast<__half2*>(&h[k]), f[i]);
+                                h[k] = *reinterpret_cast<const uint32_t*>(&y);
+                            }
                         }
                     }
                     *reinterpret_cast<uint4*>(dst + tile_byte(r, 2 * piece)) = make_uint4(h[0], h[1], h[2], h[3]);

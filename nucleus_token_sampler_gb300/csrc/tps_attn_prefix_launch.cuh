@@ -49,6 +49,11 @@ cudaError_t launch_prefix_shape(const AttnArgs& a, cudaStream_t stream)
     if (e != cudaSuccess) return e;
     const uint64_t bit = 1ull << (dev & 63);
     if (!(allowed.load(std::memory_order_acquire) & bit)) {
+        // The warps that ask for more registers wait for those that the others give back: the sum has to be there.
+        cudaFuncAttributes fa;
+        e = cudaFuncGetAttributes(&fa, k);
+        if (e != cudaSuccess) return e;
+        if (Shape::kSplitRegs && fa.numRegs < Shape::kRegsLaunch) return cudaErrorInvalidConfiguration;
         e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape::kSmem);
         if (e != cudaSuccess) return e;
         allowed.fetch_or(bit, std::memory_order_release);
