@@ -23,6 +23,7 @@ decltype(&tps_qk_norm_rope) f_norm;
 decltype(&tps_kv_write) f_write;
 decltype(&tps_kv_read) f_read;
 decltype(&tps_prefix_attention) f_attention;
+bool bound;               // the pointers above are set
 PyObject* on_error;       // called with (return code, entry point's name); raises
 PyObject* out_of_memory;  // PyTorch's exception class
 
@@ -297,6 +298,7 @@ PyObject* bind(PyObject* const* a, Py_ssize_t n)
     Py_XSETREF(on_error, a[4]);
     Py_INCREF(a[5]);
     Py_XSETREF(out_of_memory, a[5]);
+    bound = f_norm && f_write && f_read && f_attention;
     return keep(Py_None);
 }
 
@@ -305,6 +307,7 @@ template <PyObject* (*F)(PyObject* const*, Py_ssize_t)>
 PyObject* guarded(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
     try {
+        if (!bound && F != bind) throw std::runtime_error("the module is not bound to the library");
         return F(a, n);
     } catch (const Raised&) {
         return nullptr;

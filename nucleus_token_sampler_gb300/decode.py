@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import threading
 
 import torch
 
@@ -49,20 +50,23 @@ def declare(lib):
 
 
 _Tensor = torch.Tensor
-_ops = None
+_ops = None  # the native module once it is bound: other threads read this without the lock
+_ops_lock = threading.Lock()
 
 
 def _torch_ops():
     """The native module that checks tensors and calls the library (csrc/tps_torch.cpp), loaded with it."""
     global _ops
-    if _ops is None:
-        from . import load, load_binding
-        lib = load()
-        _ops = load_binding()
-        address = lambda f: ctypes.cast(f, ctypes.c_void_p).value
-        _ops.bind(address(lib.tps_qk_norm_rope), address(lib.tps_kv_write), address(lib.tps_kv_read),
-                  address(lib.tps_prefix_attention), _fail, torch.OutOfMemoryError)
-    return _ops
+    with _ops_lock:
+        if _ops is None:
+            from . import load, load_binding
+            lib = load()
+            ops = load_binding()
+            address = lambda f: ctypes.cast(f, ctypes.c_void_p).value
+            ops.bind(address(lib.tps_qk_norm_rope), address(lib.tps_kv_write), address(lib.tps_kv_read),
+                     address(lib.tps_prefix_attention), _fail, torch.OutOfMemoryError)
+            _ops = ops
+        return _ops
 
 
 def _fail(rc, name):

@@ -1,6 +1,11 @@
 """The decode-step entry points reject bad arguments before anything reaches the GPU, in the C ABI and
 in the binding."""
 import ctypes
+import os
+import subprocess
+import sys
+import threading
+import time
 
 import pytest
 import torch
@@ -107,3 +112,46 @@ def test_binding_refuses_tensors_that_are_not_on_a_gpu():
         tps.KVCache.empty(2, 2, 16, 64, "int4")
     with pytest.raises(ValueError):
         tps.prefix_attention(x.bfloat16(), None, None, 0, None, None)
+
+
+def test_first_use_from_two_threads_finds_the_module_bound(monkeypatch):
+    """The native module's entry points are null until `bind` has run: no thread may get hold of it before."""
+    class Slow:
+        def __init__(self):
+            self.bound = False
+
+        def bind(self, *args):
+            time.sleep(0.05)
+            self.bound = True
+    made = []
+
+    def load_binding():
+        made.append(Slow())
+        return made[-1]
+    monkeypatch.setattr(tps, "load_binding", load_binding)
+    monkeypatch.setattr(decode, "_ops", None)
+    seen = []
+
+    def use():
+        ops = decode._ops or decode._torch_ops()  # as every call begins
+        seen.append(ops.bound)
+    threads = [threading.Thread(target=use) for _ in range(8)]
+    for t in threads:
+        t.start()
+        time.sleep(0.01)
+    for t in threads:
+        t.join()
+    assert seen == [True] * 8 and len(made) == 1
+
+
+def test_the_native_module_refuses_calls_before_it_is_bound():
+    code = ("import nucleus_token_sampler_gb300 as tps\n"
+            "ops = tps.load_binding()\n"
+            "for f in (ops.norm, ops.write, ops.read, ops.attention):\n"
+            "    try:\n"
+            "        f()\n"
+            "    except RuntimeError as e:\n"
+            "        assert 'bound' in str(e), e\n"
+            "    else:\n"
+            "        raise AssertionError('not refused')\n")
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
