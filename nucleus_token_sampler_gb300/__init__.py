@@ -87,39 +87,46 @@ def _binding_command(out):
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile ``libtps.so`` for sm_103a with nvcc (the translation units in parallel, then one link) and,
     beside them, the native part of the tensor binding."""
-    lib, binding = force or _stale(), force or _binding_stale()
+    return _build(force or _stale(), force or _binding_stale(), verbose)
+
+
+def _build(lib: bool, binding: bool, verbose: bool = False) -> str:
     if not (lib or binding):
         return _LIB
     objdir = os.path.join(_HERE, "_build", f"obj{os.getpid()}")
     os.makedirs(objdir, exist_ok=True)
-    objs, procs = [], []
-    made = os.path.join(objdir, "binding.so")
-    if binding:
-        procs.append(("tps_torch.cpp", subprocess.Popen(_binding_command(made))))
-    for f in _SOURCES if lib else []:
-        o = os.path.join(objdir, f.replace(".cu", ".o"))
-        cmd = _NVCC + (["-Xptxas=-v"] if verbose else []) + ["-c", "-o", o, os.path.join(_CSRC, f)]
-        procs.append((f, subprocess.Popen(cmd)))
-        objs.append(o)
-    failed = [f for f, p in procs if p.wait() != 0]
+    try:
+        made, objs, procs, failed = os.path.join(objdir, "binding.so"), [], [], []
+
+        def start(name, cmd):
+            try:
+                procs.append((name, subprocess.Popen(cmd)))
+            except OSError:
+                failed.append(name)
+        if binding:
+            start("tps_torch.cpp", _binding_command(made))
+        for f in _SOURCES if lib else []:
+            o = os.path.join(objdir, f.replace(".cu", ".o"))
+            start(f, _NVCC + (["-Xptxas=-v"] if verbose else []) + ["-c", "-o", o, os.path.join(_CSRC, f)])
+            objs.append(o)
+        failed += [f for f, p in procs if p.wait() != 0]
+        if lib and not any(f in _SOURCES for f in failed):
+            tmp = _LIB + f".tmp{os.getpid()}"
+            subprocess.run(_NVCC + ["-shared", "-o", tmp] + objs, check=True)
+            os.replace(tmp, _LIB)
+        if binding and "tps_torch.cpp" not in failed:
+            os.replace(made, _BINDING)
+    finally:
+        shutil.rmtree(objdir)
     if failed:
         raise RuntimeError(f"compilation failed: {', '.join(failed)}")
-    if lib:
-        tmp = _LIB + f".tmp{os.getpid()}"
-        subprocess.run(_NVCC + ["-shared", "-o", tmp] + objs, check=True)
-        os.replace(tmp, _LIB)
-    if binding:
-        os.replace(made, _BINDING)
-    for o in objs:
-        os.remove(o)
-    os.rmdir(objdir)
     return _LIB
 
 
 def load_binding():
     """The native part of the tensor binding (built first if it is missing or older than its sources)."""
     with _lock:
-        build()
+        _build(False, _binding_stale())
         loader = importlib.machinery.ExtensionFileLoader("_tps_torch", _BINDING)
         spec = importlib.util.spec_from_loader("_tps_torch", loader)
         module = importlib.util.module_from_spec(spec)
@@ -128,11 +135,12 @@ def load_binding():
 
 
 def load():
-    """Load the CUDA library (building it first if it is missing or older than its sources)."""
+    """Load the CUDA library (building it first if it is missing or older than its sources).  The sampling
+    calls need nothing else: the tensor module's compiler and headers are asked for by load_binding alone."""
     global _lib
     with _lock:
         if _lib is None:
-            build()
+            _build(_stale(), False)
             lib = ctypes.CDLL(_LIB)
             P, I64, I32, U64 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_uint64
             lib.tps_sample.restype = I32

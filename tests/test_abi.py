@@ -228,3 +228,20 @@ def test_stall_test_hook_checks_its_wait_limit():
     assert call(0) == 1 and call(10**9 + 1) == 1
     assert call(1000, dtype=9) == 2          # then the sampling call's checks
     assert call(1000, B=0) == 0
+
+
+def test_the_sampler_loads_without_the_tensor_module(monkeypatch):
+    """The tensor module needs g++, Python's headers and the installed PyTorch's; the sampling calls do not."""
+    monkeypatch.setattr(tps, "_lib", None)
+    monkeypatch.setattr(tps, "_binding_stale", lambda: True)
+    monkeypatch.setattr(tps, "_binding_command", lambda out: ["false"])
+    assert tps.load().tps_version() == 100
+    with pytest.raises(RuntimeError):
+        tps.load_binding()
+    with pytest.raises(RuntimeError):
+        tps.build()
+    monkeypatch.setattr(tps, "_binding_command", lambda out: ["/no/such/compiler"])
+    monkeypatch.setattr(tps, "_lib", None)
+    assert tps.load().tps_version() == 100
+    with pytest.raises(RuntimeError):
+        tps.load_binding()
