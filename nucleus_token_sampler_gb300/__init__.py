@@ -45,8 +45,8 @@ ROW_STATUS = {0: "ok", 1: "nan", 2: "all_masked", 3: "bad_param", 4: "timeout"}
 _ERRORS = {1: "invalid argument", 2: "unknown dtype", 3: "vocabulary too large", 4: "misaligned pointer",
            5: "CUDA runtime error", 6: "more scratch than the fixed array of tps_sample_noalloc holds, or than the workspace given"}
 
-# The native part of the tensor binding: a CPython module compiled against the installed PyTorch.
-_BINDING = os.path.join(_HERE, "_tps_torch.so")
+# The native part of the tensor binding: a CPython module compiled against the installed PyTorch, for this interpreter.
+_BINDING = os.path.join(_HERE, "_tps_torch" + importlib.machinery.EXTENSION_SUFFIXES[0])
 _BINDING_SOURCE = os.path.join(_CSRC, "tps_torch.cpp")
 
 _lock = threading.Lock()

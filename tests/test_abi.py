@@ -245,3 +245,10 @@ def test_the_sampler_loads_without_the_tensor_module(monkeypatch):
     assert tps.load().tps_version() == 100
     with pytest.raises(RuntimeError):
         tps.load_binding()
+
+
+def test_the_tensor_module_is_named_for_its_interpreter():
+    """Another Python sharing the directory must not load a module built for this one."""
+    import importlib.machinery
+    assert tps._BINDING.endswith("/_tps_torch" + importlib.machinery.EXTENSION_SUFFIXES[0])
+    assert "cpython" in os.path.basename(tps._BINDING)
