@@ -402,7 +402,8 @@ int tps_kv_read(const tps_kv_cache* cache, const int64_t* slots, int64_t T, void
  *   scale        of the products q.k.
  *   out_status   [B] int32 or NULL: TPS_ROW_BAD_PARAM where a page of a token that is seen lies
  *                outside [0, n_pages) or suffix_len outside [0, table_width * page_size], else TPS_ROW_OK.
- *                The outputs of queries that such a page or length concerns are NaN.
+ *                The outputs of queries that such a page or length concerns are NaN.  TPS_ROW_TIMEOUT where a
+ *                wait ran out (one second) for any head of the sequence: its outputs are NaN.
  *   workspace    device memory of tps_prefix_attention_workspace bytes, 256-byte aligned, or NULL: taken
  *                from the library's stream-ordered pool and returned on the call's stream.
  */
@@ -435,6 +436,16 @@ typedef struct {
  * Returns TPS_ERR_ARG / _ALIGN / _SCRATCH (workspace too small) / _CUDA.
  */
 int tps_prefix_attention(const tps_kv_cache* cache, const tps_attention* args, void* stream);
+
+/*
+ * tps_prefix_attention_stall_test -- a test hook for the bounded waits (not for production use).  As
+ * tps_prefix_attention, except that no key or value of key head `stall_head` (-1: none) is ever fetched, and every
+ * wait for data or for a hand-over gives up after `wait_ns` nanoseconds (1 .. 10^9) instead of one second.
+ * The waits for copies already in flight keep their full limit.  The stalled head's outputs are NaN and the sequences'
+ * status TPS_ROW_TIMEOUT; the call returns and the context stays usable.
+ */
+int tps_prefix_attention_stall_test(const tps_kv_cache* cache, const tps_attention* args, int stall_head,
+                                    uint64_t wait_ns, void* stream);
 
 /* Bytes of workspace tps_prefix_attention needs for these arguments on the current device (pointers
  * are not looked at), or -1 for arguments it would reject.  Host-only query. */

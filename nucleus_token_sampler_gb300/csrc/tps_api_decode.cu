@@ -190,6 +190,13 @@ int64_t tps_prefix_attention_workspace(const tps_kv_cache* cache, const tps_atte
 
 int tps_prefix_attention(const tps_kv_cache* cache, const tps_attention* args, void* stream)
 {
+    return tps_prefix_attention_stall_test(cache, args, -1, tps::kAttnWaitNs, stream);
+}
+
+int tps_prefix_attention_stall_test(const tps_kv_cache* cache, const tps_attention* args, int stall_head, uint64_t wait_ns,
+                                    void* stream)
+{
+    if (wait_ns < 1 || wait_ns > tps::kAttnWaitNs) return TPS_ERR_ARG;
     int rc = check_attention(cache, args, true);
     if (rc != TPS_OK) return rc;
     if (args->B == 0) return TPS_OK;
@@ -200,6 +207,8 @@ int tps_prefix_attention(const tps_kv_cache* cache, const tps_attention* args, v
     if (rc != TPS_OK) return rc;
     a.c = *cache;
     a.a = *args;
+    a.stall_head = stall_head;
+    a.wait_ns = wait_ns;
     a.G = args->n_q_heads / cache->n_heads;
     a.page_shift = 4;
     while ((1 << a.page_shift) < cache->page_size) ++a.page_shift;
@@ -221,7 +230,8 @@ int tps_prefix_attention(const tps_kv_cache* cache, const tps_attention* args, v
     a.ml = reinterpret_cast<float2*>(ws + a.p.off_ml);
     a.line_part = reinterpret_cast<float*>(ws + a.p.off_line_part);
     a.line_ml = reinterpret_cast<float2*>(ws + a.p.off_line_ml);
-    if (a.p.units) {
+    if (args->out_status) e = cudaMemsetAsync(args->out_status, 0, (size_t)args->B * sizeof(int32_t), st);  // the joins raise it
+    if (e == cudaSuccess && a.p.units) {
         e = cache->format == TPS_KV_BF16  ? tps::launch_attn_prefix_bf16(a, st)
             : cache->format == TPS_KV_FP8 ? tps::launch_attn_prefix_fp8(a, st)
                                           : tps::launch_attn_prefix_int8(a, st);

@@ -195,14 +195,14 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     volatile int* abort_flag = &ctl.abort;
-    // Wait for a phase; false once any role has given up (this one after kAttnWaitNs).
+    // Wait for a phase; false once any role has given up (this one after a.wait_ns).
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         if (mbar_try_wait(bar, parity)) return true;
         const uint64_t t0 = globaltimer_ns();
         for (;;) {
             if (mbar_try_wait(bar, parity, 20000u)) return true;  // suspended, not spinning
             if (*abort_flag) return false;
-            if (globaltimer_ns() - t0 > kAttnWaitNs) {
+            if (globaltimer_ns() - t0 > a.wait_ns) {
                 *abort_flag = 1;
                 return false;
             }
@@ -545,7 +545,7 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
         int page = page_of(way.block * kBlockKeys + lane * box);
         Turn<kSlots> turn(1);  // a slot's first fill waits for nothing: the phase before its first
         int fills = 0;
-        while (way.left > 0 && alive) {
+        while (way.left > 0 && alive && way.head != a.stall_head) {
             const int head = way.head, token = way.block * kBlockKeys, left = prefix - token;
             const int live = min(boxes, (left + box - 1) / box);
             const int row = (token + lane * box) & (a.c.page_size - 1);

@@ -36,7 +36,6 @@ constexpr int kRowsThreads = 128;
 constexpr int kRowsWarps = kRowsThreads / 32;
 constexpr float kSlack = 8.f;  // base-2 units a score may exceed the reference by
 constexpr float kLift = 7.f;   // float16 weights are lifted by 2^7: at most 2^15
-constexpr uint64_t kAttnWaitNs = 1000000000ull;  // every wait's limit
 constexpr float kPieceBadPage = -1.f, kPieceTimeout = -2.f;  // a piece's sum where it is no sum
 
 __device__ __forceinline__ float exp2_fast(float x)
@@ -220,8 +219,8 @@ template <int D, int kFormat> struct RowsShared {
 // of one head's tokens in order.
 template <int D, int kFormat> struct Walk {
     using C = Chunk<D, kFormat>;
-    const tps_kv_cache& c;
-    int shift, head;
+    const AttnArgs& a;
+    int head;
     unsigned char* ring;
     uint64_t* full;
     const int32_t* pages;
@@ -235,25 +234,27 @@ template <int D, int kFormat> struct Walk {
     __device__ __forceinline__ void look(const int32_t* pages_, int first_, int64_t tokens)
     {
         pages = pages_;
-        page = first_ < tokens ? pages[first_ >> shift] : 0;
+        page = first_ < tokens ? pages[first_ >> a.page_shift] : 0;
     }
     // Ask for the next chunk: one lane for each of its copies.
     __device__ __forceinline__ void request()
     {
-        const int lane = threadIdx.x & 31, stage = (int)(fills % C::kStages);
+        const int lane = threadIdx.x & 31, stage = (int)(fills % C::kStages), shift = a.page_shift;
+        const tps_kv_cache& c = a.c;
         int id = page;
         if (id < 0 || id >= c.n_pages) fault = 1, id = 0;
         const int64_t row = (((int64_t)id * c.n_heads + head) << shift) + (ahead & ((1 << shift) - 1));
         ahead += step;
         if (ahead < last) page = pages[ahead >> shift];
         unsigned char* dst = ring + stage * C::kBytes;
+        ++fills;
+        if (head == a.stall_head) return;
         if (lane == 0) mbar_arrive_expect_tx(&full[stage], C::kBytes);
         __syncwarp();
         if (lane == 0) bulk_g2s(dst, static_cast<const char*>(c.k) + row * C::kRowBytes, 16 * C::kRowBytes, &full[stage]);
         if (lane == 1) bulk_g2s(dst + C::kValues, static_cast<const char*>(c.v) + row * C::kRowBytes, 16 * C::kRowBytes, &full[stage]);
         if (C::k8 && lane == 2) bulk_g2s(dst + C::kKeyScales, static_cast<const char*>(c.k_scale) + row * 2, 32, &full[stage]);
         if (C::k8 && lane == 3) bulk_g2s(dst + C::kValueScales, static_cast<const char*>(c.v_scale) + row * 2, 32, &full[stage]);
-        ++fills;
     }
     // Begin, after look(): the first chunks are on their way when this returns (the ring holds nothing still used).
     __device__ __forceinline__ void start(int first_, int step_, int last_)
@@ -287,8 +288,8 @@ __device__ __forceinline__ int attend(RowState<D, N>& st, Walk<D, kFormat>& walk
     uint32_t at = walk.fills - min(chunks, (uint32_t)C::kStages);  // the fill that is used next
     for (int t0 = walk.first; t0 < last; t0 += walk.step, ++at) {
         const int stage = (int)(at % C::kStages);
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&walk.full[stage], (at / C::kStages) & 1, kAttnWaitNs))) {
-            for (; at != walk.fills; ++at)  // what is on the way lands before the warp goes on (bounded again)
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&walk.full[stage], (at / C::kStages) & 1, walk.a.wait_ns))) {
+            for (; at != walk.fills && walk.head != walk.a.stall_head; ++at)  // what is on the way lands before the warp goes on (bounded again)
                 mbar_wait_bounded(&walk.full[at % C::kStages], (at / C::kStages) & 1, kAttnWaitNs);
             return 2;
         }
@@ -750,6 +751,14 @@ struct PrefixPieces {
     }
 };
 
+// A sequence's status, cleared ahead of the call's first kernel: the worst of what its heads and row tiles met
+// (state 1: a bad page or length, 2: a wait that ran out, which concerns one CTA and so maybe a single head).
+static_assert(TPS_ROW_TIMEOUT > TPS_ROW_BAD_PARAM && TPS_ROW_BAD_PARAM > TPS_ROW_OK && TPS_ROW_OK == 0, "the worst is the largest");
+__device__ __forceinline__ void report_row(const AttnArgs& a, int64_t b, int state)
+{
+    if (a.a.out_status) atomicMax(&a.a.out_status[b], state == 2 ? TPS_ROW_TIMEOUT : TPS_ROW_BAD_PARAM);
+}
+
 template <int kFormat>
 __device__ __forceinline__ float log_sum(float top, float l, bool bad)
 {
@@ -796,7 +805,7 @@ __global__ void __launch_bounds__(kRowsThreads, N == 1 ? 4 : 3) attn_suffix_kern
     const bool own_prefix = !p.shared && a.a.prefix_len;
     const int32_t* own_pages = a.a.page_table + b * a.a.table_ld;
     const int64_t capacity = a.a.table_width << a.page_shift;
-    Walk<D, kFormat> walk{a.c, a.page_shift, head, sm.ring[warp], sm.full[warp]};
+    Walk<D, kFormat> walk{a, head, sm.ring[warp], sm.full[warp]};
     walk.look(own_prefix ? a.a.prefix_pages : own_pages, first, own_prefix ? a.a.prefix_len : capacity);
     RowState<D, N> st;
     load_query<D, kFormat, N>(st, rows, [&](int r) { return static_cast<const __nv_bfloat16*>(a.a.q) + out_row(r) * D; });
@@ -887,8 +896,7 @@ __global__ void __launch_bounds__(kRowsThreads, N == 1 ? 4 : 3) attn_suffix_kern
             }
         any_bad = __any_sync(0xFFFFFFFFu, any_bad);
         any_late = __any_sync(0xFFFFFFFFu, any_late);
-        if (lane == 0 && head == 0 && tile == p.suffix_tiles - 1 && a.a.out_status)
-            a.a.out_status[b] = any_late ? TPS_ROW_TIMEOUT : (any_bad ? TPS_ROW_BAD_PARAM : TPS_ROW_OK);
+        if (lane == 0 && any_bad) report_row(a, b, any_late ? 2 : 1);
     } else {
         store_rows<D, kFormat, N>(sm, st, rows);
         if (lane == 0 && (fault || !fits)) atomicMax(&sm.bad, max(fault, 1));
@@ -963,8 +971,7 @@ __global__ void __launch_bounds__(kRowsThreads, N == 1 ? 4 : 3) attn_suffix_kern
             asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(acc[k].w * inv), "f"(acc[k].z * inv));
             *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.a.out) + orow * D + col * 4) = w;
             if (col == 0 && a.a.out_lse) a.a.out_lse[orow] = log_sum<kFormat>(js.top[r], js.l[r], state != 0);
-            if (i == 0 && rank == 0 && head == 0 && tile == p.suffix_tiles - 1 && a.a.out_status)
-                a.a.out_status[b] = state == 2 ? TPS_ROW_TIMEOUT : (state ? TPS_ROW_BAD_PARAM : TPS_ROW_OK);
+            if (col == 0 && state) report_row(a, b, state);
         }
         if (ncl > 1) {  // no CTA may leave while others read its shared memory
             cluster_arrive();
@@ -1049,7 +1056,7 @@ __global__ void __launch_bounds__(kRowsThreads, N == 1 ? 4 : 3) attn_line_kernel
     const int64_t* before = sums.before;
     const int64_t total = before[kLineMax] * heads;
 
-    Walk<D, kFormat> walk{a.c, a.page_shift, 0, sm.ring[warp], sm.full[warp]};
+    Walk<D, kFormat> walk{a, 0, sm.ring[warp], sm.full[warp]};
     const int64_t share = (total + p.line_ctas - 1) / p.line_ctas, u0 = blockIdx.x * share, u1 = min(u0 + share, total);
     bool gave_up = false;
     for (int64_t u = u0; u < u1;) {
@@ -1165,8 +1172,7 @@ __global__ void __launch_bounds__(kRowsThreads) attn_join_kernel(const AttnArgs 
         asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(acc[k].w * inv), "f"(acc[k].z * inv));
         *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.a.out) + orow * D + col * 4) = w;
         if (col == 0 && a.a.out_lse) a.a.out_lse[orow] = log_sum<kFormat>(js.top[r], js.l[r], state != 0);
-        if (i == 0 && col == 0 && head == 0 && tile == p.suffix_tiles - 1 && a.a.out_status)
-            a.a.out_status[b] = state == 2 ? TPS_ROW_TIMEOUT : (state ? TPS_ROW_BAD_PARAM : TPS_ROW_OK);
+        if (col == 0 && state) report_row(a, b, state);
     }
 }
 

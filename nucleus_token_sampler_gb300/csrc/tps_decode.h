@@ -70,7 +70,10 @@ struct AttnArgs {
     float2* ml;      // [pieces, tile_rows]: maximum in base-2 units, sum (negative: a bad page id)
     float* line_part;
     float2* line_ml;
+    int stall_head;    // of tps_prefix_attention_stall_test, else -1
+    uint64_t wait_ns;  // limit of every wait for data or for another role (copies in flight: kAttnWaitNs)
 };
+constexpr uint64_t kAttnWaitNs = 1000000000ull;
 
 // The shared part, then the own tokens and the join.
 cudaError_t launch_attn_prefix_bf16(const AttnArgs& a, cudaStream_t stream);

@@ -45,6 +45,8 @@ def declare(lib):
     lib.tps_kv_read.argtypes = [_P, _P, _I64, _P, _P, ctypes.c_int, _P]
     lib.tps_prefix_attention.restype = ctypes.c_int
     lib.tps_prefix_attention.argtypes = [_P, _P, _P]
+    lib.tps_prefix_attention_stall_test.restype = ctypes.c_int
+    lib.tps_prefix_attention_stall_test.argtypes = [_P, _P, ctypes.c_int, ctypes.c_uint64, _P]
     lib.tps_prefix_attention_workspace.restype = _I64
     lib.tps_prefix_attention_workspace.argtypes = [_P, _P]
 
@@ -205,7 +207,8 @@ def prefix_attention(q, cache: KVCache, prefix_pages, prefix_len: int, page_tabl
     ``suffix_len - Tq + 1 + t`` own tokens.  ``scale``: of q.k, by default D ** -0.5.  Returns the
     bfloat16 output of q's shape, or (output, log-sum-exp) with ``want_lse`` (float32, q's shape without
     D).  A query that sees no token yields 0 and -inf.  ``status``: an int32 [B] tensor that gets 3 for a
-    sequence with a page outside the cache or a length outside its table (its outputs are NaN), else 0.
+    sequence with a page outside the cache or a length outside its table (its outputs are NaN), 4 where a
+    wait on the GPU ran out for any of its heads (their outputs are NaN), else 0.
     ``workspace``: a uint8 tensor of at least ``prefix_attention_workspace(...)`` bytes to use instead of
     the library's memory pool."""
     c = _cache(cache)

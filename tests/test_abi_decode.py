@@ -155,3 +155,10 @@ def test_the_native_module_refuses_calls_before_it_is_bound():
             "    else:\n"
             "        raise AssertionError('not refused')\n")
     subprocess.run([sys.executable, "-c", code], check=True, cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+
+
+def test_stall_test_hook_of_the_attention_checks_its_wait_limit():
+    lib = tps.load()
+    a = decode._Attention(B=0, q_len=1, n_q_heads=4, scale=1.0)
+    for wait, rc in ((0, 1), (10 ** 9 + 1, 1), (1, 0), (10 ** 9, 0)):
+        assert lib.tps_prefix_attention_stall_test(ctypes.byref(cache()), ctypes.byref(a), 0, wait, None) == rc

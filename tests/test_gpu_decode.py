@@ -11,6 +11,7 @@ Tolerances.  A bfloat16 result is off by at most half a unit, 2^-8 of its magnit
    sum p |v|; the scores' float32 sums are off by at most 2^-18 of the largest sum of |products|, and base-2
    exponentials, the joins of parts and weights below 2^-31 of the largest by less than 2^-14.
 """
+import ctypes
 import math
 
 import pytest
@@ -464,3 +465,34 @@ def test_attention_short_prefixes_with_several_items_a_cta(fmt, B, Tq, Hq, Hkv, 
         assert (st == 0).all() and torch.isfinite(out).all() and torch.isfinite(lse).all()
     some = torch.cat([torch.arange(8), torch.arange(B // 2 - 4, B // 2 + 4), torch.arange(B - 8, B)]).to(DEV)
     _check_attention((out[some], lse[some]), q[some], plain.values(c), pp, prefix, table[some], n[some], D ** -0.5, fmt)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "int8"])
+@pytest.mark.parametrize("B,Tq,Hq,Hkv,D,prefix,lens", [
+    (40, 1, 24, 3, 128, 1500, [30, 7]),    # the prefix shared, a cluster or a CTA for each sequence
+    (40, 1, 24, 3, 64, 0, [30, 700]),      # one launch
+    (3, 1, 24, 3, 128, 300, [0, 20]),      # one launch, the prefix walked over by each sequence
+    (20, 5, 24, 3, 64, 2000, [4500, 20]),  # the own tokens cut evenly, three row tiles
+    (900, 1, 6, 3, 64, 400, [5, 20])])     # a warp for each sequence
+def test_attention_status_tells_of_a_wait_that_ran_out_in_any_head(fmt, B, Tq, Hq, Hkv, D, prefix, lens):
+    """One head's keys and values never arrive: its outputs are NaN, and the status says so whichever head it is."""
+    c, q, pp, table, n = _case(_gen(79), B, Tq, Hq, Hkv, D, prefix, lens, 16, fmt)
+    want = tps.prefix_attention(q, c, pp, prefix, table, n)
+    lib, G = tps.load(), Hq // Hkv
+    size = tps.prefix_attention_workspace(q.shape, c, prefix, table.shape[1])
+    ws = torch.zeros(max(size, 1), dtype=torch.uint8, device=DEV)
+    for head in range(Hkv):
+        out, lse = torch.empty_like(q), torch.empty(q.shape[:3], device=DEV)
+        st = torch.full((B,), 9, dtype=torch.int32, device=DEV)
+        a = tps.decode._Attention(q.data_ptr(), out.data_ptr(), lse.data_ptr(), pp.data_ptr(), table.data_ptr(), n.data_ptr(),
+                                  st.data_ptr(), ws.data_ptr(), size, B, prefix, table.shape[1], table.shape[1], Tq, Hq, D ** -0.5)
+        assert lib.tps_prefix_attention_stall_test(c._bytes, ctypes.byref(a), head, 2_000_000,
+                                                   torch.cuda.current_stream().cuda_stream) == 0
+        torch.cuda.synchronize()
+        assert (st == 4).all(), (head, st.tolist())
+        mine = out[:, :, head * G:(head + 1) * G]
+        assert mine.isnan().all() and lse[:, :, head * G:(head + 1) * G].isnan().all()
+        good = ~out.isnan().any(-1)
+        assert torch.equal(out[good], want[good])
+    again = tps.prefix_attention(q, c, pp, prefix, table, n, status=st)
+    assert (st == 0).all() and torch.equal(again, want)
