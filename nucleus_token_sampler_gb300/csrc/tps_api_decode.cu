@@ -13,6 +13,9 @@
 namespace {
 
 constexpr int kMaxHeads = 65535;
+// Tokens of a prefix or of a sequence's pages: the walks over them count in 32 bits and go on by at most 512 past the
+// last one, a tile's boxes by 4,096.
+constexpr int64_t kMaxTokens = (int64_t(1) << 31) - (1 << 16);
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 int elem_bytes(int dtype) { return dtype == TPS_F32 ? 4 : (dtype == TPS_BF16 ? 2 : 0); }
@@ -103,7 +106,7 @@ int check_attention(const tps_kv_cache* c, const tps_attention* a, bool pointers
     const int rc = check_cache(c, pointers);
     if (rc != TPS_OK) return rc;
     if (c->head_dim != 64 && c->head_dim != 128) return TPS_ERR_ARG;
-    if (a->B < 0 || a->prefix_len < 0 || a->prefix_len > INT32_MAX || a->table_width < 0 || a->table_width > INT32_MAX ||
+    if (a->B < 0 || a->prefix_len < 0 || a->prefix_len > kMaxTokens || a->table_width < 0 || a->table_width > kMaxTokens / c->page_size ||
         a->table_ld < a->table_width || a->q_len < 1 || a->n_q_heads < 1 || a->n_q_heads % c->n_heads != 0 ||
         !std::isfinite(a->scale))
         return TPS_ERR_ARG;

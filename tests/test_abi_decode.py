@@ -162,3 +162,19 @@ def test_stall_test_hook_of_the_attention_checks_its_wait_limit():
     a = decode._Attention(B=0, q_len=1, n_q_heads=4, scale=1.0)
     for wait, rc in ((0, 1), (10 ** 9 + 1, 1), (1, 0), (10 ** 9, 0)):
         assert lib.tps_prefix_attention_stall_test(ctypes.byref(cache()), ctypes.byref(a), 0, wait, None) == rc
+
+
+@pytest.mark.parametrize("page", [16, 256])
+def test_attention_refuses_lengths_whose_token_numbers_would_pass_32_bits(page):
+    """A walk counts tokens in 32 bits and goes on by up to 512 past the last one."""
+    most, c = 2 ** 31 - 2 ** 16, cache(page_size=page)
+    lib, wide = tps.load(), most // page
+
+    def size(**kw):
+        a = dict(B=1, prefix_len=40, table_width=2, table_ld=2, q_len=1, n_q_heads=2, scale=1.0)
+        a.update(kw)
+        return lib.tps_prefix_attention_workspace(ctypes.byref(c), ctypes.byref(decode._Attention(**a)))
+    for kw in (dict(prefix_len=most + 1), dict(prefix_len=2 ** 31 - 1), dict(table_width=wide + 1, table_ld=wide + 1),
+               dict(table_width=2 ** 31 - 1, table_ld=2 ** 31 - 1)):
+        assert attention(c=c, **kw) == 1 and size(**kw) == -1
+    assert attention(c=c, B=0, prefix_len=most, table_width=wide, table_ld=wide) == 0
