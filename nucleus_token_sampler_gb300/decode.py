@@ -120,7 +120,8 @@ class KVCache:
     """A paged key/value cache of one layer: ``k`` and ``v`` [pages, heads, page_size, head_dim], of
     bfloat16 values or of 8-bit codes (float8_e4m3fn, int8) with one bfloat16 scale per (token, head) in
     ``k_scale`` and ``v_scale`` [pages, heads, page_size].  Token slot s lives in page s // page_size at
-    row s % page_size.  The tensors belong to the caller; ``KVCache.empty`` makes new ones."""
+    row s % page_size.  The tensors belong to the caller; ``KVCache.empty`` makes new ones.  A cache keeps the
+    tensors it was made with (the calls hold their addresses): for others make another cache."""
 
     FORMATS = {"bf16": (0, torch.bfloat16), "fp8": (1, torch.float8_e4m3fn), "int8": (2, torch.int8)}
 
@@ -146,12 +147,17 @@ class KVCache:
                     raise ValueError(f"{name}: a bfloat16 cache has no scales")
             else:
                 _dense(t, name, (pages, heads, page), torch.bfloat16, dev)
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self._k, self._v, self._k_scale, self._v_scale = k, v, k_scale, v_scale
         self.n_pages, self.n_heads, self.page_size, self.head_dim = pages, heads, page, D
         self.device = k.device
         ptr = lambda t: None if t is None else t.data_ptr()
         self._index = dev.index
         self._bytes = bytes(_Cache(ptr(k), ptr(v), ptr(k_scale), ptr(v_scale), pages, heads, page, D, self.FORMATS[self.format][0]))
+
+    k = property(lambda self: self._k)
+    v = property(lambda self: self._v)
+    k_scale = property(lambda self: self._k_scale)
+    v_scale = property(lambda self: self._v_scale)
 
     @classmethod
     def empty(cls, n_pages: int, n_heads: int, page_size: int, head_dim: int, format: str = "fp8", device="cuda"):

@@ -178,3 +178,11 @@ def test_attention_refuses_lengths_whose_token_numbers_would_pass_32_bits(page):
                dict(table_width=2 ** 31 - 1, table_ld=2 ** 31 - 1)):
         assert attention(c=c, **kw) == 1 and size(**kw) == -1
     assert attention(c=c, B=0, prefix_len=most, table_width=wide, table_ld=wide) == 0
+
+
+@pytest.mark.parametrize("name", ["k", "v", "k_scale", "v_scale"])
+def test_a_cache_keeps_the_tensors_it_was_made_with(name):
+    """The calls go to the addresses these tensors had: another tensor in their place would leave freed memory written to."""
+    c = tps.KVCache.__new__(tps.KVCache)
+    with pytest.raises(AttributeError):
+        setattr(c, name, torch.zeros(1))
