@@ -11,13 +11,21 @@ constexpr int kNormResident = 1024;  // threads of an SM that the launch fills
 
 bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
+void launch_kernel(void (*kernel)(tps_norm_rope), const tps_norm_rope& a, unsigned grid, int threads, cudaStream_t stream)
+{
+    kernel<<<grid, threads, 0, stream>>>(a);
+}
+
 template <typename T, int L, int kWalks>
 cudaError_t launch_walks(const tps_norm_rope& a, unsigned grid, int threads, cudaStream_t stream)
 {
+    const bool whole = a.rot_dim == a.head_dim;
     if (a.interleaved)
-        norm_rope_kernel<T, L, true, kWalks><<<grid, threads, 0, stream>>>(a);
+        whole ? launch_kernel(norm_rope_kernel<T, L, true, true, kWalks>, a, grid, threads, stream)
+              : launch_kernel(norm_rope_kernel<T, L, true, false, kWalks>, a, grid, threads, stream);
     else
-        norm_rope_kernel<T, L, false, kWalks><<<grid, threads, 0, stream>>>(a);
+        whole ? launch_kernel(norm_rope_kernel<T, L, false, true, kWalks>, a, grid, threads, stream)
+              : launch_kernel(norm_rope_kernel<T, L, false, false, kWalks>, a, grid, threads, stream);
     return cudaGetLastError();
 }
 

@@ -63,14 +63,15 @@ __device__ __forceinline__ void load_floats(const float* p, float (&x)[N])
     }
 }
 
-template <typename T, int L, bool kInterleaved, int kWalks>
+// kWhole: every component turns (rot = D), which saves the question 2% at 16,383 tokens (66.1 / 67.4 us).
+template <typename T, int L, bool kInterleaved, bool kWhole, int kWalks>
 __global__ void __launch_bounds__(kNormMaxThreads) norm_rope_kernel(const tps_norm_rope a)
 {
     constexpr int N = Pack<T>::kN;
     const int u = threadIdx.x % L, groups = blockDim.x / L, group = threadIdx.x / L;
     const int rot = a.rot_dim, half = rot / 2, D = a.head_dim;
     const int units = D / (2 * N), turning = rot / (2 * N);
-    const bool live = u < units, turn = u < turning;
+    const bool live = u < units, turn = kWhole || u < turning;
     int ia, ib;  // the unit's two vectors
     if (turn) {
         ia = kInterleaved ? u * 2 * N : u * N;
@@ -106,12 +107,12 @@ __global__ void __launch_bounds__(kNormMaxThreads) norm_rope_kernel(const tps_no
         // halves: element j of the two vectors turns by angle u N + j; adjacent: elements 2j, 2j + 1 of the
         // pair of vectors by angle u N + j.  Either way the unit uses angles [u N, u N + N).
         float c[N], s[N];
-        if (turn && known) {
+        if (turn && live && known) {
             load_floats<N>(a.cos_sin + (int64_t)pos * rot + u * N, c);
             load_floats<N>(a.cos_sin + (int64_t)pos * rot + half + u * N, s);
         } else {
 #pragma unroll
-            for (int j = 0; j < N; ++j) c[j] = known ? 1.f : nan, s[j] = known ? 0.f : nan;
+            for (int j = 0; j < N; ++j) c[j] = 1.f, s[j] = 0.f;
         }
         if (next_tok < a.T) pos = a.positions[next_tok];
         for (int h0 = 0; h0 < H; h0 += groups * kWalks) {
@@ -136,7 +137,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) norm_rope_kernel(const tps_no
 #pragma unroll
                 for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
                 if (!live || h >= H) continue;
-                const float r = rsqrtf(fmaf(ss, inv_d, a.eps));
+                const float r = known ? rsqrtf(fmaf(ss, inv_d, a.eps)) : nan;
                 const float* w = is_q ? a.q_weight : a.k_weight;
                 if (w) {
                     float wa[N], wb[N];
@@ -148,7 +149,9 @@ __global__ void __launch_bounds__(kNormMaxThreads) norm_rope_kernel(const tps_no
 #pragma unroll
                     for (int j = 0; j < N; ++j) x[j] *= r, y[j] *= r;
                 }
-                if (kInterleaved && turn) {
+                if (!turn) {
+                    // as they are: through a product with sine 0 an infinity would reach its partner as NaN
+                } else if (kInterleaved) {
 #pragma unroll
                     for (int j = 0; j < N; j += 2) {  // pairs inside each vector
                         const float x0 = x[j], y0 = y[j];
@@ -158,7 +161,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) norm_rope_kernel(const tps_no
                         y[j] = y0 * c[m] - y[j + 1] * s[m];
                         y[j + 1] = y[j + 1] * c[m] + y0 * s[m];
                     }
-                } else {  // components that do not turn have cosine 1 and sine 0
+                } else {
 #pragma unroll
                     for (int j = 0; j < N; ++j) {
                         const float x0 = x[j];

@@ -496,3 +496,20 @@ def test_attention_status_tells_of_a_wait_that_ran_out_in_any_head(fmt, B, Tq, H
         assert torch.equal(out[good], want[good])
     again = tps.prefix_attention(q, c, pp, prefix, table, n, status=st)
     assert (st == 0).all() and torch.equal(again, want)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D,R,interleaved", [(128, 64, False), (128, 64, True), (96, 32, False), (64, 0, False), (36, 8, True)])
+def test_norm_rope_components_that_do_not_turn_keep_to_themselves(dtype, D, R, interleaved):
+    """An infinity makes itself NaN and its head's other components 0, as the formula does; only pairs that turn mix."""
+    q = torch.randn(4, 2, D, device=DEV).to(dtype)
+    q[1, 0, D - 3] = math.inf
+    q[2, 1, R] = -math.inf
+    w = torch.ones(D, device=DEV)
+    w[D - 1] = math.inf
+    pos, table = torch.arange(4, device=DEV).int(), _table(9, R)
+    for weight in (None, w):
+        got, _ = tps.qk_norm_rope(q, q, weight, weight, pos, table, interleaved=interleaved)
+        want = plain.norm_rope(q, weight, pos, table, 1e-6, interleaved)
+        assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got.isinf(), want.isinf())
+        assert (got[1:3][~got[1:3].isnan() & ~got[1:3].isinf()].abs() < 100).all()
