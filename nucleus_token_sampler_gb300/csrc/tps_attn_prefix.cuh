@@ -345,9 +345,10 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
                     for (int i = 1; i < 32; ++i) t = fmaxf(t, s[i]);
                     return t;
                 };
-                // Raise the references that need it: scale the sum, the output and the weights of chunks 0 .. done - 1.
-                auto raise = [&](float top, int done) {
-                    const float to = top > ref ? ceilf(top) : ref;
+                // Raise the reference of a row that needs it (the warp's others go along with factor 1, so that no row's
+                // bits depend on its neighbours): scale the sum, the output and the weights of chunks 0 .. done - 1.
+                auto raise = [&](bool need, float top, int done) {
+                    const float to = need && top > ref ? ceilf(top) : ref;
                     const float f = to == ref ? 1.f : exp2_fast(ref - to);
                     ref = to;
                     sum *= f;
@@ -420,8 +421,9 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
                     ready(sb, ch + 1);
                     float b = add - (ref == neg ? 0.f : ref) + (k8 ? kLift : 0.f);
                     float2 x = add2(weigh(sa, ch, b), weigh(sb, ch + 1, b));
-                    if (__any_sync(0xFFFFFFFFu, !(x.x + x.y <= kMost) || ref == neg)) {
-                        raise(fmaf(fmaxf(largest(sa), largest(sb)), c, add), ch);
+                    const bool need = !(x.x + x.y <= kMost) || ref == neg;
+                    if (__any_sync(0xFFFFFFFFu, need)) {
+                        raise(need, fmaf(fmaxf(largest(sa), largest(sb)), c, add), ch);
                         b = add - (ref == neg ? 0.f : ref) + (k8 ? kLift : 0.f);
                         tmem_wait_st();
                         x = add2(weigh(sa, ch, b), weigh(sb, ch + 1, b));

@@ -513,3 +513,16 @@ def test_norm_rope_components_that_do_not_turn_keep_to_themselves(dtype, D, R, i
         want = plain.norm_rope(q, weight, pos, table, 1e-6, interleaved)
         assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got.isinf(), want.isinf())
         assert (got[1:3][~got[1:3].isnan() & ~got[1:3].isinf()].abs() < 100).all()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "int8"])
+@pytest.mark.parametrize("B,G,prefix,lens", [(64, 4, 900, [10, 33]), (24, 1, 2000, [5]), (600, 4, 500, [3]), (3, 4, 200, [30])])
+def test_attention_has_the_same_bits_whatever_its_neighbours_are(fmt, B, G, prefix, lens):
+    """Every other sequence gets other queries: its neighbours, rows of the same warps and tiles, keep every bit."""
+    c, q, pp, table, n = _case(_gen(80), B, 1, 2 * G, 2, 128, prefix, lens, 32, fmt)
+    want, lse = tps.prefix_attention(q, c, pp, prefix, table, n, want_lse=True)
+    for factor in (30.0, 1000.0, 0.0):
+        q2 = q.clone()
+        q2[::2] = (q2[::2].float() * factor).bfloat16()
+        got, again = tps.prefix_attention(q2, c, pp, prefix, table, n, want_lse=True)
+        assert torch.equal(got[1::2], want[1::2]) and torch.equal(again[1::2], lse[1::2])
