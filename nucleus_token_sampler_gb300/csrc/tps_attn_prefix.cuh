@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
         uint32_t s_parity = 0, o_parity = 0;
         Turn<kScalars> scalar(0);
         const uint32_t sign = a.qk_scale < 0.f ? 0x80008000u : 0u;
-        const float unit = fmaxf(fabsf(a.qk_scale), 1e-30f);  // never 0: a masked score times it stays -inf
+        const float unit = fabsf(a.qk_scale);
         Way way(p);
         for (; way.left > 0 && alive; way.next(p)) {
             // The warp's 32 query rows, D / 8 lanes to a row: as they are (bf16) or brought into float16's range.
@@ -319,6 +319,7 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
                     inv = exp2_fast(-add);
                     scalar.next();
                 }
+                c = fmaxf(c, 0x1p-126f);  // never 0: a masked score, -inf, times it stays -inf (any other times that is nothing)
                 const int left = prefix - (way.block + v) * kBlockKeys;
                 float2 total = make_float2(0.f, 0.f);
                 // int8: a score's key scale (the codes are in the tile as they are).  Scores past the prefix become -inf.

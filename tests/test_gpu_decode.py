@@ -526,3 +526,24 @@ def test_attention_has_the_same_bits_whatever_its_neighbours_are(fmt, B, G, pref
         q2[::2] = (q2[::2].float() * factor).bfloat16()
         got, again = tps.prefix_attention(q2, c, pp, prefix, table, n, want_lse=True)
         assert torch.equal(got[1::2], want[1::2]) and torch.equal(again[1::2], lse[1::2])
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "int8"])
+@pytest.mark.parametrize("B", [2, 100])
+def test_attention_products_below_every_float(fmt, B):
+    """Queries near 2^-125 on keys with the smallest scale: the scores are 0, in blocks that end past the prefix too."""
+    c, q, pp, table, n = _case(_gen(81), B, 1, 4, 1, 64, 700, [30], 32, fmt)
+    c.k_scale[~c.k_scale.isnan()] = 2.0 ** -40
+    q[:] = (q.float().clamp(-3, 3) * 2.0 ** -126).bfloat16()
+    _check_attention(tps.prefix_attention(q, c, pp, 700, table, n, want_lse=True), q, plain.values(c), pp, 700, table, n, 0.125, fmt)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "int8"])
+@pytest.mark.parametrize("B", [2, 100])
+@pytest.mark.parametrize("scale,mag", [(0.0, 1.0), (0.0, 2.0 ** 104), (1e-36, 2.0 ** 100)])
+def test_attention_with_a_scale_of_nothing(fmt, B, scale, mag):
+    """All tokens weigh the same at scale 0, and nearly so where the products are as large as the scale is small."""
+    c, q, pp, table, n = _case(_gen(85), B, 1, 4, 1, 64, 700, [30], 32, fmt)
+    q[:] = (q.float() * mag).bfloat16()
+    _check_attention(tps.prefix_attention(q, c, pp, 700, table, n, want_lse=True, scale=scale), q, plain.values(c), pp, 700, table, n,
+                     scale, fmt)
