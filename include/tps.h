@@ -352,7 +352,8 @@ int tps_qk_norm_rope(const tps_norm_rope* args, void* stream);
  *         exact, and a stored value is exact in bfloat16.
  *   INT8  codes rint(x_i / s), s = a / 127 rounded up to bfloat16.
  * Both scales are at least 2^-40 and stored as bfloat16; a vector with a NaN or an infinity gets the
- * scale NaN and codes 0, so that it reads as NaN. */
+ * scale NaN and codes 0, so that it reads as NaN.  A caller's own codes may have other scales: a value is code * scale,
+ * though to tps_prefix_attention a value's scale below 2^-80 may count as anything up to 2^-80. */
 typedef enum { TPS_KV_BF16 = 0, TPS_KV_FP8 = 1, TPS_KV_INT8 = 2 } tps_kv_format;
 
 /*

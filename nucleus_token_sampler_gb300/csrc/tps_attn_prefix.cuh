@@ -600,7 +600,8 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
         // ---------------------------------------------------------------------------- scales
         // A tile's unit is a power of two next to its largest scale, the one below for fp8 and the one above for int8,
         // whose weights (up to 2^15) are multiplied by the scales; 1 if there is none.  fp8: a token's scale in that
-        // unit is the factor of its codes.  int8: the scores and the weights take the scales.  One warp for every tile in
+        // unit is the factor of its codes.  int8: the scores and the weights take the scales.  A unit is at least 2^-80
+        // (kLeastScale), so that the sum, which is divided by the values', stays finite.  One warp for every tile in
         // turn: a barrier's phase may only be waited for by a role that sees each of its phases.
         Way way(p);
         Turn<kRaw> raw_turn(0);
@@ -627,7 +628,7 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
                     const uint32_t up = kFormat == TPS_KV_INT8 ? 0x7FFFFFu : 0u;
-                    const int e = most > 0.f ? max(-126, min((int)((__float_as_uint(most) + up) >> 23) - 127, 126)) : 0;
+                    const int e = most > 0.f ? max(-80, min((int)((__float_as_uint(most) + up) >> 23) - 127, 126)) : 0;
                     const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
                     if constexpr (kFormat == TPS_KV_INT8) {
                         *reinterpret_cast<float4*>(&ctl.value_scale[scalar.slot][lane * 4]) =

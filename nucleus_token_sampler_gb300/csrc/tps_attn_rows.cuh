@@ -102,9 +102,11 @@ __device__ __forceinline__ void code_pairs(uint32_t w, uint32_t& p01, uint32_t& 
     }
 }
 
-// A stored scale is at least 2^-40; what lies below (a slot never written, or what stands in rows past the end,
-// whose weight is 0) counts as that, so that 1 / s is finite.
-__device__ __forceinline__ float floor_scale(float s) { return s >= 0x1p-40f || s != s ? s : 0x1p-40f; }
+// A value's scale goes into its weight as a power and out of the sum again: w / s. A stored scale is at least 2^-40; what
+// lies below 2^-80 (0 of a slot never written, what stands in rows past the end, whose weight is 0) counts as that, so
+// that a sum of 2^31 weights up to 2^15, each over its scale, is finite.
+constexpr float kLeastScale = 0x1p-80f;
+__device__ __forceinline__ float floor_scale(float s) { return s >= kLeastScale || s != s ? s : kLeastScale; }
 
 // Components of a head that a lane holds for k-step s: 4 consecutive ones from here on.
 template <int kFormat>
@@ -347,7 +349,7 @@ __device__ __forceinline__ int attend(RowState<D, N>& st, Walk<D, kFormat>& walk
             for (int h = 0; h < 2; ++h) {
                 const uint32_t ks = *reinterpret_cast<const uint16_t*>(buf + C::kKeyScales + (g + 8 * h) * 2);
                 const uint32_t vs = *reinterpret_cast<const uint16_t*>(buf + C::kValueScales + (g + 8 * h) * 2);
-                const float kf = floor_scale(__uint_as_float(ks << 16)), s = floor_scale(__uint_as_float(vs << 16));
+                const float kf = __uint_as_float(ks << 16), s = floor_scale(__uint_as_float(vs << 16));
                 add[h] = log2_fast(s);
                 inv_s[h] = s == s ? __fdividef(1.f, s) : 1.f;  // NaN reaches the weight through `add` where it is seen
 #pragma unroll

@@ -547,3 +547,19 @@ def test_attention_with_a_scale_of_nothing(fmt, B, scale, mag):
     q[:] = (q.float() * mag).bfloat16()
     _check_attention(tps.prefix_attention(q, c, pp, 700, table, n, want_lse=True, scale=scale), q, plain.values(c), pp, 700, table, n,
                      scale, fmt)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "int8"])
+@pytest.mark.parametrize("B", [2, 40, 200])
+@pytest.mark.parametrize("factor", [1.3, 2.0 ** -25, 2.0 ** -50, 2.0 ** 30])
+def test_attention_on_a_callers_own_codes_and_scales(fmt, B, factor):
+    """Scales that are no powers of two, and scales below and above those kv_write makes of ordinary values: one
+    tensor's at a time, so that scores stay ordinary where the values are not."""
+    D, prefix = 64, 400
+    for name in ("k_scale", "v_scale"):
+        c, q, pp, table, n = _case(_gen(84), B, 1, 4, 1, D, prefix, [60], 32, fmt)
+        s = getattr(c, name)
+        s.copy_((s.float() * factor).bfloat16())
+        scale = 0.125 / factor if name == "k_scale" else 0.125
+        _check_attention(tps.prefix_attention(q, c, pp, prefix, table, n, want_lse=True, scale=scale), q, plain.values(c), pp, prefix,
+                         table, n, scale, fmt)
