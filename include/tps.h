@@ -428,7 +428,8 @@ typedef struct {
  * all share and their own tokens, both held in `cache` (head_dim 64 or 128).  The products with the
  * shared keys and values are computed once for the whole batch.  Products are accumulated and
  * softmax statistics held in float32; softmax weights are rounded to 16 bits for the second product
- * (bfloat16 for TPS_KV_BF16: at most 2^-8 of sum p |v|; float16 for 8-bit formats: at most 2^-11).
+ * (bfloat16 for TPS_KV_BF16: at most 2^-8 of sum p |v|; float16 for 8-bit formats: at most 2^-11 of p |v| for each
+ * token, or 2^-23 of its code times the row's largest p * scale where that is more).
  * Not accepted (TPS_ERR_ARG): more than 2^31 - 2^16 tokens of prefix_len or of table_width pages, 2^31 query
  * rows, 2^24 rows of one sequence and key head, or 2^31 pairs of a block of 128 shared tokens and a tile of 128 or
  * 256 rows.  No result depends on another sequence's data, and cache rows past a sequence's length are

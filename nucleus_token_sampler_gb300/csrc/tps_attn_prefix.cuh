@@ -10,6 +10,14 @@
 // value's scale in float32, before its one rounding.  The block's units stay scalars outside: z = (q.k') nk, and the
 // weights take log2(nv) in their exponent (the row sum divides by nv again).
 //
+// float16 holds a scale in its block's unit only so far: a token may attract all the weight with values 2^-20 of its
+// neighbours' (whose small weights, in the same unit, keep few bits), and next to a key 2^26 times the others' those
+// would vanish.  A block whose scales lie further apart than 2^kSpread (or, in fp8, are no powers of two) is wide: its
+// codes stay as they are, each score takes its key's scale and each weight's exponent its value's, as for own tokens,
+// and the sum takes that out again.  A cache of nothing but wide blocks takes 49 us instead of 35 (64 x 8,191 in fp8) or
+// 711 instead of 298 (1,024 x 16,384); that the softmax can do so costs the other blocks registers and instructions
+// (33.5 and 290 us without it, 143 and 146 in int8 for 48 x 5 x 20,011).
+//
 // What bounds it: with R of some hundreds, the matrix unit (512 clocks per 128 x 128 tile at D = 128) and
 // next to it the exponentials (one for each of its 16,384 weights) and the conversion of 8-bit codes; with
 // fewer rows, the bytes of the cache.  One CTA per SM; the blocks of all items form one line that is
@@ -44,16 +52,19 @@
 namespace tps {
 
 constexpr int kScalars = 8;         // blocks whose scale factors are kept
+constexpr int kSpread = 8;          // down to 2^-8 of its block's unit a scale times any code is exact (fp8), and small weights keep their bits
 
 template <int D, int kFormat, int kTiles> struct PrefixShape {
     static constexpr bool k8 = kFormat != TPS_KV_BF16;
     static constexpr int kMmaWarp = 4 * kTiles, kLoadWarp = kMmaWarp + 1, kScaleWarp = kMmaWarp + 2;
     static constexpr int kConvertWarp = kMmaWarp + 4, kConvertWarps = 8;
     static constexpr int kThreads = (kConvertWarp + (k8 ? kConvertWarps : 0)) * 32;
-    // Registers where the roles share them out: 640 threads at 96 at launch, 2 x 144 + 3 x 64 = 5 x 96, or 512 threads at
-    // 128, 200 + 3 x 104 = 4 x 128.
+    // Registers where the roles share them out: 640 threads at 96 at launch, 2 x 144 + 3 x 64 = 5 x 96 (fp8, whose
+    // conversion needs fewer: 2 x 152 + 3 x 56), or 512 threads at 128, 200 + 3 x 104 = 4 x 128.
     static constexpr bool kSplitRegs = kFormat == TPS_KV_INT8 || (k8 && kTiles == 2);
-    static constexpr int kRegsLaunch = kTiles == 2 ? 96 : 128, kRegsSoftmax = kTiles == 2 ? 144 : 200, kRegsOthers = kTiles == 2 ? 64 : 104;
+    static constexpr bool kFp8 = kFormat == TPS_KV_FP8;
+    static constexpr int kRegsLaunch = kTiles == 2 ? 96 : 128, kRegsSoftmax = kTiles == 2 ? (kFp8 ? 152 : 144) : 200,
+                         kRegsOthers = kTiles == 2 ? (kFp8 ? 56 : 64) : 104;
     static_assert(kTiles * kRegsSoftmax + 3 * kRegsOthers <= (kTiles + 3) * kRegsLaunch, "no more than the launch gave");
     static constexpr int kTileBytes = 128 * D * 2;         // a query, key or value tile
     static constexpr int kRing = k8 && D == 128 && kTiles == 2 ? 3 : 4;  // key and value tiles in shared memory
@@ -68,8 +79,10 @@ template <int D, int kFormat, int kTiles> struct PrefixShape {
         uint32_t tmem;
         int abort, bad;
         float key_unit[kScalars], value_exp[kScalars];
-        // int8: of the block's tokens, the values' in the block's unit, at most 1
-        alignas(16) float key_scale[kFormat == TPS_KV_INT8 ? kScalars : 1][128], value_scale[kFormat == TPS_KV_INT8 ? kScalars : 1][128];
+        int wide[kScalars];  // 1: the block's keys, 2: its values
+        // Of the block's tokens: keys' scales (int8, or wide), values' in the block's unit, at most 1 (int8), or one over
+        // them and their base-2 logarithms (wide).
+        alignas(16) float key_scale[k8 ? kScalars : 1][128], value_scale[k8 ? kScalars : 1][128], value_log[k8 ? kScalars : 1][128];
         alignas(16) __half factor[kFormat == TPS_KV_FP8 ? kRaw : 1][128];  // fp8: of the tokens of a code tile
     };
     static constexpr size_t kSmem =
@@ -311,12 +324,14 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
                 s_parity ^= 1;
                 tc_fence_after();
                 float c = row_unit, add = 0.f, inv = 1.f;
+                int wide = 0;
                 const int scales = scalar.slot;
                 if (k8) {
                     if (!(alive = wait_all(&ctl.scalar_full[scalar.slot], scalar.parity))) break;
                     c *= ctl.key_unit[scalar.slot];
                     add = ctl.value_exp[scalar.slot];
                     inv = exp2_fast(-add);
+                    wide = ctl.wide[scalar.slot];
                     scalar.next();
                 }
                 c = fmaxf(c, 0x1p-126f);  // never 0: a masked score, -inf, times it stays -inf (any other times that is nothing)
@@ -408,6 +423,39 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
                     tmem_st16(s_addr + ch * 16, w);
                     return add2(part[0], part[1]);
                 };
+                // 32 scores of a wide block, against their largest: the exponents take the scales, and the sum adds up the
+                // weights without their values' scales.
+                auto weigh_wide = [&](float (&s)[32], int ch) {
+                    const bool keys = kFormat == TPS_KV_FP8 && (wide & 1), values = wide & 2;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        float4 l = reinterpret_cast<const float4*>(ctl.value_log[scales] + ch * 32)[i / 4];
+                        if (!values) l = make_float4(add, add, add, add);
+                        const float ll[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float y = keys ? s[i + j] * ctl.key_scale[scales][ch * 32 + i + j] : s[i + j];
+                            s[i + j] = s[i + j] == neg ? neg : fmaf(y, c, ll[j]);
+                        }
+                    }
+                    const float top = largest(s);
+                    const bool need = top > ref + kSlack;
+                    if (__any_sync(0xFFFFFFFFu, need)) raise(need, top, ch);
+                    const float b = (ref == neg ? 0.f : -ref) + kLift;
+                    float2 t = make_float2(0.f, 0.f);
+                    uint32_t w[16];
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        const float2 x = make_float2(exp2_fast(s[i] + b), exp2_fast(s[i + 1] + b));
+                        const float2 inv_s = reinterpret_cast<const float2*>(ctl.value_scale[scales] + ch * 32)[i / 2];
+                        t = fma2(x, values ? inv_s : make_float2(1.f, 1.f), t);
+                        const __half2 h = __floats2half2_rn(x.x, x.y);
+                        w[i / 2] = *reinterpret_cast<const uint32_t*>(&h);
+                    }
+                    tmem_wait_st();
+                    tmem_st16(s_addr + ch * 16, w);
+                    return t;
+                };
                 // 64 scores at a time, first weighed against the reference as it stands: a weight above 2^kSlack
                 // (times the lift) shows in their sum, so the usual step looks for no maximum at all.
                 constexpr float kMost = k8 ? 32768.f : 256.f;  // 2^(kSlack + kLift), 2^kSlack
@@ -423,11 +471,17 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
                     float b = add - (ref == neg ? 0.f : ref) + (k8 ? kLift : 0.f);
                     float2 x = add2(weigh(sa, ch, b), weigh(sb, ch + 1, b));
                     const bool need = !(x.x + x.y <= kMost) || ref == neg;
-                    if (__any_sync(0xFFFFFFFFu, need)) {
-                        raise(need, fmaf(fmaxf(largest(sa), largest(sb)), c, add), ch);
-                        b = add - (ref == neg ? 0.f : ref) + (k8 ? kLift : 0.f);
-                        tmem_wait_st();
-                        x = add2(weigh(sa, ch, b), weigh(sb, ch + 1, b));
+                    if (__any_sync(0xFFFFFFFFu, need || wide)) {  // a wide block comes this way every time
+                        if (!k8 || !wide) {
+                            raise(need, fmaf(fmaxf(largest(sa), largest(sb)), c, add), ch);
+                            b = add - (ref == neg ? 0.f : ref) + (k8 ? kLift : 0.f);
+                            tmem_wait_st();
+                            x = add2(weigh(sa, ch, b), weigh(sb, ch + 1, b));
+                        } else {
+                            x = weigh_wide(sa, ch);  // may scale the total, so not inside its sum
+                            total = add2(total, x);
+                            x = weigh_wide(sb, ch + 1);
+                        }
                     }
                     total = add2(total, x);
                 }
@@ -608,6 +662,7 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
         Turn<kScalars> scalar(0);
         for (; way.left > 0 && alive; way.step(p), scalar.next()) {
             const int left = prefix - way.block * kBlockKeys;
+            int wide = 0;
 #pragma unroll
             for (int kv = 0; kv < 2; ++kv, raw_turn.next()) {
                 const int rs = raw_turn.slot;
@@ -624,25 +679,43 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
                     *reinterpret_cast<float4*>(&ctl.key_scale[scalar.slot][lane * 4]) = make_float4(s[0], s[1], s[2], s[3]);
                     if (lane == 0) ctl.key_unit[scalar.slot] = 1.f;
                 } else {
-                    float most = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
-                    const uint32_t up = kFormat == TPS_KV_INT8 ? 0x7FFFFFu : 0u;
-                    const int e = most > 0.f ? max(-80, min((int)((__float_as_uint(most) + up) >> 23) - 127, 126)) : 0;
+                    // The largest scale and the smallest that is not 0, by their bits (0 counts as 2^16).
+                    const uint32_t high = __vmaxu2(w.x, w.y), low = __vminu2(__vsub2(w.x, 0x10001u), __vsub2(w.y, 0x10001u));
+                    const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, max(high >> 16, high & 0xFFFFu));
+                    const bool odd = kFormat == TPS_KV_FP8 && ((w.x | w.y) & 0x7F007Fu) != 0;  // not a power of two
+                    const uint32_t least = __reduce_min_sync(0xFFFFFFFFu, odd ? 0u : min(low >> 16, low & 0xFFFFu)) + 1;
+                    const int e = most ? max(-80, min((int)((most + (kFormat == TPS_KV_INT8 ? 0x7Fu : 0u)) >> 7) - 127, 126)) : 0;
                     const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-                    if constexpr (kFormat == TPS_KV_INT8) {
-                        *reinterpret_cast<float4*>(&ctl.value_scale[scalar.slot][lane * 4]) =
-                            make_float4(s[0] * inv, s[1] * inv, s[2] * inv, s[3] * inv);
-                    } else {
-                        const __half2 lo = __floats2half2_rn(s[0] * inv, s[1] * inv), hi = __floats2half2_rn(s[2] * inv, s[3] * inv);
+                    const bool far = least < (uint32_t)(e + 127 - kSpread) << 7;
+                    float f[4];  // in the block's unit
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) f[i] = s[i] * inv;
+                    if (far) {
+                        wide |= 1 << kv;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if (kv) {
+                                const float y = floor_scale(s[i]);
+                                ctl.value_log[scalar.slot][lane * 4 + i] = log2_fast(y);
+                                ctl.value_scale[scalar.slot][lane * 4 + i] = y == y ? 1.f / y : 1.f;  // NaN comes by its logarithm
+                            } else {
+                                ctl.key_scale[scalar.slot][lane * 4 + i] = s[i];
+                            }
+                            f[i] = 1.f;
+                        }
+                    } else if (kFormat == TPS_KV_INT8) {
+                        *reinterpret_cast<float4*>(&ctl.value_scale[scalar.slot][lane * 4]) = make_float4(f[0], f[1], f[2], f[3]);
+                    }
+                    if constexpr (kFormat == TPS_KV_FP8) {
+                        const __half2 lo = __floats2half2_rn(f[0], f[1]), hi = __floats2half2_rn(f[2], f[3]);
                         *reinterpret_cast<uint2*>(&ctl.factor[rs][lane * 4]) =
                             make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
                     }
                     if (lane == 0) {
                         if (kv)
-                            ctl.value_exp[scalar.slot] = (float)e;
+                            ctl.value_exp[scalar.slot] = far ? 0.f : (float)e, ctl.wide[scalar.slot] = wide;
                         else
-                            ctl.key_unit[scalar.slot] = __uint_as_float((uint32_t)(127 + e) << 23);
+                            ctl.key_unit[scalar.slot] = far ? 1.f : __uint_as_float((uint32_t)(127 + e) << 23);
                     }
                 }
                 __syncwarp();

@@ -563,3 +563,45 @@ def test_attention_on_a_callers_own_codes_and_scales(fmt, B, factor):
         scale = 0.125 / factor if name == "k_scale" else 0.125
         _check_attention(tps.prefix_attention(q, c, pp, prefix, table, n, want_lse=True, scale=scale), q, plain.values(c), pp, prefix,
                          table, n, scale, fmt)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "int8"])
+@pytest.mark.parametrize("B", [2, 40, 200])
+@pytest.mark.parametrize("power", [-12, -20, -30])
+def test_attention_to_a_token_whose_values_are_far_below_its_neighbours(fmt, B, power):
+    """One key takes nearly all the weight, and its values are 2^power of the others'."""
+    g = _gen(82)
+    D, prefix, page = 128, 300, 16
+    c, q, pp, table, n = _case(g, B, 1, 8, 2, D, prefix, [40], page, fmt)
+    u = torch.randn(1, 2, D, generator=g, device=DEV)
+    q[:] = (u.repeat_interleave(4, 1) * torch.linspace(0.75, 1.5, B * 8, device=DEV).view(B, 8, 1)).unsqueeze(1).bfloat16()
+    at = torch.tensor([5, 200], device=DEV)
+    slots = pp.long()[at // page] * page + at % page
+    k = (torch.tensor([12.0, 11.0], device=DEV).view(2, 1, 1) * u).bfloat16()
+    v = (torch.randn(2, 2, D, generator=g, device=DEV) * 2.0 ** power).bfloat16()
+    tps.kv_write(c, k, v, slots)
+    kv = plain.values(c)
+    _check_attention(tps.prefix_attention(q, c, pp, prefix, table, n, want_lse=True), q, kv, pp, prefix, table, n, D ** -0.5, fmt)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "int8"])
+@pytest.mark.parametrize("B", [2, 40, 200])
+@pytest.mark.parametrize("power", [8, 16, 26])
+def test_attention_beside_a_token_whose_keys_are_far_above_its_neighbours(fmt, B, power):
+    """A key 2^power times the others', whose score is so low that it takes no weight, costs its neighbours nothing."""
+    g = _gen(83)
+    D, prefix, page = 128, 300, 16
+    c, q, pp, table, n = _case(g, B, 1, 8, 2, D, prefix, [40], page, fmt)
+    at = torch.tensor([17], device=DEV)
+    slots = pp.long()[at // page] * page + at % page
+    u = torch.randn(1, 2, D, generator=g, device=DEV)
+    q[:] = (q.float().abs() * u.sign().repeat_interleave(4, 1)).bfloat16()
+    tps.kv_write(c, (-u.sign() * 2.0 ** power).bfloat16(), torch.zeros(1, 2, D, device=DEV).bfloat16(), slots)
+    kv = plain.values(c)
+    out, lse = tps.prefix_attention(q, c, pp, prefix, table, n, want_lse=True)
+    want, wl, mag, _ = plain.attention(q, kv, pp, prefix, table, n, D ** -0.5)
+    kv[0][pp[1].long(), :, 1] = 0
+    big = plain.attention(q, kv, pp, prefix, table, n, D ** -0.5)[3]
+    rest = 2.0 ** -18 * big + 2.0 ** -14
+    assert ((out.double() - want).abs() <= 2.0 ** -8 * want.abs() + (2.0 ** -11 + rest).unsqueeze(-1) * mag).all()
+    assert ((lse.double() - wl).abs() <= rest + 2.0 ** -22 * wl.abs()).all()
