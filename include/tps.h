@@ -432,9 +432,9 @@ typedef struct {
  * token, or 2^-23 of its code times the row's largest p * scale where that is more).
  * Not accepted (TPS_ERR_ARG): more than 2^31 - 2^16 tokens of prefix_len or of table_width pages, 2^31 query
  * rows, 2^24 rows of one sequence and key head, or 2^31 pairs of a block of 128 shared tokens and a tile of 128 or
- * 256 rows.  No result depends on another sequence's data, and cache rows past a sequence's length are
- * never used, whatever they hold; a NaN or an infinity in an own token's VALUE, though, also reaches
- * those of the sequence's queries that causality hides the token from (0 * NaN in the second product).
+ * 256 rows.  No result depends on another sequence's data, nor on tokens that are hidden from it or cache
+ * rows past a sequence's length, whatever they hold (an fp8 cache's NaN codes excepted, which kv_write never
+ * stores: those reach all queries of their sequence).
  * Returns TPS_ERR_ARG / _ALIGN / _SCRATCH (workspace too small) / _CUDA.
  */
 int tps_prefix_attention(const tps_kv_cache* cache, const tps_attention* args, void* stream);

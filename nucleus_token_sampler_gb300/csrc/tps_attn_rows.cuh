@@ -229,7 +229,7 @@ template <int D, int kFormat> struct Walk {
     uint32_t fills;  // copies into the ring so far, over the life of the kernel (parity of the barriers)
     int first, step, last, ahead;  // `ahead`: the next chunk to ask for
     int page;                      // its page, read one request early and not looked at before the next one
-    int fault;                     // 1: a page that is not the cache's
+    int fault;                     // 1: a page that is not the cache's; 4: values taken out of a product (add_not_finite)
 
     // The page of the chunk at `first`, if the list reaches as far as `tokens`: may be called before the number of
     // tokens is known, so that this read does not wait for that one.
@@ -244,7 +244,7 @@ template <int D, int kFormat> struct Walk {
         const int lane = threadIdx.x & 31, stage = (int)(fills % C::kStages), shift = a.page_shift;
         const tps_kv_cache& c = a.c;
         int id = page;
-        if (id < 0 || id >= c.n_pages) fault = 1, id = 0;
+        if (id < 0 || id >= c.n_pages) fault |= 1, id = 0;
         const int64_t row = (((int64_t)id * c.n_heads + head) << shift) + (ahead & ((1 << shift) - 1));
         ahead += step;
         if (ahead < last) page = pages[ahead >> shift];
@@ -268,6 +268,39 @@ template <int D, int kFormat> struct Walk {
     }
 };
 
+// bfloat16 values of tokens that not every row sees: the product would bring a hidden token's NaN or infinity to every row
+// (0 * NaN), so attend() takes those components out of it, and the rows that see the token get them here.
+__device__ __forceinline__ uint32_t not_finite(uint32_t w)  // the halves that are not, else 0
+{
+    return ((w & 0x7F80u) == 0x7F80u ? w & 0xFFFFu : 0u) | ((w & 0x7F800000u) == 0x7F800000u ? w & 0xFFFF0000u : 0u);
+}
+template <int D, int kFormat, int N>
+__device__ __forceinline__ void add_not_finite(RowState<D, N>& st, const Walk<D, kFormat>& walk, const int (&lim)[N][2], int all_see)
+{
+    const int g = (threadIdx.x & 31) >> 2, shift = walk.a.page_shift;
+#pragma unroll 1
+    for (int t0 = walk.first; t0 < walk.last; t0 += walk.step)
+#pragma unroll 1
+        for (int t = max(t0, all_see); t < min(t0 + 16, walk.last); ++t) {
+            const int id = walk.pages[t >> shift];
+            if (id < 0 || id >= walk.a.c.n_pages) continue;
+            const int64_t row = (((int64_t)id * walk.a.c.n_heads + walk.head) << shift) + (t & ((1 << shift) - 1));
+            const uint32_t* v = static_cast<const uint32_t*>(walk.a.c.v) + (row * D + g * (D / 8)) / 2;
+#pragma unroll
+            for (int w = 0; w < D / 16; ++w) {
+                const uint32_t x = not_finite(v[w]);
+#pragma unroll
+                for (int n = 0; n < N; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        if (t < lim[n][e]) {
+                            st.o[n][w][e] += __uint_as_float(x << 16);
+                            st.o[n][w][2 + e] += __uint_as_float(x & 0xFFFF0000u);
+                        }
+            }
+        }
+}
+
 // Attend to the chunks of a walk that has been started; row 8 n + 2 quad + e sees the tokens below
 // lim[n][e].  Returns 0, or 1 after a page that is not the cache's, 2 after a wait that ran out.
 template <int D, int kFormat, int N>
@@ -281,7 +314,7 @@ __device__ __forceinline__ int attend(RowState<D, N>& st, Walk<D, kFormat>& walk
     const int lane = threadIdx.x & 31, g = lane >> 2, quad = lane & 3;
     const float neg = -__int_as_float(0x7F800000);
     const int last = walk.last;
-    if (walk.first >= last) return walk.fault;
+    if (walk.first >= last) return walk.fault & 1;
     int all_see = last;  // tokens that every row sees
 #pragma unroll
     for (int n = 0; n < N; ++n) all_see = min(all_see, min(lim[n][0], lim[n][1]));
@@ -295,7 +328,19 @@ __device__ __forceinline__ int attend(RowState<D, N>& st, Walk<D, kFormat>& walk
                 mbar_wait_bounded(&walk.full[at % C::kStages], (at / C::kStages) & 1, kAttnWaitNs);
             return 2;
         }
-        const unsigned char* buf = walk.ring + stage * C::kBytes;
+        unsigned char* buf = walk.ring + stage * C::kBytes;
+        if (!k8 && all_see < last && t0 + 16 > all_see) {
+            uint4* v = reinterpret_cast<uint4*>(buf + C::kValues);
+#pragma unroll 1
+            for (int i = lane; i < C::kRowBytes; i += 32) {  // 16-byte pieces of 16 rows
+                const int t = t0 + i / (C::kRowBytes / 16);
+                if (t < all_see || t >= last) continue;
+                const uint4 x = v[i], y = make_uint4(not_finite(x.x), not_finite(x.y), not_finite(x.z), not_finite(x.w));
+                if (y.x | y.y | y.z | y.w) walk.fault |= 4;
+                v[i] = make_uint4(x.x ^ y.x, x.y ^ y.y, x.z ^ y.z, x.w ^ y.w);
+            }
+            __syncwarp();
+        }
         uint32_t vreg[4][kValWords];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -456,6 +501,8 @@ __device__ __forceinline__ int attend(RowState<D, N>& st, Walk<D, kFormat>& walk
             }
         }
     }
+    if (!k8 && __any_sync(0xFFFFFFFFu, walk.fault & 4)) add_not_finite(st, walk, lim, all_see);
+    walk.fault &= 1;
     return walk.fault;
 }
 

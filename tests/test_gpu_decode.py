@@ -605,3 +605,35 @@ def test_attention_beside_a_token_whose_keys_are_far_above_its_neighbours(fmt, B
     rest = 2.0 ** -18 * big + 2.0 ** -14
     assert ((out.double() - want).abs() <= 2.0 ** -8 * want.abs() + (2.0 ** -11 + rest).unsqueeze(-1) * mag).all()
     assert ((lse.double() - wl).abs() <= rest + 2.0 ** -22 * wl.abs()).all()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "int8"])
+@pytest.mark.parametrize("B,Tq,Hq,Hkv,D,prefix,lens", [
+    (3, 5, 8, 2, 128, 40, [5, 21, 33]), (2, 16, 4, 4, 64, 0, [16, 40]), (40, 3, 8, 1, 64, 2000, [30]),
+    (3, 7, 8, 2, 64, 100, [4200, 17]), (900, 2, 4, 2, 64, 100, [20, 5])])
+def test_attention_values_that_are_not_finite_stay_with_those_who_see_them(fmt, B, Tq, Hq, Hkv, D, prefix, lens):
+    """NaN and infinities in the values of the last own tokens: queries they are hidden from keep every bit, the others get
+    what the formula gives."""
+    c, q, pp, table, n = _case(_gen(86), B, Tq, Hq, Hkv, D, prefix, lens, 16, fmt)
+    b = torch.arange(B, device=DEV)
+    slots = lambda back: table[b, (n.long() - back) // 16].long() * 16 + (n.long() - back) % 16
+    k = torch.randn(B, Hkv, D, generator=_gen(87), device=DEV).bfloat16()
+    v = torch.zeros(2, B, Hkv, D, device=DEV).bfloat16()
+    for back in (1, 2):
+        tps.kv_write(c, k, v[0], slots(back))
+    calm, calm_lse = tps.prefix_attention(q, c, pp, prefix, table, n, want_lse=True)
+    v[0, :, :, 3] = math.nan
+    v[0, :, 0, D - 1] = math.inf
+    v[1, :, Hkv - 1, 7] = -math.inf
+    for back in (1, 2):
+        tps.kv_write(c, k, v[back - 1], slots(back))
+    out, lse = tps.prefix_attention(q, c, pp, prefix, table, n, want_lse=True)
+    assert torch.equal(out[:, :-2], calm[:, :-2])
+    some = slice(0, 4)
+    want = plain.attention(q[some], plain.values(c), pp, prefix, table[some], n[some], D ** -0.5)[0]
+    got = out[some]
+    assert torch.equal(got.isnan(), want.isnan())
+    if fmt == "bf16":
+        assert torch.equal(got.isposinf(), want.isposinf()) and torch.equal(got.isneginf(), want.isneginf())
+        assert torch.equal(lse, calm_lse)
+        assert want[:, -1].isnan().any() and want[:, -2:].isinf().any()
