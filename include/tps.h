@@ -35,7 +35,10 @@
  *     stream-ordered memory pool the library creates once per device, and returns it on the call's
  *     stream; the pool keeps up to 64 MiB reserved between calls.  tps_sample_noalloc uses a fixed
  *     array instead.  tps_prefix_attention takes its workspace from the same pool unless it is given one
- *     (tps_prefix_attention_workspace says how much); no other call allocates device memory;
+ *     (tps_prefix_attention_workspace says how much).  Its pieces take 128 KB for each SM and each 256 query
+ *     rows of a key head (99 MB for 1,024 sequences of 5 tokens, 32 heads on 8): a caller whose calls need more than the
+ *     pool keeps and who synchronises between them had better hand in a workspace.  No other call allocates
+ *     device memory;
  *   - the library never synchronises the host, keeps no state between calls beyond that pool and
  *     a per-device cache of queried limits, and may be called from several host threads at once;
  *   - `stream` is a cudaStream_t (NULL = the legacy default stream); all work is enqueued on it;

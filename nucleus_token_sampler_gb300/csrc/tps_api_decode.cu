@@ -40,7 +40,8 @@ int check_cache(const tps_kv_cache* c, bool pointers)
 // itself: one launch instead of two, and nothing to join, for reading the prefix again from the L2 cache.
 // With 8 key heads of 128, alone / shared, us: bfloat16 8 x 500 9.2 / 9.7, 5 x 1,000 11.0 / 10.0, 8 x 1,000 11.1 /
 // 10.1, 2 x 2,000 14.7 / 10.5, 8 x 2,000 21.3 / 12.8; fp8 (whose shared part converts its codes) 5 x 1,000 10.9 /
-// 13.3, 8 x 1,000 12.3 / 13.3, 8 x 2,000 20.6 / 16.0, 5 x 2,000 16.8 / 14.7, 2 x 4,000 16.3 / 15.9.
+// 13.3, 8 x 1,000 12.3 / 13.3, 8 x 2,000 20.6 / 16.0, 5 x 2,000 16.8 / 14.7, 2 x 4,000 16.3 / 15.9.  The product of tokens
+// and triples is not all that decides: 8 x 500 in bfloat16 and 8 x 1,000 in fp8 fall on the slower side, by 0.5 and 1.0 us.
 constexpr int64_t kAloneBf16 = 24576, kAlone8 = 49152;
 // Sequences (times heads and row tiles) per SM from which each warp takes one for itself, and where they hold few
 // tokens.  4 warps of a CTA / one warp each, on a prefix of 4,000, bfloat16, us: 768 items of up to 60 tokens 30.3 /
@@ -49,7 +50,8 @@ constexpr int64_t kOneWarpItems = 8, kOneWarpShort = 5, kShortTokens = 128;
 // Tokens of one sequence (at most) from which the own tokens are cut evenly over the SMs, for up to kLinePairs
 // sequences times row tiles.  Clusters / even cuts, 16 sequences with 8 key heads of 128, us: bfloat16 2,000 tokens
 // 36.7 / 38.0, 4,000 58.6 / 49.8; fp8 4,000 41.3 / 44.2, 9,000 69.2 / 59.6; 48 sequences: bfloat16 4,000 107 / 113,
-// 8,000 196 / 171; fp8 4,000 106 / 99.
+// 8,000 196 / 171; fp8 4,000 106 / 99.  (16 x 4,000 in bfloat16 lies just below the rule, on the slower side.)  The tokens
+// are those that the page table has room for; the lengths are on the device.
 constexpr int64_t kLineTokens = 4096, kLinePairs = 1024;
 
 int plan_attention(const tps_kv_cache& c, const tps_attention& a, int sms, tps::AttnPlan* out)

@@ -34,7 +34,7 @@ cudaError_t launch_units(const tps_norm_rope& a, int sms, cudaStream_t stream)
 {
     // Few tokens: a CTA for each, all of its heads at once as far as 256 threads reach.  Many: two heads for
     // each group of lanes, and no more CTAs than are resident, each walking over its tokens.  One / two heads, 40
-    // heads of 128 in bfloat16, us: 608 tokens 3.5 / 5.1, 1,216 6.5 / 7.0, 2,700 15.7 / 14.6, 16,383 78.5 / 67.2.
+    // heads of 128 in bfloat16 (other shapes were not swept), us: 608 tokens 3.5 / 5.1, 1,216 6.5 / 7.0, 2,700 15.7 / 14.6, 16,383 78.5 / 67.2.
     const int H = a.n_q_heads + a.n_k_heads;
     const bool two = a.T > 12 * sms && H > 1;
     const int want = two ? (H + 1) / 2 : H;                                  // groups
