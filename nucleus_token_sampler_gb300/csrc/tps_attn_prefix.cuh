@@ -206,6 +206,7 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ctl.tmem;
+    clear_status(a);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     volatile int* abort_flag = &ctl.abort;

@@ -804,12 +804,21 @@ struct PrefixPieces {
     }
 };
 
-// A sequence's status, cleared ahead of the call's first kernel: the worst of what its heads and row tiles met
-// (state 1: a bad page or length, 2: a wait that ran out, which concerns one CTA and so maybe a single head).
+// A sequence's status: the worst of what its heads and row tiles met (state 1: a bad page or length, 2: a wait that
+// ran out, which concerns one CTA and so maybe a single head).  The call's first kernel clears it, and the joins raise
+// it after their wait for that kernel; a call that is one kernel has a small one ahead for this alone (8 x 300: 9.4 us
+// without a status array, 10.1 with one).
 static_assert(TPS_ROW_TIMEOUT > TPS_ROW_BAD_PARAM && TPS_ROW_BAD_PARAM > TPS_ROW_OK && TPS_ROW_OK == 0, "the worst is the largest");
 __device__ __forceinline__ void report_row(const AttnArgs& a, int64_t b, int state)
 {
     if (a.a.out_status) atomicMax(&a.a.out_status[b], state == 2 ? TPS_ROW_TIMEOUT : TPS_ROW_BAD_PARAM);
+}
+
+__device__ __forceinline__ void clear_status(const AttnArgs& a)
+{
+    if (a.a.out_status)
+        for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < a.a.B; i += (int64_t)gridDim.x * blockDim.x)
+            a.a.out_status[i] = TPS_ROW_OK;
 }
 
 template <int kFormat>
@@ -1103,6 +1112,7 @@ __global__ void __launch_bounds__(kRowsThreads, N == 1 ? 4 : 3) attn_line_kernel
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = lane & 3;
     const int heads = a.c.n_heads, pairs = (int)(a.a.B * p.suffix_tiles), Tq = a.a.q_len, G = a.G;
     init_rings(sm);
+    if (!p.shared) clear_status(a);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int shared_len = p.shared ? 0 : (int)a.a.prefix_len, shared_blocks = (shared_len + kLineBlock - 1) / kLineBlock;
     line_sums(sums, a, kRows);

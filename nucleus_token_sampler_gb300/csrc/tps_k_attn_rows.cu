@@ -1,6 +1,7 @@
 // The 8- and 16-row attention kernels for each head size and cache format, and their launches.
 #include "tps_attn_rows.cuh"
 
+#include <algorithm>
 #include <atomic>
 
 namespace tps {
@@ -19,6 +20,12 @@ cudaError_t allow_smem(Kernel k, size_t bytes, std::atomic<uint64_t>& allowed)
     e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e == cudaSuccess) allowed.fetch_or(bit, std::memory_order_release);
     return e;
+}
+
+__global__ void clear_status_kernel(const AttnArgs a)
+{
+    clear_status(a);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 template <int D, int kFormat, int N, bool kOneWarp>
@@ -105,7 +112,14 @@ cudaError_t line(const AttnArgs& a, bool after_prefix, cudaStream_t stream)
 template <int D, int kFormat>
 cudaError_t own(const AttnArgs& a, bool after_prefix, cudaStream_t stream)
 {
-    return a.p.line ? line<D, kFormat>(a, after_prefix, stream) : suffix<D, kFormat>(a, after_prefix, stream);
+    if (a.p.line) return line<D, kFormat>(a, after_prefix, stream);
+    if (!after_prefix && a.a.out_status) {
+        clear_status_kernel<<<(unsigned)std::min<int64_t>((a.a.B + 255) / 256, 1024), 256, 0, stream>>>(a);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+        after_prefix = true;
+    }
+    return suffix<D, kFormat>(a, after_prefix, stream);
 }
 
 template <int D>
