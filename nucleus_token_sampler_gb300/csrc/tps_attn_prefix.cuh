@@ -23,9 +23,9 @@
 // fewer rows, the bytes of the cache.  One CTA per SM; the blocks of all items form one line that is
 // cut evenly (AttnPlan).  A CTA holds one or two tiles of 128 query rows: with two, one tile's softmax
 // runs while the other's products do, and each block of keys and values is loaded and converted once
-// for 256 rows.  Measured with 8 key heads of 128: 1,024 x 4 rows on 16,384 tokens take 175 us in bfloat16 (1.57
-// PFLOP/s, the matrix unit 54% busy at half that length under a profiler) and 229 us in fp8 (1.20 PFLOP/s; the conversion
-// and the softmax share the issue slots); 48 x 25 rows of 64 on 20,011 tokens 115 us in int8 (0.43 PFLOP/s: half the
+// for 256 rows.  Measured with 8 key heads of 128: 1,024 x 4 rows on 16,384 tokens take 169 us in bfloat16 (1.62
+// PFLOP/s, the matrix unit 53% busy at half that length under a profiler) and 223 us in fp8 (1.23 PFLOP/s; the conversion
+// and the softmax share the issue slots); 48 x 25 rows of 64 on 20,011 tokens 114 us in int8 (0.43 PFLOP/s: half the
 // products for the same weights; 95 us where the values' scales were rounded into the codes, which cost a second
 // 2^-11); 4 x 4 rows on 16,384 tokens 26 us with the join (2.6 TB/s).  A third score buffer, so that scores run ahead of
 // the softmax, helped D = 64 (92.1 -> 88.8 us in bfloat16) and cost D = 128 more (125.5 -> 132.9 us): each tile has

@@ -8,7 +8,7 @@
 // 16-byte vectors whose elements rotate with each other, so a rotation needs no other lane: for
 // halves the vectors at u and rot/2 + u, for adjacent pairs two neighbours.  The cosines and sines of a
 // lane's unit are the same for every head, so each lane loads them once per token and walks over the
-// heads.  16,383 tokens x 40 heads x 128 in bfloat16 take 66 us (5.2 TB/s, 77% of a plain copy's rate), 8
+// heads.  16,383 tokens x 40 heads x 128 in bfloat16 take 66 us (5.2 TB/s, 76% of a plain copy's rate), 8
 // tokens 2.4 us.  Shapes that do not split into such units (head sizes or strides off 16 bytes) take one
 // warp per head and scalar accesses.
 #pragma once
