@@ -109,6 +109,13 @@ double number(PyObject* o)
     return v;
 }
 
+bool truth(PyObject* o)
+{
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw Raised{};
+    return v == 1;
+}
+
 // cache: (the bytes of a tps_kv_cache, device index)
 const tps_kv_cache& cache_of(PyObject* bytes)
 {
@@ -158,7 +165,7 @@ PyObject* norm(PyObject* const* a, Py_ssize_t n)
     if (Hq > INT32_MAX || Hk > INT32_MAX || D > INT32_MAX) refuse("too many heads or components");
     p.n_q_heads = (int32_t)Hq, p.n_k_heads = (int32_t)Hk, p.head_dim = (int32_t)D, p.rot_dim = (int32_t)R;
     p.eps = (float)number(a[6]);
-    p.interleaved = PyObject_IsTrue(a[7]) == 1;
+    p.interleaved = truth(a[7]);
     const c10::cuda::CUDAGuard guard(dev);
     PyObject *oq, *ok;
     if (a[8] == Py_None) {
@@ -276,7 +283,7 @@ PyObject* attention(PyObject* const* a, Py_ssize_t n)
     } else {
         p.out = dense(a[9], "out", q.sizes(), at::kBFloat16, dev);
     }
-    const bool want = PyObject_IsTrue(a[8]) == 1;
+    const bool want = truth(a[8]);
     if (want) {
         lse = new_tensor(q.sizes().slice(0, q.dim() - 1), at::kFloat, dev);
         p.out_lse = static_cast<float*>(lse.data_ptr());

@@ -637,3 +637,16 @@ def test_attention_values_that_are_not_finite_stay_with_those_who_see_them(fmt, 
         assert torch.equal(got.isposinf(), want.isposinf()) and torch.equal(got.isneginf(), want.isneginf())
         assert torch.equal(lse, calm_lse)
         assert want[:, -1].isnan().any() and want[:, -2:].isinf().any()
+
+
+def test_flags_that_have_no_truth_value_are_refused():
+    """Their exception reaches the caller, and nothing is launched."""
+    class Neither:
+        def __bool__(self):
+            raise KeyError("neither")
+    q = torch.randn(3, 2, 64, device=DEV)
+    with pytest.raises(KeyError):
+        tps.qk_norm_rope(q, q, None, None, torch.arange(3, device=DEV).int(), _table(4, 64), interleaved=Neither())
+    c, q, pp, table, n = _case(_gen(88), 2, 1, 4, 1, 64, 20, [3], 16, "bf16")
+    with pytest.raises(KeyError):
+        tps.prefix_attention(q, c, pp, 20, table, n, want_lse=Neither())
