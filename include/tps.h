@@ -77,7 +77,9 @@ typedef enum {
                                depth", 'Failure modes': fail the request rather than sample)    */
     TPS_ROW_ALL_MASKED = 2, /* every logit is -inf                                              */
     TPS_ROW_BAD_PARAM = 3,  /* temperature, top_p or min_p is NaN or infinite                    */
-    TPS_ROW_TIMEOUT = 4     /* a bounded wait inside the kernel gave up; the row was not sampled */
+    TPS_ROW_TIMEOUT = 4,    /* a bounded wait inside the kernel gave up; the row was not sampled */
+    TPS_ROW_NO_PAGES = 5    /* tps_kv_extend: too few free pages; tps_kv_trim: no room for them in
+                               the list.  The sequence is as it was                             */
 } tps_row_status;
 
 /*
@@ -455,6 +457,151 @@ int tps_prefix_attention_stall_test(const tps_kv_cache* cache, const tps_attenti
 /* Bytes of workspace tps_prefix_attention needs for these arguments on the current device (pointers
  * are not looked at), or -1 for arguments it would reject.  Host-only query. */
 int64_t tps_prefix_attention_workspace(const tps_kv_cache* cache, const tps_attention* args);
+
+/*
+ * tps_kv_pages -- the pages of B sequences and the list of free ones, for tps_kv_extend and tps_kv_trim.
+ *   page_table   [B, table_width] int32 (ld table_ld): sequence b's pages in order; entries from its
+ *                ceil(seq_len / page_size) pages on hold anything.
+ *   seq_len      [B] int32: tokens of each sequence.
+ *   change       [B] int32: extend: new tokens; trim: tokens that are kept.
+ *   free_pages   [n_free] int32: the first free_count[0] entries are free pages (at most n_free of them count).
+ *   out_status   [B] int32 or NULL: TPS_ROW_BAD_PARAM for a sequence whose numbers are not possible (a negative one,
+ *                more tokens than its table has room for, or, extending, than there are rows; trimming, more kept
+ *                than there are), TPS_ROW_NO_PAGES, else TPS_ROW_OK.  Sequences with either are left as they were.
+ *   page_size    16, 32, 64, 128 or 256.
+ * page_table, seq_len, free_pages and free_count are updated in place.
+ */
+typedef struct {
+    int32_t* page_table;
+    int32_t* seq_len;
+    const int32_t* change;
+    int32_t* free_pages;
+    int32_t* free_count;
+    int32_t* out_status;
+    int64_t B, table_width, table_ld, n_free;
+    int32_t page_size;
+} tps_kv_pages;
+
+/*
+ * tps_kv_extend -- room for `change` new tokens of each sequence, whose rows are packed in order into `tokens` rows.
+ * Pages come from the end of the list, for the first sequence first; once a sequence's do not suffice, no later one that
+ * needs any gets one.  Rows of a sequence that is refused, and those behind the last sequence's, get no slot.
+ *   slots        [tokens] int64: each row's slot in the cache, or -1 (for tps_kv_write).
+ *   positions    [tokens] int32: its position in its sequence (0 without a slot; for tps_qk_norm_rope).
+ *   cu_seqlens   [B + 1] int32: where each sequence's rows begin, and where the last one's end (for
+ *                tps_prompt_attention).  A sequence whose rows are more than there are has what is left.
+ * Calls with many rows draw 4 bytes for each sequence from the library's memory pool.
+ */
+int tps_kv_extend(const tps_kv_pages* pages, int64_t tokens, int64_t* slots, int32_t* positions, int32_t* cu_seqlens, void* stream);
+
+/*
+ * tps_kv_trim -- keep the first `change` tokens of each sequence (0: it has ended) and give the pages of the others
+ * back, such that a trim to the lengths before an extension restores the list entry for entry.
+ */
+int tps_kv_trim(const tps_kv_pages* pages, void* stream);
+
+/*
+ * tps_tree -- arguments of tps_tree_attention.
+ *   q            [B, n_nodes, n_q_heads, D] bfloat16, dense, 16-byte aligned; n_q_heads a multiple of the cache's
+ *                n_heads (query head i reads key head i / (n_q_heads / n_heads)).
+ *   out          [B, n_nodes, n_q_heads, D] bfloat16, dense, 16-byte aligned.
+ *   out_lse      [B, n_nodes, n_q_heads] float or NULL: ln of the sum of e^{scale q.k} (-inf: no token).
+ *   page_table   [B, table_width] int32: the pages of each sequence's tokens (ld table_ld).
+ *   seq_len      [B] int32: tokens of each sequence in the cache, its drafted ones among them (the last ones).
+ *   tree_len     [B] int32: how many those are, at most n_nodes, or NULL: n_nodes.  A node past them yields 0 and the
+ *                log-sum -inf, and its bits count for nothing.
+ *   tree         [B, n_nodes] uint64 (ld tree_ld; 0: one tree for all): bit j of node i is set where i sees node j (mostly
+ *                itself and those above it).  Node i sees all tokens before the tree, too.
+ *   n_nodes      1 .. 64.      scale  of the products q.k.
+ *   out_status   [B] int32 or NULL: TPS_ROW_BAD_PARAM where a page of a token lies outside [0, n_pages), seq_len outside
+ *                [0, table_width * page_size] or tree_len outside [0, min(n_nodes, seq_len)] (its outputs are NaN),
+ *                TPS_ROW_TIMEOUT where a wait ran out (one second) beside any of the sequence's work (the
+ *                outputs that it kept from being computed are NaN), else TPS_ROW_OK.
+ *   workspace    device memory of tps_tree_attention_workspace bytes, 256-byte aligned, or NULL: taken from the
+ *                library's stream-ordered pool and returned on the call's stream.
+ */
+typedef struct {
+    const void* q;
+    void* out;
+    float* out_lse;
+    const int32_t* page_table;
+    const int32_t* seq_len;
+    const int32_t* tree_len;
+    const uint64_t* tree;
+    int32_t* out_status;
+    void* workspace;
+    int64_t workspace_bytes;
+    int64_t B, table_width, table_ld, tree_ld;
+    int32_t n_nodes, n_q_heads;
+    float scale;
+} tps_tree;
+
+/*
+ * tps_tree_attention -- softmax attention of each sequence's drafted tokens over its tokens in `cache` (head_dim 64 or
+ * 128) and over each other as the tree says: one node is a decode step, a chain the verification of one draft, a
+ * tree that of several at once.  All nodes and query heads of a key head share each of its keys and values.
+ * Precision as tps_prefix_attention.  Not accepted (TPS_ERR_ARG): more than 2^31 - 2^16 tokens of table_width pages, 2^31
+ * blocks of 128 tokens of all tables, key heads and tiles of 256 rows.  No result depends on another sequence's data,
+ * nor (beyond a rounding, in 8-bit formats) on tokens that are hidden from it or cache rows past a
+ * sequence's length, whatever they hold (an fp8 cache's NaN codes excepted, as there).
+ * Returns TPS_ERR_ARG / _ALIGN / _SCRATCH (workspace too small) / _CUDA.
+ */
+int tps_tree_attention(const tps_kv_cache* cache, const tps_tree* args, void* stream);
+
+/* tps_tree_attention_stall_test -- a test hook for the bounded waits, as tps_prefix_attention_stall_test.  What shares an SM
+ * with the stalled head's work is NaN, too. */
+int tps_tree_attention_stall_test(const tps_kv_cache* cache, const tps_tree* args, int stall_head, uint64_t wait_ns, void* stream);
+
+/* Bytes of workspace tps_tree_attention needs for these arguments on the current device (pointers are not looked
+ * at), or -1 for arguments it would reject: two pieces for each SM, 39 MB at most.  Host-only query. */
+int64_t tps_tree_attention_workspace(const tps_kv_cache* cache, const tps_tree* args);
+
+/*
+ * tps_prompt -- arguments of tps_prompt_attention.  Strides are in elements, multiples of 8; the last axis (one
+ * head's D components) is contiguous.
+ *   q            [T, n_q_heads, D] bfloat16, 16-byte aligned; n_q_heads a multiple of n_k_heads (query head i
+ *                reads key head i / (n_q_heads / n_k_heads)).
+ *   k, v         [T, n_k_heads, D] bfloat16, 16-byte aligned.
+ *   *_ld, *_hd   token and head strides, e.g. of one fused projection's output; at least D where the axis has
+ *                more than one element.
+ *   out          [T, n_q_heads, D] bfloat16, dense, 16-byte aligned.
+ *   out_lse      [T, n_q_heads] float or NULL: ln of the sum of e^{scale q.k}.
+ *   cu_seqlens   [B + 1] int32: sequence b's tokens are the rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1.  Rows that
+ *                belong to no sequence are neither computed nor written.
+ *   scale        of the products q.k.
+ *   out_status   [B] int32 or NULL: TPS_ROW_BAD_PARAM where the bounds are not in order (a bound outside [0, T] or below
+ *                an earlier one: nothing of that sequence is written), TPS_ROW_TIMEOUT where a wait ran out (one
+ *                second) for any part of the sequence (the outputs of that part are NaN), else TPS_ROW_OK.
+ */
+typedef struct {
+    const void* q;
+    const void* k;
+    const void* v;
+    void* out;
+    float* out_lse;
+    const int32_t* cu_seqlens;
+    int32_t* out_status;
+    int64_t T, B;
+    int64_t q_ld, q_hd, k_ld, k_hd, v_ld, v_hd;
+    int32_t n_q_heads, n_k_heads, head_dim;
+    float scale;
+} tps_prompt;
+
+/*
+ * tps_prompt_attention -- causal softmax attention of B whole prompts, packed one behind another (head_dim 64 or
+ * 128): token t of a sequence sees its tokens 0 .. t.  Products are accumulated and softmax statistics held in
+ * float32; the weights are rounded to bfloat16 for the second product (at most 2^-8 of sum p |v|), the result once.
+ * No result depends on another sequence's rows, on later tokens or on rows of no sequence, whatever they hold.
+ * A call of more tiles than the device has SMs, or with out_status, draws a list of them (16 bytes for each 256 query
+ * rows of a key head, and for each sequence) from the library's memory pool.
+ * Not accepted (TPS_ERR_ARG): more than 2^31 - 2^16 tokens, or 2^31 triples of a key head, a sequence and 256 of its query rows.
+ * Returns TPS_ERR_ARG / _ALIGN / _CUDA.
+ */
+int tps_prompt_attention(const tps_prompt* args, void* stream);
+
+/* tps_prompt_attention_stall_test -- a test hook for the bounded waits, as tps_prefix_attention_stall_test: no key or
+ * value of key head `stall_head` (-1: none) is fetched.  What shares an SM with that head's work is NaN, too. */
+int tps_prompt_attention_stall_test(const tps_prompt* args, int stall_head, uint64_t wait_ns, void* stream);
 
 /* Kernels one tps_sample_kernel call with these arguments launches (0 for arguments the call would
  * reject): 1 for the cluster kernel alone; 2 for the streaming kernel (a one-CTA kernel clears its

@@ -19,10 +19,12 @@ import threading
 import torch
 
 from . import decode
-from .decode import KVCache, kv_read, kv_write, prefix_attention, prefix_attention_workspace, qk_norm_rope
+from .decode import (KVCache, kv_extend, kv_read, kv_trim, kv_write, prefix_attention, prefix_attention_workspace,
+                     prompt_attention, qk_norm_rope, tree_attention, tree_attention_workspace)
 
 __all__ = ["build", "load", "sample", "sample_rejection", "apply_penalties", "spec_accept", "qk_norm_rope", "KVCache", "kv_write",
-           "kv_read", "prefix_attention", "prefix_attention_workspace", "TPS_F32", "TPS_BF16", "ROW_STATUS", "library_path", "max_vocab",
+           "kv_read", "kv_extend", "kv_trim", "prefix_attention", "prefix_attention_workspace", "prompt_attention",
+           "tree_attention", "tree_attention_workspace", "TPS_F32", "TPS_BF16", "ROW_STATUS", "library_path", "max_vocab",
            "cluster_size", "kernels_per_call", "version"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -33,15 +35,17 @@ _INCLUDE = os.path.join(os.path.dirname(_HERE), "include")
 _SOURCES = ["tps_api.cu", "tps_k_cluster_f32.cu", "tps_k_cluster_bf16.cu", "tps_k_stream_f32.cu",
             "tps_k_stream_bf16.cu", "tps_k_penalty.cu", "tps_k_spec.cu", "tps_k_reject.cu",
             "tps_api_decode.cu", "tps_k_norm_rope.cu", "tps_k_kv.cu", "tps_k_attn_rows.cu",
-            "tps_k_attn_prefix_bf16.cu", "tps_k_attn_prefix_fp8.cu", "tps_k_attn_prefix_int8.cu"]
+            "tps_k_attn_prefix_bf16.cu", "tps_k_attn_prefix_fp8.cu", "tps_k_attn_prefix_int8.cu", "tps_k_attn_prompt.cu", "tps_k_pages.cu", "tps_k_attn_tree.cu",
+            "tps_k_attn_tree_bf16.cu", "tps_k_attn_tree_fp8.cu", "tps_k_attn_tree_int8.cu"]
 _HEADERS = ["tps_device.cuh", "tps_common.cuh", "tps_cluster.cuh", "tps_stream.cuh", "tps_penalty.cuh",
             "tps_spec.cuh", "tps_reject.cuh", "tps_kernels.h", "tps_decode.h", "tps_norm_rope.cuh", "tps_kv.cuh",
-            "tps_attn_rows.cuh", "tps_attn_prefix.cuh", "tps_attn_prefix_launch.cuh", "tps_tcgen05.cuh"]
+            "tps_attn_rows.cuh", "tps_attn_prefix.cuh", "tps_attn_prefix_launch.cuh", "tps_attn_prompt.cuh", "tps_pages.cuh",
+            "tps_attn_tree.cuh", "tps_tcgen05.cuh"]
 _NVCC = ["nvcc", "-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
          "-Xcompiler", "-fPIC"]
 
 TPS_F32, TPS_BF16 = 0, 1
-ROW_STATUS = {0: "ok", 1: "nan", 2: "all_masked", 3: "bad_param", 4: "timeout"}
+ROW_STATUS = {0: "ok", 1: "nan", 2: "all_masked", 3: "bad_param", 4: "timeout", 5: "no_pages"}
 _ERRORS = {1: "invalid argument", 2: "unknown dtype", 3: "vocabulary too large", 4: "misaligned pointer",
            5: "CUDA runtime error", 6: "more scratch than the fixed array of tps_sample_noalloc holds, or than the workspace given"}
 

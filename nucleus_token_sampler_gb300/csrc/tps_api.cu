@@ -545,6 +545,7 @@ const char* tps_status_string(int status)
     case 100 + TPS_ROW_ALL_MASKED: return "every logit of the row is -inf";
     case 100 + TPS_ROW_BAD_PARAM: return "temperature, top_p or min_p is not finite";
     case 100 + TPS_ROW_TIMEOUT: return "a bounded wait in the kernel gave up";
+    case 100 + TPS_ROW_NO_PAGES: return "too few free pages, or no room in their list";
     default: return "unknown status";
     }
 }

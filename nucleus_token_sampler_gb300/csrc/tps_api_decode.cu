@@ -121,6 +121,95 @@ int check_attention(const tps_kv_cache* c, const tps_attention* a, bool pointers
     return TPS_OK;
 }
 
+// A stride that a tensor map takes: whole 16-byte units, no two elements of the axis in one place.
+bool map_stride(int64_t elements, int64_t n, int D) { return n <= 1 || (elements >= D && elements % 8 == 0 && elements < (int64_t(1) << 38)); }
+
+// `tiles`: the most pairs of a sequence and 256 of its query rows (of one key head's group) there can be.
+int check_prompt(const tps_prompt* p, tps::PromptArgs* a, int64_t* tiles)
+{
+    if (!p) return TPS_ERR_ARG;
+    if (p->head_dim != 64 && p->head_dim != 128) return TPS_ERR_ARG;
+    if (p->T < 0 || p->T > kMaxTokens || p->B < 0 || p->B > INT32_MAX || p->n_k_heads < 1 || p->n_k_heads > kMaxHeads || p->n_q_heads < 1 ||
+        p->n_q_heads > kMaxHeads || p->n_q_heads % p->n_k_heads != 0 || !std::isfinite(p->scale))
+        return TPS_ERR_ARG;
+    if (p->B == 0) return TPS_OK;
+    if (!p->cu_seqlens || (p->T > 0 && (!p->q || !p->k || !p->v || !p->out))) return TPS_ERR_ARG;
+    if (!map_stride(p->q_ld, p->T, p->head_dim) || !map_stride(p->k_ld, p->T, p->head_dim) || !map_stride(p->v_ld, p->T, p->head_dim) ||
+        !map_stride(p->q_hd, p->n_q_heads, p->head_dim) || !map_stride(p->k_hd, p->n_k_heads, p->head_dim) ||
+        !map_stride(p->v_hd, p->n_k_heads, p->head_dim))
+        return TPS_ERR_ARG;
+    if (!aligned(p->q, 16) || !aligned(p->k, 16) || !aligned(p->v, 16) || !aligned(p->out, 16) || !aligned(p->out_lse, 4) ||
+        !aligned(p->cu_seqlens, 4) || !aligned(p->out_status, 4))
+        return TPS_ERR_ALIGN;
+    a->v = p->v, a->out = p->out, a->out_lse = p->out_lse, a->cu_seqlens = p->cu_seqlens, a->out_status = p->out_status;
+    a->T = p->T, a->B = p->B, a->v_ld = p->v_ld, a->v_hd = p->v_hd;
+    a->Hq = p->n_q_heads, a->G = p->n_q_heads / p->n_k_heads;
+    a->groups = (a->G + 127) / 128;
+    a->group = (a->G + a->groups - 1) / a->groups;
+    a->heads_v = p->n_k_heads * a->groups;
+    a->tile_tokens = 128 / a->group;
+    a->level_shift = 0;
+    while ((p->T / tps::kBlockKeys + 1) >> a->level_shift >= 2048) ++a->level_shift;
+    a->qk_scale = (float)((double)p->scale * 1.4426950408889634);
+    *tiles = p->T / (2 * a->tile_tokens) + p->B;
+    return *tiles > (INT32_MAX - 65536) / a->heads_v ? TPS_ERR_ARG : TPS_OK;
+}
+
+int check_tree(const tps_kv_cache* c, const tps_tree* t, bool pointers)
+{
+    if (!t) return TPS_ERR_ARG;
+    const int rc = check_cache(c, pointers);
+    if (rc != TPS_OK) return rc;
+    if (c->head_dim != 64 && c->head_dim != 128) return TPS_ERR_ARG;
+    if (t->B < 0 || t->table_width < 0 || t->table_width > kMaxTokens / c->page_size || t->table_ld < t->table_width || t->n_nodes < 1 ||
+        t->n_nodes > 64 || t->n_q_heads < 1 || t->n_q_heads > kMaxHeads || t->n_q_heads % c->n_heads != 0 ||
+        (t->tree_ld != 0 && t->tree_ld < t->n_nodes) || !std::isfinite(t->scale))
+        return TPS_ERR_ARG;
+    if (!pointers || t->B == 0) return TPS_OK;
+    if (!t->q || !t->out || !t->seq_len || !t->tree || (t->table_width > 0 && !t->page_table)) return TPS_ERR_ARG;
+    if (!aligned(t->q, 16) || !aligned(t->out, 16) || !aligned(t->out_lse, 4) || !aligned(t->page_table, 4) || !aligned(t->seq_len, 4) ||
+        !aligned(t->tree_len, 4) || !aligned(t->tree, 8) || !aligned(t->out_status, 4) || !aligned(t->workspace, 256))
+        return TPS_ERR_ALIGN;
+    return TPS_OK;
+}
+
+int plan_tree(const tps_kv_cache& c, const tps_tree& t, int sms, tps::TreePlan* out)
+{
+    tps::TreePlan p = {};
+    const int64_t R = (int64_t)t.n_nodes * (t.n_q_heads / c.n_heads);  // at most 2^22
+    p.R = (int)R;
+    p.tile_rows = R <= 128 ? 128 : 256;
+    p.n_tiles = (int)((R + p.tile_rows - 1) / p.tile_rows);
+    const int64_t items = (int64_t)p.n_tiles * c.n_heads;  // of a sequence
+    const int64_t most = std::max<int64_t>((t.table_width * c.page_size + tps::kBlockKeys - 1) / tps::kBlockKeys, 1) * items;
+    if (most > INT32_MAX || t.B > INT32_MAX / most) return TPS_ERR_ARG;
+    p.ctas = (int)std::min<int64_t>(sms, most * t.B);
+    p.off_ml = (size_t)2 * p.ctas * p.tile_rows * c.head_dim * sizeof(float);
+    p.off_rec = p.off_ml + (size_t)2 * p.ctas * p.tile_rows * sizeof(float2);
+    p.bytes = p.off_rec + (size_t)p.ctas * sizeof(tps::TreeRecord);
+    *out = p;
+    return TPS_OK;
+}
+
+int check_pages(const tps_kv_pages* p, tps::PagesArgs* a)
+{
+    if (!p) return TPS_ERR_ARG;
+    const int ps = p->page_size;
+    if (ps < 16 || ps > 256 || (ps & (ps - 1)) != 0 || p->B < 0 || p->B > INT32_MAX || p->table_width < 0 ||
+        p->table_width > kMaxTokens / ps || p->table_ld < p->table_width || p->n_free < 0 || p->n_free > INT32_MAX)
+        return TPS_ERR_ARG;
+    if (!p->free_count || (p->n_free > 0 && !p->free_pages) || (p->B > 0 && (!p->seq_len || !p->change || (p->table_width > 0 && !p->page_table))))
+        return TPS_ERR_ARG;
+    if (!aligned(p->page_table, 4) || !aligned(p->seq_len, 4) || !aligned(p->change, 4) || !aligned(p->free_pages, 4) ||
+        !aligned(p->free_count, 4) || !aligned(p->out_status, 4))
+        return TPS_ERR_ALIGN;
+    a->p = *p;
+    a->page_shift = 4;
+    while ((1 << a->page_shift) < ps) ++a->page_shift;
+    a->page_mask = ps - 1;
+    return TPS_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -245,6 +334,108 @@ int tps_prefix_attention_stall_test(const tps_kv_cache* cache, const tps_attenti
         const cudaError_t ef = cudaFreeAsync(ws, st);
         if (e == cudaSuccess) e = ef;
     }
+    return e == cudaSuccess ? TPS_OK : tps::report_cuda(e);
+}
+
+int64_t tps_tree_attention_workspace(const tps_kv_cache* cache, const tps_tree* args)
+{
+    if (check_tree(cache, args, false) != TPS_OK) return -1;
+    if (args->B == 0) return 0;
+    int sms = 0;
+    tps::TreePlan p;
+    if (!tps::host_sms(&sms) || plan_tree(*cache, *args, sms, &p) != TPS_OK) return -1;
+    return (int64_t)p.bytes;
+}
+
+int tps_tree_attention(const tps_kv_cache* cache, const tps_tree* args, void* stream)
+{
+    return tps_tree_attention_stall_test(cache, args, -1, tps::kAttnWaitNs, stream);
+}
+
+int tps_tree_attention_stall_test(const tps_kv_cache* cache, const tps_tree* args, int stall_head, uint64_t wait_ns, void* stream)
+{
+    if (wait_ns < 1 || wait_ns > tps::kAttnWaitNs) return TPS_ERR_ARG;
+    int rc = check_tree(cache, args, true);
+    if (rc != TPS_OK) return rc;
+    if (args->B == 0) return TPS_OK;
+    int sms = 0;
+    if (!tps::host_sms(&sms)) return tps::report_cuda(cudaGetLastError());
+    tps::TreeArgs a = {};
+    rc = plan_tree(*cache, *args, sms, &a.p);
+    if (rc != TPS_OK) return rc;
+    a.c = *cache;
+    a.a = *args;
+    a.stall_head = stall_head;
+    a.wait_ns = wait_ns;
+    a.G = args->n_q_heads / cache->n_heads;
+    a.page_shift = 4;
+    while ((1 << a.page_shift) < cache->page_size) ++a.page_shift;
+    a.qk_scale = (float)((double)args->scale * 1.4426950408889634);
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    unsigned char* ws = static_cast<unsigned char*>(args->workspace);
+    cudaError_t e = cudaSuccess;
+    if (ws) {
+        if (args->workspace_bytes < (int64_t)a.p.bytes) return TPS_ERR_SCRATCH;
+    } else {
+        void* mem = nullptr;
+        e = tps::pool_alloc(&mem, a.p.bytes, st);
+        if (e != cudaSuccess) return tps::report_cuda(e);
+        ws = static_cast<unsigned char*>(mem);
+    }
+    a.part = reinterpret_cast<float*>(ws);
+    a.ml = reinterpret_cast<float2*>(ws + a.p.off_ml);
+    a.rec = reinterpret_cast<tps::TreeRecord*>(ws + a.p.off_rec);
+    e = cache->format == TPS_KV_BF16  ? tps::launch_attn_tree_bf16(a, st)
+        : cache->format == TPS_KV_FP8 ? tps::launch_attn_tree_fp8(a, st)
+                                      : tps::launch_attn_tree_int8(a, st);
+    if (e == cudaSuccess) e = tps::launch_tree_join(a, st);
+    if (!args->workspace) {
+        const cudaError_t ef = cudaFreeAsync(ws, st);
+        if (e == cudaSuccess) e = ef;
+    }
+    return e == cudaSuccess ? TPS_OK : tps::report_cuda(e);
+}
+
+int tps_kv_extend(const tps_kv_pages* pages, int64_t tokens, int64_t* slots, int32_t* positions, int32_t* cu_seqlens, void* stream)
+{
+    tps::PagesArgs a = {};
+    const int rc = check_pages(pages, &a);
+    if (rc != TPS_OK) return rc;
+    if (tokens < 0 || tokens > INT32_MAX || !cu_seqlens || (tokens > 0 && (!slots || !positions))) return TPS_ERR_ARG;
+    if (!aligned(slots, 8) || !aligned(positions, 4) || !aligned(cu_seqlens, 4)) return TPS_ERR_ALIGN;
+    a.tokens = tokens, a.slots = slots, a.positions = positions, a.cu_seqlens = cu_seqlens;
+    const cudaError_t e = tps::launch_kv_extend(a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? TPS_OK : tps::report_cuda(e);
+}
+
+int tps_kv_trim(const tps_kv_pages* pages, void* stream)
+{
+    tps::PagesArgs a = {};
+    const int rc = check_pages(pages, &a);
+    if (rc != TPS_OK) return rc;
+    if (pages->B == 0) return TPS_OK;
+    const cudaError_t e = tps::launch_kv_trim(a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? TPS_OK : tps::report_cuda(e);
+}
+
+int tps_prompt_attention(const tps_prompt* args, void* stream)
+{
+    return tps_prompt_attention_stall_test(args, -1, tps::kAttnWaitNs, stream);
+}
+
+int tps_prompt_attention_stall_test(const tps_prompt* args, int stall_head, uint64_t wait_ns, void* stream)
+{
+    if (wait_ns < 1 || wait_ns > tps::kAttnWaitNs) return TPS_ERR_ARG;
+    tps::PromptArgs a = {};
+    int64_t tiles = 0;
+    const int rc = check_prompt(args, &a, &tiles);
+    if (rc != TPS_OK) return rc;
+    if (args->B == 0 || (args->T == 0 && !args->out_status)) return TPS_OK;
+    int sms = 0;
+    if (!tps::host_sms(&sms)) return tps::report_cuda(cudaGetLastError());
+    a.stall_head = stall_head;
+    a.wait_ns = wait_ns;
+    const cudaError_t e = tps::launch_attn_prompt(a, *args, tiles, sms, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? TPS_OK : tps::report_cuda(e);
 }
 

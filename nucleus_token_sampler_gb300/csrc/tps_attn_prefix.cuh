@@ -47,6 +47,7 @@
 #include <cuda_fp16.h>
 
 #include "tps_attn_rows.cuh"
+#include "tps_attn_tree.cuh"
 #include "tps_decode.h"
 #include "tps_tcgen05.cuh"
 
@@ -79,6 +80,9 @@ template <int D, int kFormat, int kTiles> struct PrefixShape {
         uint64_t raw_full[kRaw], factor_full[kRaw], raw_empty[kRaw], scalar_full[kScalars];
         uint32_t tmem;
         int abort, bad;
+        TreeStart start;          // of trees: where this CTA's line begins
+        int64_t sums[kThreads / 32];
+        int marks[kTreeMarks];    // by item: kMark*
         float key_unit[kScalars], value_exp[kScalars];
         int wide[kScalars];  // 1: the block's keys, 2: its values
         // Of the block's tokens: keys' scales (int8, or wide), values' in the block's unit, at most 1 (int8), or one over
@@ -90,12 +94,6 @@ template <int D, int kFormat, int kTiles> struct PrefixShape {
         (size_t)(kTiles + kRing) * kTileBytes + (k8 ? (size_t)kRaw * kRawBytes : 0) + sizeof(Control) + 1024;
     static_assert(kSmem <= 232448, "fits one CTA's shared memory");
 };
-
-// Byte of 16-byte chunk c of row r in a tile: 64-element column blocks of 128 rows, 128-byte swizzle.
-__device__ __forceinline__ uint32_t tile_byte(int r, int c)
-{
-    return (uint32_t)((c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-}
 
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
 {
@@ -137,16 +135,22 @@ struct Way {
         head = item / p.n_tiles;
         tile = item - head * p.n_tiles;
     }
-    __device__ __forceinline__ int blocks(const AttnPlan& p) const { return min(left, p.nblk - block); }  // of this item
-    __device__ __forceinline__ void next(const AttnPlan& p)
+    __device__ __forceinline__ explicit Way(const AttnArgs& a, const TreeStart&) : Way(a.p) {}
+    __device__ __forceinline__ int blocks(const AttnArgs& a) const { return min(left, a.p.nblk - block); }  // of this item
+    __device__ __forceinline__ int tokens(const AttnArgs& a) const { return (int)a.a.prefix_len; }
+    __device__ __forceinline__ int open(const AttnArgs& a) const { return (int)a.a.prefix_len; }  // tokens that every row sees
+    __device__ __forceinline__ const int32_t* pages(const AttnArgs& a) const { return a.a.prefix_pages; }
+    __device__ __forceinline__ void next(const AttnArgs& a)
     {
-        left -= blocks(p);
+        const AttnPlan& p = a.p;
+        left -= blocks(a);
         block = 0;
         ++item;
         if (++tile == p.n_tiles) tile = 0, ++head;
     }
-    __device__ __forceinline__ void step(const AttnPlan& p)  // one block on
+    __device__ __forceinline__ void step(const AttnArgs& a)  // one block on
     {
+        const AttnPlan& p = a.p;
         --left;
         if (++block == p.nblk) {
             block = 0;
@@ -167,10 +171,25 @@ template <int kSlots> struct Turn {
     }
 };
 
-template <int D, int kFormat, int kTiles>
+__device__ __forceinline__ int way_item(const Way& w) { return w.item; }
+__device__ __forceinline__ int way_item(const TreeWay&) { return 0; }  // never asked for
+
+// kTree: not one shared prefix, but each sequence's own tokens, the last of which are a tree (tps_attn_tree.cuh).
+template <bool kTree> struct LineOf {
+    using Args = AttnArgs;
+    using Walk = Way;
+};
+template <> struct LineOf<true> {
+    using Args = TreeArgs;
+    using Walk = TreeWay;
+};
+
+template <int D, int kFormat, int kTiles, bool kTree>
 __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
-    attn_prefix_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap)
+    attn_prefix_kernel(const __grid_constant__ typename LineOf<kTree>::Args a, const __grid_constant__ CUtensorMap kmap,
+                       const __grid_constant__ CUtensorMap vmap)
 {
+    using Walk = typename LineOf<kTree>::Walk;
     using Shape = PrefixShape<D, kFormat, kTiles>;
     using Control = typename Shape::Control;
     constexpr bool k8 = Shape::k8;
@@ -182,9 +201,8 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
     unsigned char* raw_ring = ring + kRing * Shape::kTileBytes;
     Control& ctl = *reinterpret_cast<Control*>(raw_ring + (k8 ? kRaw * Shape::kRawBytes : 0));
 
-    const AttnPlan& p = a.p;
+    const auto& p = a.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int prefix = (int)a.a.prefix_len;
 
     if (threadIdx.x == 0) {
         mbar_init(&ctl.q_full, 4 * kTiles);
@@ -202,11 +220,12 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
         fence_proxy_async();
     }
     if (warp == Shape::kMmaWarp) tmem_alloc(&ctl.tmem, Shape::kTmemCols);
+    if constexpr (kTree) tree_start<Shape::kThreads>(a, ctl.start, ctl.sums);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ctl.tmem;
-    clear_status(a);
+    if constexpr (!kTree) clear_status(a);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     volatile int* abort_flag = &ctl.abort;
@@ -243,10 +262,12 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
         unsigned char* my_q = q_tile + m * Shape::kTileBytes;
         uint32_t s_parity = 0, o_parity = 0;
         Turn<kScalars> scalar(0);
+        [[maybe_unused]] TreeRecord record;
+        if constexpr (kTree) record.begin(ctl.start.seq);
         const uint32_t sign = a.qk_scale < 0.f ? 0x80008000u : 0u;
         const float unit = fabsf(a.qk_scale);
-        Way way(p);
-        for (; way.left > 0 && alive; way.next(p)) {
+        Walk way(a, ctl.start);
+        for (; way.left > 0 && alive; way.next(a)) {
             // The warp's 32 query rows, D / 8 lanes to a row: as they are (bf16) or brought into float16's range.
             float row_unit = unit;
             {
@@ -257,8 +278,10 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
                 const int64_t bt = first <= 0x7FFFFFFF ? (uint32_t)first / (uint32_t)a.G : first / a.G;
                 int gi = (int)(first - bt * a.G);
                 const int wraps = kRows / a.G, rem = kRows - wraps * a.G;
+                int64_t ahead = bt;  // query tokens ahead of the row's
+                if constexpr (kTree) ahead += (int64_t)way.seq * a.a.n_nodes;
                 const __nv_bfloat16* src =
-                    static_cast<const __nv_bfloat16*>(a.a.q) + bt * row_elems + ((int64_t)way.head * a.G + gi) * D + piece * 8;
+                    static_cast<const __nv_bfloat16*>(a.a.q) + ahead * row_elems + ((int64_t)way.head * a.G + gi) * D + piece * 8;
                 // All on their way at once, straight to their places; loops and not unrolled code, whose instructions
                 // would be fetched for this one use.
                 auto place = [&](int i) { return my_q + tile_byte((warp & 3) * 32 + i * kRows + sub, piece); };
@@ -320,7 +343,10 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
                 if (lane == 0) mbar_arrive(&ctl.q_full);
             }
             float ref = neg, sum = 0.f;
-            const int blocks = way.blocks(p);
+            const int blocks = way.blocks(a), in_item = way.tile * (128 * kTiles) + in_tile;
+            [[maybe_unused]] TreeRow mine = {};
+            if constexpr (kTree) mine = tree_row(a, way, in_item);
+            [[maybe_unused]] const bool idle = in_item - lane >= p.R;
             for (int v = 0; v < blocks; ++v) {
                 if (!(alive = wait_all(&ctl.s_full[m], s_parity))) break;
                 s_parity ^= 1;
@@ -336,8 +362,13 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
                     wide = ctl.wide[scalar.slot];
                     scalar.next();
                 }
+                if (kTree && idle) {  // no row of the warp is a query's
+                    tc_fence_before();
+                    mbar_arrive(&ctl.p_full[m]);
+                    continue;
+                }
                 c = fmaxf(c, 0x1p-126f);  // never 0: a masked score, -inf, times it stays -inf (any other times that is nothing)
-                const int left = prefix - (way.block + v) * kBlockKeys;
+                const int left = way.tokens(a) - (way.block + v) * kBlockKeys, open = way.open(a) - (way.block + v) * kBlockKeys;
                 float2 total = make_float2(0.f, 0.f);
                 // int8: a score's key scale (the codes are in the tile as they are).  Scores past the prefix become -inf.
                 auto ready = [&](float (&s)[32], int ch) {
@@ -351,7 +382,13 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
                             s[4 * i] = y.x, s[4 * i + 1] = y.y, s[4 * i + 2] = z.x, s[4 * i + 3] = z.y;
                         }
                     }
-                    if (left < ch * 32 + 32) {
+                    if (kTree && open < ch * 32 + 32) {
+                        const uint32_t seen = tree_seen(mine.seen, ch * 32 - open);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (!(seen >> i & 1)) s[i] = neg;
+                    }
+                    if (!kTree && left < ch * 32 + 32) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             if (ch * 32 + i >= left) s[i] = neg;
@@ -494,8 +531,17 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
             }
             if (alive) alive = wait_all(&ctl.o_full[m], o_parity);
             o_parity ^= 1;
-            const int64_t piece = (int64_t)blockIdx.x + way.item;
-            if (alive) {
+            if constexpr (kTree) {
+                if (!alive) break;
+                tc_fence_after();
+                tree_output<D, kFormat>(a, way, blocks, mine, in_tile, in_item, o_addr, ref, sum,
+                                        *(volatile int*)&ctl.marks[way.ordinal % kTreeMarks] | (way.bad ? kMarkBad : 0));
+                tc_fence_before();
+                record.note(way.seq, way.head * p.n_tiles + way.tile, way.block, way.block + blocks == way.nblk);
+                continue;
+            }
+            [[maybe_unused]] const int64_t piece = kTree ? 0 : (int64_t)blockIdx.x + way_item(way);
+            if (!kTree && alive) {
                 tc_fence_after();
                 float4* dst = reinterpret_cast<float4*>(a.part + piece * p.tile_rows * D) + in_tile;
 #pragma unroll 1
@@ -509,11 +555,20 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
                 }
                 tc_fence_before();
             }
-            a.ml[piece * p.tile_rows + in_tile] = make_float2(ref, !alive ? kPieceTimeout : (*(volatile int*)&ctl.bad ? kPieceBadPage : sum));
+            if (!kTree) a.ml[piece * p.tile_rows + in_tile] = make_float2(ref, !alive ? kPieceTimeout : (*(volatile int*)&ctl.bad ? kPieceBadPage : sum));
         }
-        if (!alive)  // the pieces of the items that were not reached
-            for (Way rest(p); rest.left > 0; rest.next(p))
-                a.ml[((int64_t)blockIdx.x + rest.item) * p.tile_rows + in_tile] = make_float2(neg, kPieceTimeout);
+        if constexpr (kTree) {
+            if (!alive)  // all that the CTA had to do
+                for (Walk rest(a, ctl.start); rest.left > 0; rest.next(a)) {
+                    tree_give_up<D>(a, rest, in_tile);
+                    record.note(rest.seq, rest.head * p.n_tiles + rest.tile, rest.block, rest.block + rest.blocks(a) == rest.nblk);
+                }
+            record.timeout = !alive;
+            if (in_tile == 0) a.rec[blockIdx.x] = record;
+        } else if (!alive) {  // the pieces of the items that were not reached
+            for (Walk rest(a, ctl.start); rest.left > 0; rest.next(a))
+                a.ml[((int64_t)blockIdx.x + way_item(rest)) * p.tile_rows + in_tile] = make_float2(neg, kPieceTimeout);
+        }
     } else if (warp == Shape::kMmaWarp) {
         // ---------------------------------------------------------------------------- products
         // The whole warp walks along and one lane issues: a hand-over costs a few instructions, and the
@@ -541,9 +596,9 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
                 tc_commit(&ctl.s_full[m]);
             }
         };
-        Way way(p);
-        for (; way.left > 0 && alive; way.next(p)) {
-            const int blocks = way.blocks(p);
+        Walk way(a, ctl.start);
+        for (; way.left > 0 && alive; way.next(a)) {
+            const int blocks = way.blocks(a);
             if (!(alive = wait_all(&ctl.q_full, q_parity))) break;
             q_parity ^= 1;
             int kslot = take();
@@ -555,7 +610,7 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
             for (int v = 0; v < blocks && alive; ++v) {
                 const int vslot = take();
                 if (!alive) break;
-                if (!k8 && prefix < (way.block + v + 1) * kBlockKeys) {  // its rows past the prefix are zeroed
+                if (!k8 && way.open(a) < (way.block + v + 1) * kBlockKeys) {  // its rows that not every query sees are dealt with
                     if (!(alive = wait_all(&ctl.tail[vslot], tail_parity >> vslot & 1))) break;
                     tail_parity ^= 1u << vslot;
                 }
@@ -599,21 +654,34 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
         uint64_t* filled = k8 ? ctl.raw_full : ctl.full;
         uint64_t* freed = k8 ? ctl.raw_empty : ctl.empty;
         const int box = min(a.c.page_size, kBlockKeys), boxes = kBlockKeys / box;
-        auto page_of = [&](int token) { return lane < boxes && token < prefix ? a.a.prefix_pages[token >> a.page_shift] : 0; };
-        Way way(p);
-        int page = page_of(way.block * kBlockKeys + lane * box);
+        Walk way(a, ctl.start);
+        auto page_of = [&](int token) { return lane < boxes && token < way.tokens(a) ? way.pages(a)[token >> a.page_shift] : 0; };
+        int page = way.left > 0 ? page_of(way.block * kBlockKeys + lane * box) : 0;
+        [[maybe_unused]] int item = -1;
         Turn<kSlots> turn(1);  // a slot's first fill waits for nothing: the phase before its first
         int fills = 0;
         while (way.left > 0 && alive && way.head != a.stall_head) {
-            const int head = way.head, token = way.block * kBlockKeys, left = prefix - token;
+            const int head = way.head, token = way.block * kBlockKeys, left = way.tokens(a) - token, open = way.open(a) - token;
             const int live = min(boxes, (left + box - 1) / box);
+            [[maybe_unused]] int* mark = nullptr;
+            if constexpr (kTree) {
+                mark = &ctl.marks[way.ordinal % kTreeMarks];
+                if (item != way.ordinal) {
+                    item = way.ordinal;
+                    if (lane == 0) *(volatile int*)mark = 0;
+                    __syncwarp();
+                }
+            }
             const int row = (token + lane * box) & (a.c.page_size - 1);
             int id = page;
             if (id < 0 || id >= a.c.n_pages) {
-                *(volatile int*)&ctl.bad = 1;
+                if constexpr (kTree)
+                    atomicOr(mark, kMarkBad);
+                else
+                    *(volatile int*)&ctl.bad = 1;
                 id = 0;
             }
-            way.step(p);
+            way.step(a);
             if (way.left > 0) page = page_of(way.block * kBlockKeys + lane * box);  // the next block's, not looked at before it is needed
             for (int kv = 0; kv < 2; ++kv) {
                 if (!(alive = wait_all(&freed[turn.slot], turn.parity))) break;
@@ -636,11 +704,14 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
                 const int slot = turn.slot;
                 turn.next();
                 ++fills;
-                if (!k8 && kv && left < kBlockKeys) {
+                if (!k8 && kv && open < kBlockKeys) {
                     // Rows past the prefix hold anything (0 * NaN is NaN): zero them once the copy has landed.  Each slot has
                     // a signal of its own: its next one comes after the slot was given back, so after this one's wait.  One
                     // signal for all could complete two phases before the first was waited for, where items are one block long.
                     if (!(alive = wait_all(bar, parity))) break;
+                    if constexpr (kTree) {  // a drafted token is hidden from some rows: what is not finite is added by those that see it
+                        if (hide_not_finite<D>(dst, max(open, 0), left)) atomicOr(mark, kMarkNotFinite);
+                    }
                     for (int i = lane; i < (kBlockKeys - left) * (D / 8); i += 32)
                         *reinterpret_cast<uint4*>(dst + tile_byte(left + i / (D / 8), i % (D / 8))) = make_uint4(0u, 0u, 0u, 0u);
                     fence_proxy_async();
@@ -659,11 +730,11 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
         // unit is the factor of its codes.  int8: the scores and the weights take the scales.  A unit is at least 2^-80
         // (kLeastScale), so that the sum, which is divided by the values', stays finite.  One warp for every tile in
         // turn: a barrier's phase may only be waited for by a role that sees each of its phases.
-        Way way(p);
+        Walk way(a, ctl.start);
         Turn<kRaw> raw_turn(0);
         Turn<kScalars> scalar(0);
-        for (; way.left > 0 && alive; way.step(p), scalar.next()) {
-            const int left = prefix - way.block * kBlockKeys;
+        for (; way.left > 0 && alive; way.step(a), scalar.next()) {
+            const int left = way.tokens(a) - way.block * kBlockKeys;
             int wide = 0;
 #pragma unroll
             for (int kv = 0; kv < 2; ++kv, raw_turn.next()) {
@@ -688,7 +759,8 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
                     const uint32_t least = __reduce_min_sync(0xFFFFFFFFu, odd ? 0u : min(low >> 16, low & 0xFFFFu)) + 1;
                     const int e = most ? max(-80, min((int)((most + (kFormat == TPS_KV_INT8 ? 0x7Fu : 0u)) >> 7) - 127, 126)) : 0;
                     const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-                    const bool far = least < (uint32_t)(e + 127 - kSpread) << 7;
+                    // Trees: a value's scale that is not finite must not meet the weight 0 of a row that does not see the token.
+                    const bool far = least < (uint32_t)(e + 127 - kSpread) << 7 || (kTree && most >= 0x7F80u);
                     float f[4];  // in the block's unit
 #pragma unroll
                     for (int i = 0; i < 4; ++i) f[i] = s[i] * inv;
@@ -738,11 +810,11 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
         // the eight hit different banks.
         const int piece = kPieces == 8 ? (t & 3) + 4 * ((t >> 2 ^ t >> 3) & 1) : t % kPieces;
         const int sub = kPieces == 8 ? (t >> 5) * 4 + (t >> 4 & 1) * 2 + (t >> 2 & 1) : t / kPieces;
-        Way way(p);
+        Walk way(a, ctl.start);
         Turn<kRaw> raw_turn(0);
         Turn<kRing> turn(1);
-        for (; way.left > 0 && alive; way.step(p)) {
-            const int left = prefix - way.block * kBlockKeys;
+        for (; way.left > 0 && alive; way.step(a)) {
+            const int left = way.tokens(a) - way.block * kBlockKeys;
 #pragma unroll 1
             for (int kv = 0; kv < 2; ++kv, raw_turn.next(), turn.next()) {
                 const int rs = raw_turn.slot;

@@ -1,5 +1,5 @@
-// tps_attn_prefix_launch.cuh -- launch of the tcgen05 prefix kernel for one cache format (each format is
-// a translation unit of its own).
+// tps_attn_prefix_launch.cuh -- launch of the tcgen05 prefix and tree kernels for one cache format (each
+// format of either is a translation unit of its own).
 #pragma once
 
 #include <atomic>
@@ -38,11 +38,11 @@ inline cudaError_t encode_cache(CUtensorMap* map, const tps_kv_cache& c, void* b
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int D, int kFormat, int kTiles>
-cudaError_t launch_prefix_shape(const AttnArgs& a, cudaStream_t stream)
+template <int D, int kFormat, int kTiles, bool kTree>
+cudaError_t launch_prefix_shape(const typename LineOf<kTree>::Args& a, cudaStream_t stream)
 {
     using Shape = PrefixShape<D, kFormat, kTiles>;
-    auto k = attn_prefix_kernel<D, kFormat, kTiles>;
+    auto k = attn_prefix_kernel<D, kFormat, kTiles, kTree>;
     static std::atomic<uint64_t> allowed{0};  // devices on which the shared memory has been asked for
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -68,13 +68,13 @@ cudaError_t launch_prefix_shape(const AttnArgs& a, cudaStream_t stream)
     return cudaGetLastError();
 }
 
-template <int kFormat>
-cudaError_t launch_prefix_format(const AttnArgs& a, cudaStream_t stream)
+template <int kFormat, bool kTree>
+cudaError_t launch_prefix_format(const typename LineOf<kTree>::Args& a, cudaStream_t stream)
 {
     const bool two = a.p.tile_rows == 256;
     if (a.c.head_dim == 64)
-        return two ? launch_prefix_shape<64, kFormat, 2>(a, stream) : launch_prefix_shape<64, kFormat, 1>(a, stream);
-    return two ? launch_prefix_shape<128, kFormat, 2>(a, stream) : launch_prefix_shape<128, kFormat, 1>(a, stream);
+        return two ? launch_prefix_shape<64, kFormat, 2, kTree>(a, stream) : launch_prefix_shape<64, kFormat, 1, kTree>(a, stream);
+    return two ? launch_prefix_shape<128, kFormat, 2, kTree>(a, stream) : launch_prefix_shape<128, kFormat, 1, kTree>(a, stream);
 }
 
 }  // namespace tps

@@ -81,4 +81,82 @@ cudaError_t launch_attn_prefix_fp8(const AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_attn_prefix_int8(const AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_attn_own(const AttnArgs& a, bool after_prefix, cudaStream_t stream);
 
+
+// A tree-attention call (tps_attn_tree.cuh): an item is one sequence, key head and `tile_rows` of the R = n_nodes G rows.
+struct TreePlan {
+    int R, tile_rows, n_tiles, ctas;
+    size_t off_ml, off_rec, bytes;
+};
+struct TreeRecord;
+struct TreeArgs {
+    tps_kv_cache c;
+    tps_tree a;
+    TreePlan p;
+    int G, page_shift;
+    float qk_scale;
+    float* part;      // [2 ctas][D / 4][tile_rows][4], as AttnArgs
+    float2* ml;       // [2 ctas, tile_rows]
+    TreeRecord* rec;  // [ctas]
+    int stall_head;
+    uint64_t wait_ns;
+};
+// What a CTA leaves for the join.
+struct TreeRecord {
+    int open_seq, open_item;   // the item that it began and did not finish: piece 1 of its two (-1: none)
+    int continued, ended;      // its first item began in an earlier CTA: piece 0; and ends here
+    int first_seq, last_seq;   // sequences that it had any part of
+    int timeout;
+    int spare;
+#ifdef __CUDACC__
+    __device__ __forceinline__ void begin(int seq) { open_seq = -1, open_item = continued = ended = timeout = spare = 0, first_seq = last_seq = seq; }
+    __device__ __forceinline__ void note(int seq, int item, int block, bool end)  // a part of an item
+    {
+        last_seq = seq;
+        if (block > 0) continued = 1, ended = end;
+        if (block == 0 && !end) open_seq = seq, open_item = item;
+    }
+#endif
+};
+constexpr int kTreeJoinRows = 32;
+cudaError_t launch_attn_tree_bf16(const TreeArgs& a, cudaStream_t stream);
+cudaError_t launch_attn_tree_fp8(const TreeArgs& a, cudaStream_t stream);
+cudaError_t launch_attn_tree_int8(const TreeArgs& a, cudaStream_t stream);
+cudaError_t launch_tree_join(const TreeArgs& a, cudaStream_t stream);
+
+// One prompt-attention call (tps_attn_prompt.cuh).
+struct PromptArgs {
+    const void* v;
+    void* out;
+    float* out_lse;
+    const int32_t* cu_seqlens;
+    int32_t* out_status;
+    int64_t T, B, v_ld, v_hd;
+    int Hq, G;                // query heads, of one key head
+    int group, groups;        // of them in one tile; such groups of a key head
+    int heads_v;              // groups of all key heads
+    int tile_tokens;          // query tokens of a tile of 128 rows
+    int level_shift;          // lengths in blocks are sorted by their bits from here on
+    float qk_scale;           // scale * log2(e)
+    const int4* list;         // tiles (a sequence's begin and end, the first token, the sequence), longest first; or NULL: each
+    const int* n_tiles;       // CTA finds its only one
+    int stall_head;           // as in AttnArgs
+    uint64_t wait_ns;
+};
+// `tiles`: the most there can be.
+cudaError_t launch_attn_prompt(const PromptArgs& a, const tps_prompt& p, int64_t tiles, int sms, cudaStream_t stream);
+
+// A call of tps_kv_extend (tps_pages.cuh) or, without what comes after `page_mask`, of tps_kv_trim.
+struct PagesArgs {
+    tps_kv_pages p;
+    int page_shift, page_mask;
+    int64_t tokens;
+    int64_t* slots;
+    int32_t* positions;
+    int32_t* cu_seqlens;
+    int32_t* first;  // [B] for the second kernel: position of a sequence's first new token, -1 where there is none
+    bool wide;       // slots and positions begin on 16 bytes
+};
+cudaError_t launch_kv_extend(const PagesArgs& a, cudaStream_t stream);
+cudaError_t launch_kv_trim(const PagesArgs& a, cudaStream_t stream);
+
 }  // namespace tps

@@ -126,7 +126,15 @@ __device__ __forceinline__ bool elect_one()
     return r != 0;
 }
 
-// One box of a four-dimensional tensor map into shared memory.
+// One box of a three- or four-dimensional tensor map into shared memory.
+__device__ __forceinline__ void tma_load3(void* dst, const void* map, int x, int y, int z, uint64_t* bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
 __device__ __forceinline__ void tma_load4(void* dst, const void* map, int x, int y, int z, int w, uint64_t* bar)
 {
     asm volatile(

@@ -35,6 +35,23 @@ class _Attention(ctypes.Structure):  # tps_attention
                 + [("q_len", _I32), ("n_q_heads", _I32), ("scale", ctypes.c_float)])
 
 
+class _Prompt(ctypes.Structure):  # tps_prompt
+    _fields_ = ([(n, _P) for n in ("q", "k", "v", "out", "out_lse", "cu_seqlens", "out_status")]
+                + [(n, _I64) for n in ("T", "B", "q_ld", "q_hd", "k_ld", "k_hd", "v_ld", "v_hd")]
+                + [(n, _I32) for n in ("n_q_heads", "n_k_heads", "head_dim")] + [("scale", ctypes.c_float)])
+
+
+class _Tree(ctypes.Structure):  # tps_tree
+    _fields_ = ([(n, _P) for n in ("q", "out", "out_lse", "page_table", "seq_len", "tree_len", "tree", "out_status", "workspace")]
+                + [(n, _I64) for n in ("workspace_bytes", "B", "table_width", "table_ld", "tree_ld")]
+                + [("n_nodes", _I32), ("n_q_heads", _I32), ("scale", ctypes.c_float)])
+
+
+class _Pages(ctypes.Structure):  # tps_kv_pages
+    _fields_ = ([(n, _P) for n in ("page_table", "seq_len", "change", "free_pages", "free_count", "out_status")]
+                + [(n, _I64) for n in ("B", "table_width", "table_ld", "n_free")] + [("page_size", _I32)])
+
+
 def declare(lib):
     """The argument and result types of this module's entry points."""
     lib.tps_qk_norm_rope.restype = ctypes.c_int
@@ -47,6 +64,20 @@ def declare(lib):
     lib.tps_prefix_attention.argtypes = [_P, _P, _P]
     lib.tps_prefix_attention_stall_test.restype = ctypes.c_int
     lib.tps_prefix_attention_stall_test.argtypes = [_P, _P, ctypes.c_int, ctypes.c_uint64, _P]
+    lib.tps_tree_attention.restype = ctypes.c_int
+    lib.tps_tree_attention.argtypes = [_P, _P, _P]
+    lib.tps_tree_attention_stall_test.restype = ctypes.c_int
+    lib.tps_tree_attention_stall_test.argtypes = [_P, _P, ctypes.c_int, ctypes.c_uint64, _P]
+    lib.tps_tree_attention_workspace.restype = _I64
+    lib.tps_tree_attention_workspace.argtypes = [_P, _P]
+    lib.tps_kv_extend.restype = ctypes.c_int
+    lib.tps_kv_extend.argtypes = [_P, _I64, _P, _P, _P, _P]
+    lib.tps_kv_trim.restype = ctypes.c_int
+    lib.tps_kv_trim.argtypes = [_P, _P]
+    lib.tps_prompt_attention.restype = ctypes.c_int
+    lib.tps_prompt_attention.argtypes = [_P, _P]
+    lib.tps_prompt_attention_stall_test.restype = ctypes.c_int
+    lib.tps_prompt_attention_stall_test.argtypes = [_P, ctypes.c_int, ctypes.c_uint64, _P]
     lib.tps_prefix_attention_workspace.restype = _I64
     lib.tps_prefix_attention_workspace.argtypes = [_P, _P]
 
@@ -66,7 +97,8 @@ def _torch_ops():
             ops = load_binding()
             address = lambda f: ctypes.cast(f, ctypes.c_void_p).value
             ops.bind(address(lib.tps_qk_norm_rope), address(lib.tps_kv_write), address(lib.tps_kv_read),
-                     address(lib.tps_prefix_attention), _fail, torch.OutOfMemoryError)
+                     address(lib.tps_prefix_attention), address(lib.tps_prompt_attention), address(lib.tps_kv_extend),
+                     address(lib.tps_kv_trim), address(lib.tps_tree_attention), _fail, torch.OutOfMemoryError)
             _ops = ops
         return _ops
 
@@ -201,6 +233,37 @@ def kv_read(cache: KVCache, slots, *, dtype=torch.bfloat16, out=None, stream=Non
     return ops.read(c._bytes, c._index, slots, code, out)
 
 
+def kv_extend(page_table, seq_len, new_len, free_pages, free_count, page_size: int, tokens: int, *, out=None, status=None,
+              stream=None):
+    """Room in the paged cache for ``new_len`` ([B] int32) more tokens of each sequence, without the host knowing any
+    length: ``page_table`` ([B, W] int32), ``seq_len`` ([B] int32) and ``free_count`` ([1] int32) are updated in place, with
+    pages from the end of the first ``free_count`` entries of ``free_pages`` (int32), for the first sequence first.
+
+    The new tokens are packed, in order, into ``tokens`` rows (their sum, or more: a captured graph's fixed number).  Returns
+    (slots [tokens] int64, positions [tokens] int32, cu_seqlens [B + 1] int32), as ``kv_write``, ``qk_norm_rope`` and
+    ``prompt_attention`` take them; ``out`` is such a triple to write to.  A row without a sequence gets slot -1 and position 0.
+    ``status``: an int32 [B] tensor that gets 5 for a sequence whose pages are more than are left (then no later one that
+    needs any gets one either), 3 for impossible numbers (a negative one, more tokens than W pages or than ``tokens`` rows
+    hold), else 0; sequences with 3 or 5 stay as they were and their rows get no slots."""
+    ops = _ops or _torch_ops()
+    if stream is not None:
+        with _on(stream, page_table.device):
+            return ops.extend(page_table, seq_len, new_len, free_pages, free_count, page_size, tokens, out, status)
+    return ops.extend(page_table, seq_len, new_len, free_pages, free_count, page_size, tokens, out, status)
+
+
+def kv_trim(page_table, seq_len, keep_len, free_pages, free_count, page_size: int, *, status=None, stream=None) -> None:
+    """Keep the first ``keep_len`` ([B] int32) tokens of each sequence (drafted tokens that were not accepted leave; 0: the
+    sequence has ended) and put the pages of the others at the end of the free list; tensors as for ``kv_extend``, whose
+    inverse this is entry for entry.  ``status`` gets 3 where not 0 <= keep_len <= seq_len (within W pages), 5 where the
+    list has no room, else 0; sequences with 3 or 5 stay as they were."""
+    ops = _ops or _torch_ops()
+    if stream is not None:
+        with _on(stream, page_table.device):
+            return ops.trim(page_table, seq_len, keep_len, free_pages, free_count, page_size, status)
+    return ops.trim(page_table, seq_len, keep_len, free_pages, free_count, page_size, status)
+
+
 def prefix_attention(q, cache: KVCache, prefix_pages, prefix_len: int, page_table, suffix_len, *, scale=None,
                      want_lse: bool = False, out=None, status=None, workspace=None, stream=None):
     """Softmax attention of a batch of sequences over ``prefix_len`` tokens that all of them share (in the
@@ -237,3 +300,55 @@ def prefix_attention_workspace(q_shape, cache: KVCache, prefix_len: int, table_w
     if n < 0:
         raise ValueError("arguments that prefix_attention would refuse")
     return n
+
+
+def tree_attention(q, cache: KVCache, page_table, seq_len, tree, *, nodes=None, scale=None, want_lse: bool = False, out=None,
+                   status=None, workspace=None, stream=None):
+    """Softmax attention of each sequence's drafted tokens over its tokens in the cache and over each other, as a tree says
+    (one node is a decode step; a chain is the verification of one draft).
+
+    ``q``: [B, N, Hq, D] bfloat16, contiguous, N from 1 to 64; Hq a multiple of the cache's heads, D 64 or 128.  The
+    cache holds ``seq_len`` ([B] int32) tokens of each sequence in the pages of its row of ``page_table`` ([B, W] int32); the
+    last N of them are the drafted ones, or, with ``nodes`` ([B] int32), the last ``nodes`` (the rest of its q is padding, whose
+    outputs are 0 and -inf).  ``tree``: int64 [N] or [B, N], bit j of entry i set where node i sees node j: with parents that
+    come before their children, ``tree[i] = 1 << i | tree[parent[i]]``.  Every node sees all tokens before the tree.
+    ``scale``: of q.k, by default D ** -0.5.  Returns the bfloat16 output of q's shape, or (output, log-sum-exp [B, N, Hq]
+    float32) with ``want_lse``.  ``status``: an int32 [B] tensor that gets 3 for a sequence with a page outside the cache or
+    impossible lengths (its outputs are NaN), 4 where a wait on the GPU ran out beside it (outputs it concerns are NaN), else 0.
+    ``workspace``: a uint8 tensor of at least ``tree_attention_workspace(...)`` bytes to use instead of the library's
+    memory pool."""
+    c = _cache(cache)
+    ops = _ops or _torch_ops()
+    if stream is not None:
+        with _on(stream, c.device):
+            return ops.tree(q, c._bytes, c._index, page_table, seq_len, tree, nodes, scale, want_lse, out, status, workspace)
+    return ops.tree(q, c._bytes, c._index, page_table, seq_len, tree, nodes, scale, want_lse, out, status, workspace)
+
+
+def tree_attention_workspace(q_shape, cache: KVCache, table_width: int) -> int:
+    """Bytes of workspace ``tree_attention`` needs for a query of this shape."""
+    from . import load
+    B, N, Hq = q_shape[:3]
+    t = _Tree(B=B, table_width=table_width, table_ld=table_width, n_nodes=N, n_q_heads=Hq, scale=1.0)
+    n = load().tps_tree_attention_workspace(_cache(cache)._bytes, ctypes.byref(t))
+    if n < 0:
+        raise ValueError("arguments that tree_attention would refuse")
+    return n
+
+
+def prompt_attention(q, k, v, cu_seqlens, *, scale=None, want_lse: bool = False, out=None, status=None, stream=None):
+    """Causal softmax attention of whole prompts, packed one behind another: sequence b's tokens are the rows
+    ``cu_seqlens[b]`` .. ``cu_seqlens[b + 1] - 1`` (``cu_seqlens``: [B + 1] int32 on the device), and each of its
+    tokens sees itself and those before it.
+
+    ``q``: [T, Hq, D], ``k``, ``v``: [T, Hk, D] bfloat16 CUDA tensors, D 64 or 128, Hq a multiple of Hk (query head i
+    reads key head i // (Hq // Hk)); token and head strides are free in steps of 8 elements, so all three may be cut
+    out of one projection.  ``scale``: of q.k, by default D ** -0.5.  Returns the bfloat16 output [T, Hq, D], or (output,
+    log-sum-exp [T, Hq] float32) with ``want_lse``; ``out`` is written to if given.  Rows of no sequence are not written (in
+    new tensors they hold anything).  ``status``: an int32 [B] tensor that gets 3 for a sequence whose bounds are
+    not in order (nothing of it is written), 4 where a wait on the GPU ran out (outputs it concerns are NaN), else 0."""
+    ops = _ops or _torch_ops()
+    if stream is not None:
+        with _on(stream, q.device):
+            return ops.prompt(q, k, v, cu_seqlens, scale, want_lse, out, status)
+    return ops.prompt(q, k, v, cu_seqlens, scale, want_lse, out, status)
