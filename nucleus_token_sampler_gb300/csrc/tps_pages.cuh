@@ -51,18 +51,36 @@ __device__ __forceinline__ void block_sums(PagesShared& sh, int64_t& x, int64_t&
     x += px, y += py;
 }
 
-// The last of n ascending numbers that is at most x (the first one is).
-__device__ __forceinline__ int owner(const int* first, int64_t n, int x)
+// For each x, the last of n ascending numbers that is at most x (the first one is); n is at most kPagesThreads.  Several
+// at once: a step is a chain of one read.
+template <int N> __device__ __forceinline__ void owners(const int* first, int n, const int (&x)[N], int (&at)[N])
 {
-    int64_t lo = 0, hi = n;
-    while (hi - lo > 1) {
-        const int64_t mid = (lo + hi) >> 1;
-        if (first[mid] <= x)
-            lo = mid;
-        else
-            hi = mid;
+#pragma unroll
+    for (int k = 0; k < N; ++k) at[k] = 0;
+#pragma unroll
+    for (int step = kPagesThreads / 2; step > 0; step >>= 1)
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            if (at[k] + step < n && first[at[k] + step] <= x[k]) at[k] += step;
+}
+
+// do_one(i, the sequence that `first` gives i to) for all i below `count`, four of a thread at a time: load_one's values are on
+// their way together.
+template <typename Value, typename Load, typename Store>
+__device__ __forceinline__ void for_each_owned(const int* first, int n, int64_t count, Load load_one, Store store_one)
+{
+    for (int64_t base = 0; base < count; base += 4 * kPagesThreads) {
+        int x[4], at[4];
+        Value v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k] = (int)min(base + k * kPagesThreads + (int)threadIdx.x, count - 1);
+        owners(first, n, x, at);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = load_one(x[k], at[k]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (base + k * kPagesThreads + (int)threadIdx.x < count) store_one(x[k], at[k], v[k]);
     }
-    return (int)lo;
 }
 
 // Of the sequences that are served, the one most ahead: `sum` pages have gone with it.
@@ -109,18 +127,20 @@ template <bool kSlots> __global__ void __launch_bounds__(kPagesThreads) kv_exten
             if (!kSlots) a.first[b] = done ? (int)s : -1;
         }
         __syncthreads();
-        const int64_t live = min(p.B - base, (int64_t)kPagesThreads), now = (int64_t)sh.moved;
-        for (int64_t i = tid; i < now - moved; i += kPagesThreads) {
-            const int w = owner(sh.pages, live, (int)i);
-            p.page_table[(base + w) * p.table_ld + sh.has[w] + (i - sh.pages[w])] = p.free_pages[count - 1 - (moved + i)];
-        }
+        const int live = (int)min(p.B - base, (int64_t)kPagesThreads);
+        const int64_t now = (int64_t)sh.moved;
+        for_each_owned<int>(
+            sh.pages, live, now - moved, [&](int i, int) { return p.free_pages[count - 1 - (moved + i)]; },
+            [&](int i, int w, int page) { p.page_table[(base + w) * p.table_ld + sh.has[w] + (i - sh.pages[w])] = page; });
         if (kSlots) {
             __syncthreads();
-            for (int64_t i = tid; i < min(all_tokens, a.tokens - packed); i += kPagesThreads) {
-                const int w = owner(sh.tokens, live, (int)i), s0 = sh.length[w], at = s0 + (int)i - sh.tokens[w];
-                a.slots[packed + i] = s0 >= 0 ? slot_of(a, base + w, at) : -1;
-                a.positions[packed + i] = s0 >= 0 ? at : 0;
-            }
+            for_each_owned<int64_t>(
+                sh.tokens, live, min(all_tokens, a.tokens - packed),
+                [&](int i, int w) { return sh.length[w] >= 0 ? slot_of(a, base + w, sh.length[w] + i - sh.tokens[w]) : -1; },
+                [&](int i, int w, int64_t slot) {
+                    a.slots[packed + i] = slot;
+                    a.positions[packed + i] = sh.length[w] >= 0 ? sh.length[w] + i - sh.tokens[w] : 0;
+                });
         }
         moved = now;
         asked += all_pages;
@@ -140,10 +160,25 @@ template <bool kSlots> __global__ void __launch_bounds__(kPagesThreads) kv_exten
 static __global__ void __launch_bounds__(kSlotsThreads) kv_slots_kernel(const __grid_constant__ PagesArgs a)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan
-    const int64_t i0 = ((int64_t)blockIdx.x * kSlotsThreads + threadIdx.x) * kSlotsEach;
-    if (i0 >= a.tokens) return;
+    const int64_t begin = (int64_t)blockIdx.x * kSlotsThreads * kSlotsEach, i0 = begin + (int64_t)threadIdx.x * kSlotsEach;
     const int total = a.cu_seqlens[a.p.B];
-    int64_t b = i0 < total ? owner(a.cu_seqlens, a.p.B, (int)i0) : 0;
+    // The last sequence that begins at or before the CTA's first row, and before its last: all threads count.
+    int64_t low = -1, high = -1;
+    for (int64_t base = 0; base < a.p.B; base += kSlotsThreads) {
+        const int64_t b = base + threadIdx.x;
+        const int at = b < a.p.B ? a.cu_seqlens[b] : INT32_MAX;
+        low += __syncthreads_count(at <= begin);
+        high += __syncthreads_count(at < begin + kSlotsThreads * kSlotsEach);
+    }
+    if (i0 >= a.tokens) return;
+    int64_t b = low;
+    while (i0 < total && high - b > 1) {
+        const int64_t mid = (b + high + 1) >> 1;
+        if (a.cu_seqlens[mid] <= i0)
+            b = mid;
+        else
+            high = mid - 1;
+    }
     int64_t slot[kSlotsEach];
     int position[kSlotsEach];
 #pragma unroll
@@ -199,11 +234,10 @@ static __global__ void __launch_bounds__(kPagesThreads) kv_trim_kernel(const __g
             if (pass == 1) {
                 if (p.B <= kPagesThreads) total = (int64_t)sh.moved;
                 // pages of this chunk that go back: those up to `total`
-                const int64_t live = min(p.B - base, (int64_t)kPagesThreads), here = min(all_pages, total - min(asked, total));
-                for (int64_t i = tid; i < here; i += kPagesThreads) {
-                    const int w = owner(sh.pages, live, (int)i);
-                    p.free_pages[count + total - 1 - (asked + i)] = p.page_table[(base + w) * p.table_ld + sh.has[w] + (i - sh.pages[w])];
-                }
+                for_each_owned<int>(
+                    sh.pages, (int)min(p.B - base, (int64_t)kPagesThreads), min(all_pages, total - min(asked, total)),
+                    [&](int i, int w) { return p.page_table[(base + w) * p.table_ld + sh.has[w] + (i - sh.pages[w])]; },
+                    [&](int i, int, int page) { p.free_pages[count + total - 1 - (asked + i)] = page; });
             }
             asked += all_pages;
             __syncthreads();
