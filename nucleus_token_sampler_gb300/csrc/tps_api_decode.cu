@@ -148,6 +148,7 @@ int check_prompt(const tps_prompt* p, tps::PromptArgs* a, int64_t* tiles)
     a->group = (a->G + a->groups - 1) / a->groups;
     a->heads_v = p->n_k_heads * a->groups;
     a->tile_tokens = 128 / a->group;
+    a->sectors = aligned(p->out, 32);
     a->level_shift = 0;
     while ((p->T / tps::kBlockKeys + 1) >> a->level_shift >= 2048) ++a->level_shift;
     a->qk_scale = (float)((double)p->scale * 1.4426950408889634);
@@ -178,7 +179,8 @@ int plan_tree(const tps_kv_cache& c, const tps_tree& t, int sms, tps::TreePlan* 
     tps::TreePlan p = {};
     const int64_t R = (int64_t)t.n_nodes * (t.n_q_heads / c.n_heads);  // at most 2^22
     p.R = (int)R;
-    p.tile_rows = R <= 128 ? 128 : 256;
+    // Tiles of 256 rows load and convert keys and values for twice as many; those of 128 leave fewer rows unused.
+    p.tile_rows = (R + 127) / 128 % 2 ? 128 : 256;
     p.n_tiles = (int)((R + p.tile_rows - 1) / p.tile_rows);
     const int64_t items = (int64_t)p.n_tiles * c.n_heads;  // of a sequence
     const int64_t most = std::max<int64_t>((t.table_width * c.page_size + tps::kBlockKeys - 1) / tps::kBlockKeys, 1) * items;

@@ -38,7 +38,8 @@ constexpr int kDirty = 8;  // items whose marks are kept: the loads run at most 
 
 template <int D> struct PromptShape {
     static constexpr int kTileBytes = 128 * D * 2;
-    static constexpr int kRing = D == 128 ? 5 : 8;  // key and value tiles in shared memory
+        static constexpr int kRing = D == 128 ? 5 : 8;
+  // key and value tiles in shared memory
     static constexpr int kOutCol = 256;             // TMEM: scores (and weights) of tile m at 128 m, outputs at 256 + D m
     struct Control {
         uint64_t full[kRing], empty[kRing], go[kRing], clean[kRing];
@@ -171,6 +172,19 @@ struct PromptWalk {
     __device__ __forceinline__ bool more() const { return it.token >= 0; }
 };
 
+// 32 bytes, as a whole sector where the output begins on one.
+__device__ __forceinline__ void store32(const PromptArgs& a, void* p, const uint32_t* w)
+{
+    if (!a.sectors) {
+        static_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        static_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        return;
+    }
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
+                 "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
 template <int D>
 __global__ void __launch_bounds__(kPromptThreads, 1)
     attn_prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
@@ -189,7 +203,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < kRing; ++i) mbar_init(&ctl.full[i], 1), mbar_init(&ctl.empty[i], 1), mbar_init(&ctl.go[i], 1), mbar_init(&ctl.clean[i], 2);
         for (int i = 0; i < 2; ++i)
-            mbar_init(&ctl.q_full[i], 1), mbar_init(&ctl.q_empty[i], 1), mbar_init(&ctl.s_full[i], 1), mbar_init(&ctl.p_full[i], 128),
+            mbar_init(&ctl.q_full[i], 1), mbar_init(&ctl.q_empty[i], 1), mbar_init(&ctl.s_full[i], 1), mbar_init(&ctl.p_full[i], 4),
                 mbar_init(&ctl.o_full[i], 1);
         mbar_init(&ctl.drain, 1);
         ctl.abort = 0;
@@ -308,8 +322,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                     tmem_st16(s_addr + ch * 16, w);
                     return add2(part[0], part[1]);
                 };
-                // 64 scores at a time, first weighed against the reference as it stands: a weight above 2^kSlack
-                // shows in their sum, so the usual step looks for no maximum at all.
+                // 64 scores at a time, first weighed against the reference as it stands (an item's first 64 have none): a weight
+                // above 2^kSlack shows in their sum, so the usual step looks for no maximum at all.
 #pragma unroll
                 for (int ch = 0; ch < 4; ch += 2) {
                     if (ch * 32 >= wide) break;  // no row of the tile sees these: the product leaves them out, too
@@ -322,21 +336,24 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                         hide(sa, ch);
                         hide(sb, ch + 1);
                     }
-                    float b = ref == neg ? 0.f : -ref;
-                    float2 x = add2(weigh(sa, ch, b), weigh(sb, ch + 1, b));
-                    const bool need = !(x.x + x.y <= 256.f) || ref == neg;
-                    if (__any_sync(0xFFFFFFFFu, need)) {
-                        raise(need, fmaxf(largest(sa), largest(sb)) * c, ch);
-                        b = ref == neg ? 0.f : -ref;
-                        tmem_wait_st();
+                    float2 x;
+                    for (bool again = v == 0 && ch == 0, need = again;;) {
+                        if (again) raise(need, fmaxf(largest(sa), largest(sb)) * c, ch);
+                        const float b = ref == neg ? 0.f : -ref;
                         x = add2(weigh(sa, ch, b), weigh(sb, ch + 1, b));
+                        if (again) break;
+                        need = !(x.x + x.y <= 256.f) || ref == neg;
+                        if (!__any_sync(0xFFFFFFFFu, need)) break;
+                        again = true;
+                        tmem_wait_st();
                     }
                     total = add2(total, x);
                 }
                 sum += total.x + total.y;
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(&ctl.p_full[m]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl.p_full[m]);
             }
             if (alive) alive = wait_all(&ctl.o_full[m], o_parity);
             o_parity ^= 1;
@@ -372,7 +389,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                         w[j] = *reinterpret_cast<const uint32_t*>(&y);
                     }
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) dst[i / 8 + j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+                    for (int j = 0; j < 4; j += 2) store32(a, dst + i / 8 + j, w + 4 * j);
                 }
             }
             tc_fence_before();
@@ -515,10 +532,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 q_filled |= 1u << m;
             };
             block(0, false);
+            if (alive) block(0, true);
             if (alive) query(0);
             if (alive) query(1);
-            for (int v = 0; v < it.last && alive; ++v) {
-                if (v > 0) block(v, false);
+            for (int v = 1; v < it.last && alive; ++v) {
+                block(v, false);
                 if (alive) block(v, true);
             }
         }
@@ -549,18 +567,31 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 const int base = v * kBlockKeys, end = it.end - it.begin - base;          // rows from here on are not the sequence's
                 const int first = max(it.token - it.begin + 1 - base, 0);                 // rows from here on are hidden from some row
                 const int from = first * (D / 8) + half * 32 + lane;
-#pragma unroll 4
+                // 0 times what is not finite is NaN, and stays it: one instruction for two values finds whether there is any.
+                __nv_bfloat162 sum[4] = {};
+                const __nv_bfloat162 zero = {};
+#pragma unroll 8
                 for (int i = from; i < kBlockKeys * (D / 8); i += 64) {
-                    const int r = i / (D / 8);
-                    uint4* p = reinterpret_cast<uint4*>(tile + tile_byte(r, i % (D / 8)));
-                    const uint4 x = *p;
-                    uint4 y = make_uint4(not_finite(x.x), not_finite(x.y), not_finite(x.z), not_finite(x.w));
-                    if (y.x | y.y | y.z | y.w) {
-                        found |= r < end;
-                        *p = make_uint4(x.x ^ y.x, x.y ^ y.y, x.z ^ y.z, x.w ^ y.w);
-                    }
+                    const uint4 x = *reinterpret_cast<const uint4*>(tile + tile_byte(i / (D / 8), i % (D / 8)));
+                    sum[0] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.x), zero, sum[0]);
+                    sum[1] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.y), zero, sum[1]);
+                    sum[2] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.z), zero, sum[2]);
+                    sum[3] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.w), zero, sum[3]);
                 }
-                fence_proxy_async();
+                sum[0] = __hadd2(__hadd2(sum[0], sum[1]), __hadd2(sum[2], sum[3]));
+                if (*reinterpret_cast<const uint32_t*>(&sum[0]) & 0x7FFF7FFFu) {
+#pragma unroll 1
+                    for (int i = from; i < kBlockKeys * (D / 8); i += 64) {
+                        const int r = i / (D / 8);
+                        uint4* p = reinterpret_cast<uint4*>(tile + tile_byte(r, i % (D / 8)));
+                        const uint4 x = *p, y = make_uint4(not_finite(x.x), not_finite(x.y), not_finite(x.z), not_finite(x.w));
+                        if (y.x | y.y | y.z | y.w) {
+                            found |= r < end;
+                            *p = make_uint4(x.x ^ y.x, x.y ^ y.y, x.z ^ y.z, x.w ^ y.w);
+                        }
+                    }
+                    fence_proxy_async();
+                }
                 const bool any = __any_sync(0xFFFFFFFFu, found);
                 if (lane == 0) {
                     if (any) *(volatile int*)&ctl.dirty[item % kDirty][half] = 1;
@@ -577,9 +608,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     if (warp == kPromptMma) tmem_free(tmem, 512);
 }
 
-// The tiles of all sequences, longest first, into a.list, and the sequences' statuses.  One CTA: two passes over
-// the bounds, a warp for each sequence in turn and a lane for each of its tiles; tiles of like length (kPromptLevels
-// steps) come in any order, which no result depends on.
+// The tiles of all sequences, longest first, into a.list, and the sequences' statuses.  One CTA, two passes over
+// the bounds; tiles of like length (kPromptLevels steps) come in any order, which no result depends on.
 constexpr int kPromptLevels = 2048;
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads) prompt_plan_kernel(const PromptArgs a, int4* list, int* n_tiles)
@@ -609,14 +639,18 @@ __global__ void __launch_bounds__(kThreads) prompt_plan_kernel(const PromptArgs 
             __syncthreads();
             if (tid == kThreads - 1) top_before = top;
             const int tiles = valid ? prompt_tiles(a, lo, hi) : 0;
-            for (uint32_t have = __ballot_sync(0xFFFFFFFFu, tiles > 0); have; have &= have - 1) {
-                const int w = __ffs(have) - 1;
-                const int l = __shfl_sync(0xFFFFFFFFu, lo, w), h = __shfl_sync(0xFFFFFFFFu, hi, w), n = __shfl_sync(0xFFFFFFFFu, tiles, w);
-                for (int t = lane; t < n; t += 32) {
-                    const int keys = min((int64_t)h - l, (int64_t)(t + 1) * span);
-                    const int level = min((keys + kBlockKeys - 1) / kBlockKeys >> a.level_shift, kPromptLevels - 1);
-                    const int at = atomicAdd(&count[level], 1);
-                    if (pass == 1) list[at] = make_int4(l, h, l + t * span, (int)(b - lane + w));
+            auto put = [&](int l, int h, int t, int64_t seq) {
+                const int keys = (int)min((int64_t)h - l, (int64_t)(t + 1) * span);
+                const int at = atomicAdd(&count[min((keys + kBlockKeys - 1) / kBlockKeys >> a.level_shift, kPromptLevels - 1)], 1);
+                if (pass == 1) list[at] = make_int4(l, h, l + t * span, (int)seq);
+            };
+            if (__all_sync(0xFFFFFFFFu, tiles <= 8)) {  // short ones: a lane each
+                for (int t = 0; t < tiles; ++t) put(lo, hi, t, b);
+            } else {  // long ones: a lane for each tile, sequence after sequence
+                for (uint32_t have = __ballot_sync(0xFFFFFFFFu, tiles > 0); have; have &= have - 1) {
+                    const int w = __ffs(have) - 1;
+                    const int l = __shfl_sync(0xFFFFFFFFu, lo, w), h = __shfl_sync(0xFFFFFFFFu, hi, w), n = __shfl_sync(0xFFFFFFFFu, tiles, w);
+                    for (int t = lane; t < n; t += 32) put(l, h, t, b - lane + w);
                 }
             }
         }

@@ -135,6 +135,7 @@ struct PromptArgs {
     int group, groups;        // of them in one tile; such groups of a key head
     int heads_v;              // groups of all key heads
     int tile_tokens;          // query tokens of a tile of 128 rows
+    bool sectors;             // the output begins on 32 bytes
     int level_shift;          // lengths in blocks are sorted by their bits from here on
     float qk_scale;           // scale * log2(e)
     const int4* list;         // tiles (a sequence's begin and end, the first token, the sequence), longest first; or NULL: each
