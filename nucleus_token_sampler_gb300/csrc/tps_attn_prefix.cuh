@@ -53,10 +53,14 @@
 
 namespace tps {
 
-constexpr int kScalars = 8;         // blocks whose scale factors are kept
 constexpr int kSpread = 8;          // down to 2^-8 of its block's unit a scale times any code is exact (fp8), and small weights keep their bits
 
-template <int D, int kFormat, int kTiles> struct PrefixShape {
+// What a kernel's line of blocks is: one prefix that all share, or each sequence's own tokens, the last of which are a tree
+// (tps_attn_tree.cuh).  kTreesInTurn: both softmax groups have the same 128 rows, and the item's blocks in turn.
+constexpr int kShared = 0, kTrees = 1, kTreesInTurn = 2;
+
+template <int D, int kFormat, int kTiles, int kLine> struct PrefixShape {
+    static constexpr int kQueries = kLine == kTreesInTurn ? 1 : kTiles;  // query tiles in shared memory
     static constexpr bool k8 = kFormat != TPS_KV_BF16;
     static constexpr int kMmaWarp = 4 * kTiles, kLoadWarp = kMmaWarp + 1, kScaleWarp = kMmaWarp + 2;
     static constexpr int kConvertWarp = kMmaWarp + 4, kConvertWarps = 8;
@@ -69,8 +73,12 @@ template <int D, int kFormat, int kTiles> struct PrefixShape {
                          kRegsOthers = kTiles == 2 ? (kFp8 ? 56 : 64) : 104;
     static_assert(kTiles * kRegsSoftmax + 3 * kRegsOthers <= (kTiles + 3) * kRegsLaunch, "no more than the launch gave");
     static constexpr int kTileBytes = 128 * D * 2;         // a query, key or value tile
-    static constexpr int kRing = k8 && D == 128 && kTiles == 2 ? 3 : 4;  // key and value tiles in shared memory
-    static constexpr int kRaw = D == 128 ? 3 : 4;          // tiles of 8-bit codes
+    // Key and value tiles in shared memory, and tiles of 8-bit codes.  Trees, whose sequences are read from DRAM and not again and
+    // again from the L2 cache, have as many as fit (up to what the marks and scalars kept allow).
+    static constexpr int kRing = kLine == kTreesInTurn && !k8 ? (D == 128 ? 5 : 8) : (k8 && D == 128 && kQueries == 2 ? 3 : 4);
+    static constexpr int kRaw = D == 128 ? 3 : (kLine == kShared ? 4 : 8);
+    // Blocks whose scale factors are kept: loads, conversions, products and softmax run this far apart at most.
+    static constexpr int kScalars = kLine != kShared && D == 64 ? 16 : 8;
     static constexpr int kRawBytes = 128 * D + 128 * 2;    // codes and scales of a tile
     static constexpr int kTmemCols = kTiles == 2 ? 512 : 256;
     static constexpr int kScoreCol = 0, kOutCol = 128 * kTiles;  // tile m: scores at 128 m, outputs at kOutCol + D m
@@ -83,6 +91,11 @@ template <int D, int kFormat, int kTiles> struct PrefixShape {
         TreeStart start;          // of trees: where this CTA's line begins
         int64_t sums[kThreads / 32];
         int marks[kTreeMarks];    // by item: kMark*
+        // In turn: a row's factor for the group that did not load it, what the groups' halves of it come to, by 32 rows
+        // whether a wait of either ran out.
+        float row_factor[kLine == kTreesInTurn ? 128 : 1];
+        float2 half[2][kLine == kTreesInTurn ? 128 : 1];
+        int dead[4];
         float key_unit[kScalars], value_exp[kScalars];
         int wide[kScalars];  // 1: the block's keys, 2: its values
         // Of the block's tokens: keys' scales (int8, or wide), values' in the block's unit, at most 1 (int8), or one over
@@ -91,7 +104,7 @@ template <int D, int kFormat, int kTiles> struct PrefixShape {
         alignas(16) __half factor[kFormat == TPS_KV_FP8 ? kRaw : 1][128];  // fp8: of the tokens of a code tile
     };
     static constexpr size_t kSmem =
-        (size_t)(kTiles + kRing) * kTileBytes + (k8 ? (size_t)kRaw * kRawBytes : 0) + sizeof(Control) + 1024;
+        (size_t)(kQueries + kRing) * kTileBytes + (k8 ? (size_t)kRaw * kRawBytes : 0) + sizeof(Control) + 1024;
     static_assert(kSmem <= 232448, "fits one CTA's shared memory");
 };
 
@@ -174,30 +187,31 @@ template <int kSlots> struct Turn {
 __device__ __forceinline__ int way_item(const Way& w) { return w.item; }
 __device__ __forceinline__ int way_item(const TreeWay&) { return 0; }  // never asked for
 
-// kTree: not one shared prefix, but each sequence's own tokens, the last of which are a tree (tps_attn_tree.cuh).
-template <bool kTree> struct LineOf {
-    using Args = AttnArgs;
-    using Walk = Way;
-};
-template <> struct LineOf<true> {
+template <int kLine> struct LineOf {
     using Args = TreeArgs;
     using Walk = TreeWay;
 };
+template <> struct LineOf<kShared> {
+    using Args = AttnArgs;
+    using Walk = Way;
+};
 
-template <int D, int kFormat, int kTiles, bool kTree>
-__global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
-    attn_prefix_kernel(const __grid_constant__ typename LineOf<kTree>::Args a, const __grid_constant__ CUtensorMap kmap,
+template <int D, int kFormat, int kTiles, int kLine>
+__global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles, kLine>::kThreads, 1)
+    attn_prefix_kernel(const __grid_constant__ typename LineOf<kLine>::Args a, const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap vmap)
 {
-    using Walk = typename LineOf<kTree>::Walk;
-    using Shape = PrefixShape<D, kFormat, kTiles>;
+    constexpr bool kTree = kLine != kShared, kTurns = kLine == kTreesInTurn;
+    using Walk = typename LineOf<kLine>::Walk;
+    using Shape = PrefixShape<D, kFormat, kTiles, kLine>;
+    static_assert(!kTurns || (kTiles == 2 && Shape::kRing >= 4), "two groups, and a ring that holds two blocks");
     using Control = typename Shape::Control;
     constexpr bool k8 = Shape::k8;
     constexpr int kRing = Shape::kRing, kRaw = Shape::kRaw;
     extern __shared__ unsigned char raw_smem[];
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~(uintptr_t)1023);
     unsigned char* q_tile = smem;
-    unsigned char* ring = smem + kTiles * Shape::kTileBytes;
+    unsigned char* ring = smem + Shape::kQueries * Shape::kTileBytes;
     unsigned char* raw_ring = ring + kRing * Shape::kTileBytes;
     Control& ctl = *reinterpret_cast<Control*>(raw_ring + (k8 ? kRaw * Shape::kRawBytes : 0));
 
@@ -205,10 +219,10 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        mbar_init(&ctl.q_full, 4 * kTiles);
+        mbar_init(&ctl.q_full, 4 * Shape::kQueries);
         for (int i = 0; i < kRing; ++i) mbar_init(&ctl.full[i], k8 ? Shape::kConvertWarps : 1), mbar_init(&ctl.empty[i], 1), mbar_init(&ctl.tail[i], 1);
         for (int i = 0; i < kTiles; ++i) mbar_init(&ctl.s_full[i], 1), mbar_init(&ctl.p_full[i], 128), mbar_init(&ctl.o_full[i], 1);
-        for (int i = 0; i < kScalars; ++i) mbar_init(&ctl.scalar_full[i], 1);
+        for (int i = 0; i < Shape::kScalars; ++i) mbar_init(&ctl.scalar_full[i], 1);
         for (int i = 0; i < kRaw; ++i) {
             mbar_init(&ctl.raw_full[i], 1);
             mbar_init(&ctl.factor_full[i], 1);
@@ -217,6 +231,7 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
         mbar_init(&ctl.drain, 1);
         ctl.abort = 0;
         ctl.bad = 0;
+        for (int i = 0; i < 4; ++i) ctl.dead[i] = 0;
         fence_proxy_async();
     }
     if (warp == Shape::kMmaWarp) tmem_alloc(&ctl.tmem, Shape::kTmemCols);
@@ -255,13 +270,13 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
     if (warp < 4 * kTiles) {
         // ---------------------------------------------------------------------------- softmax
         const int m = warp >> 2;
-        const int in_tile = (int)threadIdx.x;  // row of the CTA's kTiles * 128
+        const int in_tile = kTurns ? (int)threadIdx.x & 127 : (int)threadIdx.x;  // row of the CTA's kQueries * 128
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_addr = tmem + lanes + Shape::kScoreCol + 128 * m, o_addr = tmem + lanes + Shape::kOutCol + D * m;
         const float neg = -__int_as_float(0x7F800000);
-        unsigned char* my_q = q_tile + m * Shape::kTileBytes;
+        unsigned char* my_q = q_tile + (kTurns ? 0 : m * Shape::kTileBytes);
         uint32_t s_parity = 0, o_parity = 0;
-        Turn<kScalars> scalar(0);
+        Turn<Shape::kScalars> scalar(0);
         [[maybe_unused]] TreeRecord record;
         if constexpr (kTree) record.begin(ctl.start.seq);
         const uint32_t sign = a.qk_scale < 0.f ? 0x80008000u : 0u;
@@ -270,10 +285,10 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
         for (; way.left > 0 && alive; way.next(a)) {
             // The warp's 32 query rows, D / 8 lanes to a row: as they are (bf16) or brought into float16's range.
             float row_unit = unit;
-            {
+            if (!kTurns || m == 0) {
                 constexpr int kLanes = D / 8, kRows = 32 / kLanes, kSteps = 32 / kRows;  // lanes of a row, rows at a time
                 const int piece = lane % kLanes, sub = lane / kLanes;
-                const int64_t first = (int64_t)way.tile * (128 * kTiles) + warp * 32 + sub, row_elems = (int64_t)a.a.n_q_heads * D;
+                const int64_t first = (int64_t)way.tile * (128 * Shape::kQueries) + warp * 32 + sub, row_elems = (int64_t)a.a.n_q_heads * D;
                 // row = bt G + gi lies at bt * row_elems + (head G + gi) D; kRows rows on without a division
                 const int64_t bt = first <= 0x7FFFFFFF ? (uint32_t)first / (uint32_t)a.G : first / a.G;
                 int gi = (int)(first - bt * a.G);
@@ -338,19 +353,28 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
                     }
                 }
                 row_unit = unit / row_f;
+                if (kTurns && k8) ctl.row_factor[in_tile] = row_f;
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl.q_full);
             }
             float ref = neg, sum = 0.f;
-            const int blocks = way.blocks(a), in_item = way.tile * (128 * kTiles) + in_tile;
+            const int blocks = way.blocks(a), in_item = way.tile * (128 * Shape::kQueries) + in_tile;
             [[maybe_unused]] TreeRow mine = {};
             if constexpr (kTree) mine = tree_row(a, way, in_item);
             [[maybe_unused]] const bool idle = in_item - lane >= p.R;
             for (int v = 0; v < blocks; ++v) {
+                if (kTurns && (v & 1) != m) {  // the other group's: its scalars' phase is seen all the same
+                    if (k8) {
+                        if (!(alive = wait_all(&ctl.scalar_full[scalar.slot], scalar.parity))) break;
+                        scalar.next();
+                    }
+                    continue;
+                }
                 if (!(alive = wait_all(&ctl.s_full[m], s_parity))) break;
                 s_parity ^= 1;
                 tc_fence_after();
+                if (kTurns && k8 && m == 1 && v == 1) row_unit = unit / ctl.row_factor[in_tile];
                 float c = row_unit, add = 0.f, inv = 1.f;
                 int wide = 0;
                 const int scales = scalar.slot;
@@ -408,7 +432,7 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
                     ref = to;
                     sum *= f;
                     total.x *= f, total.y *= f;
-                    if (v > 0) {
+                    if (kTurns ? v > 1 : v > 0) {
 #pragma unroll 1
                         for (int i = 0; i < D; i += 16) {
                             uint32_t o[16];
@@ -495,48 +519,70 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
                     tmem_st16(s_addr + ch * 16, w);
                     return t;
                 };
-                // 64 scores at a time, first weighed against the reference as it stands: a weight above 2^kSlack
-                // (times the lift) shows in their sum, so the usual step looks for no maximum at all.
+                // 64 scores at a time, first weighed against the reference as it stands (an item's first 64 have none): a weight
+                // above 2^kSlack (times the lift) shows in their sum, so the usual step looks for no maximum at all.  Loops
+                // and not unrolled code: with several roles at work the instructions have to come from the cache again and again.
                 constexpr float kMost = k8 ? 32768.f : 256.f;  // 2^(kSlack + kLift), 2^kSlack
-#pragma unroll
-                for (int ch = 0; ch < 4; ch += 2) {
-                    float sa[32], sb[32];
-                    tmem_ld32(s_addr + ch * 32, sa);
-                    tmem_ld32(s_addr + ch * 32 + 32, sb);
-                    tmem_wait_ld(sa);
-                    tmem_wait_ld(sb);
-                    ready(sa, ch);
-                    ready(sb, ch + 1);
-                    float b = add - (ref == neg ? 0.f : ref) + (k8 ? kLift : 0.f);
-                    float2 x = add2(weigh(sa, ch, b), weigh(sb, ch + 1, b));
-                    const bool need = !(x.x + x.y <= kMost) || ref == neg;
-                    if (__any_sync(0xFFFFFFFFu, need || wide)) {  // a wide block comes this way every time
-                        if (!k8 || !wide) {
-                            raise(need, fmaf(fmaxf(largest(sa), largest(sb)), c, add), ch);
-                            b = add - (ref == neg ? 0.f : ref) + (k8 ? kLift : 0.f);
-                            tmem_wait_st();
-                            x = add2(weigh(sa, ch, b), weigh(sb, ch + 1, b));
-                        } else {
-                            x = weigh_wide(sa, ch);  // may scale the total, so not inside its sum
-                            total = add2(total, x);
-                            x = weigh_wide(sb, ch + 1);
-                        }
+                constexpr int kUnroll = kTree ? 1 : 2;
+                if (k8 && wide) {
+#pragma unroll 1
+                    for (int ch = 0; ch < 4; ++ch) {
+                        float s[32];
+                        tmem_ld32(s_addr + ch * 32, s);
+                        tmem_wait_ld(s);
+                        ready(s, ch);
+                        const float2 x = weigh_wide(s, ch);  // may scale the total, so not inside its sum
+                        total = add2(total, x);
                     }
-                    total = add2(total, x);
+                } else {
+#pragma unroll kUnroll
+                    for (int ch = 0; ch < 4; ch += 2) {
+                        float sa[32], sb[32];
+                        tmem_ld32(s_addr + ch * 32, sa);
+                        tmem_ld32(s_addr + ch * 32 + 32, sb);
+                        tmem_wait_ld(sa);
+                        tmem_wait_ld(sb);
+                        ready(sa, ch);
+                        ready(sb, ch + 1);
+                        float2 x;
+                        for (bool again = v == (kTurns ? m : 0) && ch == 0, need = again;;) {
+                            if (again) raise(need, fmaf(fmaxf(largest(sa), largest(sb)), c, add), ch);
+                            const float b = add - (ref == neg ? 0.f : ref) + (k8 ? kLift : 0.f);
+                            x = add2(weigh(sa, ch, b), weigh(sb, ch + 1, b));
+                            if (again) break;
+                            need = !(x.x + x.y <= kMost) || ref == neg;
+                            if (!__any_sync(0xFFFFFFFFu, need)) break;
+                            again = true;
+                            tmem_wait_st();
+                        }
+                        total = add2(total, x);
+                    }
                 }
                 sum = fmaf(total.x + total.y, inv, sum);
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(&ctl.p_full[m]);
             }
-            if (alive) alive = wait_all(&ctl.o_full[m], o_parity);
-            o_parity ^= 1;
+            if (!kTurns || m < blocks) {
+                if (alive) alive = wait_all(&ctl.o_full[m], o_parity);
+                o_parity ^= 1;
+            }
             if constexpr (kTree) {
+                float2 other = make_float2(neg, 0.f);
+                if constexpr (kTurns) {  // the groups' halves of the row, for each of which a half of the columns
+                    if (!alive) *(volatile int*)&ctl.dead[warp & 3] = 1;
+                    ctl.half[m][in_tile] = make_float2(ref, sum);
+                    pair_sync(warp & 3);
+                    alive = *(volatile int*)&ctl.dead[warp & 3] == 0;
+                    other = ctl.half[m ^ 1][in_tile];
+                }
                 if (!alive) break;
                 tc_fence_after();
-                tree_output<D, kFormat>(a, way, blocks, mine, in_tile, in_item, o_addr, ref, sum,
-                                        *(volatile int*)&ctl.marks[way.ordinal % kTreeMarks] | (way.bad ? kMarkBad : 0));
+                tree_output<D, kFormat, kTurns>(a, way, blocks, mine, in_tile, in_item, m, tmem + lanes + Shape::kOutCol, o_addr,
+                                                make_float2(ref, sum), other,
+                                                *(volatile int*)&ctl.marks[way.ordinal % kTreeMarks] | (way.bad ? kMarkBad : 0));
                 tc_fence_before();
+                if (kTurns) pair_sync(warp & 3);  // both halves have been read
                 record.note(way.seq, way.head * p.n_tiles + way.tile, way.block, way.block + blocks == way.nblk);
                 continue;
             }
@@ -564,7 +610,7 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
                     record.note(rest.seq, rest.head * p.n_tiles + rest.tile, rest.block, rest.block + rest.blocks(a) == rest.nblk);
                 }
             record.timeout = !alive;
-            if (in_tile == 0) a.rec[blockIdx.x] = record;
+            if (threadIdx.x == 0) a.rec[blockIdx.x] = record;
         } else if (!alive) {  // the pieces of the items that were not reached
             for (Walk rest(a, ctl.start); rest.left > 0; rest.next(a))
                 a.ml[((int64_t)blockIdx.x + way_item(rest)) * p.tile_rows + in_tile] = make_float2(neg, kPieceTimeout);
@@ -587,7 +633,7 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
         };
         auto scores = [&](int m, int slot) {
             if (leader) {
-                const uint64_t qd = q_desc + (uint64_t)(m * (Shape::kTileBytes >> 4)), kd = k_desc + (uint64_t)(slot * (Shape::kTileBytes >> 4));
+                const uint64_t qd = q_desc + (uint64_t)((kTurns ? 0 : m) * (Shape::kTileBytes >> 4)), kd = k_desc + (uint64_t)(slot * (Shape::kTileBytes >> 4));
 #pragma unroll
                 for (int s = 0; s < D / 16; ++s) {
                     const uint64_t off = (uint64_t)(((s >> 2) * (128 * 128) + (s & 3) * 32) >> 4);
@@ -596,11 +642,50 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
                 tc_commit(&ctl.s_full[m]);
             }
         };
+        auto weigh_values = [&](int m, int slot, bool add) {  // the second product, of the weights in TMEM
+            const uint64_t vd = v_desc + (uint64_t)(slot * (Shape::kTileBytes >> 4));
+#pragma unroll
+            for (int s = 0; s < kBlockKeys / 16; ++s)
+                mma_ts(tmem + Shape::kOutCol + D * m, tmem + Shape::kScoreCol + 128 * m + s * 8, vd + (uint64_t)(s * (2048 >> 4)), kOutDesc, s > 0 || add);
+        };
         Walk way(a, ctl.start);
+        [[maybe_unused]] uint32_t fill = 0;  // in turn: of the item's first key tile
         for (; way.left > 0 && alive; way.next(a)) {
             const int blocks = way.blocks(a);
             if (!(alive = wait_all(&ctl.q_full, q_parity))) break;
             q_parity ^= 1;
+            if constexpr (kTurns) {
+                // Keys are taken two blocks ahead of values, whose tiles come between: K0 K1 V0 K2 V1 ... of K0 V0 K1 V1 ...
+                auto filled = [&](uint32_t f) { return alive = wait_all(&ctl.full[f % kRing], f / kRing & 1); };
+                auto keys = [&](int v) {
+                    const uint32_t f = fill + 2 * v;
+                    if (!filled(f)) return;
+                    tc_fence_after();
+                    scores(v & 1, f % kRing);
+                    if (leader) tc_commit(&ctl.empty[f % kRing]);
+                };
+                keys(0);
+                if (alive && blocks > 1) keys(1);
+                for (int v = 0; v < blocks && alive; ++v) {
+                    const int m = v & 1, slot = (int)((fill + 2 * v + 1) % kRing);
+                    if (!filled(fill + 2 * v + 1)) break;
+                    if (!k8 && way.open(a) < (way.block + v + 1) * kBlockKeys) {  // its rows that not every query sees are dealt with
+                        if (!(alive = wait_all(&ctl.tail[slot], tail_parity >> slot & 1))) break;
+                        tail_parity ^= 1u << slot;
+                    }
+                    if (!(alive = wait_all(&ctl.p_full[m], p_parity >> m & 1))) break;
+                    p_parity ^= 1u << m;
+                    tc_fence_after();
+                    if (leader) {
+                        weigh_values(m, slot, v > 1);
+                        if (v + 2 >= blocks) tc_commit(&ctl.o_full[m]);
+                        tc_commit(&ctl.empty[slot]);
+                    }
+                    if (v + 2 < blocks) keys(v + 2);
+                }
+                fill += 2 * blocks;
+                continue;
+            }
             int kslot = take();
             if (!alive) break;
             tc_fence_after();
@@ -619,11 +704,7 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
                     if (!(alive = wait_all(&ctl.p_full[m], p_parity))) break;
                     tc_fence_after();
                     if (leader) {
-                        const uint64_t vd = v_desc + (uint64_t)(vslot * (Shape::kTileBytes >> 4));
-#pragma unroll
-                        for (int s = 0; s < kBlockKeys / 16; ++s)
-                            mma_ts(tmem + Shape::kOutCol + D * m, tmem + Shape::kScoreCol + 128 * m + s * 8, vd + (uint64_t)(s * (2048 >> 4)),
-                                   kOutDesc, s > 0 || v > 0);
+                        weigh_values(m, vslot, v > 0);
                         if (v + 1 == blocks) tc_commit(&ctl.o_full[m]);
                     }
                     if (v + 1 < blocks) {
@@ -732,7 +813,7 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles>::kThreads, 1)
         // turn: a barrier's phase may only be waited for by a role that sees each of its phases.
         Walk way(a, ctl.start);
         Turn<kRaw> raw_turn(0);
-        Turn<kScalars> scalar(0);
+        Turn<Shape::kScalars> scalar(0);
         for (; way.left > 0 && alive; way.step(a), scalar.next()) {
             const int left = way.tokens(a) - way.block * kBlockKeys;
             int wide = 0;

@@ -38,11 +38,11 @@ inline cudaError_t encode_cache(CUtensorMap* map, const tps_kv_cache& c, void* b
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int D, int kFormat, int kTiles, bool kTree>
-cudaError_t launch_prefix_shape(const typename LineOf<kTree>::Args& a, cudaStream_t stream)
+template <int D, int kFormat, int kTiles, int kLine>
+cudaError_t launch_prefix_shape(const typename LineOf<kLine>::Args& a, cudaStream_t stream)
 {
-    using Shape = PrefixShape<D, kFormat, kTiles>;
-    auto k = attn_prefix_kernel<D, kFormat, kTiles, kTree>;
+    using Shape = PrefixShape<D, kFormat, kTiles, kLine>;
+    auto k = attn_prefix_kernel<D, kFormat, kTiles, kLine>;
     static std::atomic<uint64_t> allowed{0};  // devices on which the shared memory has been asked for
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -68,13 +68,22 @@ cudaError_t launch_prefix_shape(const typename LineOf<kTree>::Args& a, cudaStrea
     return cudaGetLastError();
 }
 
-template <int kFormat, bool kTree>
-cudaError_t launch_prefix_format(const typename LineOf<kTree>::Args& a, cudaStream_t stream)
+template <int kFormat>
+cudaError_t launch_prefix_format(const AttnArgs& a, cudaStream_t stream)
 {
     const bool two = a.p.tile_rows == 256;
     if (a.c.head_dim == 64)
-        return two ? launch_prefix_shape<64, kFormat, 2, kTree>(a, stream) : launch_prefix_shape<64, kFormat, 1, kTree>(a, stream);
-    return two ? launch_prefix_shape<128, kFormat, 2, kTree>(a, stream) : launch_prefix_shape<128, kFormat, 1, kTree>(a, stream);
+        return two ? launch_prefix_shape<64, kFormat, 2, kShared>(a, stream) : launch_prefix_shape<64, kFormat, 1, kShared>(a, stream);
+    return two ? launch_prefix_shape<128, kFormat, 2, kShared>(a, stream) : launch_prefix_shape<128, kFormat, 1, kShared>(a, stream);
+}
+
+template <int kFormat>
+cudaError_t launch_tree_format(const TreeArgs& a, cudaStream_t stream)
+{
+    const bool two = a.p.tile_rows == 256;
+    if (a.c.head_dim == 64)
+        return two ? launch_prefix_shape<64, kFormat, 2, kTrees>(a, stream) : launch_prefix_shape<64, kFormat, 2, kTreesInTurn>(a, stream);
+    return two ? launch_prefix_shape<128, kFormat, 2, kTrees>(a, stream) : launch_prefix_shape<128, kFormat, 2, kTreesInTurn>(a, stream);
 }
 
 }  // namespace tps

@@ -6,6 +6,9 @@
 // 128 or 256, so that each of the sequence's keys and values is loaded, and converted, once for the whole tree.  Only the
 // blocks that hold drafted tokens are masked.
 //
+// Up to 128 rows: two groups of softmax warps take the item's blocks in turn, each with an output of its own, which are joined
+// at the item's end.  While one's softmax runs, the other's products do; with one group both would wait for each other.
+//
 // Split.  The blocks of 128 tokens of all sequences, key heads and row tiles form one line, which is cut evenly over one
 // CTA per SM: long and short sequences, few and many of them fill the SMs alike.  The lengths are on the device, so each CTA
 // sums them up to find its place.  An item (sequence, key head, row tile) that lies in one CTA is finished there: at most
@@ -30,7 +33,7 @@ __device__ __forceinline__ uint32_t tile_byte(int r, int c)
 struct TreeStart {
     int seq, item, block, left;  // sequence, item of it (key head, row tile), block; blocks of the CTA
 };
-constexpr int kTreeMarks = 8;                    // items whose marks are kept: loads run at most a ring of single blocks ahead of the output
+constexpr int kTreeMarks = 16;                   // items whose marks are kept: loads run at most a ring of single blocks ahead of the output
 constexpr int kMarkBad = 1, kMarkNotFinite = 2;  // a page that is not the cache's; values taken out of the product
 
 // A CTA's way along the line: items of sequence after sequence, each of the sequence's own number of blocks (one, where it has no tokens).
@@ -172,22 +175,43 @@ __device__ __forceinline__ int64_t tree_row_at(const TreeArgs& a, int seq, int h
     return ((int64_t)seq * a.a.n_nodes + node) * a.a.n_q_heads + (int64_t)head * a.G + (in_item - node * a.G);
 }
 
-// The outputs of a warp's rows: finished, or a piece.
-template <int D, int kFormat>
-__device__ __forceinline__ void tree_output(const TreeArgs& a, const TreeWay& way, int blocks, const TreeRow& mine, int in_tile, int in_item,
-                                            uint32_t o_addr, float ref, float sum, int marks)
+// The two warps that have 32 rows in turn wait for one another.
+__device__ __forceinline__ void pair_sync(int pair) { asm volatile("barrier.cta.sync.aligned %0, 64;" ::"r"(pair + 1) : "memory"); }
+
+// The outputs of a warp's rows: finished, or a piece.  `mine_sum`: reference and sum; in turn, `other_sum` is the other group's
+// part of the row, whose output lies D columns from this one's, and each group writes a half of the columns.
+template <int D, int kFormat, bool kTurns>
+__device__ __forceinline__ void tree_output(const TreeArgs& a, const TreeWay& way, int blocks, const TreeRow& mine, int in_tile, int in_item, int m,
+                                            uint32_t out_col, uint32_t o_addr, float2 mine_sum, float2 other_sum, int marks)
 {
     if (in_item - (int)(threadIdx.x & 31) >= a.p.R) return;  // none of the warp's
-    const bool whole = tree_whole(way, blocks), bad = marks & kMarkBad, in = in_item < a.p.R, empty = !mine.live || sum == 0.f;
+    const bool both = kTurns && blocks > 1, in = in_item < a.p.R, bad = marks & kMarkBad, whole = tree_whole(way, blocks);
+    float ref = mine_sum.x, sum = mine_sum.y, f = 1.f, g = 0.f;
+    if (both) {
+        ref = fmaxf(mine_sum.x, other_sum.x);
+        f = mine_sum.x == ref ? 1.f : exp2_fast(mine_sum.x - ref), g = other_sum.x == ref ? 1.f : exp2_fast(other_sum.x - ref);
+        sum = mine_sum.y * f + other_sum.y * g;
+    } else if (kTurns && m == 1) {  // one block: the other group's
+        ref = other_sum.x, sum = other_sum.y;
+    }
+    const bool empty = !mine.live || sum == 0.f;
     const int64_t at = tree_row_at(a, way.seq, way.head, in_item), piece = tree_piece(way);
     const float inv = bad ? __int_as_float(0x7FC00000) : (empty ? 0.f : 1.f / sum);
     uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.a.out) + at * D);
     float4* part = reinterpret_cast<float4*>(a.part + piece * a.p.tile_rows * D) + in_tile;
+    const int from = kTurns ? m * (D / 2) : 0, to = kTurns ? from + D / 2 : D;
 #pragma unroll 1
-    for (int i = 0; i < D; i += 32) {
+    for (int i = from; i < to; i += 32) {
         float o[32];
-        tmem_ld32(o_addr + i, o);
+        tmem_ld32((kTurns ? (both ? o_addr : out_col) : o_addr) + i, o);
         tmem_wait_ld(o);
+        if (both) {
+            float o2[32];
+            tmem_ld32(out_col + D * (m ^ 1) + i, o2);
+            tmem_wait_ld(o2);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = o[j] * f + o2[j] * g;
+        }
         if (!in) continue;
         if (kFormat == TPS_KV_BF16 && (marks & kMarkNotFinite) && !bad) {  // what was taken out of the product, for a row that sees it
             for (uint64_t left = mine.seen; left; left &= left - 1) {
@@ -218,7 +242,7 @@ __device__ __forceinline__ void tree_output(const TreeArgs& a, const TreeWay& wa
             for (int j = 0; j < 32; j += 4) part[(i + j) / 4 * a.p.tile_rows] = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
         }
     }
-    if (!in) return;
+    if (!in || (kTurns && m == 1)) return;
     if (whole) {
         if (a.a.out_lse) a.a.out_lse[at] = log_sum<kFormat>(ref, mine.live ? sum : 0.f, bad);
     } else {

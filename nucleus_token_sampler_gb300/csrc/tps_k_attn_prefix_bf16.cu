@@ -5,7 +5,7 @@ namespace tps {
 
 cudaError_t launch_attn_prefix_bf16(const AttnArgs& a, cudaStream_t stream)
 {
-    return launch_prefix_format<TPS_KV_BF16, false>(a, stream);
+    return launch_prefix_format<TPS_KV_BF16>(a, stream);
 }
 
 }  // namespace tps

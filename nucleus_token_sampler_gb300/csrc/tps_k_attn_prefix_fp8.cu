@@ -5,7 +5,7 @@ namespace tps {
 
 cudaError_t launch_attn_prefix_fp8(const AttnArgs& a, cudaStream_t stream)
 {
-    return launch_prefix_format<TPS_KV_FP8, false>(a, stream);
+    return launch_prefix_format<TPS_KV_FP8>(a, stream);
 }
 
 }  // namespace tps

@@ -5,7 +5,7 @@ namespace tps {
 
 cudaError_t launch_attn_prefix_int8(const AttnArgs& a, cudaStream_t stream)
 {
-    return launch_prefix_format<TPS_KV_INT8, false>(a, stream);
+    return launch_prefix_format<TPS_KV_INT8>(a, stream);
 }
 
 }  // namespace tps

@@ -8,7 +8,7 @@ namespace {
 constexpr int kJoinThreads = 256;
 
 // Blocks (c, y) with c below a.p.ctas: rows kTreeJoinRows y and up of the item that CTA c began and did not finish, from its piece and the
-// first pieces of the CTAs after it; a lane for each row, a warp for each 4 columns in turn.  The blocks after them
+// first pieces of the CTAs after it; a lane for each row, an eighth of the columns for each warp.  The blocks after them
 // tell the statuses, a warp for each sequence.
 template <int D, int kFormat> __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_constant__ TreeArgs a)
 {
@@ -31,49 +31,54 @@ template <int D, int kFormat> __global__ void __launch_bounds__(kJoinThreads) tr
     const int cta = (int)blockIdx.x;
     const TreeRecord mine = a.rec[cta];
     if (mine.open_seq < 0) return;
-    int last = cta + 1;
-    while (last + 1 < ctas && !a.rec[last].ended) ++last;
-    const int tile = mine.open_item % a.p.n_tiles, head = mine.open_item / a.p.n_tiles;
+    int last = cta;
+    for (uint32_t ends = 0; !ends;) {  // 32 CTAs at a time
+        const int c = last + 1 + lane;
+        ends = __ballot_sync(0xFFFFFFFFu, c >= ctas - 1 || a.rec[c].ended);
+        last += ends ? __ffs(ends) : 32;
+    }
+    const int n = last - cta + 1, tile = mine.open_item % a.p.n_tiles, head = mine.open_item / a.p.n_tiles;
     const int row = (int)blockIdx.y * kTreeJoinRows + lane, in_item = tile * rows + row;
     if (in_item - lane >= a.p.R) return;
     const bool in = in_item < a.p.R;
-    const float neg = -__int_as_float(0x7F800000);
-    const float2* ml = a.ml + row;
-    auto piece = [&](int c) { return c == cta ? 2 * (int64_t)c + 1 : 2 * (int64_t)c; };
-    float top = neg, sum = 0.f;
+    auto piece = [&](int i) { return 2 * (int64_t)(cta + i) + (i == 0); };
+    // Maxima and sums of every piece, then its factor.
+    extern __shared__ float2 factor[];  // [n][32]: maximum, sum; then .x is the factor
+    for (int i = warp; i < n; i += kJoinThreads / 32) factor[i * 32 + lane] = in ? a.ml[piece(i) * rows + row] : make_float2(0.f, 0.f);
+    __syncthreads();
+    float top = -__int_as_float(0x7F800000), sum = 0.f;
     bool bad = false;
-    if (in) {
 #pragma unroll 4
-        for (int c = cta; c <= last; ++c) {
-            const float2 x = ml[piece(c) * rows];
-            bad |= x.y < 0.f;
-            if (x.y != 0.f) top = fmaxf(top, x.x);
-        }
+    for (int i = 0; i < n; ++i) {
+        const float2 x = factor[i * 32 + lane];
+        bad |= x.y < 0.f;
+        if (x.y != 0.f) top = fmaxf(top, x.x);
+    }
+    auto weight = [&](float2 x) { return x.y == 0.f ? 0.f : (x.x == top ? 1.f : exp2_fast(x.x - top)); };
 #pragma unroll 4
-        for (int c = cta; c <= last; ++c) {
-            const float2 x = ml[piece(c) * rows];
-            if (x.y != 0.f) sum += x.y * (x.x == top ? 1.f : exp2_fast(x.x - top));
+    for (int i = 0; i < n; ++i) sum += factor[i * 32 + lane].y * weight(factor[i * 32 + lane]);
+    __syncthreads();
+    for (int i = warp; i < n; i += kJoinThreads / 32) factor[i * 32 + lane].x = weight(factor[i * 32 + lane]);
+    __syncthreads();
+    if (!in) return;
+    constexpr int kEach = D / 4 / (kJoinThreads / 32);  // columns of four of a warp
+    const float4* part = reinterpret_cast<const float4*>(a.part) + row;
+    float4 o[kEach] = {};
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+        const float f = factor[i * 32 + lane].x;
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const float4 y = part[(piece(i) * (D / 4) + warp * kEach + k) * rows];
+            if (f != 0.f) o[k].x += y.x * f, o[k].y += y.y * f, o[k].z += y.z * f, o[k].w += y.w * f;
         }
     }
-    const float inv = bad ? __int_as_float(0x7FC00000) : 1.f / sum;
-    const int64_t at = tree_row_at(a, mine.open_seq, head, in ? in_item : 0);
-    if (!in) return;
-    for (int d = warp; d < D / 4; d += kJoinThreads / 32) {
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int c = cta; c <= last; ++c) {
-            const float2 x = ml[piece(c) * rows];
-            const float4 y = *(reinterpret_cast<const float4*>(a.part + piece(c) * rows * D) + d * rows + row);
-            if (x.y == 0.f) continue;
-            const float f = x.x == top ? 1.f : exp2_fast(x.x - top);
-            o.x += y.x * f, o.y += y.y * f, o.z += y.z * f, o.w += y.w * f;
-        }
-        if (sum == 0.f && !bad)
-            o = make_float4(0.f, 0.f, 0.f, 0.f);
-        else
-            o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
-        const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x, o.y), hi = __floats2bfloat162_rn(o.z, o.w);
-        reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.a.out) + at * D)[d] =
+    const float inv = bad ? __int_as_float(0x7FC00000) : (sum == 0.f ? 0.f : 1.f / sum);
+    const int64_t at = tree_row_at(a, mine.open_seq, head, in_item);
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(o[k].x * inv, o[k].y * inv), hi = __floats2bfloat162_rn(o[k].z * inv, o[k].w * inv);
+        reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.a.out) + at * D)[warp * kEach + k] =
             make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
     }
     if (warp == 0 && a.a.out_lse) a.a.out_lse[at] = log_sum<kFormat>(top, sum, bad);
@@ -90,6 +95,7 @@ template <int D, int kFormat> cudaError_t join(const TreeArgs& a, cudaStream_t s
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.p.ctas + status), y, 1);
     cfg.blockDim = dim3(kJoinThreads, 1, 1);
+    cfg.dynamicSmemBytes = (size_t)a.p.ctas * 32 * sizeof(float2);
     cfg.stream = stream;
     cfg.attrs = &at;
     cfg.numAttrs = 1;

@@ -5,7 +5,7 @@ namespace tps {
 
 cudaError_t launch_attn_tree_fp8(const TreeArgs& a, cudaStream_t stream)
 {
-    return launch_prefix_format<TPS_KV_FP8, true>(a, stream);
+    return launch_tree_format<TPS_KV_FP8>(a, stream);
 }
 
 }  // namespace tps
