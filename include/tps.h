@@ -490,7 +490,7 @@ typedef struct {
  *   positions    [tokens] int32: its position in its sequence (0 without a slot; for tps_qk_norm_rope).
  *   cu_seqlens   [B + 1] int32: where each sequence's rows begin, and where the last one's end (for
  *                tps_prompt_attention).  A sequence whose rows are more than there are has what is left.
- * Calls with many rows draw 4 bytes for each sequence from the library's memory pool.
+ * Calls with many rows draw 8 bytes for each sequence from the library's memory pool.
  */
 int tps_kv_extend(const tps_kv_pages* pages, int64_t tokens, int64_t* slots, int32_t* positions, int32_t* cu_seqlens, void* stream);
 

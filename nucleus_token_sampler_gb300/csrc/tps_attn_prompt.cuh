@@ -38,8 +38,7 @@ constexpr int kDirty = 8;  // items whose marks are kept: the loads run at most 
 
 template <int D> struct PromptShape {
     static constexpr int kTileBytes = 128 * D * 2;
-        static constexpr int kRing = D == 128 ? 5 : 8;
-  // key and value tiles in shared memory
+    static constexpr int kRing = D == 128 ? 5 : 8;  // key and value tiles in shared memory
     static constexpr int kOutCol = 256;             // TMEM: scores (and weights) of tile m at 128 m, outputs at 256 + D m
     struct Control {
         uint64_t full[kRing], empty[kRing], go[kRing], clean[kRing];

@@ -154,7 +154,9 @@ struct PagesArgs {
     int64_t* slots;
     int32_t* positions;
     int32_t* cu_seqlens;
-    int32_t* first;  // [B] for the second kernel: position of a sequence's first new token, -1 where there is none
+    // [B + 1] for the second kernel: the position of a sequence's first new token (-1: none) and the pages taken ahead of its
+    // own; at last the number of free pages there were.
+    int2* first;
     bool wide;       // slots and positions begin on 16 bytes
 };
 cudaError_t launch_kv_extend(const PagesArgs& a, cudaStream_t stream);

@@ -7,10 +7,11 @@
 // sequence has the slot table[x / p] p + x mod p.  Giving back is the inverse, entry for entry: a trim that undoes an
 // extension leaves list and count as they were.
 //
-// What bounds it: the launch and a chain of few dependent loads (lengths, a scan, free pages, table entries).  One CTA
-// makes the plan: sums over up to 1,024 sequences at a time in shared memory, then a thread for each new page and for each
-// new token, which finds its sequence by bisection, so that long and short sequences cost alike and stores are whole
-// sectors.  From kPagesAlone tokens on a second kernel, of as many CTAs as that takes, writes the slots.
+// What bounds it: the launch and a chain of few dependent loads (lengths, a scan, free pages or table entries).  Up to 1,024
+// sequences at a time are summed up in shared memory; then there is a thread for each new token, which finds its sequence by
+// bisection, so that long and short sequences cost alike and stores are whole sectors.  A page's first token also puts it in the
+// table: the pages need no pass of their own, and no token waits for the table.  Many tokens of up to 1,024 sequences are
+// shared by a cluster of CTAs, each of which sums up for itself; more still by a second kernel over all SMs.
 #pragma once
 
 #include "tps_decode.h"
@@ -57,19 +58,18 @@ template <int N> __device__ __forceinline__ void owners(const int* first, int n,
 {
 #pragma unroll
     for (int k = 0; k < N; ++k) at[k] = 0;
-#pragma unroll
-    for (int step = kPagesThreads / 2; step > 0; step >>= 1)
+    for (int step = 1 << (31 - __clz(max(n - 1, 1))); step > 0; step >>= 1)
 #pragma unroll
         for (int k = 0; k < N; ++k)
             if (at[k] + step < n && first[at[k] + step] <= x[k]) at[k] += step;
 }
 
-// do_one(i, the sequence that `first` gives i to) for all i below `count`, four of a thread at a time: load_one's values are on
-// their way together.
+// For all i below `count`, shared over the cluster's CTAs: load_one(i, the sequence that `first` gives i to), then
+// store_one(i, sequence, that value); four of a thread at a time, whose loads are on their way together.
 template <typename Value, typename Load, typename Store>
 __device__ __forceinline__ void for_each_owned(const int* first, int n, int64_t count, Load load_one, Store store_one)
 {
-    for (int64_t base = 0; base < count; base += 4 * kPagesThreads) {
+    for (int64_t base = (int64_t)blockIdx.x * (4 * kPagesThreads); base < count; base += (int64_t)gridDim.x * (4 * kPagesThreads)) {
         int x[4], at[4];
         Value v[4];
 #pragma unroll
@@ -90,9 +90,26 @@ __device__ __forceinline__ void note_moved(PagesShared& sh, bool served, int64_t
     if (who && (threadIdx.x & 31) == 31 - __clz(who)) atomicMax(&sh.moved, (unsigned long long)sum);
 }
 
-__device__ __forceinline__ int64_t slot_of(const PagesArgs& a, int64_t b, int at)
+// The page of a new token at position `at` of sequence b: one it has (`has` of them), or, of the free list, the one `from` down
+// from its end and so on.
+__device__ __forceinline__ int page_of(const PagesArgs& a, int64_t b, int at, int has, int64_t count, int64_t from)
 {
-    return ((int64_t)a.p.page_table[b * a.p.table_ld + (at >> a.page_shift)] << a.page_shift) + (at & a.page_mask);
+    const int page = at >> a.page_shift;
+    return *(page < has ? a.p.page_table + b * a.p.table_ld + page : a.p.free_pages + (count - 1 - (from + (page - has))));
+}
+// A page's first token puts it in the table, if it is new.
+__device__ __forceinline__ void note_page(const PagesArgs& a, int64_t b, int at, int has, int page)
+{
+    if ((at & a.page_mask) == 0 && at >> a.page_shift >= has) a.p.page_table[b * a.p.table_ld + (at >> a.page_shift)] = page;
+}
+
+// In a cluster nothing that another CTA may still read is overwritten before all have read it; it has one chunk of sequences.
+__device__ __forceinline__ void all_have_read()
+{
+    if (gridDim.x > 1) {
+        cluster_arrive();
+        cluster_wait();
+    }
 }
 
 template <bool kSlots> __global__ void __launch_bounds__(kPagesThreads) kv_extend_kernel(const __grid_constant__ PagesArgs a)
@@ -100,8 +117,9 @@ template <bool kSlots> __global__ void __launch_bounds__(kPagesThreads) kv_exten
     __shared__ PagesShared sh;
     const tps_kv_pages& p = a.p;
     const int tid = (int)threadIdx.x;
+    const bool first_cta = blockIdx.x == 0;
     const int64_t count = min((int64_t)max(*p.free_count, 0), p.n_free), room = p.table_width << a.page_shift;
-    int64_t asked = 0, packed = 0, moved = 0;  // pages asked for, rows so far, pages taken from the list
+    int64_t asked = 0, packed = 0;  // pages asked for, rows so far
     if (tid == 0) sh.moved = 0;
     for (int64_t base = 0; base < p.B; base += kPagesThreads) {
         const int64_t b = base + tid;
@@ -113,55 +131,57 @@ template <bool kSlots> __global__ void __launch_bounds__(kPagesThreads) kv_exten
         int64_t pages = need, tokens = rows, all_pages, all_tokens;
         block_sums(sh, pages, tokens, all_pages, all_tokens);
         // Once a sequence's pages or rows are too many, so are those of all that come after it and ask for any: what
-        // has been taken is always a piece of the list without gaps.
+        // is taken is always a piece of the list without gaps, and each sequence's pages lie as far from its end as the sum says.
         const bool fits = rows == 0 || packed + tokens <= a.tokens, there = need == 0 || asked + pages <= count, done = valid && fits && there;
         note_moved(sh, done && need > 0, asked + pages);
-        sh.pages[tid] = (int)min(pages - need, (int64_t)INT32_MAX);
+        sh.pages[tid] = (int)min(asked + pages - need, (int64_t)INT32_MAX);
         sh.tokens[tid] = (int)min(tokens - rows, max(a.tokens - packed, (int64_t)0));
         sh.length[tid] = done ? (int)s : -1;
         sh.has[tid] = (int)has;
-        if (in) {
+        if (in && first_cta) {
             if (p.out_status) p.out_status[b] = done ? TPS_ROW_OK : (valid && fits ? TPS_ROW_NO_PAGES : TPS_ROW_BAD_PARAM);
             a.cu_seqlens[b] = (int)min(packed + tokens - rows, a.tokens);
-            if (done) p.seq_len[b] = (int)(s + n);
-            if (!kSlots) a.first[b] = done ? (int)s : -1;
+            if (!kSlots) a.first[b] = make_int2(sh.length[tid], sh.pages[tid]);
         }
         __syncthreads();
-        const int live = (int)min(p.B - base, (int64_t)kPagesThreads);
-        const int64_t now = (int64_t)sh.moved;
-        for_each_owned<int>(
-            sh.pages, live, now - moved, [&](int i, int) { return p.free_pages[count - 1 - (moved + i)]; },
-            [&](int i, int w, int page) { p.page_table[(base + w) * p.table_ld + sh.has[w] + (i - sh.pages[w])] = page; });
-        if (kSlots) {
-            __syncthreads();
-            for_each_owned<int64_t>(
-                sh.tokens, live, min(all_tokens, a.tokens - packed),
-                [&](int i, int w) { return sh.length[w] >= 0 ? slot_of(a, base + w, sh.length[w] + i - sh.tokens[w]) : -1; },
-                [&](int i, int w, int64_t slot) {
-                    a.slots[packed + i] = slot;
-                    a.positions[packed + i] = sh.length[w] >= 0 ? sh.length[w] + i - sh.tokens[w] : 0;
+        if (kSlots)
+            for_each_owned<int>(
+                sh.tokens, (int)min(p.B - base, (int64_t)kPagesThreads), min(all_tokens, a.tokens - packed),
+                [&](int i, int w) {
+                    return sh.length[w] >= 0 ? page_of(a, base + w, sh.length[w] + i - sh.tokens[w], sh.has[w], count, sh.pages[w]) : 0;
+                },
+                [&](int i, int w, int page) {
+                    const int at = sh.length[w] + i - sh.tokens[w];
+                    const bool ok = sh.length[w] >= 0;
+                    a.slots[packed + i] = ok ? ((int64_t)page << a.page_shift) + (at & a.page_mask) : -1;
+                    a.positions[packed + i] = ok ? at : 0;
+                    if (ok) note_page(a, base + w, at, sh.has[w], page);
                 });
-        }
-        moved = now;
+        all_have_read();
+        if (in && first_cta && done) p.seq_len[b] = (int)(s + n);
         asked += all_pages;
         packed += all_tokens;
         __syncthreads();  // the chunk's numbers have been read
     }
-    if (tid == 0) {
+    if (tid == 0 && first_cta) {
+        if (!kSlots) a.first[p.B] = make_int2((int)count, 0);
         a.cu_seqlens[p.B] = (int)min(packed, a.tokens);
-        *p.free_count = (int)(count - moved);
+        *p.free_count = (int)(count - (int64_t)sh.moved);
     }
     if (kSlots)
-        for (int64_t i = packed + tid; i < a.tokens; i += kPagesThreads) a.slots[i] = -1, a.positions[i] = 0;
+        for (int64_t i = packed + (int64_t)blockIdx.x * kPagesThreads + tid; i < a.tokens; i += (int64_t)gridDim.x * kPagesThreads)
+            a.slots[i] = -1, a.positions[i] = 0;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// The slots and positions of many tokens, kSlotsEach to a thread.
+// The slots, positions and new pages of many tokens, kSlotsEach tokens to a thread.  (The sequences' lengths and the count of free
+// pages have been moved on: `first` holds what they were.)
 static __global__ void __launch_bounds__(kSlotsThreads) kv_slots_kernel(const __grid_constant__ PagesArgs a)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan
     const int64_t begin = (int64_t)blockIdx.x * kSlotsThreads * kSlotsEach, i0 = begin + (int64_t)threadIdx.x * kSlotsEach;
     const int total = a.cu_seqlens[a.p.B];
+    const int64_t count = a.first[a.p.B].x;
     // The last sequence that begins at or before the CTA's first row, and before its last: all threads count.
     int64_t low = -1, high = -1;
     for (int64_t base = 0; base < a.p.B; base += kSlotsThreads) {
@@ -181,13 +201,23 @@ static __global__ void __launch_bounds__(kSlotsThreads) kv_slots_kernel(const __
     }
     int64_t slot[kSlotsEach];
     int position[kSlotsEach];
+    int64_t of = -1;  // the sequence that the numbers below are of
+    int2 first = {};
+    int begins = 0, ends = 0, has = 0;
 #pragma unroll
     for (int j = 0; j < kSlotsEach; ++j) {
         slot[j] = -1, position[j] = 0;
         if (i0 + j < total) {
-            while (a.cu_seqlens[b + 1] <= i0 + j) ++b;
-            const int s = a.first[b], at = s + (int)(i0 + j) - a.cu_seqlens[b];
-            if (s >= 0) slot[j] = slot_of(a, b, at), position[j] = at;
+            if (of < 0 || ends <= i0 + j) {
+                while ((ends = a.cu_seqlens[b + 1]) <= i0 + j) ++b;
+                of = b, begins = a.cu_seqlens[b], first = a.first[b], has = (first.x + a.page_mask) >> a.page_shift;
+            }
+            const int at = first.x + (int)(i0 + j) - begins;
+            if (first.x >= 0) {
+                const int page = page_of(a, b, at, has, count, first.y);
+                slot[j] = ((int64_t)page << a.page_shift) + (at & a.page_mask), position[j] = at;
+                note_page(a, b, at, has, page);
+            }
         }
     }
     if (i0 + kSlotsEach <= a.tokens && a.wide) {
@@ -204,6 +234,7 @@ static __global__ void __launch_bounds__(kPagesThreads) kv_trim_kernel(const __g
     __shared__ PagesShared sh;
     const tps_kv_pages& p = a.p;
     const int tid = (int)threadIdx.x;
+    const bool first_cta = blockIdx.x == 0;
     const int64_t count = min((int64_t)max(*p.free_count, 0), p.n_free), room = p.table_width << a.page_shift;
     if (tid == 0) sh.moved = 0;
     int64_t total = 0;
@@ -225,10 +256,7 @@ static __global__ void __launch_bounds__(kPagesThreads) kv_trim_kernel(const __g
             if (pass == 1) {
                 sh.pages[tid] = (int)min(pages - back, (int64_t)INT32_MAX);
                 sh.has[tid] = (int)keep;
-                if (in) {
-                    if (p.out_status) p.out_status[b] = done ? TPS_ROW_OK : (valid ? TPS_ROW_NO_PAGES : TPS_ROW_BAD_PARAM);
-                    if (done) p.seq_len[b] = (int)k;
-                }
+                if (in && first_cta && p.out_status) p.out_status[b] = done ? TPS_ROW_OK : (valid ? TPS_ROW_NO_PAGES : TPS_ROW_BAD_PARAM);
             }
             __syncthreads();
             if (pass == 1) {
@@ -238,13 +266,15 @@ static __global__ void __launch_bounds__(kPagesThreads) kv_trim_kernel(const __g
                     sh.pages, (int)min(p.B - base, (int64_t)kPagesThreads), min(all_pages, total - min(asked, total)),
                     [&](int i, int w) { return p.page_table[(base + w) * p.table_ld + sh.has[w] + (i - sh.pages[w])]; },
                     [&](int i, int, int page) { p.free_pages[count + total - 1 - (asked + i)] = page; });
+                all_have_read();
+                if (in && first_cta && done) p.seq_len[b] = (int)k;
             }
             asked += all_pages;
             __syncthreads();
         }
         total = (int64_t)sh.moved;
     }
-    if (tid == 0) *p.free_count = (int)(count + total);
+    if (tid == 0 && first_cta) *p.free_count = (int)(count + total);
 }
 
 }  // namespace tps
