@@ -10,8 +10,8 @@
 // What bounds it: the launch and a chain of few dependent loads (lengths, a scan, free pages or table entries).  Up to 1,024
 // sequences at a time are summed up in shared memory; then there is a thread for each new token, which finds its sequence by
 // bisection, so that long and short sequences cost alike and stores are whole sectors.  A page's first token also puts it in the
-// table: the pages need no pass of their own, and no token waits for the table.  Many tokens of up to 1,024 sequences are
-// shared by a cluster of CTAs, each of which sums up for itself; more still by a second kernel over all SMs.
+// table: the pages need no pass of their own, and no token waits for the table.  From some 2,000 tokens on they are a second
+// kernel's, over all SMs; a trim of many pages is shared by a cluster of CTAs, each of which sums up for itself.
 #pragma once
 
 #include "tps_decode.h"
@@ -103,21 +103,11 @@ __device__ __forceinline__ void note_page(const PagesArgs& a, int64_t b, int at,
     if ((at & a.page_mask) == 0 && at >> a.page_shift >= has) a.p.page_table[b * a.p.table_ld + (at >> a.page_shift)] = page;
 }
 
-// In a cluster nothing that another CTA may still read is overwritten before all have read it; it has one chunk of sequences.
-__device__ __forceinline__ void all_have_read()
-{
-    if (gridDim.x > 1) {
-        cluster_arrive();
-        cluster_wait();
-    }
-}
-
 template <bool kSlots> __global__ void __launch_bounds__(kPagesThreads) kv_extend_kernel(const __grid_constant__ PagesArgs a)
 {
     __shared__ PagesShared sh;
     const tps_kv_pages& p = a.p;
     const int tid = (int)threadIdx.x;
-    const bool first_cta = blockIdx.x == 0;
     const int64_t count = min((int64_t)max(*p.free_count, 0), p.n_free), room = p.table_width << a.page_shift;
     int64_t asked = 0, packed = 0;  // pages asked for, rows so far
     if (tid == 0) sh.moved = 0;
@@ -138,7 +128,7 @@ template <bool kSlots> __global__ void __launch_bounds__(kPagesThreads) kv_exten
         sh.tokens[tid] = (int)min(tokens - rows, max(a.tokens - packed, (int64_t)0));
         sh.length[tid] = done ? (int)s : -1;
         sh.has[tid] = (int)has;
-        if (in && first_cta) {
+        if (in) {
             if (p.out_status) p.out_status[b] = done ? TPS_ROW_OK : (valid && fits ? TPS_ROW_NO_PAGES : TPS_ROW_BAD_PARAM);
             a.cu_seqlens[b] = (int)min(packed + tokens - rows, a.tokens);
             if (!kSlots) a.first[b] = make_int2(sh.length[tid], sh.pages[tid]);
@@ -157,20 +147,18 @@ template <bool kSlots> __global__ void __launch_bounds__(kPagesThreads) kv_exten
                     a.positions[packed + i] = ok ? at : 0;
                     if (ok) note_page(a, base + w, at, sh.has[w], page);
                 });
-        all_have_read();
-        if (in && first_cta && done) p.seq_len[b] = (int)(s + n);
+        if (in && done) p.seq_len[b] = (int)(s + n);
         asked += all_pages;
         packed += all_tokens;
         __syncthreads();  // the chunk's numbers have been read
     }
-    if (tid == 0 && first_cta) {
+    if (tid == 0) {
         if (!kSlots) a.first[p.B] = make_int2((int)count, 0);
         a.cu_seqlens[p.B] = (int)min(packed, a.tokens);
         *p.free_count = (int)(count - (int64_t)sh.moved);
     }
     if (kSlots)
-        for (int64_t i = packed + (int64_t)blockIdx.x * kPagesThreads + tid; i < a.tokens; i += (int64_t)gridDim.x * kPagesThreads)
-            a.slots[i] = -1, a.positions[i] = 0;
+        for (int64_t i = packed + tid; i < a.tokens; i += kPagesThreads) a.slots[i] = -1, a.positions[i] = 0;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
@@ -226,6 +214,15 @@ static __global__ void __launch_bounds__(kSlotsThreads) kv_slots_kernel(const __
         *reinterpret_cast<int4*>(a.positions + i0) = make_int4(position[0], position[1], position[2], position[3]);
     } else {
         for (int j = 0; j < kSlotsEach && i0 + j < a.tokens; ++j) a.slots[i0 + j] = slot[j], a.positions[i0 + j] = position[j];
+    }
+}
+
+// In a cluster nothing that another CTA may still read is overwritten before all have read it; it has one chunk of sequences.
+__device__ __forceinline__ void all_have_read()
+{
+    if (gridDim.x > 1) {
+        cluster_arrive();
+        cluster_wait();
     }
 }
 
