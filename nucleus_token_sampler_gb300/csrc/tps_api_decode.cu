@@ -184,7 +184,7 @@ int plan_tree(const tps_kv_cache& c, const tps_tree& t, int sms, tps::TreePlan* 
     p.n_tiles = (int)((R + p.tile_rows - 1) / p.tile_rows);
     const int64_t items = (int64_t)p.n_tiles * c.n_heads;  // of a sequence
     const int64_t most = std::max<int64_t>((t.table_width * c.page_size + tps::kBlockKeys - 1) / tps::kBlockKeys, 1) * items;
-    if (most > INT32_MAX || t.B > INT32_MAX / most) return TPS_ERR_ARG;
+    if (most > INT32_MAX || t.B > INT32_MAX / most) return TPS_ERR_ARG;  // the kernels count the line's blocks in 32 bits
     p.ctas = (int)std::min<int64_t>(sms, most * t.B);
     p.off_ml = (size_t)2 * p.ctas * p.tile_rows * c.head_dim * sizeof(float);
     p.off_rec = p.off_ml + (size_t)2 * p.ctas * p.tile_rows * sizeof(float2);

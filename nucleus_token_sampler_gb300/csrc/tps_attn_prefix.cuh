@@ -89,7 +89,7 @@ template <int D, int kFormat, int kTiles, int kLine> struct PrefixShape {
         uint32_t tmem;
         int abort, bad;
         TreeStart start;          // of trees: where this CTA's line begins
-        int64_t sums[kThreads / 32];
+        uint32_t sums[kThreads / 32];
         int marks[kTreeMarks];    // by item: kMark*
         // In turn: a row's factor for the group that did not load it, what the groups' halves of it come to, by 32 rows
         // whether a wait of either ran out.

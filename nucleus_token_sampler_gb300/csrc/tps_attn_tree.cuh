@@ -31,7 +31,8 @@ __device__ __forceinline__ uint32_t tile_byte(int r, int c)
 }
 
 struct TreeStart {
-    int seq, item, block, left;  // sequence, item of it (key head, row tile), block; blocks of the CTA
+    int seq, head, tile, block, left;  // sequence, key head and row tile of its item, block; blocks of the CTA
+    int len, nodes;                    // of the sequence, as they are
 };
 constexpr int kTreeMarks = 16;                   // items whose marks are kept: loads run at most a ring of single blocks ahead of the output
 constexpr int kMarkBad = 1, kMarkNotFinite = 2;  // a page that is not the cache's; values taken out of the product
@@ -44,9 +45,8 @@ struct TreeWay {
     int next_len, next_nodes;                   // of the next sequence, read ahead
     __device__ __forceinline__ explicit TreeWay(const TreeArgs& a, const TreeStart& s)
     {
-        seq = s.seq, block = s.block, left = s.left, ordinal = 0;
-        head = s.item / a.p.n_tiles, tile = s.item - head * a.p.n_tiles;
-        look(a, seq);
+        seq = s.seq, head = s.head, tile = s.tile, block = s.block, left = s.left, ordinal = 0;
+        next_len = s.len, next_nodes = s.nodes;
         enter(a);
     }
     __device__ __forceinline__ void look(const TreeArgs& a, int b)
@@ -94,39 +94,41 @@ struct TreeWay {
     }
 };
 
-// Where a CTA's equal share of the line begins, found by all its threads.
+// Where a CTA's equal share of the line begins, found by all its threads.  (The host has seen to it that the line's blocks, and
+// a share more, can be counted in 32 bits: divisions of 64 took 2,000 clocks at the start of every CTA.)
 template <int kThreads>
-__device__ __forceinline__ void tree_start(const TreeArgs& a, TreeStart& start, int64_t (&sums)[kThreads / 32])
+__device__ __forceinline__ void tree_start(const TreeArgs& a, TreeStart& start, uint32_t (&sums)[kThreads / 32])
 {
-    const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5, items = a.c.n_heads * a.p.n_tiles;
-    const int64_t each = (a.a.B + kThreads - 1) / kThreads, from = min(each * tid, a.a.B), to = min(from + each, a.a.B);
-    auto blocks = [&](int64_t b) {
-        const int len = a.a.seq_len[b], nodes = a.a.tree_len ? a.a.tree_len[b] : a.a.n_nodes;
-        return TreeWay::tree_bad(a, len, nodes) ? 1 : TreeWay::tree_blocks(len);
+    const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t items = a.c.n_heads * a.p.n_tiles, B = (uint32_t)a.a.B, each = B <= kThreads ? 1 : (B + kThreads - 1) / kThreads;
+    const uint32_t from = min(each * tid, B), to = min(from + each, B);
+    int len = 0, nodes = 0;
+    auto blocks = [&](uint32_t b) {
+        len = a.a.seq_len[b], nodes = a.a.tree_len ? a.a.tree_len[b] : a.a.n_nodes;
+        return (uint32_t)(TreeWay::tree_bad(a, len, nodes) ? 1 : TreeWay::tree_blocks(len));
     };
-    int64_t mine = 0;
-    for (int64_t b = from; b < to; ++b) mine += blocks(b);
-    int64_t sum = mine;
+    uint32_t mine = 0;
+    for (uint32_t b = from; b < to; ++b) mine += blocks(b);
+    uint32_t sum = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t x = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+        const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, sum, o);
         if (lane >= o) sum += x;
     }
     if (lane == 31) sums[warp] = sum;
-    if (tid == 0) start = TreeStart{0, 0, 0, 0};
+    if (tid == 0) start = TreeStart{0, 0, 0, 0, 0, 0, 0};
     __syncthreads();
-    int64_t all = 0;
+    uint32_t all = 0;
     for (int w = 0; w < kThreads / 32; ++w) {
         if (w < warp) sum += sums[w];
         all += sums[w];
     }
-    const int64_t units = all * items, share = (units + gridDim.x - 1) / gridDim.x, u0 = share * blockIdx.x;
+    const uint32_t units = all * items, share = (units + gridDim.x - 1) / gridDim.x, u0 = share * blockIdx.x;
     if (u0 >= (sum - mine) * items && u0 < sum * items) {
-        int64_t before = sum - mine, b = from;
-        int n = blocks(b);
+        uint32_t before = sum - mine, b = from, n = each == 1 ? mine : blocks(b);
         while (u0 >= (before + n) * items) before += n, n = blocks(++b);
-        const int rest = (int)(u0 - before * items);
-        start = TreeStart{(int)b, rest / n, rest % n, (int)min(share, units - u0)};
+        const uint32_t rest = u0 - before * items, item = rest / n, head = a.p.n_tiles == 1 ? item : item / a.p.n_tiles;
+        start = TreeStart{(int)b, (int)head, (int)(item - head * a.p.n_tiles), (int)(rest - item * n), (int)min(share, units - u0), len, nodes};
     }
 }
 
