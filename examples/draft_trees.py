@@ -52,7 +52,7 @@ class Requests:
         slots, positions, cu = self.extend(lengths, tokens.numel())
         x = self._layers(tokens, positions, slots, lambda q, k, v, cache: tps.prompt_attention(q, k, v, cu))
         logits = (rms(x[cu[1:].long() - 1]) @ model.head).float()
-        self.pending = tps.sample(logits, 0.0, 0, 1.0, 0.0, 0, 0)["token"]  # greedy: the next token of each request
+        self.pending = tps.sample(logits, 0.0, 0, 1.0, 0.0, 0, 0)  # greedy: the next token of each request
 
     def extend(self, new, tokens):
         out = tps.kv_extend(self.table, self.length, new, self.free, self.count, self.page, tokens, status=self.status)
@@ -86,7 +86,7 @@ class Requests:
             return tps.tree_attention(q.view(B, N, *q.shape[1:]), cache, self.table, self.length, self.tree)
         x = self._layers(nodes.flatten(), positions, slots, attend)
         logits = (rms(x) @ self.model.head).float()
-        after = tps.sample(logits, 0.0, 0, 1.0, 0.0, 0, 0)["token"].view(B, N)
+        after = tps.sample(logits, 0.0, 0, 1.0, 0.0, 0, 0).view(B, N)
         chains, kept, ahead = [], [], after.tolist()
         for b, row in enumerate(nodes.tolist()):
             chain, node = [0], 0
