@@ -152,6 +152,7 @@ int check_prompt(const tps_prompt* p, tps::PromptArgs* a, int64_t* tiles)
     a->level_shift = 0;
     while ((p->T / tps::kBlockKeys + 1) >> a->level_shift >= 2048) ++a->level_shift;
     a->qk_scale = (float)((double)p->scale * 1.4426950408889634);
+    if (!std::isfinite(a->qk_scale)) return TPS_ERR_ARG;
     *tiles = p->T / (2 * a->tile_tokens) + p->B;
     return *tiles > (INT32_MAX - 65536) / a->heads_v ? TPS_ERR_ARG : TPS_OK;
 }
@@ -164,7 +165,7 @@ int check_tree(const tps_kv_cache* c, const tps_tree* t, bool pointers)
     if (c->head_dim != 64 && c->head_dim != 128) return TPS_ERR_ARG;
     if (t->B < 0 || t->table_width < 0 || t->table_width > kMaxTokens / c->page_size || t->table_ld < t->table_width || t->n_nodes < 1 ||
         t->n_nodes > 64 || t->n_q_heads < 1 || t->n_q_heads > kMaxHeads || t->n_q_heads % c->n_heads != 0 ||
-        (t->tree_ld != 0 && t->tree_ld < t->n_nodes) || !std::isfinite(t->scale))
+        (t->tree_ld != 0 && t->tree_ld < t->n_nodes) || !std::isfinite((float)((double)t->scale * 1.4426950408889634)))
         return TPS_ERR_ARG;
     if (!pointers || t->B == 0) return TPS_OK;
     if (!t->q || !t->out || !t->seq_len || !t->tree || (t->table_width > 0 && !t->page_table)) return TPS_ERR_ARG;

@@ -34,7 +34,8 @@
 namespace tps {
 
 constexpr int kPromptThreads = 384, kPromptMma = 8, kPromptLoad = 9, kPromptHidden = 10;
-constexpr int kDirty = 8;  // items whose marks are kept: the loads run at most seven items ahead of an epilogue
+constexpr int kDirty = 8;        // items whose marks are kept: the loads run at most seven items ahead of an epilogue
+constexpr uint64_t kLong = 64;   // waits for what may come after the whole of a long sequence, in limits of the others
 
 template <int D> struct PromptShape {
     static constexpr int kTileBytes = 128 * D * 2;
@@ -257,7 +258,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             const int most = it.limit(a, m, 127);  // of any row of the tile
             float ref = neg, sum = 0.f;
             for (int v = 0; v < blocks && alive; ++v) {
-                if (!(alive = wait_all(&ctl.s_full[m], s_parity))) break;
+                // An item's first scores may come long after this tile's last ones: while the other tile has a long sequence's end.
+                if (!(alive = __all_sync(0xFFFFFFFFu, wait(&ctl.s_full[m], s_parity, v == 0 ? a.wait_ns * kLong : a.wait_ns)))) break;
                 s_parity ^= 1;
                 tc_fence_after();
                 const bool masked = v >= it.open;
@@ -559,7 +561,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 const int64_t f = fill + 2 * v + 1;
                 const int slot = (int)(f % kRing);
                 // The signal comes when the copy is asked for: in a long sequence long after the item has begun.
-                if (!(alive = __all_sync(0xFFFFFFFFu, wait(&ctl.go[slot], go_parity >> slot & 1, a.wait_ns * 64)))) break;
+                if (!(alive = __all_sync(0xFFFFFFFFu, wait(&ctl.go[slot], go_parity >> slot & 1, a.wait_ns * kLong)))) break;
                 go_parity ^= 1u << slot;
                 if (!(alive = wait_all(&ctl.full[slot], (uint32_t)(f / kRing) & 1))) break;
                 unsigned char* tile = ring + slot * Shape::kTileBytes;

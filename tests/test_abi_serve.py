@@ -20,7 +20,7 @@ def prompt(**kw):
 @pytest.mark.parametrize("kw,rc", [
     (dict(T=-1), 1), (dict(T=2 ** 31 - 2 ** 16 + 1), 1), (dict(B=-1), 1), (dict(B=2 ** 31), 1), (dict(n_q_heads=0), 1), (dict(n_k_heads=0), 1),
     (dict(n_q_heads=7), 1), (dict(n_q_heads=65536), 1), (dict(head_dim=96), 1), (dict(head_dim=0), 1), (dict(scale=float("nan")), 1),
-    (dict(scale=float("inf")), 1), (dict(q=None), 1), (dict(k=None), 1), (dict(v=None), 1), (dict(out=None), 1), (dict(cu_seqlens=None), 1),
+    (dict(scale=float("inf")), 1), (dict(scale=3e38), 1), (dict(q=None), 1), (dict(k=None), 1), (dict(v=None), 1), (dict(out=None), 1), (dict(cu_seqlens=None), 1),
     (dict(q_ld=60), 1), (dict(q_ld=100), 1), (dict(k_hd=0), 1), (dict(v_hd=-64), 1), (dict(v_ld=1 << 40), 1), (dict(q=FAKE + 8), 4),
     (dict(k=FAKE + 2), 4), (dict(v=FAKE + 4), 4), (dict(out=FAKE + 8), 4), (dict(out_lse=FAKE + 2), 4), (dict(cu_seqlens=FAKE + 1), 4),
     (dict(out_status=FAKE + 2), 4), (dict(T=2 ** 31 - 2 ** 16, n_q_heads=2048, n_k_heads=1024, q_ld=2 ** 20, k_ld=2 ** 20, v_ld=2 ** 20), 1),
@@ -87,7 +87,7 @@ def tree(c=None, **kw):
 @pytest.mark.parametrize("kw,rc", [
     (dict(B=-1), 1), (dict(table_width=-1, table_ld=0), 1), (dict(table_ld=1), 1), (dict(table_width=2 ** 27, table_ld=2 ** 27), 1), (dict(n_nodes=0), 1),
     (dict(n_nodes=65, tree_ld=65), 1), (dict(tree_ld=4), 1), (dict(n_q_heads=0), 1), (dict(n_q_heads=3), 1), (dict(n_q_heads=2 ** 16), 1),
-    (dict(scale=float("nan")), 1), (dict(q=None), 1), (dict(out=None), 1), (dict(page_table=None), 1), (dict(seq_len=None), 1), (dict(tree=None), 1),
+    (dict(scale=float("nan")), 1), (dict(scale=-3e38), 1), (dict(q=None), 1), (dict(out=None), 1), (dict(page_table=None), 1), (dict(seq_len=None), 1), (dict(tree=None), 1),
     (dict(q=FAKE + 8), 4), (dict(out=FAKE + 8), 4), (dict(out_lse=FAKE + 2), 4), (dict(page_table=FAKE + 2), 4), (dict(seq_len=FAKE + 2), 4),
     (dict(tree_len=FAKE + 2), 4), (dict(tree=FAKE + 4), 4), (dict(out_status=FAKE + 2), 4), (dict(workspace=FAKE + 128), 4),
     (dict(B=0, q=None, tree=None), 0)])
