@@ -188,7 +188,8 @@ int plan_tree(const tps_kv_cache& c, const tps_tree& t, int sms, tps::TreePlan* 
     if (most > INT32_MAX || t.B > INT32_MAX / most) return TPS_ERR_ARG;  // the kernels count the line's blocks in 32 bits
     p.ctas = (int)std::min<int64_t>(sms, most * t.B);
     p.off_ml = (size_t)2 * p.ctas * p.tile_rows * c.head_dim * sizeof(float);
-    p.off_rec = p.off_ml + (size_t)2 * p.ctas * p.tile_rows * sizeof(float2);
+    p.off_lost = p.off_ml + (size_t)2 * p.ctas * p.tile_rows * sizeof(float2);
+    p.off_rec = p.off_lost + (size_t)2 * p.ctas * p.tile_rows * sizeof(float);
     p.bytes = p.off_rec + (size_t)p.ctas * sizeof(tps::TreeRecord);
     *out = p;
     return TPS_OK;
@@ -387,6 +388,7 @@ int tps_tree_attention_stall_test(const tps_kv_cache* cache, const tps_tree* arg
     }
     a.part = reinterpret_cast<float*>(ws);
     a.ml = reinterpret_cast<float2*>(ws + a.p.off_ml);
+    a.lost = reinterpret_cast<float*>(ws + a.p.off_lost);
     a.rec = reinterpret_cast<tps::TreeRecord*>(ws + a.p.off_rec);
     e = cache->format == TPS_KV_BF16  ? tps::launch_attn_tree_bf16(a, st)
         : cache->format == TPS_KV_FP8 ? tps::launch_attn_tree_fp8(a, st)

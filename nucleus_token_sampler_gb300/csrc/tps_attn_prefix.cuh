@@ -94,7 +94,7 @@ template <int D, int kFormat, int kTiles, int kLine> struct PrefixShape {
         // In turn: a row's factor for the group that did not load it, what the groups' halves of it come to, by 32 rows
         // whether a wait of either ran out.
         float row_factor[kLine == kTreesInTurn ? 128 : 1];
-        float2 half[2][kLine == kTreesInTurn ? 128 : 1];
+        float3 half[2][kLine == kTreesInTurn ? 128 : 1];
         int dead[4];
         float key_unit[kScalars], value_exp[kScalars];
         int wide[kScalars];  // 1: the block's keys, 2: its values
@@ -359,6 +359,7 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles, kLine>::kThrea
                 if (lane == 0) mbar_arrive(&ctl.q_full);
             }
             float ref = neg, sum = 0.f;
+            [[maybe_unused]] float lost = 0.f;  // trees, bf16: what rounding took from the weights that `sum` has as the product has them
             const int blocks = way.blocks(a), in_item = way.tile * (128 * Shape::kQueries) + in_tile;
             [[maybe_unused]] TreeRow mine = {};
             if constexpr (kTree) mine = tree_row(a, way, in_item);
@@ -431,6 +432,7 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles, kLine>::kThrea
                     const float f = to == ref ? 1.f : exp2_fast(ref - to);
                     ref = to;
                     sum *= f;
+                    if (kTree && !k8) lost *= f;
                     total.x *= f, total.y *= f;
                     if (kTurns ? v > 1 : v > 0) {
 #pragma unroll 1
@@ -558,8 +560,19 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles, kLine>::kThrea
                         total = add2(total, x);
                     }
                 }
-                sum = fmaf(total.x + total.y, inv, sum);
-                tmem_wait_st();
+                if constexpr (kTree && !k8) {
+                    float mass = total.x + total.y;
+                    tmem_wait_st();
+                    if (open < kBlockKeys && way.block + v == 0) {  // as for whole prompts (tps_attn_prompt.cuh)
+                        const float rounded = weight_sum(s_addr, 4);
+                        lost += mass - rounded;
+                        mass = rounded;
+                    }
+                    sum += mass;
+                } else {
+                    sum = fmaf(total.x + total.y, inv, sum);
+                    tmem_wait_st();
+                }
                 tc_fence_before();
                 mbar_arrive(&ctl.p_full[m]);
             }
@@ -568,10 +581,10 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles, kLine>::kThrea
                 o_parity ^= 1;
             }
             if constexpr (kTree) {
-                float2 other = make_float2(neg, 0.f);
+                float3 other = make_float3(neg, 0.f, 0.f);
                 if constexpr (kTurns) {  // the groups' halves of the row, for each of which a half of the columns
                     if (!alive) *(volatile int*)&ctl.dead[warp & 3] = 1;
-                    ctl.half[m][in_tile] = make_float2(ref, sum);
+                    ctl.half[m][in_tile] = make_float3(ref, sum, lost);
                     pair_sync(warp & 3);
                     alive = *(volatile int*)&ctl.dead[warp & 3] == 0;
                     other = ctl.half[m ^ 1][in_tile];
@@ -579,7 +592,7 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles, kLine>::kThrea
                 if (!alive) break;
                 tc_fence_after();
                 tree_output<D, kFormat, kTurns>(a, way, blocks, mine, in_tile, in_item, m, tmem + lanes + Shape::kOutCol, o_addr,
-                                                make_float2(ref, sum), other,
+                                                make_float3(ref, sum, lost), other,
                                                 *(volatile int*)&ctl.marks[way.ordinal % kTreeMarks] | (way.bad ? kMarkBad : 0));
                 tc_fence_before();
                 if (kTurns) pair_sync(warp & 3);  // both halves have been read

@@ -167,6 +167,21 @@ template <int D> __device__ __forceinline__ bool hide_not_finite(unsigned char* 
     return found;
 }
 
+// The sum of a row's bfloat16 weights as the second product has them, 32 to each of `groups` 16 columns.
+__device__ __forceinline__ float weight_sum(uint32_t addr, int groups)
+{
+    float2 sum = make_float2(0.f, 0.f);
+#pragma unroll 1
+    for (int i = 0; i < groups; ++i) {
+        uint32_t w[16];
+        tmem_ld16(addr + i * 16, w);
+        tmem_wait_ld(w);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) sum.x += __uint_as_float(w[j] << 16), sum.y += __uint_as_float(w[j] & 0xFFFF0000u);
+    }
+    return sum.x + sum.y;
+}
+
 __device__ __forceinline__ bool tree_whole(const TreeWay& way, int blocks) { return way.block == 0 && blocks == way.nblk; }
 // A CTA's piece of an item that began in an earlier one, and of one that goes on in the next.
 __device__ __forceinline__ int64_t tree_piece(const TreeWay& way) { return 2 * (int64_t)blockIdx.x + (way.block == 0 ? 1 : 0); }
@@ -180,21 +195,21 @@ __device__ __forceinline__ int64_t tree_row_at(const TreeArgs& a, int seq, int h
 // The two warps that have 32 rows in turn wait for one another.
 __device__ __forceinline__ void pair_sync(int pair) { asm volatile("barrier.cta.sync.aligned %0, 64;" ::"r"(pair + 1) : "memory"); }
 
-// The outputs of a warp's rows: finished, or a piece.  `mine_sum`: reference and sum; in turn, `other_sum` is the other group's
+// The outputs of a warp's rows: finished, or a piece.  `mine_sum`: reference, sum and what rounding took from it; in turn, `other_sum` is the other group's
 // part of the row, whose output lies D columns from this one's, and each group writes a half of the columns.
 template <int D, int kFormat, bool kTurns>
 __device__ __forceinline__ void tree_output(const TreeArgs& a, const TreeWay& way, int blocks, const TreeRow& mine, int in_tile, int in_item, int m,
-                                            uint32_t out_col, uint32_t o_addr, float2 mine_sum, float2 other_sum, int marks)
+                                            uint32_t out_col, uint32_t o_addr, float3 mine_sum, float3 other_sum, int marks)
 {
     if (in_item - (int)(threadIdx.x & 31) >= a.p.R) return;  // none of the warp's
     const bool both = kTurns && blocks > 1, in = in_item < a.p.R, bad = marks & kMarkBad, whole = tree_whole(way, blocks);
-    float ref = mine_sum.x, sum = mine_sum.y, f = 1.f, g = 0.f;
+    float ref = mine_sum.x, sum = mine_sum.y, lost = mine_sum.z, f = 1.f, g = 0.f;
     if (both) {
         ref = fmaxf(mine_sum.x, other_sum.x);
         f = mine_sum.x == ref ? 1.f : exp2_fast(mine_sum.x - ref), g = other_sum.x == ref ? 1.f : exp2_fast(other_sum.x - ref);
-        sum = mine_sum.y * f + other_sum.y * g;
+        sum = mine_sum.y * f + other_sum.y * g, lost = mine_sum.z * f + other_sum.z * g;
     } else if (kTurns && m == 1) {  // one block: the other group's
-        ref = other_sum.x, sum = other_sum.y;
+        ref = other_sum.x, sum = other_sum.y, lost = other_sum.z;
     }
     const bool empty = !mine.live || sum == 0.f;
     const int64_t at = tree_row_at(a, way.seq, way.head, in_item), piece = tree_piece(way);
@@ -246,9 +261,10 @@ __device__ __forceinline__ void tree_output(const TreeArgs& a, const TreeWay& wa
     }
     if (!in || (kTurns && m == 1)) return;
     if (whole) {
-        if (a.a.out_lse) a.a.out_lse[at] = log_sum<kFormat>(ref, mine.live ? sum : 0.f, bad);
+        if (a.a.out_lse) a.a.out_lse[at] = log_sum<kFormat>(ref, mine.live ? sum + lost : 0.f, bad);
     } else {
         a.ml[piece * a.p.tile_rows + in_tile] = make_float2(ref, bad ? kPieceBadPage : (mine.live ? sum : 0.f));
+        a.lost[piece * a.p.tile_rows + in_tile] = lost;
     }
 }
 

@@ -85,7 +85,7 @@ cudaError_t launch_attn_own(const AttnArgs& a, bool after_prefix, cudaStream_t s
 // A tree-attention call (tps_attn_tree.cuh): an item is one sequence, key head and `tile_rows` of the R = n_nodes G rows.
 struct TreePlan {
     int R, tile_rows, n_tiles, ctas;
-    size_t off_ml, off_rec, bytes;
+    size_t off_ml, off_lost, off_rec, bytes;
 };
 struct TreeRecord;
 struct TreeArgs {
@@ -96,6 +96,7 @@ struct TreeArgs {
     float qk_scale;
     float* part;      // [2 ctas][D / 4][tile_rows][4], as AttnArgs
     float2* ml;       // [2 ctas, tile_rows]
+    float* lost;      // [2 ctas, tile_rows]: what rounding took from the sums
     TreeRecord* rec;  // [ctas]
     int stall_head;
     uint64_t wait_ns;

@@ -81,7 +81,14 @@ template <int D, int kFormat> __global__ void __launch_bounds__(kJoinThreads) tr
         reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.a.out) + at * D)[warp * kEach + k] =
             make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
     }
-    if (warp == 0 && a.a.out_lse) a.a.out_lse[at] = log_sum<kFormat>(top, sum, bad);
+    if (warp == 0 && a.a.out_lse) {
+        float lost = 0.f;
+        for (int i = 0; i < n; ++i) {
+            const float f = factor[i * 32 + lane].x;
+            if (f != 0.f) lost += f * a.lost[piece(i) * rows + row];
+        }
+        a.a.out_lse[at] = log_sum<kFormat>(top, sum + lost, bad);
+    }
 }
 
 template <int D, int kFormat> cudaError_t join(const TreeArgs& a, cudaStream_t stream)

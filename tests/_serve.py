@@ -40,12 +40,14 @@ def prompt(q, k, v, bounds, scale):
 
 
 def check(got, lse, want, weights=None, where=None):
-    """Tolerances: a bfloat16 result is off by at most 2^-8 of its magnitude; the weights' rounding by `weights`
-    (bfloat16: 2^-8) of sum p |v|, or by a fifth element of `want`; the scores' float32 sums by at most 2^-18 of the largest sum of
+    """Tolerances: a bfloat16 result is off by at most 2^-8 of its magnitude.  Weights p (1 + d), |d| <= u = `weights` (bfloat16:
+    2^-8), whose sum takes some of them (M) rounded and the others not, yield sum p (1 + d) v / (1 + sum over M of p d), which is
+    off by (sum p d v - o sum over M of p d) / (1 + sum over M of p d): at most u / (1 - u) (sum p |v| + |o|).  Or by a fifth element
+    of `want`.  Further the scores' float32 sums by at most 2^-18 of the largest sum of
     |products|, and base-2 exponentials, joins of parts and weights below 2^-31 of the largest by less than 2^-14.  The last
     rounding is of the value as computed: with e off before it, |x + e| 2^-8 <= (|x| + e) 2^-8, so e counts 1 + 2^-8 times."""
     out, wl, mag, big = want[:4]
-    off = want[4] if len(want) == 5 else weights * mag
+    off = want[4] if len(want) == 5 else weights / (1 - weights) * (mag + out.abs())
     if where is not None:
         got, lse, out, wl, mag, big, off = (x[where] for x in (got, lse, out, wl, mag, big, off))
     rest = 2.0 ** -18 * big + 2.0 ** -14

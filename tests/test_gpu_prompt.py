@@ -75,6 +75,16 @@ def test_scores_that_rise_and_fall_along_the_keys():
     plain.check(out, lse, plain.prompt(q, k, v, zip(cu, cu[1:]), 128 ** -0.5), BF16)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_lone_token_has_its_value_as_it_is(D):
+    """The rounded weight is divided by itself."""
+    cu, c = _bounds([1, 300, 1, 2])
+    q, k, v = _heads(11, 304, 6, 2, D)
+    out = tps.prompt_attention(q, k, v, c)
+    for t in (0, 1, 301, 302):
+        assert torch.equal(out[t], v[t].repeat_interleave(3, 0))
+
+
 def test_strides_out_and_rows_of_no_sequence():
     cu, c = _bounds([100, 0, 140], first=3)
     T = cu[-1] + 9

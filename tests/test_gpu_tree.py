@@ -105,6 +105,16 @@ def test_lines_cut_over_many_ctas(fmt, N, Hq, Hk, D, page, lens):
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_lone_token_has_its_value_as_it_is(D):
+    """The rounded weight is divided by itself."""
+    q, c, table, lens, tree, _ = _case(12, [3, 1, 130, 70], 1, 6, 2, D, 16, "bf16")
+    one = torch.ones_like(lens)
+    out = tps.tree_attention(q, c, table, one, tree)
+    for b in range(4):
+        assert torch.equal(out[b, 0], c.v[table[b, 0], :, 0].repeat_interleave(3, 0))
+
+
 @pytest.mark.parametrize("fmt", ["bf16", "fp8", "int8"])
 def test_padded_batches_and_sequences_without_tokens(fmt):
     nodes = [0, 3, 8, 0, 1, 5, 8, 2]
