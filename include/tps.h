@@ -10,7 +10,9 @@
  * probable tokens is below p; 'A strong answer': the greedy branch and per-request p).
  * An optional stage ahead of that chain, tps_apply_penalties, applies repetition, frequency and
  * presence penalties to the raw logits in place.  Further ahead stand the operators of a decode step whose
- * batch shares a long prompt: tps_qk_norm_rope, tps_kv_write, tps_kv_read and tps_prefix_attention.
+ * batch shares a long prompt: tps_qk_norm_rope, tps_kv_write, tps_kv_read and tps_prefix_attention; and of requests
+ * of their own lengths: tps_kv_extend and tps_kv_trim (pages and slots), tps_prompt_attention (whole prompts) and
+ * tps_tree_attention (drafted trees).
  *
  * Rules, per row (T = temperature[b], k = top_k[b], p = top_p[b], m = min_p[b]):
  *   - T <= 0: greedy; the token is the lowest index holding the largest logit.
@@ -37,7 +39,9 @@
  *     array instead.  tps_prefix_attention takes its workspace from the same pool unless it is given one
  *     (tps_prefix_attention_workspace says how much).  Its pieces take 128 KB for each SM and each 256 query
  *     rows of a key head (99 MB for 1,024 sequences of 5 tokens, 32 heads on 8): a caller whose calls need more than the
- *     pool keeps and who synchronises between them had better hand in a workspace.  No other call allocates
+ *     pool keeps and who synchronises between them had better hand in a workspace.
+ *     tps_tree_attention takes its own the same way (two pieces for each SM, 40 MB at most).  tps_prompt_attention draws a
+ *     list of its tiles (a few KB), and tps_kv_extend, from 2,048 new tokens on, 8 bytes for each sequence.  No other call allocates
  *     device memory;
  *   - the library never synchronises the host, keeps no state between calls beyond that pool and
  *     a per-device cache of queried limits, and may be called from several host threads at once;
@@ -67,7 +71,8 @@ typedef enum {
     TPS_ERR_ALIGN = 4,         /* logits, out_probs or a parameter array is not element-aligned */
     TPS_ERR_CUDA = 5,          /* the CUDA runtime refused the launch (see tps_last_cuda_error) */
     TPS_ERR_SCRATCH = 6        /* tps_sample_noalloc: the call needs more than its fixed scratch;
-                                  tps_prefix_attention: the workspace given is too small      */
+                                  tps_prefix_attention and tps_tree_attention: the workspace
+                                  given is too small                                          */
 } tps_status;
 
 /* Per-row outcome written to out_status. */
@@ -490,7 +495,7 @@ typedef struct {
  *   positions    [tokens] int32: its position in its sequence (0 without a slot; for tps_qk_norm_rope).
  *   cu_seqlens   [B + 1] int32: where each sequence's rows begin, and where the last one's end (for
  *                tps_prompt_attention).  A sequence whose rows are more than there are has what is left.
- * Calls with many rows draw 8 bytes for each sequence from the library's memory pool.
+ * Calls with 2,048 rows or more draw 8 bytes for each sequence from the library's memory pool.
  */
 int tps_kv_extend(const tps_kv_pages* pages, int64_t tokens, int64_t* slots, int32_t* positions, int32_t* cu_seqlens, void* stream);
 
@@ -554,7 +559,7 @@ int tps_tree_attention(const tps_kv_cache* cache, const tps_tree* args, void* st
 int tps_tree_attention_stall_test(const tps_kv_cache* cache, const tps_tree* args, int stall_head, uint64_t wait_ns, void* stream);
 
 /* Bytes of workspace tps_tree_attention needs for these arguments on the current device (pointers are not looked
- * at), or -1 for arguments it would reject: two pieces for each SM, 39 MB at most.  Host-only query. */
+ * at), or -1 for arguments it would reject: two pieces for each SM, 40 MB at most.  Host-only query. */
 int64_t tps_tree_attention_workspace(const tps_kv_cache* cache, const tps_tree* args);
 
 /*

@@ -24,8 +24,16 @@
 // last), and 0 times that is NaN: warps of their own look through the hidden rows of those value tiles, and take what is
 // not finite out of the product; a row that does see the token adds it at the end.
 //
-// What bounds it: the matrix unit (each 128 x 128 tile at D = 128 takes it 512 clocks for the scores and 512 for the
-// outputs) and beside it the exponentials.  One persistent CTA per SM.  Tiles of unequal length are dealt out by length,
+// What bounds it: for long prompts the matrix unit (a 128 x 128 tile at D = 128 takes it 634 clocks for the scores, whose operands both
+// come from shared memory, and 559 for the outputs; at D = 64 378 and 367) and, under the power limit, its clock; at D = 64 the
+// hand-overs between the roles (a commit is seen some 450 clocks after the product, a signal 100 after it is given), as one
+// tile's softmax and its next scores wait for each other; for short prompts the 7,000 clocks or so from one item's last
+// weights to the next one's.  Measured: 16,384 tokens, 32 heads on 8 of 128, 1,430 us (1.54 PFLOP/s); 4 prompts of 2,500 to 4,001, 16
+// heads, 155 us (1.15); 24 of 700 to 2,011, 40 heads on 8 of 64, 384 us (0.64); 64 of 1 to 250, 32 on 8 of 128, 50 us (3.3 TB/s); one of 300
+// 10.7 us.  Tried and not kept: two threads for each row (16 softmax warps; 1,531, 173, 430, 66 us where this took 1,416,
+// 173, 390, 74), the outputs by way of shared memory (52 us for 49, 64 short prompts; by bulk stores 50), two pairs of query
+// tiles (375 for 374 us at D = 64), a tile's next scores while the softmax still works on the present ones (D = 64: 401 us for
+// 374).  One persistent CTA per SM.  Tiles of unequal length are dealt out by length,
 // longest first, to and fro over the CTAs (a small kernel ahead sorts them); where all tiles fit the SMs at once each CTA finds its
 // own and there is one launch.  Roles:
 //   warps 0 .. 7    softmax, one thread per row: scores from TMEM, weights back over them
@@ -629,6 +637,7 @@ template <int kThreads>
 __global__ void __launch_bounds__(kThreads) prompt_plan_kernel(const PromptArgs a, int4* list, int* n_tiles)
 {
     __shared__ int count[kPromptLevels], scan[kThreads / 32], tops[kThreads / 32], top_before;
+    __shared__ int3 long_ones[kThreads];  // begin, end, tiles
     const int tid = (int)threadIdx.x, warp = tid >> 5, lane = tid & 31;
     for (int i = tid; i < kPromptLevels; i += kThreads) count[i] = 0;
     const int span = 2 * a.tile_tokens;
@@ -658,14 +667,13 @@ __global__ void __launch_bounds__(kThreads) prompt_plan_kernel(const PromptArgs 
                 const int at = atomicAdd(&count[min((keys + kBlockKeys - 1) / kBlockKeys >> a.level_shift, kPromptLevels - 1)], 1);
                 if (pass == 1) list[at] = make_int4(l, h, l + t * span, (int)seq);
             };
-            if (__all_sync(0xFFFFFFFFu, tiles <= 8)) {  // short ones: a lane each
+            if (!__syncthreads_or(tiles > 8)) {  // short ones: a thread each
                 for (int t = 0; t < tiles; ++t) put(lo, hi, t, b);
-            } else {  // long ones: a lane for each tile, sequence after sequence
-                for (uint32_t have = __ballot_sync(0xFFFFFFFFu, tiles > 0); have; have &= have - 1) {
-                    const int w = __ffs(have) - 1;
-                    const int l = __shfl_sync(0xFFFFFFFFu, lo, w), h = __shfl_sync(0xFFFFFFFFu, hi, w), n = __shfl_sync(0xFFFFFFFFu, tiles, w);
-                    for (int t = lane; t < n; t += 32) put(l, h, t, b - lane + w);
-                }
+            } else {  // long ones: a warp each, a lane for each tile
+                long_ones[tid] = make_int3(lo, hi, tiles);
+                __syncthreads();
+                for (int i = warp; i < min(a.B - base, (int64_t)kThreads); i += kThreads / 32)
+                    for (int t = lane; t < long_ones[i].z; t += 32) put(long_ones[i].x, long_ones[i].y, t, base + i);
             }
         }
         __syncthreads();

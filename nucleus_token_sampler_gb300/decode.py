@@ -1,6 +1,6 @@
-"""The decode-step operators in front of the sampler: per-head norm and rotation, the paged key/value
-cache and the attention of a batch that shares a long prefix.  Like the rest of the binding these
-functions only check tensors and hand pointers and the CUDA stream to the C ABI (``include/tps.h``); the
+"""The operators in front of the sampler: per-head norm and rotation, the paged key/value cache with its
+page tables and slots, and the attention of a batch that shares a long prefix, of whole prompts and of
+drafted trees.  Like the rest of the binding these functions only check tensors and hand pointers and the CUDA stream to the C ABI (``include/tps.h``); the
 checking is native code too (``csrc/tps_torch.cpp``), because in Python it takes longer than a decode step's
 kernels."""
 from __future__ import annotations
