@@ -36,11 +36,11 @@ _SOURCES = ["tps_api.cu", "tps_k_cluster_f32.cu", "tps_k_cluster_bf16.cu", "tps_
             "tps_k_stream_bf16.cu", "tps_k_penalty.cu", "tps_k_spec.cu", "tps_k_reject.cu",
             "tps_api_decode.cu", "tps_k_norm_rope.cu", "tps_k_kv.cu", "tps_k_attn_rows.cu",
             "tps_k_attn_prefix_bf16.cu", "tps_k_attn_prefix_fp8.cu", "tps_k_attn_prefix_int8.cu", "tps_k_attn_prompt.cu", "tps_k_pages.cu", "tps_k_attn_tree.cu",
-            "tps_k_attn_tree_bf16.cu", "tps_k_attn_tree_fp8.cu", "tps_k_attn_tree_int8.cu"]
+            "tps_k_attn_tree_bf16.cu", "tps_k_attn_tree_fp8.cu", "tps_k_attn_tree_int8.cu", "tps_k_attn_rows_tree.cu"]
 _HEADERS = ["tps_device.cuh", "tps_common.cuh", "tps_cluster.cuh", "tps_stream.cuh", "tps_penalty.cuh",
             "tps_spec.cuh", "tps_reject.cuh", "tps_kernels.h", "tps_decode.h", "tps_norm_rope.cuh", "tps_kv.cuh",
             "tps_attn_rows.cuh", "tps_attn_prefix.cuh", "tps_attn_prefix_launch.cuh", "tps_attn_prompt.cuh", "tps_pages.cuh",
-            "tps_attn_tree.cuh", "tps_tcgen05.cuh"]
+            "tps_attn_tree.cuh", "tps_attn_rows_launch.cuh", "tps_tcgen05.cuh"]
 _NVCC = ["nvcc", "-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
          "-Xcompiler", "-fPIC"]
 

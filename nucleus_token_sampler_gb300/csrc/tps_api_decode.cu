@@ -175,6 +175,27 @@ int check_tree(const tps_kv_cache* c, const tps_tree* t, bool pointers)
     return TPS_OK;
 }
 
+// Rows of a sequence and key head up to which trees over an 8-bit cache take the kernels of a prefix call's own tokens, whose products of 8
+// or 16 rows convert no code twice and fill no tile of 128: less work for each token, though each 16 rows would read them again.
+// tcgen05 / those, us: 8 sequences of up to 4,000 in fp8, 8 key heads of 128, 4 rows 39 / 20, 16 rows 40 / 32, 32 rows 41 / 52; 32 of up
+// to 8,000 in int8, heads of 64, 5 rows 140 / 71, 15 rows 140 / 83, 30 rows 142 / 153; 256 of up to 3,000 in fp8, 8 rows 501 / 269.
+// In bfloat16, which needs no conversion, 1 of 1,000, 4 rows 15.6 / 8.2, 16 rows 15.9 / 13.2, but 256 of up to 3,000, 4 rows 363 / 432.
+constexpr int kTreeFewRows = 16;
+bool tree_few(const tps_kv_cache& c, const tps_tree& t)
+{
+    return c.format != TPS_KV_BF16 && (int64_t)t.n_nodes * (t.n_q_heads / c.n_heads) <= kTreeFewRows;
+}
+// The same call as one on own tokens alone.
+tps_attention tree_as_own(const tps_tree& t)
+{
+    tps_attention a = {};
+    a.q = t.q, a.out = t.out, a.out_lse = t.out_lse, a.page_table = t.page_table, a.suffix_len = t.seq_len, a.out_status = t.out_status;
+    a.workspace = t.workspace, a.workspace_bytes = t.workspace_bytes;
+    a.B = t.B, a.table_width = t.table_width, a.table_ld = t.table_ld;
+    a.q_len = t.n_nodes, a.n_q_heads = t.n_q_heads, a.scale = t.scale;
+    return a;
+}
+
 int plan_tree(const tps_kv_cache& c, const tps_tree& t, int sms, tps::TreePlan* out)
 {
     tps::TreePlan p = {};
@@ -212,6 +233,46 @@ int check_pages(const tps_kv_pages* p, tps::PagesArgs* a)
     while ((1 << a->page_shift) < ps) ++a->page_shift;
     a->page_mask = ps - 1;
     return TPS_OK;
+}
+
+// The launches of a planned call (a.p, and a.tree with what belongs to it) and its workspace.
+int run_attention(tps::AttnArgs& a, const tps_kv_cache& cache, const tps_attention& args, int stall_head, uint64_t wait_ns, cudaStream_t st)
+{
+    a.c = cache;
+    a.a = args;
+    a.stall_head = stall_head;
+    a.wait_ns = wait_ns;
+    a.G = args.n_q_heads / cache.n_heads;
+    a.page_shift = 4;
+    while ((1 << a.page_shift) < cache.page_size) ++a.page_shift;
+    a.qk_scale = (float)((double)args.scale * 1.4426950408889634);
+    unsigned char* ws = static_cast<unsigned char*>(args.workspace);
+    cudaError_t e = cudaSuccess;
+    if (a.p.bytes) {
+        if (ws) {
+            if (args.workspace_bytes < (int64_t)a.p.bytes) return TPS_ERR_SCRATCH;
+        } else {
+            void* mem = nullptr;
+            e = tps::pool_alloc(&mem, a.p.bytes, st);
+            if (e != cudaSuccess) return tps::report_cuda(e);
+            ws = static_cast<unsigned char*>(mem);
+        }
+    }
+    a.part = reinterpret_cast<float*>(ws);
+    a.ml = reinterpret_cast<float2*>(ws + a.p.off_ml);
+    a.line_part = reinterpret_cast<float*>(ws + a.p.off_line_part);
+    a.line_ml = reinterpret_cast<float2*>(ws + a.p.off_line_ml);
+    if (a.p.units) {
+        e = cache.format == TPS_KV_BF16  ? tps::launch_attn_prefix_bf16(a, st)
+            : cache.format == TPS_KV_FP8 ? tps::launch_attn_prefix_fp8(a, st)
+                                          : tps::launch_attn_prefix_int8(a, st);
+    }
+    if (e == cudaSuccess) e = a.tree ? tps::launch_attn_tree_rows(a, st) : tps::launch_attn_own(a, a.p.units > 0, st);
+    if (a.p.bytes && !args.workspace) {
+        const cudaError_t ef = cudaFreeAsync(ws, st);
+        if (e == cudaSuccess) e = ef;
+    }
+    return e == cudaSuccess ? TPS_OK : tps::report_cuda(e);
 }
 
 }  // namespace
@@ -300,45 +361,10 @@ int tps_prefix_attention_stall_test(const tps_kv_cache* cache, const tps_attenti
     if (args->B == 0) return TPS_OK;
     int sms = 0;
     if (!tps::host_sms(&sms)) return tps::report_cuda(cudaGetLastError());
-    tps::AttnArgs a;
+    tps::AttnArgs a = {};
     rc = plan_attention(*cache, *args, sms, &a.p);
     if (rc != TPS_OK) return rc;
-    a.c = *cache;
-    a.a = *args;
-    a.stall_head = stall_head;
-    a.wait_ns = wait_ns;
-    a.G = args->n_q_heads / cache->n_heads;
-    a.page_shift = 4;
-    while ((1 << a.page_shift) < cache->page_size) ++a.page_shift;
-    a.qk_scale = (float)((double)args->scale * 1.4426950408889634);
-    const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    unsigned char* ws = static_cast<unsigned char*>(args->workspace);
-    cudaError_t e = cudaSuccess;
-    if (a.p.bytes) {
-        if (ws) {
-            if (args->workspace_bytes < (int64_t)a.p.bytes) return TPS_ERR_SCRATCH;
-        } else {
-            void* mem = nullptr;
-            e = tps::pool_alloc(&mem, a.p.bytes, st);
-            if (e != cudaSuccess) return tps::report_cuda(e);
-            ws = static_cast<unsigned char*>(mem);
-        }
-    }
-    a.part = reinterpret_cast<float*>(ws);
-    a.ml = reinterpret_cast<float2*>(ws + a.p.off_ml);
-    a.line_part = reinterpret_cast<float*>(ws + a.p.off_line_part);
-    a.line_ml = reinterpret_cast<float2*>(ws + a.p.off_line_ml);
-    if (a.p.units) {
-        e = cache->format == TPS_KV_BF16  ? tps::launch_attn_prefix_bf16(a, st)
-            : cache->format == TPS_KV_FP8 ? tps::launch_attn_prefix_fp8(a, st)
-                                          : tps::launch_attn_prefix_int8(a, st);
-    }
-    if (e == cudaSuccess) e = tps::launch_attn_own(a, a.p.units > 0, st);
-    if (a.p.bytes && !args->workspace) {
-        const cudaError_t ef = cudaFreeAsync(ws, st);
-        if (e == cudaSuccess) e = ef;
-    }
-    return e == cudaSuccess ? TPS_OK : tps::report_cuda(e);
+    return run_attention(a, *cache, *args, stall_head, wait_ns, static_cast<cudaStream_t>(stream));
 }
 
 int64_t tps_tree_attention_workspace(const tps_kv_cache* cache, const tps_tree* args)
@@ -346,9 +372,13 @@ int64_t tps_tree_attention_workspace(const tps_kv_cache* cache, const tps_tree* 
     if (check_tree(cache, args, false) != TPS_OK) return -1;
     if (args->B == 0) return 0;
     int sms = 0;
+    if (!tps::host_sms(&sms)) return -1;
+    if (tree_few(*cache, *args)) {
+        tps::AttnPlan p;
+        return plan_attention(*cache, tree_as_own(*args), sms, &p) == TPS_OK ? (int64_t)p.bytes : -1;
+    }
     tps::TreePlan p;
-    if (!tps::host_sms(&sms) || plan_tree(*cache, *args, sms, &p) != TPS_OK) return -1;
-    return (int64_t)p.bytes;
+    return plan_tree(*cache, *args, sms, &p) == TPS_OK ? (int64_t)p.bytes : -1;
 }
 
 int tps_tree_attention(const tps_kv_cache* cache, const tps_tree* args, void* stream)
@@ -364,6 +394,14 @@ int tps_tree_attention_stall_test(const tps_kv_cache* cache, const tps_tree* arg
     if (args->B == 0) return TPS_OK;
     int sms = 0;
     if (!tps::host_sms(&sms)) return tps::report_cuda(cudaGetLastError());
+    if (tree_few(*cache, *args)) {
+        tps::AttnArgs few = {};
+        const tps_attention own = tree_as_own(*args);
+        rc = plan_attention(*cache, own, sms, &few.p);
+        if (rc != TPS_OK) return rc;
+        few.tree = args->tree, few.tree_ld = args->tree_ld, few.tree_len = args->tree_len;
+        return run_attention(few, *cache, own, stall_head, wait_ns, static_cast<cudaStream_t>(stream));
+    }
     tps::TreeArgs a = {};
     rc = plan_tree(*cache, *args, sms, &a.p);
     if (rc != TPS_OK) return rc;

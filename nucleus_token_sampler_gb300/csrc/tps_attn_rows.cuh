@@ -272,6 +272,25 @@ template <int D, int kFormat> struct Walk {
     }
 };
 
+// Of a call on trees (tps_tree_attention with few rows): a sequence's tokens, the drafted ones among them, the last; none of either
+// where the lengths are not possible.
+struct TreeTokens {
+    int len, nodes;
+    bool fits;
+};
+__device__ __forceinline__ TreeTokens tree_tokens(const AttnArgs& a, int64_t b)
+{
+    const int len = a.a.suffix_len[b], nodes = a.tree_len ? a.tree_len[b] : a.a.q_len;
+    const bool fits = len >= 0 && nodes >= 0 && nodes <= a.a.q_len && nodes <= len && len <= a.a.table_width << a.page_shift;
+    return fits ? TreeTokens{len, nodes, true} : TreeTokens{0, 0, false};
+}
+// Whether row r of the sequence sees drafted token j (from 0 on).
+__device__ __forceinline__ bool tree_sees(const AttnArgs& a, int64_t b, const TreeTokens& t, int r, int j)
+{
+    const int node = min(r / a.G, a.a.q_len - 1);
+    return j < t.nodes && node < t.nodes && (a.tree[b * a.tree_ld + node] >> j & 1);
+}
+
 // bfloat16 values of tokens that not every row sees: the product would bring a hidden token's NaN or infinity to every row
 // (0 * NaN), so attend() takes those components out of it, and the rows that see the token get them here.
 __device__ __forceinline__ uint32_t not_finite(uint32_t w)  // the halves that are not, else 0
@@ -307,9 +326,12 @@ __device__ __forceinline__ void add_not_finite(RowState<D, N>& st, const Walk<D,
 
 // Attend to the chunks of a walk that has been started; row 8 n + 2 quad + e sees the tokens below
 // lim[n][e].  Returns 0, or 1 after a page that is not the cache's, 2 after a wait that ran out.
-template <int D, int kFormat, int N>
-__device__ __forceinline__ int attend(RowState<D, N>& st, Walk<D, kFormat>& walk, const int (&lim)[N][2])
+// kTree: of the sequence's drafted tokens, which begin at `tree`, a row sees those that its mask names; its first row is r0.
+template <int D, int kFormat, int N, bool kTree = false>
+__device__ __forceinline__ int attend(RowState<D, N>& st, Walk<D, kFormat>& walk, const int (&lim)[N][2], int64_t b = 0, int r0 = 0,
+                                      const TreeTokens tree = {})
 {
+    static_assert(!kTree || kFormat != TPS_KV_BF16, "hidden bfloat16 values that are not finite are told by length alone");
     using C = Chunk<D, kFormat>;
     constexpr bool k8 = C::k8;
     constexpr int kKeyLoads = C::kRowBytes / 64;  // 16-byte pieces of one key row held by its quad's lane
@@ -323,6 +345,7 @@ __device__ __forceinline__ int attend(RowState<D, N>& st, Walk<D, kFormat>& walk
 #pragma unroll
     for (int n = 0; n < N; ++n) all_see = min(all_see, min(lim[n][0], lim[n][1]));
     all_see = (int)__reduce_min_sync(0xFFFFFFFFu, (uint32_t)all_see);
+    if (kTree) all_see = min(all_see, tree.len - tree.nodes);
     const uint32_t chunks = (uint32_t)((last - walk.first + walk.step - 1) / walk.step);
     uint32_t at = walk.fills - min(chunks, (uint32_t)C::kStages);  // the fill that is used next
     for (int t0 = walk.first; t0 < last; t0 += walk.step, ++at) {
@@ -415,6 +438,15 @@ __device__ __forceinline__ int attend(RowState<D, N>& st, Walk<D, kFormat>& walk
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     if (t0 + g + 8 * (i >> 1) >= lim[n][i & 1]) z[n][i] = neg;
+            if (kTree) {
+#pragma unroll
+                for (int n = 0; n < N; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int j = t0 + g + 8 * (i >> 1) - (tree.len - tree.nodes);
+                        if (j >= 0 && !tree_sees(walk.a, b, tree, r0 + 8 * n + 2 * quad + (i & 1), j)) z[n][i] = neg;
+                    }
+            }
             if (t0 + 16 > last) {  // rows past the end hold anything, and 0 * NaN is NaN
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -829,12 +861,27 @@ __device__ __forceinline__ float log_sum(float top, float l, bool bad)
     return l == 0.f ? -__int_as_float(0x7F800000) : (top + log2f(l) - lift) * 0.693147180559945f;
 }
 
+// Rows from `past` of the sequence on are padding's: they have seen nothing.
+template <int D, int N> __device__ __forceinline__ void clear_padding(RowState<D, N>& st, int r0, int past)
+{
+    const int quad = threadIdx.x & 3;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            if (r0 + 8 * n + 2 * quad + e >= past) {
+                st.m[n][e] = -__int_as_float(0x7F800000), st.l[n][e] = 0.f;
+#pragma unroll
+                for (int t = 0; t < D / 16; ++t) st.o[n][t][e] = st.o[n][t][2 + e] = 0.f;
+            }
+}
+
 // One sequence's own tokens for one key head, then the join with the pieces of the shared prefix, the
 // division by the sum and the output.  With many sequences each warp has one for itself, and joins in
 // registers; else the four warps of a CTA, or of a cluster of CTAs, take its chunks in turn and join
 // through (distributed) shared memory.  A small call has no pieces: every sequence walks over the prefix
 // itself (AttnPlan::shared).
-template <int D, int kFormat, int N, bool kOneWarp>
+template <int D, int kFormat, int N, bool kOneWarp, bool kTree>
 __global__ void __launch_bounds__(kRowsThreads, N == 1 ? 4 : 3) attn_suffix_kernel(const AttnArgs a)
 {
     constexpr int kRows = 8 * N;
@@ -852,10 +899,13 @@ __global__ void __launch_bounds__(kRowsThreads, N == 1 ? 4 : 3) attn_suffix_kern
     const int head = (int)(bh - (uint32_t)b * a.c.n_heads);
     if (kOneWarp && b >= a.a.B) return;  // the last CTA's spare warps
     const int Tq = a.a.q_len, G = a.G, r0 = tile * kRows, rows = min(kRows, Tq * G - r0);
-    const int len = a.a.suffix_len[b];
-    const bool fits = len >= 0 && len <= a.a.table_width << a.page_shift;
+    TreeTokens tree = {};
+    if constexpr (kTree) tree = tree_tokens(a, b);
+    const int len = kTree ? tree.len : a.a.suffix_len[b];
+    const bool fits = kTree ? tree.fits : len >= 0 && len <= a.a.table_width << a.page_shift;
     // Row r of the sequence is query r / G, head r % G of the group: own tokens that it sees.
     auto seen = [&](int r) {
+        if constexpr (kTree) return len;
         const int n = len - Tq + 1 + (Tq == 1 ? 0 : min(r, Tq * G - 1) / G);
         return fits && n > 0 ? n : 0;
     };
@@ -887,7 +937,8 @@ __global__ void __launch_bounds__(kRowsThreads, N == 1 ? 4 : 3) attn_suffix_kern
     for (int n = 0; n < N; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) lim[n][e] = seen(r0 + 8 * n + 2 * quad + e);
-    fault = max(fault, attend<D, kFormat, N>(st, walk, lim));
+    fault = max(fault, attend<D, kFormat, N, kTree>(st, walk, lim, b, r0, tree));
+    if constexpr (kTree) clear_padding(st, r0, tree.nodes * G);
     const float neg = -__int_as_float(0x7F800000);
     const int64_t row0 = b * Tq * G + r0;  // the tile's first row among the key head's R
 
@@ -1057,8 +1108,12 @@ struct OwnTokens {
     int seen;
     bool fits;
 };
-__device__ __forceinline__ OwnTokens own_tokens(const AttnArgs& a, int64_t b, int row)
+template <bool kTree> __device__ __forceinline__ OwnTokens own_tokens(const AttnArgs& a, int64_t b, int row)
 {
+    if constexpr (kTree) {
+        const TreeTokens t = tree_tokens(a, b);
+        return OwnTokens{t.len, t.fits};
+    }
     const int len = a.a.suffix_len[b], Tq = a.a.q_len;
     const bool fits = len >= 0 && len <= a.a.table_width << a.page_shift;
     const int n = len - Tq + 1 + (Tq == 1 ? 0 : min(row, Tq * a.G - 1) / a.G);
@@ -1069,7 +1124,7 @@ __device__ __forceinline__ OwnTokens own_tokens(const AttnArgs& a, int64_t b, in
 struct LineSums {
     int64_t before[kLineMax + 1], warp_sum[kRowsWarps];
 };
-__device__ __forceinline__ void line_sums(LineSums& sm, const AttnArgs& a, int tile_rows)
+template <bool kTree> __device__ __forceinline__ void line_sums(LineSums& sm, const AttnArgs& a, int tile_rows)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int pairs = (int)(a.a.B * a.p.suffix_tiles), rows = a.a.q_len * a.G;
@@ -1082,7 +1137,7 @@ __device__ __forceinline__ void line_sums(LineSums& sm, const AttnArgs& a, int t
         mine[i] = sum;
         if (bt < pairs) {
             const int b = bt / a.p.suffix_tiles, tile = bt - b * a.p.suffix_tiles;
-            sum += shared_blocks + (own_tokens(a, b, min(rows, (tile + 1) * tile_rows) - 1).seen + kLineBlock - 1) / kLineBlock;
+            sum += shared_blocks + (own_tokens<kTree>(a, b, min(rows, (tile + 1) * tile_rows) - 1).seen + kLineBlock - 1) / kLineBlock;
         }
     }
     int64_t upto = sum;
@@ -1101,7 +1156,7 @@ __device__ __forceinline__ void line_sums(LineSums& sm, const AttnArgs& a, int t
     __syncthreads();
 }
 
-template <int D, int kFormat, int N>
+template <int D, int kFormat, int N, bool kTree>
 __global__ void __launch_bounds__(kRowsThreads, N == 1 ? 4 : 3) attn_line_kernel(const AttnArgs a)
 {
     constexpr int kRows = 8 * N;
@@ -1115,7 +1170,7 @@ __global__ void __launch_bounds__(kRowsThreads, N == 1 ? 4 : 3) attn_line_kernel
     if (!p.shared) clear_status(a);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int shared_len = p.shared ? 0 : (int)a.a.prefix_len, shared_blocks = (shared_len + kLineBlock - 1) / kLineBlock;
-    line_sums(sums, a, kRows);
+    line_sums<kTree>(sums, a, kRows);
     const int64_t* before = sums.before;
     const int64_t total = before[kLineMax] * heads;
 
@@ -1141,7 +1196,7 @@ __global__ void __launch_bounds__(kRowsThreads, N == 1 ? 4 : 3) attn_line_kernel
         if (!gave_up) {
             // Its blocks of the prefix (where each sequence walks over it itself), then its own.
             const int p0 = min(first, shared_blocks) * kLineBlock, p1 = min(min(past, shared_blocks) * kLineBlock, shared_len);
-            const int seen = own_tokens(a, b, r0 + rows - 1).seen;
+            const int seen = own_tokens<kTree>(a, b, r0 + rows - 1).seen;
             const int t0 = max(first - shared_blocks, 0) * kLineBlock, t1 = min(max(past - shared_blocks, 0) * kLineBlock, seen);
             const int32_t* own_pages = a.a.page_table + b * a.a.table_ld;
             walk.head = head;
@@ -1166,8 +1221,11 @@ __global__ void __launch_bounds__(kRowsThreads, N == 1 ? 4 : 3) attn_line_kernel
 #pragma unroll
             for (int n = 0; n < N; ++n)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) lim[n][e] = min(t1, own_tokens(a, b, r0 + 8 * n + 2 * quad + e).seen);
-            fault = max(fault, attend<D, kFormat, N>(st, walk, lim));
+                for (int e = 0; e < 2; ++e) lim[n][e] = min(t1, own_tokens<kTree>(a, b, r0 + 8 * n + 2 * quad + e).seen);
+            TreeTokens tree = {};
+            if constexpr (kTree) tree = tree_tokens(a, b);
+            fault = max(fault, attend<D, kFormat, N, kTree>(st, walk, lim, b, r0, tree));
+            if constexpr (kTree) clear_padding(st, r0, tree.nodes * G);
             store_rows<D, kFormat, N>(sm, st, kRows);
             if (fault && lane == 0) atomicMax(&sm.bad, fault);
         }
@@ -1186,7 +1244,7 @@ __global__ void __launch_bounds__(kRowsThreads, N == 1 ? 4 : 3) attn_line_kernel
 
 // The join: a CTA for each item and strip of 32 columns.
 constexpr int kStrip = 32;
-template <int D, int kFormat>
+template <int D, int kFormat, bool kTree>
 __global__ void __launch_bounds__(kRowsThreads) attn_join_kernel(const AttnArgs a)
 {
     __shared__ JoinShared<16> js;
@@ -1199,10 +1257,10 @@ __global__ void __launch_bounds__(kRowsThreads) attn_join_kernel(const AttnArgs 
     const int tile = (int)(bt - (uint32_t)b * p.suffix_tiles);
     const int r0 = tile * p.suffix_rows, rows = min(p.suffix_rows, Tq * G - r0);
     const int64_t row0 = b * Tq * G + r0;
-    const bool fits = own_tokens(a, b, 0).fits;
+    const bool fits = own_tokens<kTree>(a, b, 0).fits;
     Pieces own{0, 0};
     const PrefixPieces pieces(p, head, row0, rows);
-    line_sums(sums, a, p.suffix_rows);  // while the line is still at work
+    line_sums<kTree>(sums, a, p.suffix_rows);  // while the line is still at work
     const int64_t total = sums.before[kLineMax] * heads, before = sums.before[bt];
     const int64_t blocks = ((int64_t)bt + 1 < a.a.B * p.suffix_tiles ? sums.before[bt + 1] : sums.before[kLineMax]) - before;
     if (blocks) {

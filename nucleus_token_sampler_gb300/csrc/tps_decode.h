@@ -72,6 +72,10 @@ struct AttnArgs {
     float2* line_ml;
     int stall_head;    // of tps_prefix_attention_stall_test, else -1
     uint64_t wait_ns;  // limit of every wait for data or for another role (copies in flight: kAttnWaitNs)
+    // Of a call on trees of few rows: each sequence's drafted tokens, the last of its `suffix_len` ones.
+    const uint64_t* tree;
+    int64_t tree_ld;
+    const int32_t* tree_len;
 };
 constexpr uint64_t kAttnWaitNs = 1000000000ull;
 
@@ -123,6 +127,7 @@ cudaError_t launch_attn_tree_bf16(const TreeArgs& a, cudaStream_t stream);
 cudaError_t launch_attn_tree_fp8(const TreeArgs& a, cudaStream_t stream);
 cudaError_t launch_attn_tree_int8(const TreeArgs& a, cudaStream_t stream);
 cudaError_t launch_tree_join(const TreeArgs& a, cudaStream_t stream);
+cudaError_t launch_attn_tree_rows(const AttnArgs& a, cudaStream_t stream);  // few rows, 8-bit caches
 
 // One prompt-attention call (tps_attn_prompt.cuh).
 struct PromptArgs {

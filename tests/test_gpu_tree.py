@@ -152,6 +152,55 @@ def test_scales_and_rising_scores(fmt, scale):
     _check(args, scale=scale)
 
 
+@pytest.mark.parametrize("fmt", ["fp8", "int8"])
+@pytest.mark.parametrize("N,Hq,Hk,D,page,lens", [(1, 8, 2, 128, 16, [1, 700, 0, 33]), (4, 8, 2, 64, 32, [300, 4, 0, 17, 90]), (16, 2, 2, 128, 64, [500, 16, 3]),
+                                                 (3, 5, 1, 64, 16, list(range(0, 400, 3))), (2, 16, 2, 128, 128, [20000, 3, 9000]), (5, 3, 1, 64, 16, [60] * 1500),
+                                                 (8, 2, 1, 64, 256, [5000, 8, 40])])
+def test_few_rows_over_eight_bits(fmt, N, Hq, Hk, D, page, lens):
+    """Trees of up to 16 rows go another way: padding, masks that are no trees, pages and lengths that are wrong."""
+    nodes = [min(n, (i * 5 + 1) % (N + 1)) for i, n in enumerate(lens)]
+    q, c, table, n, tree, k = _case(N + Hq, lens, N, Hq, Hk, D, page, fmt, nodes=nodes)
+    out, lse = _check((q, c, table, n, tree, k))
+    for b, m in enumerate(nodes):
+        assert (out[b, m:] == 0).all() and (lse[b, m:] == -math.inf).all()
+    g = torch.Generator(device=DEV).manual_seed(1)
+    wild = torch.randint(-2 ** 62, 2 ** 62, tree.shape, generator=g, device=DEV)
+    wild[0] = 0
+    _check((q, c, table, n, wild, k), scale=-0.2)
+    _check((q, c, table, n, wild[-1].contiguous(), k))
+    size = tps.tree_attention_workspace(q.shape, c, table.shape[1])
+    again = tps.tree_attention(q, c, table, n, tree, nodes=k, workspace=torch.empty(max(size, 1), dtype=torch.uint8, device=DEV))
+    assert torch.equal(again, out)
+    want, table, n, k = _want(q, c, table, n, tree, k, D ** -0.5), table.clone(), n.clone(), k.clone()
+    table[0, 0], n[1], k[2] = c.n_pages, page * table.shape[1] + 1, N + 1
+    st = torch.full((len(lens),), 9, dtype=torch.int32, device=DEV)
+    out, lse = tps.tree_attention(q, c, table, n, tree, nodes=k, want_lse=True, status=st)
+    good = torch.arange(3, len(lens), device=DEV)
+    assert st[:3].tolist() == [3 if lens[0] else 0, 3, 3] and (st[3:] == 0).all()
+    assert out[1].isnan().all() and out[2].isnan().all() and (not lens[0] or out[0].isnan().all())
+    plain.check(out, lse, want, None, good)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "int8"])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("length", [4, 16, 18, 130, 3000])
+def test_few_rows_hidden_nodes_hold_anything(fmt, bad, length):
+    q, c, table, lens, tree, _ = _case(13, [length, 300], 4, 8, 2, 64, 16, fmt)
+    base, base_lse = tps.tree_attention(q, c, table, lens, tree, want_lse=True)
+    for j in range(4):
+        at = length - 4 + j
+        page, row = int(table[0, at // 16]), at % 16
+        sees = (tree[0] >> j) & 1 == 1
+        for x in (c.k_scale, c.v_scale):
+            keep = x[page, :, row].clone()
+            x[page, :, row] = bad
+            out, lse = tps.tree_attention(q, c, table, lens, tree, want_lse=True)
+            x[page, :, row] = keep
+            assert torch.equal(out[0, ~sees], base[0, ~sees]) and torch.equal(lse[0, ~sees], base_lse[0, ~sees])
+            assert torch.equal(out[1], base[1]) and torch.equal(lse[1], base_lse[1])
+            assert x is c.k_scale or (~torch.isfinite(out[0, sees])).all()
+
+
 @pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
 @pytest.mark.parametrize("fmt", ["bf16", "fp8", "int8"])
 @pytest.mark.parametrize("length", [12, 128, 133, 900])
