@@ -521,12 +521,40 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles, kLine>::kThrea
                     tmem_st16(s_addr + ch * 16, w);
                     return t;
                 };
-                // 64 scores at a time, first weighed against the reference as it stands (an item's first 64 have none): a weight
-                // above 2^kSlack (times the lift) shows in their sum, so the usual step looks for no maximum at all.  Loops
-                // and not unrolled code: with several roles at work the instructions have to come from the cache again and again.
+                // 64 scores at a time, first weighed against the reference as it stands: a weight above 2^kSlack
+                // (times the lift) shows in their sum, so the usual step looks for no maximum at all.
                 constexpr float kMost = k8 ? 32768.f : 256.f;  // 2^(kSlack + kLift), 2^kSlack
-                constexpr int kUnroll = kTree ? 1 : 2;
-                if (k8 && wide) {
+                if constexpr (!kTree) {
+#pragma unroll
+                    for (int ch = 0; ch < 4; ch += 2) {
+                        float sa[32], sb[32];
+                        tmem_ld32(s_addr + ch * 32, sa);
+                        tmem_ld32(s_addr + ch * 32 + 32, sb);
+                        tmem_wait_ld(sa);
+                        tmem_wait_ld(sb);
+                        ready(sa, ch);
+                        ready(sb, ch + 1);
+                        float b = add - (ref == neg ? 0.f : ref) + (k8 ? kLift : 0.f);
+                        float2 x = add2(weigh(sa, ch, b), weigh(sb, ch + 1, b));
+                        const bool need = !(x.x + x.y <= kMost) || ref == neg;
+                        if (__any_sync(0xFFFFFFFFu, need || wide)) {  // a wide block comes this way every time
+                            if (!k8 || !wide) {
+                                raise(need, fmaf(fmaxf(largest(sa), largest(sb)), c, add), ch);
+                                b = add - (ref == neg ? 0.f : ref) + (k8 ? kLift : 0.f);
+                                tmem_wait_st();
+                                x = add2(weigh(sa, ch, b), weigh(sb, ch + 1, b));
+                            } else {
+                                x = weigh_wide(sa, ch);  // may scale the total, so not inside its sum
+                                total = add2(total, x);
+                                x = weigh_wide(sb, ch + 1);
+                            }
+                        }
+                        total = add2(total, x);
+                    }
+                } else if (k8 && wide) {
+                    // Trees: the same in loops and not unrolled, and without a first try where there is no reference yet. With fewer blocks
+                    // to an item the instructions come from the cache again and again: 8 x 4,093 x 16 in fp8 45 -> 42 us, 32 x 8,111 x 64 in
+                    // int8 431 -> 407. A long shared prefix takes 2 to 4% more that way.
 #pragma unroll 1
                     for (int ch = 0; ch < 4; ++ch) {
                         float s[32];
@@ -537,7 +565,7 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles, kLine>::kThrea
                         total = add2(total, x);
                     }
                 } else {
-#pragma unroll kUnroll
+#pragma unroll 1
                     for (int ch = 0; ch < 4; ch += 2) {
                         float sa[32], sb[32];
                         tmem_ld32(s_addr + ch * 32, sa);

@@ -1,5 +1,6 @@
 // tps_attn_rows.cuh -- attention of up to 16 query rows per warp over paged keys and values, and the
-// join of its parts: every sequence's own tokens, and the prefix of a call too small to share its work.
+// join of its parts: every sequence's own tokens, and the prefix of a call too small to share its work; also
+// (kTree) trees of up to 16 rows over 8-bit caches, whose masks are looked up where drafted tokens are.
 //
 // Mathematics.  With z_j = scale log2(e) q.k_j, one pass over the tokens holds a reference m, the sum
 // l = sum 2^(z_j - m) and the output o = sum 2^(z_j - m) v_j in float32; m is raised (and l, o scaled)
