@@ -509,7 +509,7 @@ int tps_kv_trim(const tps_kv_pages* pages, void* stream);
  * tps_tree -- arguments of tps_tree_attention.
  *   q            [B, n_nodes, n_q_heads, D] bfloat16, dense, 16-byte aligned; n_q_heads a multiple of the cache's
  *                n_heads (query head i reads key head i / (n_q_heads / n_heads)).
- *   out          [B, n_nodes, n_q_heads, D] bfloat16, dense, 16-byte aligned.
+ *   out          [B, n_nodes, n_q_heads, D] bfloat16, dense, 16-byte aligned; must not overlap the inputs.
  *   out_lse      [B, n_nodes, n_q_heads] float or NULL: ln of the sum of e^{scale q.k} (-inf: no token).
  *   page_table   [B, table_width] int32: the pages of each sequence's tokens (ld table_ld).
  *   seq_len      [B] int32: tokens of each sequence in the cache, its drafted ones among them (the last ones).
@@ -559,7 +559,8 @@ int tps_tree_attention(const tps_kv_cache* cache, const tps_tree* args, void* st
 int tps_tree_attention_stall_test(const tps_kv_cache* cache, const tps_tree* args, int stall_head, uint64_t wait_ns, void* stream);
 
 /* Bytes of workspace tps_tree_attention needs for these arguments on the current device (pointers are not looked
- * at), or -1 for arguments it would reject: two pieces for each SM, 40 MB at most.  Host-only query. */
+ * at), or -1 for arguments it would reject: two pieces for each SM, 40 MB at most (for trees of few rows over 8-bit caches what
+ * tps_prefix_attention needs for own tokens, from 0 to some 30 MB).  Host-only query. */
 int64_t tps_tree_attention_workspace(const tps_kv_cache* cache, const tps_tree* args);
 
 /*
@@ -570,7 +571,7 @@ int64_t tps_tree_attention_workspace(const tps_kv_cache* cache, const tps_tree* 
  *   k, v         [T, n_k_heads, D] bfloat16, 16-byte aligned.
  *   *_ld, *_hd   token and head strides, e.g. of one fused projection's output; at least D where the axis has
  *                more than one element.
- *   out          [T, n_q_heads, D] bfloat16, dense, 16-byte aligned.
+ *   out          [T, n_q_heads, D] bfloat16, dense, 16-byte aligned; must not overlap the inputs.
  *   out_lse      [T, n_q_heads] float or NULL: ln of the sum of e^{scale q.k}.
  *   cu_seqlens   [B + 1] int32: sequence b's tokens are the rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1.  Rows that
  *                belong to no sequence are neither computed nor written.
