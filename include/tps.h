@@ -559,8 +559,8 @@ int tps_tree_attention(const tps_kv_cache* cache, const tps_tree* args, void* st
 int tps_tree_attention_stall_test(const tps_kv_cache* cache, const tps_tree* args, int stall_head, uint64_t wait_ns, void* stream);
 
 /* Bytes of workspace tps_tree_attention needs for these arguments on the current device (pointers are not looked
- * at), or -1 for arguments it would reject: two pieces for each SM, 40 MB at most (for trees of few rows over 8-bit caches what
- * tps_prefix_attention needs for own tokens, from 0 to some 30 MB).  Host-only query. */
+ * at), or -1 for arguments it would reject: two pieces for each SM, 40 MB at most (for some trees of up to 16 rows, n_nodes times the
+ * query heads of a key head, what tps_prefix_attention needs for own tokens, from 0 to some 30 MB).  Host-only query. */
 int64_t tps_tree_attention_workspace(const tps_kv_cache* cache, const tps_tree* args);
 
 /*

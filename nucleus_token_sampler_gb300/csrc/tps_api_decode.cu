@@ -175,15 +175,28 @@ int check_tree(const tps_kv_cache* c, const tps_tree* t, bool pointers)
     return TPS_OK;
 }
 
-// Rows of a sequence and key head up to which trees over an 8-bit cache take the kernels of a prefix call's own tokens, whose products of 8
+// Rows of a sequence and key head up to which trees take the kernels of a prefix call's own tokens.  Over an 8-bit cache their products of 8
 // or 16 rows convert no code twice and fill no tile of 128: less work for each token, though each 16 rows would read them again.
 // tcgen05 / those, us: 8 sequences of up to 4,000 in fp8, 8 key heads of 128, 4 rows 39 / 20, 16 rows 40 / 32, 32 rows 41 / 52; 32 of up
 // to 8,000 in int8, heads of 64, 5 rows 140 / 71, 15 rows 140 / 83, 30 rows 142 / 153; 256 of up to 3,000 in fp8, 8 rows 501 / 269.
-// In bfloat16, which needs no conversion, 1 of 1,000, 4 rows 15.6 / 8.2, 16 rows 15.9 / 13.2, but 256 of up to 3,000, 4 rows 363 / 432.
 constexpr int kTreeFewRows = 16;
+// In bfloat16, which needs no conversion, it is a shorter chain for few tokens and a join without a second launch: where there are few
+// (sequence, key head) items, and where sequences are short (by their tables: only the device knows the lengths), whose tiles of 128 rows
+// cost tcgen05 some 9,000 clocks each.  Up to 8 rows, 8 heads of 128: 1 of 1,000 15.0 / 8.0, of 10,000 29.7 / 19.2, 8 of 1,000 15.7 / 11.3,
+// 32 of 3,000 73 / 63, 8 of 30,000 154 / 162, 64 of 3,000 129 / 171; 64 of 1,000 58 / 67, of 500 to 1,000 56 / 49, 256 of 500 to 1,000
+// 173 / 150, of 150 to 300 84 / 53, 1,000 of up to 128 218 / 74.
+// 9 to 16 rows: 1 head, 1 of 300 12.0 / 13.5, of 1,000 15.1 / 12.7, of 30,000 89 / 32; 8 heads, 1 of 1,000 15.3 / 12.9, 4 of 10,000
+// 42 / 49; 64 of 250 to 500 39 / 44, 256 118 / 94, 8 of up to 128 8.9 / 12.6, 1,000 of up to 128 235 / 100.
+constexpr int kTreeFewRowsBf16 = 8;
+constexpr int64_t kTreeFewItemsBf16 = 256, kTreeShortBf16 = 1024;
+constexpr int64_t kTreeItems16Bf16 = 8, kTreeShort16Bf16 = 512, kTreeManyItemsBf16 = 1024;
 bool tree_few(const tps_kv_cache& c, const tps_tree& t)
 {
-    return c.format != TPS_KV_BF16 && (int64_t)t.n_nodes * (t.n_q_heads / c.n_heads) <= kTreeFewRows;
+    const int64_t rows = (int64_t)t.n_nodes * (t.n_q_heads / c.n_heads), tokens = t.table_width * c.page_size;
+    if (rows > kTreeFewRows || c.format != TPS_KV_BF16) return rows <= kTreeFewRows;
+    auto most_items = [&](int64_t n) { return t.B <= n / c.n_heads; };
+    if (rows <= kTreeFewRowsBf16) return most_items(kTreeFewItemsBf16) || tokens <= kTreeShortBf16;
+    return tokens <= kTreeShort16Bf16 ? !most_items(kTreeManyItemsBf16 - 1) : most_items(kTreeItems16Bf16);
 }
 // The same call as one on own tokens alone.
 tps_attention tree_as_own(const tps_tree& t)

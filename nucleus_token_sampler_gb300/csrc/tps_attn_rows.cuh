@@ -1,6 +1,6 @@
 // tps_attn_rows.cuh -- attention of up to 16 query rows per warp over paged keys and values, and the
 // join of its parts: every sequence's own tokens, and the prefix of a call too small to share its work; also
-// (kTree) trees of up to 16 rows over 8-bit caches, whose masks are looked up where drafted tokens are.
+// (kTree) trees of few rows, whose masks are looked up where drafted tokens are.
 //
 // Mathematics.  With z_j = scale log2(e) q.k_j, one pass over the tokens holds a reference m, the sum
 // l = sum 2^(z_j - m) and the output o = sum 2^(z_j - m) v_j in float32; m is raised (and l, o scaled)
@@ -298,10 +298,11 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w)  // the halves that a
 {
     return ((w & 0x7F80u) == 0x7F80u ? w & 0xFFFFu : 0u) | ((w & 0x7F800000u) == 0x7F800000u ? w & 0xFFFF0000u : 0u);
 }
-template <int D, int kFormat, int N>
-__device__ __forceinline__ void add_not_finite(RowState<D, N>& st, const Walk<D, kFormat>& walk, const int (&lim)[N][2], int all_see)
+template <int D, int kFormat, int N, bool kTree>
+__device__ __forceinline__ void add_not_finite(RowState<D, N>& st, const Walk<D, kFormat>& walk, const int (&lim)[N][2], int all_see, int64_t b,
+                                               int r0, const TreeTokens& tree)
 {
-    const int g = (threadIdx.x & 31) >> 2, shift = walk.a.page_shift;
+    const int g = (threadIdx.x & 31) >> 2, quad = threadIdx.x & 3, shift = walk.a.page_shift;
 #pragma unroll 1
     for (int t0 = walk.first; t0 < walk.last; t0 += walk.step)
 #pragma unroll 1
@@ -310,6 +311,13 @@ __device__ __forceinline__ void add_not_finite(RowState<D, N>& st, const Walk<D,
             if (id < 0 || id >= walk.a.c.n_pages) continue;
             const int64_t row = (((int64_t)id * walk.a.c.n_heads + walk.head) << shift) + (t & ((1 << shift) - 1));
             const uint32_t* v = static_cast<const uint32_t*>(walk.a.c.v) + (row * D + g * (D / 8)) / 2;
+            const int j = kTree ? t - (tree.len - tree.nodes) : -1;  // a drafted token
+            bool sees[N][2];
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    sees[n][e] = t < lim[n][e] && (!kTree || j < 0 || tree_sees(walk.a, b, tree, r0 + 8 * n + 2 * quad + e, j));
 #pragma unroll
             for (int w = 0; w < D / 16; ++w) {
                 const uint32_t x = not_finite(v[w]);
@@ -317,7 +325,7 @@ __device__ __forceinline__ void add_not_finite(RowState<D, N>& st, const Walk<D,
                 for (int n = 0; n < N; ++n)
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
-                        if (t < lim[n][e]) {
+                        if (sees[n][e]) {
                             st.o[n][w][e] += __uint_as_float(x << 16);
                             st.o[n][w][2 + e] += __uint_as_float(x & 0xFFFF0000u);
                         }
@@ -332,7 +340,6 @@ template <int D, int kFormat, int N, bool kTree = false>
 __device__ __forceinline__ int attend(RowState<D, N>& st, Walk<D, kFormat>& walk, const int (&lim)[N][2], int64_t b = 0, int r0 = 0,
                                       const TreeTokens tree = {})
 {
-    static_assert(!kTree || kFormat != TPS_KV_BF16, "hidden bfloat16 values that are not finite are told by length alone");
     using C = Chunk<D, kFormat>;
     constexpr bool k8 = C::k8;
     constexpr int kKeyLoads = C::kRowBytes / 64;  // 16-byte pieces of one key row held by its quad's lane
@@ -538,7 +545,7 @@ __device__ __forceinline__ int attend(RowState<D, N>& st, Walk<D, kFormat>& walk
             }
         }
     }
-    if (!k8 && __any_sync(0xFFFFFFFFu, walk.fault & 4)) add_not_finite(st, walk, lim, all_see);
+    if (!k8 && __any_sync(0xFFFFFFFFu, walk.fault & 4)) add_not_finite<D, kFormat, N, kTree>(st, walk, lim, all_see, b, r0, tree);
     walk.fault &= 1;
     return walk.fault;
 }

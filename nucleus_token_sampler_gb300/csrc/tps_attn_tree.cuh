@@ -1,6 +1,6 @@
 // tps_attn_tree.cuh -- attention of drafted trees over the paged cache (tps_tree_attention): what it adds to the tcgen05
 // kernel of tps_attn_prefix.cuh, whose softmax, products, loads and conversions of 8-bit codes it shares, and the join.
-// (Up to 16 rows over 8-bit caches go to the kernels of tps_attn_rows.cuh.)
+// (Few rows go to the kernels of tps_attn_rows.cuh, by the rule in tps_api_decode.cu.)
 //
 // Mathematics.  A sequence's last `nodes` tokens in the cache are a tree of drafted ones; node i sees the tokens before
 // them and those nodes j whose bit is set in its mask.  All (node, query head) pairs of one key head are rows of one tile of

@@ -127,7 +127,7 @@ cudaError_t launch_attn_tree_bf16(const TreeArgs& a, cudaStream_t stream);
 cudaError_t launch_attn_tree_fp8(const TreeArgs& a, cudaStream_t stream);
 cudaError_t launch_attn_tree_int8(const TreeArgs& a, cudaStream_t stream);
 cudaError_t launch_tree_join(const TreeArgs& a, cudaStream_t stream);
-cudaError_t launch_attn_tree_rows(const AttnArgs& a, cudaStream_t stream);  // few rows, 8-bit caches
+cudaError_t launch_attn_tree_rows(const AttnArgs& a, cudaStream_t stream);  // few rows
 
 // One prompt-attention call (tps_attn_prompt.cuh).
 struct PromptArgs {

@@ -157,7 +157,23 @@ def test_scales_and_rising_scores(fmt, scale):
                                                  (3, 5, 1, 64, 16, list(range(0, 400, 3))), (2, 16, 2, 128, 128, [20000, 3, 9000]), (5, 3, 1, 64, 16, [60] * 1500),
                                                  (8, 2, 1, 64, 256, [5000, 8, 40])])
 def test_few_rows_over_eight_bits(fmt, N, Hq, Hk, D, page, lens):
-    """Trees of up to 16 rows go another way: padding, masks that are no trees, pages and lengths that are wrong."""
+    _few_rows(fmt, N, Hq, Hk, D, page, lens)
+
+
+# Up to 8 rows: up to 256 pairs of a sequence and a key head, or tables of up to 1,024 tokens.  Up to 16: up to 8 pairs, or at least
+# 1,024 with tables of up to 512.
+@pytest.mark.parametrize("N,Hq,Hk,D,page,lens", [(1, 8, 2, 128, 16, [1, 700, 0, 33]), (4, 8, 2, 64, 32, [300, 4, 0]), (16, 2, 2, 128, 64, [500, 16, 3]),
+                                                 (3, 2, 1, 64, 16, list(range(0, 400, 3))), (2, 16, 2, 128, 128, [20000, 3, 9000]),
+                                                 (5, 1, 1, 64, 16, [60] * 250), (8, 1, 1, 128, 256, [5000, 8, 40]), (8, 2, 2, 64, 16, [4100, 3, 777] * 40),
+                                                 (2, 12, 3, 128, 32, [1100, 1, 65, 64, 2] * 17), (2, 12, 3, 128, 32, [1100, 1, 65, 64, 2] * 18),
+                                                 (2, 8, 2, 128, 16, [60, 2, 33] * 150), (1, 8, 2, 128, 64, [900, 1, 257] * 230), (4, 16, 4, 128, 32, [60, 4, 133] * 120),
+                                                 (3, 40, 8, 64, 128, [300, 3, 128] * 44)])
+def test_few_rows_in_bfloat16(N, Hq, Hk, D, page, lens):
+    _few_rows("bf16", N, Hq, Hk, D, page, lens)
+
+
+def _few_rows(fmt, N, Hq, Hk, D, page, lens):
+    """Trees of few rows go another way: padding, masks that are no trees, pages and lengths that are wrong."""
     nodes = [min(n, (i * 5 + 1) % (N + 1)) for i, n in enumerate(lens)]
     q, c, table, n, tree, k = _case(N + Hq, lens, N, Hq, Hk, D, page, fmt, nodes=nodes)
     out, lse = _check((q, c, table, n, tree, k))
@@ -178,7 +194,31 @@ def test_few_rows_over_eight_bits(fmt, N, Hq, Hk, D, page, lens):
     good = torch.arange(3, len(lens), device=DEV)
     assert st[:3].tolist() == [3 if lens[0] else 0, 3, 3] and (st[3:] == 0).all()
     assert out[1].isnan().all() and out[2].isnan().all() and (not lens[0] or out[0].isnan().all())
-    plain.check(out, lse, want, None, good)
+    plain.check(out, lse, want, BF16, good)
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("N,Hq,Hk,D", [(4, 4, 2, 64), (8, 1, 1, 128), (4, 8, 2, 128), (16, 1, 1, 64)])
+@pytest.mark.parametrize("length", [16, 18, 130, 4100])
+def test_few_rows_in_bfloat16_hidden_nodes_hold_anything(bad, N, Hq, Hk, D, length):
+    q, c, table, lens, tree, _ = _case(13, [length, 300], N, Hq, Hk, D, 16, "bf16")
+    base, base_lse = tps.tree_attention(q, c, table, lens, tree, want_lse=True)
+    for j in range(N):
+        at = length - N + j
+        page, row = int(table[0, at // 16]), at % 16
+        sees = (tree[0] >> j) & 1 == 1
+        for x in (c.k, c.v):
+            keep = x[page, :, row, 5::9].clone()
+            x[page, :, row, 5::9] = bad
+            out, lse = tps.tree_attention(q, c, table, lens, tree, want_lse=True)
+            x[page, :, row, 5::9] = keep
+            assert torch.equal(out[0, ~sees], base[0, ~sees]) and torch.equal(lse[0, ~sees], base_lse[0, ~sees])
+            assert torch.equal(out[1], base[1]) and torch.equal(lse[1], base_lse[1])
+            if x is c.v:
+                other = torch.ones(D, dtype=torch.bool, device=DEV)
+                other[5::9] = False
+                assert torch.equal(lse, base_lse) and torch.equal(out[0][..., other], base[0][..., other])
+                assert (out[0, sees][..., ~other].isnan() if math.isnan(bad) else out[0, sees][..., ~other] == bad).all()
 
 
 @pytest.mark.parametrize("fmt", ["fp8", "int8"])
