@@ -182,11 +182,11 @@ int check_tree(const tps_kv_cache* c, const tps_tree* t, bool pointers)
 constexpr int kTreeFewRows = 16;
 // In bfloat16, which needs no conversion, it is a shorter chain for few tokens and a join without a second launch: where there are few
 // (sequence, key head) items, and where sequences are short (by their tables: only the device knows the lengths), whose tiles of 128 rows
-// cost tcgen05 some 9,000 clocks each.  Up to 8 rows, 8 heads of 128: 1 of 1,000 15.0 / 8.0, of 10,000 29.7 / 19.2, 8 of 1,000 15.7 / 11.3,
-// 32 of 3,000 73 / 63, 8 of 30,000 154 / 162, 64 of 3,000 129 / 171; 64 of 1,000 58 / 67, of 500 to 1,000 56 / 49, 256 of 500 to 1,000
-// 173 / 150, of 150 to 300 84 / 53, 1,000 of up to 128 218 / 74.
-// 9 to 16 rows: 1 head, 1 of 300 12.0 / 13.5, of 1,000 15.1 / 12.7, of 30,000 89 / 32; 8 heads, 1 of 1,000 15.3 / 12.9, 4 of 10,000
-// 42 / 49; 64 of 250 to 500 39 / 44, 256 118 / 94, 8 of up to 128 8.9 / 12.6, 1,000 of up to 128 235 / 100.
+// cost tcgen05 some 9,000 clocks each.  Up to 8 rows, 8 heads of 128: 1 of 1,000 15.0 / 9.0, of 10,000 29.7 / 20.4, 8 of 1,000 15.7 / 12.3,
+// 32 of 3,000 73 / 66, 8 of 30,000 154 / 161, 64 of 3,000 129 / 171; 64 of 1,000 58 / 67, of 500 to 1,000 56 / 50, 256 of 500 to 1,000
+// 173 / 152, of 150 to 300 84 / 54, 1,000 of up to 128 218 / 77.
+// 9 to 16 rows: 1 head, 1 of 300 12.0 / 13.5, of 1,000 15.1 / 15.0, of 30,000 89 / 32; 8 heads, 1 of 1,000 15.3 / 14.1, 4 of 10,000
+// 42 / 49; 64 of 250 to 500 39 / 44, 256 118 / 96, 8 of up to 128 8.9 / 12.6, 1,000 of up to 128 235 / 111.
 constexpr int kTreeFewRowsBf16 = 8;
 constexpr int64_t kTreeFewItemsBf16 = 256, kTreeShortBf16 = 1024;
 constexpr int64_t kTreeItems16Bf16 = 8, kTreeShort16Bf16 = 512, kTreeManyItemsBf16 = 1024;

@@ -292,6 +292,23 @@ __device__ __forceinline__ bool tree_sees(const AttnArgs& a, int64_t b, const Tr
     return j < t.nodes && node < t.nodes && (a.tree[b * a.tree_ld + node] >> j & 1);
 }
 
+// How many of the first drafted tokens all rows see that are not padding (whose sums are cleared); a warp's rows begin at r0.  A
+// decode step masks nothing, and a tree nothing up to its first fork.
+template <int N> __device__ __forceinline__ int all_nodes_see(const AttnArgs& a, int64_t b, int r0, const TreeTokens& t)
+{
+    uint64_t bits = ~0ull;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int node = (r0 + 8 * n + 2 * ((int)threadIdx.x & 3) + e) / a.G;
+            if (node < t.nodes) bits &= a.tree[b * a.tree_ld + node];
+        }
+    const uint32_t low = __reduce_and_sync(0xFFFFFFFFu, (uint32_t)bits), high = __reduce_and_sync(0xFFFFFFFFu, (uint32_t)(bits >> 32));
+    const int first = low != ~0u ? __ffs(~low) - 1 : high != ~0u ? 31 + __ffs(~high) : 64;  // that one of them does not see
+    return min(first, t.nodes);
+}
+
 // bfloat16 values of tokens that not every row sees: the product would bring a hidden token's NaN or infinity to every row
 // (0 * NaN), so attend() takes those components out of it, and the rows that see the token get them here.
 __device__ __forceinline__ uint32_t not_finite(uint32_t w)  // the halves that are not, else 0
@@ -353,7 +370,7 @@ __device__ __forceinline__ int attend(RowState<D, N>& st, Walk<D, kFormat>& walk
 #pragma unroll
     for (int n = 0; n < N; ++n) all_see = min(all_see, min(lim[n][0], lim[n][1]));
     all_see = (int)__reduce_min_sync(0xFFFFFFFFu, (uint32_t)all_see);
-    if (kTree) all_see = min(all_see, tree.len - tree.nodes);
+    if (kTree) all_see = min(all_see, tree.len - tree.nodes + all_nodes_see<N>(walk.a, b, r0, tree));
     const uint32_t chunks = (uint32_t)((last - walk.first + walk.step - 1) / walk.step);
     uint32_t at = walk.fills - min(chunks, (uint32_t)C::kStages);  // the fill that is used next
     for (int t0 = walk.first; t0 < last; t0 += walk.step, ++at) {
