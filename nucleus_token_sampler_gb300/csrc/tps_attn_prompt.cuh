@@ -48,7 +48,10 @@
 namespace tps {
 
 constexpr int kPromptThreads = 384, kPromptMma = 8, kPromptLoad = 9, kPromptHidden = 10;
-constexpr int kDirty = 8;        // items whose marks are kept: the loads run at most seven items ahead of an epilogue
+// Items of each tile whose marks are kept.  No product comes before the softmax of its tile's last item has ended, and the loads run at most
+// a ring of tiles ahead of the products: six items, counted for each tile by itself (prompts that fit one tile give tile 1 nothing to do,
+// and any number of them may go by while its softmax warps still have an output to write).
+constexpr int kDirty = 8;
 constexpr uint64_t kLong = 64;   // waits for what may come after the whole of a long sequence, in limits of the others
 
 template <int D> struct PromptShape {
@@ -60,7 +63,7 @@ template <int D> struct PromptShape {
         uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], drain;
         uint32_t tmem;
         int abort;
-        int dirty[kDirty][2];  // by item and warp: values were taken out of the product
+        int dirty[2][kDirty][2];  // by tile, item of that tile and warp: values were taken out of the product
     };
     static constexpr size_t kSmem = (size_t)(2 + kRing) * kTileBytes + sizeof(Control) + 1024;
     static_assert(kSmem <= 232448, "fits one CTA's shared memory");
@@ -264,8 +267,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const float neg = -__int_as_float(0x7F800000);
         const float c = fmaxf(fabsf(a.qk_scale), 0x1p-126f);  // never 0: a masked score, -inf, times it stays -inf
         uint32_t s_parity = 0, o_parity = 0;
-        int item = 0;
-        for (; walk.more(); walk.step(), ++item) {
+        int item = 0;  // of the tile
+        for (; walk.more(); walk.step()) {
             const int blocks = it.blocks(m);
             if (blocks == 0) continue;
             const int limit = it.limit(a, m, row);
@@ -382,7 +385,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             tc_fence_after();
             const int in_tile = row / a.group, h = row - in_tile * a.group, token = it.token + m * a.tile_tokens + in_tile;
             const bool mine = in_tile < a.tile_tokens && h < it.heads && token < it.end;
-            const bool dirty = alive && (*(volatile int*)&ctl.dirty[item % kDirty][0] | *(volatile int*)&ctl.dirty[item % kDirty][1]);
+            const bool dirty = alive && (*(volatile int*)&ctl.dirty[m][item % kDirty][0] | *(volatile int*)&ctl.dirty[m][item % kDirty][1]);
+            ++item;
             const int64_t at = (int64_t)token * a.Hq + it.head + h;
             const float inv = alive ? 1.f / sum : __int_as_float(0x7FC00000);
             uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at * D);
@@ -573,11 +577,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         // this wait nor the one for the copy can be a phase off.
         const int half = warp - kPromptHidden;
         uint32_t go_parity = 0;
-        int item = 0;
-        int64_t fill = 0;  // of the item's first key tile
-        for (; walk.more() && alive; walk.step(), ++item) {
+        int item[2] = {0, 0};  // of each tile
+        int64_t fill = 0;      // of the item's first key tile
+        for (; walk.more() && alive; walk.step()) {
             bool found = false;
-            if (lane == 0) *(volatile int*)&ctl.dirty[item % kDirty][half] = 0;
+            auto mark = [&](int to) {
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+                    if (it.blocks(m)) *(volatile int*)&ctl.dirty[m][item[m] % kDirty][half] = to;
+            };
+            if (lane == 0) mark(0);
             for (int v = min(it.open, it.last); v < it.last && alive; ++v) {
                 const int64_t f = fill + 2 * v + 1;
                 const int slot = (int)(f % kRing);
@@ -616,12 +625,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 }
                 const bool any = __any_sync(0xFFFFFFFFu, found);
                 if (lane == 0) {
-                    if (any) *(volatile int*)&ctl.dirty[item % kDirty][half] = 1;
+                    if (any) mark(1);
                     mbar_arrive(&ctl.clean[slot]);
                 }
                 __syncwarp();
             }
             fill += 2 * (int64_t)it.last;
+            ++item[0];
+            if (it.blocks(1)) ++item[1];
         }
     }
     tc_fence_before();

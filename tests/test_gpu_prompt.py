@@ -134,6 +134,27 @@ def test_hidden_tokens_hold_anything(Hq, Hk, D, bad):
         assert torch.equal(out[:450][other], base[:450][other]) and out[j].isnan().all()
 
 
+@pytest.mark.parametrize("Hq,Hk,D", [(1, 1, 64), (2, 2, 128)])
+def test_values_taken_out_reach_their_rows_ahead_of_many_short_prompts(Hq, Hk, D):
+    """Each CTA has a prompt of two query tiles, whose second one sees values that are not finite, and then more prompts of one
+    tile than there are marks of such values."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    lens = [140 + i % 100 for i in range(sms // Hk)] + [1 + i % 9 for i in range(12 * sms)]
+    cu, c = _bounds(lens)
+    q, k, v = (x.clone() for x in _heads(12, cu[-1], Hq, Hk, D))
+    base, base_lse = tps.prompt_attention(q, k, v, c, want_lse=True)
+    sees = torch.zeros(cu[-1], dtype=torch.bool, device=DEV)
+    for i in range(sms // Hk):
+        at = cu[i] + 128 + i % 11  # the second tile begins at 128
+        v[at, :, 3] = math.inf
+        sees[at:cu[i + 1]] = True
+    rest = torch.arange(D, device=DEV) != 3
+    for _ in range(20):
+        out, lse = tps.prompt_attention(q, k, v, c, want_lse=True)
+        assert (out[sees][..., 3] == math.inf).all() and torch.equal(out[~sees], base[~sees])
+        assert torch.equal(out[..., rest], base[..., rest]) and torch.equal(lse, base_lse)
+
+
 def test_bounds_that_are_not_in_order():
     q, k, v = _heads(5, 300, 4, 2, 64)
     for cu, good in (([0, 100, 50, 60, 200, 300], [1, 0, 0, 0, 1]), ([-1, 5, 10], [0, 1]), ([0, 301], [0]), ([0, 10, 400, 20, 30], [1, 0, 0, 0]),
