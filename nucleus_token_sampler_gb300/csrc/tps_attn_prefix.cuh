@@ -96,6 +96,7 @@ template <int D, int kFormat, int kTiles, int kLine> struct PrefixShape {
         float row_factor[kLine == kTreesInTurn ? 128 : 1];
         float3 half[2][kLine == kTreesInTurn ? 128 : 1];
         int dead[4];
+        int late;  // of trees: a softmax warp gave up
         float key_unit[kScalars], value_exp[kScalars];
         int wide[kScalars];  // 1: the block's keys, 2: its values
         // Of the block's tokens: keys' scales (int8, or wide), values' in the block's unit, at most 1 (int8), or one over
@@ -232,6 +233,7 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles, kLine>::kThrea
         ctl.abort = 0;
         ctl.bad = 0;
         for (int i = 0; i < 4; ++i) ctl.dead[i] = 0;
+        ctl.late = 0;
         fence_proxy_async();
     }
     if (warp == Shape::kMmaWarp) tmem_alloc(&ctl.tmem, Shape::kTmemCols);
@@ -645,12 +647,18 @@ __global__ void __launch_bounds__(PrefixShape<D, kFormat, kTiles, kLine>::kThrea
             if (!kTree) a.ml[piece * p.tile_rows + in_tile] = make_float2(ref, !alive ? kPieceTimeout : (*(volatile int*)&ctl.bad ? kPieceBadPage : sum));
         }
         if constexpr (kTree) {
-            if (!alive)  // all that the CTA had to do
+            if (!alive) {  // all that the CTA had to do
                 for (Walk rest(a, ctl.start); rest.left > 0; rest.next(a)) {
                     tree_give_up<D>(a, rest, in_tile);
                     record.note(rest.seq, rest.head * p.n_tiles + rest.tile, rest.block, rest.block + rest.blocks(a) == rest.nblk);
                 }
-            record.timeout = !alive;
+                *(volatile int*)&ctl.late = 1;
+            }
+            // Warps give up each for itself: one may find a phase complete just as another's limit ends, so one thread speaks for
+            // all of them only once all have come to their end.
+            __syncwarp();
+            asm volatile("barrier.cta.sync.aligned 5, %0;" ::"n"(128 * kTiles) : "memory");
+            record.timeout = *(volatile int*)&ctl.late;
             if (threadIdx.x == 0) a.rec[blockIdx.x] = record;
         } else if (!alive) {  // the pieces of the items that were not reached
             for (Walk rest(a, ctl.start); rest.left > 0; rest.next(a))

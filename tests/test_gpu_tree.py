@@ -369,6 +369,34 @@ def test_a_wait_that_runs_out_reaches_the_status(fmt, lens):
     assert torch.equal(out[fine], want[fine])
 
 
+# Rows of a key head: 48 (two softmax groups take blocks in turn), 256 (two row tiles at once), 320 (three tiles of 128 in turn).
+SHAPES = [(12, 8, 2), (64, 8, 2), (64, 10, 2)]
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "int8"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("N,Hq,Hk", SHAPES)
+@pytest.mark.parametrize("lens", [[500, 70], [60000, 200], [64, 700] * 60])
+def test_a_wait_that_runs_out_reaches_every_sequence_beside_it(fmt, D, N, Hq, Hk, lens):
+    """Of the kernel on the matrix unit.  An output is NaN, and its sequence's status tells, or it is what it is without the stall."""
+    q, c, table, n, tree, _ = _case(10, lens, N, Hq, Hk, D, 16, fmt)
+    B = len(lens)
+    out, lse, st = torch.zeros_like(q), torch.zeros(B, N, Hq, device=DEV), torch.full((B,), 9, dtype=torch.int32, device=DEV)
+    a = decode._Tree(q=q.data_ptr(), out=out.data_ptr(), out_lse=lse.data_ptr(), page_table=table.data_ptr(), seq_len=n.data_ptr(), tree=tree.data_ptr(),
+                     out_status=st.data_ptr(), B=B, table_width=table.shape[1], table_ld=table.shape[1], tree_ld=N, n_nodes=N, n_q_heads=Hq, scale=D ** -0.5)
+    stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    want, want_lse = tps.tree_attention(q, c, table, n, tree, want_lse=True)
+    assert torch.isfinite(want).all()
+    assert tps.load().tps_tree_attention_stall_test(c._bytes, ctypes.byref(a), 1, 20_000_000, stream) == 0
+    torch.cuda.synchronize()
+    assert (st == 4).all() and out[:, :, Hq // 2:].isnan().all() and lse[:, :, Hq // 2:].isnan().all()
+    fine = ~out.isnan()
+    assert torch.equal(fine.all(-1), fine.any(-1)) and torch.equal(fine.all(-1), ~lse.isnan())
+    assert torch.equal(out[fine], want[fine]) and torch.equal(lse[fine.all(-1)], want_lse[fine.all(-1)])
+    again = tps.tree_attention(q, c, table, n, tree, status=st)
+    assert (st == 0).all() and torch.equal(again, want)
+
+
 def test_refusals():
     q, c, table, lens, tree, _ = _case(11, [100, 20], 4, 4, 2, 64, 16, "bf16")
     one = torch.zeros(1, dtype=torch.int32, device=DEV)
