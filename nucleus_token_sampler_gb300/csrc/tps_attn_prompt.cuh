@@ -267,10 +267,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const float neg = -__int_as_float(0x7F800000);
         const float c = fmaxf(fabsf(a.qk_scale), 0x1p-126f);  // never 0: a masked score, -inf, times it stays -inf
         uint32_t s_parity = 0, o_parity = 0;
-        int item = 0;  // of the tile
+        int item = -1;  // of the tile
         for (; walk.more(); walk.step()) {
             const int blocks = it.blocks(m);
             if (blocks == 0) continue;
+            ++item;
             const int limit = it.limit(a, m, row);
             const int most = it.limit(a, m, 127);  // of any row of the tile
             // `lost`: what rounding took from the weights that `sum` has as the product has them.
@@ -386,7 +387,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             const int in_tile = row / a.group, h = row - in_tile * a.group, token = it.token + m * a.tile_tokens + in_tile;
             const bool mine = in_tile < a.tile_tokens && h < it.heads && token < it.end;
             const bool dirty = alive && (*(volatile int*)&ctl.dirty[m][item % kDirty][0] | *(volatile int*)&ctl.dirty[m][item % kDirty][1]);
-            ++item;
             const int64_t at = (int64_t)token * a.Hq + it.head + h;
             const float inv = alive ? 1.f / sum : __int_as_float(0x7FC00000);
             uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at * D);
@@ -577,14 +577,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         // this wait nor the one for the copy can be a phase off.
         const int half = warp - kPromptHidden;
         uint32_t go_parity = 0;
-        int item[2] = {0, 0};  // of each tile
-        int64_t fill = 0;      // of the item's first key tile
+        int item0 = 0, item1 = 0;  // of each tile
+        int64_t fill = 0;          // of the item's first key tile
         for (; walk.more() && alive; walk.step()) {
             bool found = false;
             auto mark = [&](int to) {
-#pragma unroll
-                for (int m = 0; m < 2; ++m)
-                    if (it.blocks(m)) *(volatile int*)&ctl.dirty[m][item[m] % kDirty][half] = to;
+                *(volatile int*)&ctl.dirty[0][item0 % kDirty][half] = to;
+                if (it.blocks1) *(volatile int*)&ctl.dirty[1][item1 % kDirty][half] = to;
             };
             if (lane == 0) mark(0);
             for (int v = min(it.open, it.last); v < it.last && alive; ++v) {
@@ -631,8 +630,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 __syncwarp();
             }
             fill += 2 * (int64_t)it.last;
-            ++item[0];
-            if (it.blocks(1)) ++item[1];
+            ++item0, item1 += it.blocks1 > 0;
         }
     }
     tc_fence_before();
