@@ -108,16 +108,15 @@ struct TreeArgs {
 // What a CTA leaves for the join.
 struct TreeRecord {
     int open_seq, open_item;   // the item that it began and did not finish: piece 1 of its two (-1: none)
-    int continued, ended;      // its first item began in an earlier CTA: piece 0; and ends here
+    int ended;                 // its first item began in an earlier CTA (piece 0) and ends here
     int first_seq, last_seq;   // sequences that it had any part of
-    int timeout;
-    int spare;
+    int timeout;               // a wait ran out in any of its softmax warps
 #ifdef __CUDACC__
-    __device__ __forceinline__ void begin(int seq) { open_seq = -1, open_item = continued = ended = timeout = spare = 0, first_seq = last_seq = seq; }
+    __device__ __forceinline__ void begin(int seq) { open_seq = -1, open_item = ended = timeout = 0, first_seq = last_seq = seq; }
     __device__ __forceinline__ void note(int seq, int item, int block, bool end)  // a part of an item
     {
         last_seq = seq;
-        if (block > 0) continued = 1, ended = end;
+        if (block > 0) ended = end;
         if (block == 0 && !end) open_seq = seq, open_item = item;
     }
 #endif
