@@ -374,6 +374,125 @@ SHAPES = [(12, 8, 2), (64, 8, 2), (64, 10, 2)]
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "fp8", "int8"])
+@pytest.mark.parametrize("N,Hq,Hk", SHAPES)
+@pytest.mark.parametrize("more", [0, 200])  # cut over many CTAs; whole items of several sequences in each
+def test_many_rows_padding_and_masks_that_are_no_trees(fmt, N, Hq, Hk, more):
+    lens, nodes = [0, 1, N, N, 40 + N, 500, 128 + N, 129, 256], [0, 1, N, N - 1, 1, N // 2, N, 0, 3 * N // 4]
+    lens, nodes = lens + [N + i % 90 for i in range(more)], nodes + [i % (N + 1) for i in range(more)]
+    q, c, table, n, tree, k = _case(14, lens, N, Hq, Hk, 64, 32, fmt, nodes=nodes)
+    out, lse = _check((q, c, table, n, tree, k))
+    for b, m in enumerate(nodes):
+        assert (out[b, m:] == 0).all() and (lse[b, m:] == -math.inf).all()
+    full = torch.tensor([max(x, N) for x in lens], dtype=torch.int32, device=DEV)
+    q2, c2, table2, n2, _, _ = _case(15, full.tolist(), N, Hq, Hk, 128, 16, fmt)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    wild = torch.randint(-2 ** 62, 2 ** 62, tree.shape, generator=g, device=DEV)
+    wild[2, ::3], wild[3], wild[6, 1] = 0, 0, 0  # sequences 2 and 3 are all tree: those rows see nothing
+    out, lse = _check((q2, c2, table2, n2, wild, None))
+    assert (out[2, ::3] == 0).all() and (lse[3] == -math.inf).all() and torch.isfinite(lse[6, 1]).all()
+    few = k.clone()
+    few[:4] = torch.tensor([N, 0, 1, N // 3], dtype=torch.int32, device=DEV)
+    _check((q2, c2, table2, n2, wild, few), scale=-0.2)
+    _check((q2, c2, table2, n2, wild[5].contiguous(), few))
+    q2[3, N // 3:] = math.nan  # padding's queries hold anything
+    out, _ = tps.tree_attention(q2, c2, table2, n2, wild, nodes=few, want_lse=True)
+    assert torch.isfinite(out).all() and (out[3, N // 3:] == 0).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("N,Hq,Hk", SHAPES)
+def test_a_lone_token_of_a_large_tree_has_its_value_as_it_is(D, N, Hq, Hk):
+    """The rounded weight is divided by itself: on the matrix unit, too."""
+    q, c, table, _, tree, _ = _case(12, [200] * 5, N, Hq, Hk, D, 16, "bf16")
+    one = torch.ones(5, dtype=torch.int32, device=DEV)
+    out, lse = tps.tree_attention(q, c, table, one, tree, nodes=one, want_lse=True)
+    none = tps.tree_attention(q, c, table, 130 * one, tree, nodes=0 * one)
+    for b in range(5):
+        assert torch.equal(out[b, 0], c.v[table[b, 0], :, 0].repeat_interleave(Hq // Hk, 0))
+    assert (out[:, 1:] == 0).all() and (lse[:, 1:] == -math.inf).all() and (none == 0).all()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "int8"])
+@pytest.mark.parametrize("N,Hq,Hk", SHAPES)
+@pytest.mark.parametrize("lens", [[500, 64, 300, 77, 100, 90, 133, 65], [9000, 64, 3000, 77, 100, 90, 133, 65], [500, 64, 300, 77, 100, 90, 133, 65] + [70] * 300])
+def test_bad_pages_and_lengths_beside_large_trees(fmt, N, Hq, Hk, lens):
+    q, c, table, n, tree, _ = _case(7, lens, N, Hq, Hk, 128, 32, fmt)
+    B = len(lens)
+    want = _want(q, c, table, n, tree, None, 128 ** -0.5)
+    table, n = table.clone(), n.clone()
+    table[0, lens[0] // 32], table[2, 0] = c.n_pages, -1
+    table[1, -1] = 2 ** 31 - 1  # not a page of its tokens
+    n[4], n[5], n[6] = N - 1, -3, 32 * table.shape[1] + 1
+    st, rest = torch.full((B,), 9, dtype=torch.int32, device=DEV), [0] * (B - 8)
+    good = torch.tensor([1, 3, *range(7, B)], device=DEV)
+    for status in (st, None):
+        out, lse = tps.tree_attention(q, c, table, n, tree, want_lse=True, status=status)
+        plain.check(out, lse, want, BF16, good)
+        for b in (0, 2, 4, 5, 6):
+            assert out[b].isnan().all() and lse[b].isnan().all()
+    assert st.tolist() == [3, 0, 3, 0, 3, 3, 3, 0] + rest
+    k = torch.tensor([N, N + 1, 0, N, 0, 0, 0, -1] + [N] * (B - 8), dtype=torch.int32, device=DEV)
+    out, lse = tps.tree_attention(q, c, table, n, tree, nodes=k, want_lse=True, status=st)
+    assert st.tolist() == [3, 3, 3, 0, 0, 3, 3, 3] + rest
+    plain.check(out, lse, want, BF16, torch.tensor([3, *range(8, B)], device=DEV))
+    for b in (0, 1, 2, 5, 6, 7):
+        assert out[b].isnan().all() and lse[b].isnan().all()
+    assert (out[4] == 0).all()
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "int8"])
+@pytest.mark.parametrize("N,Hq,Hk", SHAPES)
+@pytest.mark.parametrize("length,more", [(64, 0), (130, 0), (900, 0), (133, 200)])
+def test_hidden_nodes_of_large_trees_hold_anything(fmt, bad, N, Hq, Hk, length, more):
+    """A node that is not seen changes no output, whatever it holds (in 8 bits beyond its roundings); one that is seen does."""
+    q, c, table, lens, tree, _ = _case(6, [length, 300] + [N + i % 50 for i in range(more)], N, Hq, Hk, 64, 16, fmt)
+    base, base_lse = tps.tree_attention(q, c, table, lens, tree, want_lse=True)
+    want = _want(q, c, table, lens, tree, None, 0.125)
+    here = [x[0] for x in want]
+    for j in (0, N // 2, N - 1):
+        at = length - N + j
+        page, row = int(table[0, at // 16]), at % 16
+        sees = (tree[0] >> j) & 1 == 1
+        hidden = ~sees
+        for t, s in ((c.k, c.k_scale), (c.v, c.v_scale)):
+            x = t if s is None else s
+            keep = x[page, :, row].clone()
+            x[page, :, row] = bad
+            out, lse = tps.tree_attention(q, c, table, lens, tree, want_lse=True)
+            x[page, :, row] = keep
+            if fmt == "bf16":
+                assert torch.equal(out[0, hidden], base[0, hidden]) and torch.equal(lse[0, hidden], base_lse[0, hidden])
+            else:
+                plain.check(out[0], lse[0], here, BF16, hidden)
+            assert torch.equal(out[1:], base[1:]) and torch.equal(lse[1:], base_lse[1:])
+            if (x is c.v or x is c.v_scale) and (fmt == "bf16" or bad != -math.inf):  # a scale below 2^-80 counts as anything up to that
+                assert (~torch.isfinite(out[0, sees])).all()
+
+
+@pytest.mark.parametrize("fmt,N", [("bf16", 24), ("fp8", 24), ("int8", 24), ("int8", 64)])
+def test_large_trees_in_a_cache_past_four_gigabytes(fmt, N):
+    H, page, D = 8, 128, 128
+    pages = 18500 if fmt == "bf16" else 37000
+    dt = tps.KVCache.FORMATS[fmt][1]
+    k, v = (torch.empty((pages, H, page, D), dtype=torch.int16 if fmt == "bf16" else torch.int8, device=DEV).view(dt) for _ in range(2))
+    ks, vs = (None if fmt == "bf16" else torch.full((pages, H, page), math.nan, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    c = tps.KVCache(k, v, ks, vs)
+    g = torch.Generator(device=DEV).manual_seed(8)
+    T, ids = 300, torch.tensor([pages - 1, 2, pages - 2000], device=DEV)
+    slots = ids[torch.arange(T, device=DEV) // page] * page + torch.arange(T, device=DEV) % page
+    x, y = (torch.randn(T, H, D, generator=g, device=DEV).bfloat16() for _ in range(2))
+    tps.kv_write(c, x, y, slots)
+    near = tps.KVCache.empty(3, H, page, D, fmt, device=DEV)
+    tps.kv_write(near, x, y, torch.arange(T, device=DEV))
+    q, tree = torch.randn(1, N, 32, D, generator=g, device=DEV).bfloat16(), _trees(g, 1, N)
+    n = torch.tensor([T], dtype=torch.int32, device=DEV)
+    a = tps.tree_attention(q, c, ids.int()[None], n, tree)
+    assert torch.isfinite(a).all()
+    assert torch.equal(a, tps.tree_attention(q, near, torch.arange(3, dtype=torch.int32, device=DEV)[None], n, tree))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "int8"])
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("N,Hq,Hk", SHAPES)
 @pytest.mark.parametrize("lens", [[500, 70], [60000, 200], [64, 700] * 60])
