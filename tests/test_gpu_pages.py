@@ -166,6 +166,57 @@ def test_no_sequences_no_tables_and_no_list():
     _run([[], []], [0, 0], [], 0, 16, [("extend", [0, 1], 3), ("trim", [0, 0])])
 
 
+@pytest.mark.parametrize("B,width,page,most", [(1024, 32, 16, 300), (700, 50, 32, 900), (64, 600, 16, 5000), (1, 40000, 16, 600000), (300, 128, 64, 6000),
+                                               (1024, 40, 16, 640)])
+def test_trims_of_wide_tables(B, width, page, most):
+    """Up to 1,024 sequences whose tables have 32,768 places or more share a cluster: no CTA may overwrite what another still reads."""
+    assert B <= 1024 and B * width >= 32768 and most <= width * page
+    rng = random.Random(B + width)
+    table, length, free, count = _state(rng, B, width, page, most, 60, entries=B * (most // page + 1) + 60)
+    keep = [rng.choice([0, n, n, rng.randint(0, n), max(0, n - 1)]) for n in length]
+    _run(table, length, free, count, page, [("trim", keep), ("trim", [rng.randint(0, k) for k in keep]), ("trim", [0] * B), ("trim", [0] * B)])
+
+
+@pytest.mark.parametrize("B,width", [(1024, 32), (40, 900)])
+def test_trims_of_wide_tables_refused(B, width):
+    """Impossible numbers, a list without room and one with room for some, in rows that are cut out of a wider table."""
+    rng = random.Random(B)
+    table, length, _, _ = _state(rng, B, width, 16, width * 16, 0)
+    pages = sum(-(-n // 16) for n in length)
+    keep = [rng.choice([0, 0, n, n // 2, n + 1, -1, -2 ** 31, 2 ** 31 - 1]) for n in length]
+    for b in rng.sample(range(B), 9):
+        length[b] = rng.choice([-1, width * 16 + 1, 2 ** 31 - 1, -2 ** 31])
+    for room in (0, 1, pages // 7, pages // 2, pages + 5):
+        for count in (0, 3, room + 9):
+            plain = Plain(table, length, [-9] * (room + 3), count, 16)
+            wide = torch.full((B, width + 6), -1, dtype=torch.int32, device=DEV)
+            t = wide[:, 5:5 + width]
+            t.copy_(_device(table))
+            s, f, c, st = _device(length), _device([-9] * (room + 3)), _device([count]), torch.full((B,), 77, dtype=torch.int32, device=DEV)
+            before = wide.clone()
+            tps.kv_trim(t, s, _device(keep), f, c, 16, status=st)
+            assert st.tolist() == plain.trim(keep)
+            assert s.tolist() == plain.length and c.tolist() == [plain.count] and f.tolist() == plain.free and torch.equal(wide, before)
+
+
+def test_trims_of_wide_tables_undo_extensions_in_graphs():
+    """A captured extension and its trim, many times over: the list stays entry for entry."""
+    rng = random.Random(5)
+    table, length, free, count = _state(rng, 512, 80, 16, 900, 9000)
+    t, s, f, c, new, keep = _device(table), _device(length), _device(free), _device([count]), _device([rng.randint(0, 90) for _ in length]), _device(length)
+    want = [x.clone() for x in (s, f, c)]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        tps.kv_extend(t, s, new, f, c, 16, int(512 * 90))
+        tps.kv_trim(t, s, keep, f, c, 16)
+    for _ in range(200):
+        g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip((s, f, c), want))
+    held = torch.arange(80, device=DEV) < ((s + 15) // 16)[:, None]
+    assert torch.equal(t[held], _device(table)[held])
+
+
 def test_strided_tables_and_given_outputs():
     wide = torch.full((3, 10), -1, dtype=torch.int32, device=DEV)
     t, s, f, c = wide[:, 2:6], _device([0, 15, 20]), _device([9, 8, 7, 6]), _device([4])
