@@ -546,7 +546,8 @@ typedef struct {
  * 128) and over each other as the tree says: one node is a decode step, a chain the verification of one draft, a
  * tree that of several at once.  All nodes and query heads of a key head share each of its keys and values.
  * Precision as tps_prefix_attention, but that the first 128 tokens' weights are summed up rounded, in a bfloat16 cache, where
- * drafted ones are among them, as in tps_prompt_attention.  Not accepted (TPS_ERR_ARG): more than 2^31 - 2^16 tokens of table_width pages, 2^31
+ * drafted ones are among them, as in tps_prompt_attention.  Scores |scale q.k| up to 10^8 (8-bit formats: 10^7) count; a row with
+ * larger ones may be NaN.  Not accepted (TPS_ERR_ARG): more than 2^31 - 2^16 tokens of table_width pages, 2^31
  * blocks of 128 tokens of all tables, key heads and tiles of 256 rows.  No result depends on another sequence's data,
  * nor (beyond a rounding, in 8-bit formats) on tokens that are hidden from it or cache rows past a
  * sequence's length, whatever they hold (an fp8 cache's NaN codes excepted, as there).
@@ -599,6 +600,7 @@ typedef struct {
  * 128): token t of a sequence sees its tokens 0 .. t.  Products are accumulated and softmax statistics held in
  * float32; the weights are rounded to bfloat16 for the second product and, of the first 128 keys of queries near a sequence's
  * beginning, for the sum (at most 2^-8 of sum p |v| and |o|; what sees one token has its value), the result once.
+ * Scores |scale q.k| up to 10^8 count; a row with larger ones may be NaN.
  * No result depends on another sequence's rows, on later tokens or on rows of no sequence, whatever they hold.
  * A call of more tiles than the device has SMs, or with out_status, draws a list of them (16 bytes for each 256 query
  * rows of a key head, and for each sequence) from the library's memory pool.

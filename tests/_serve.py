@@ -58,3 +58,32 @@ def check(got, lse, want, weights=None, where=None):
     assert torch.equal(lse > -math.inf, seen)
     assert ((lse.double() - wl)[seen].abs() <= rest[seen] + 2.0 ** -22 * wl[seen].abs()).all()
     assert (got[~seen] == 0).all()
+
+
+def great_keys(seed, n, H, D, most):
+    """Keys [n, H, D] whose components are all the same whole number, and the power of two that scores reach `most` with (a scale of 1/8)."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    k = torch.randint(128, 256, (n, H, 1), generator=g, device="cuda").bfloat16().expand(n, H, D).contiguous()
+    return k, 2.0 ** math.floor(math.log2(most / (D * 255 / 8)))
+
+
+def great_queries(q, factor):
+    """Queries whose components are all the same, of either sign."""
+    q.copy_((torch.rand(q.shape[:-1], generator=torch.Generator(device="cuda").manual_seed(2), device="cuda") < 0.5).mul(2).sub(1).mul(factor).unsqueeze(-1))
+
+
+def check_great(got, lse, want, in_exponent):
+    """Products of such queries and keys, and their sums, are exact in float32, and scores of different keys lie so far apart that all
+    weight is on the largest ones.  They share it evenly: all are 2^r of the reference with the same r, which is what rounding of
+    a score against the reference has left (2^3 at most, in base-2 units below 2^28), and a bfloat16 weight holds 2^r as well as 1.  A value is then
+    off by the weights' rounding (`check`) and its own; a logarithm by those of the scale's base-2 form, of the score and of the result:
+    at most 2^-22 of it.
+    `in_exponent`: the scales of 8-bit values go through the scores, whose float32 sum with their logarithm is rounded to a whole number, from
+    2^23 on and below 2^24.  So each of these weights may be off by 2^(1/2) either way, or (1 + d) of what it is, -0.30 < d < 0.42:
+    sum p (1 + d) v / sum p (1 + d) is off by sum p d (v - o) / sum p (1 + d), at most 0.42 / 0.70 (sum p |v| + |o|); the
+    logarithm by ln 2 / 2, less than the 2^-22 of some 10^7 that it has."""
+    out, wl, mag = want[:3]
+    u, d = 2.0 ** -8, 0.42 / 0.70 if in_exponent else 0.0
+    assert ((got.double() - out).abs() <= u * out.abs() + (1 + u) * ((u / (1 - u) + d) * (mag + out.abs()) + 2.0 ** -14 * mag)).all()
+    seen = wl > -math.inf
+    assert torch.equal(lse > -math.inf, seen) and ((lse.double() - wl)[seen].abs() <= 2.0 ** -22 * wl[seen].abs()).all()

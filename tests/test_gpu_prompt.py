@@ -75,6 +75,17 @@ def test_scores_that_rise_and_fall_along_the_keys():
     plain.check(out, lse, plain.prompt(q, k, v, zip(cu, cu[1:]), 128 ** -0.5), BF16)
 
 
+@pytest.mark.parametrize("Hq,Hk,D", [(4, 2, 64), (3, 1, 128)])
+def test_scores_of_great_magnitude(Hq, Hk, D):
+    """Scores up to 10^8 (tests/_serve.py)."""
+    cu, c = _bounds([700, 1, 130, 300])
+    q, _, v = (x.contiguous() for x in _heads(13, cu[-1], Hq, Hk, D))
+    k, factor = plain.great_keys(13, cu[-1], Hk, D, 1e8)
+    plain.great_queries(q, factor)
+    out, lse = tps.prompt_attention(q, k, v, c, scale=0.125, want_lse=True)
+    plain.check_great(out, lse, plain.prompt(q, k, v, zip(cu, cu[1:]), 0.125), False)
+
+
 @pytest.mark.parametrize("D", [64, 128])
 def test_a_lone_token_has_its_value_as_it_is(D):
     """The rounded weight is divided by itself."""

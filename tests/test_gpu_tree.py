@@ -294,6 +294,19 @@ def test_bad_pages_and_lengths_are_told_and_stay_with_their_sequence(fmt, lens):
     assert st.tolist() == [3, 3, 3, 0, 3, 3, 3, 3] and out[1].isnan().all() and out[7].isnan().all()
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "int8"])
+@pytest.mark.parametrize("N,Hq,Hk,D", [(2, 4, 2, 64), (12, 8, 2, 128), (64, 8, 2, 64), (64, 10, 2, 128)])
+def test_scores_of_great_magnitude(fmt, N, Hq, Hk, D):
+    """Scores up to 10^8, over 8-bit caches 10^7 (tests/_serve.py)."""
+    q, c, table, lens, tree, _ = _case(16, [700, 64, 130, 30000], N, Hq, Hk, D, 16, fmt, poison=False)
+    k, factor = plain.great_keys(16, c.n_pages * 16, Hk, D, 1e8 if fmt == "bf16" else 1e7)
+    v = torch.randn(c.n_pages * 16, Hk, D, generator=torch.Generator(device=DEV).manual_seed(1), device=DEV).bfloat16()
+    tps.kv_write(c, k, v, torch.arange(c.n_pages * 16, device=DEV))
+    plain.great_queries(q, factor)
+    out, lse = tps.tree_attention(q, c, table, lens, tree, scale=0.125, want_lse=True)
+    plain.check_great(out, lse, _want(q, c, table, lens, tree, None, 0.125), fmt != "bf16")
+
+
 def test_strided_tables_given_outputs_and_workspaces():
     q, c, table, lens, tree, _ = _case(8, [400, 90, 2000], 10, 8, 2, 128, 32, "fp8")
     base = tps.tree_attention(q, c, table, lens, tree)
