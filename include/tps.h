@@ -40,8 +40,9 @@
  *     (tps_prefix_attention_workspace says how much).  Its pieces take 128 KB for each SM and each 256 query
  *     rows of a key head (99 MB for 1,024 sequences of 5 tokens, 32 heads on 8): a caller whose calls need more than the
  *     pool keeps and who synchronises between them had better hand in a workspace.
- *     tps_tree_attention takes its own the same way (two pieces for each SM, 40 MB at most).  tps_prompt_attention draws a
- *     list of its tiles (a few KB), and tps_kv_extend, from 2,048 new tokens on, 8 bytes for each sequence.  No other call allocates
+ *     tps_tree_attention takes its own the same way (tps_tree_attention_workspace says how much).  tps_prompt_attention draws a
+ *     list of its tiles (16 bytes for each sequence and each 256 query rows of one key head: 0.5 MB for a million tokens with 8
+ *     query heads to a key head), and tps_kv_extend, from 2,048 new tokens on, 8 bytes for each sequence.  No other call allocates
  *     device memory;
  *   - the library never synchronises the host, keeps no state between calls beyond that pool and
  *     a per-device cache of queried limits, and may be called from several host threads at once;
@@ -545,10 +546,14 @@ typedef struct {
  * tps_tree_attention -- softmax attention of each sequence's drafted tokens over its tokens in `cache` (head_dim 64 or
  * 128) and over each other as the tree says: one node is a decode step, a chain the verification of one draft, a
  * tree that of several at once.  All nodes and query heads of a key head share each of its keys and values.
- * Precision as tps_prefix_attention, but that the first 128 tokens' weights are summed up rounded, in a bfloat16 cache, where
- * drafted ones are among them, as in tps_prompt_attention.  Scores |scale q.k| up to 10^8 (8-bit formats: 10^7) count; a row with
- * larger ones may be NaN.  Not accepted (TPS_ERR_ARG): more than 2^31 - 2^16 tokens of table_width pages, 2^31
- * blocks of 128 tokens of all tables, key heads and tiles of 256 rows.  No result depends on another sequence's data,
+ * Precision as tps_prefix_attention, but that in a bfloat16 cache the kernel for more rows (n_nodes times the query heads of a key
+ * head; always from 17 on) sums up the first 128 tokens' weights as they are rounded, where drafted ones are among them, as
+ * tps_prompt_attention does.  Scores |scale q.k| up to 10^8 (8-bit formats: 10^7) count; a row with larger ones may be NaN.
+ * Which kernel a call takes depends on its sizes and on table_width, as only the device knows the lengths: a table (or part
+ * of one, by table_ld) no wider than the longest sequence needs lets short sequences take the faster one.
+ * Not accepted (TPS_ERR_ARG): more than 2^31 - 2^16 tokens of table_width pages, 2^31
+ * blocks of 128 tokens of all tables, key heads and tiles of 128 or 256 rows.  No result depends on what another sequence's tokens hold
+ * (how many sequences there are and how long they are says where sums are cut, and so their last roundings),
  * nor (beyond a rounding, in 8-bit formats) on tokens that are hidden from it or cache rows past a
  * sequence's length, whatever they hold (an fp8 cache's NaN codes excepted, as there).
  * Returns TPS_ERR_ARG / _ALIGN / _SCRATCH (workspace too small) / _CUDA.
@@ -560,8 +565,10 @@ int tps_tree_attention(const tps_kv_cache* cache, const tps_tree* args, void* st
 int tps_tree_attention_stall_test(const tps_kv_cache* cache, const tps_tree* args, int stall_head, uint64_t wait_ns, void* stream);
 
 /* Bytes of workspace tps_tree_attention needs for these arguments on the current device (pointers are not looked
- * at), or -1 for arguments it would reject: two pieces for each SM, 40 MB at most (for some trees of up to 16 rows, n_nodes times the
- * query heads of a key head, what tps_prefix_attention needs for own tokens, from 0 to some 30 MB).  Host-only query. */
+ * at), or -1 for arguments it would reject: two pieces for each SM that has work, 268 KB an SM at most; for some trees of up to 16 rows
+ * (n_nodes times the query heads of a key head) what tps_prefix_attention needs for own tokens, from 0 to 14 MB (152 SMs).
+ * A smaller batch may need more, by another kernel: a buffer for calls of several sizes takes the largest of their answers.
+ * Host-only query. */
 int64_t tps_tree_attention_workspace(const tps_kv_cache* cache, const tps_tree* args);
 
 /*
@@ -602,8 +609,8 @@ typedef struct {
  * beginning, for the sum (at most 2^-8 of sum p |v| and |o|; what sees one token has its value), the result once.
  * Scores |scale q.k| up to 10^8 count; a row with larger ones may be NaN.
  * No result depends on another sequence's rows, on later tokens or on rows of no sequence, whatever they hold.
- * A call of more tiles than the device has SMs, or with out_status, draws a list of them (16 bytes for each 256 query
- * rows of a key head, and for each sequence) from the library's memory pool.
+ * A call that may have more tiles than the device has SMs, or with out_status, draws a list of them (16 bytes for each 256 query
+ * rows of one key head, and for each sequence) from the library's memory pool.
  * Not accepted (TPS_ERR_ARG): more than 2^31 - 2^16 tokens, or 2^31 triples of a key head, a sequence and 256 of its query rows.
  * Returns TPS_ERR_ARG / _ALIGN / _CUDA.
  */

@@ -3,11 +3,12 @@
 // (Few rows go to the kernels of tps_attn_rows.cuh, by the rule in tps_api_decode.cu.)
 //
 // Mathematics.  A sequence's last `nodes` tokens in the cache are a tree of drafted ones; node i sees the tokens before
-// them and those nodes j whose bit is set in its mask.  All (node, query head) pairs of one key head are rows of one tile of
-// 128 or 256, so that each of the sequence's keys and values is loaded, and converted, once for the whole tree.  Only the
-// blocks that hold drafted tokens are masked.
+// them and those nodes j whose bit is set in its mask.  All (node, query head) pairs of one key head are rows of tiles of
+// 128 (where they fill an odd number of those) or 256: each of the sequence's keys and values is loaded, and converted, once for each tile,
+// so once for a tree of up to 128 rows, or of 129 to 256.  The tiles are those of a full tree, whatever a sequence's own number of
+// nodes.  Only the blocks that hold drafted tokens are masked.
 //
-// Up to 128 rows: two groups of softmax warps take the item's blocks in turn, each with an output of its own, which are joined
+// Tiles of 128 rows: two groups of softmax warps take the item's blocks in turn, each with an output of its own, which are joined
 // at the item's end.  While one's softmax runs, the other's products do; with one group both would wait for each other.
 //
 // Split.  The blocks of 128 tokens of all sequences, key heads and row tiles form one line, which is cut evenly over one
@@ -18,7 +19,7 @@
 //
 // What bounds it: a bfloat16 cache's bytes (256 sequences of 500 to 4,000 tokens and trees of five, 32 heads on 8 of 128: 455 us, 5.2
 // TB/s); in 8-bit formats the softmax and the conversion of codes, which take a block of 128 tokens 2.1 us whatever the
-// number of rows up to 128 (32 sequences of 2,000 to 8,111 tokens, trees of up to 64, 40 heads on 8 of 64, int8: 377 us); for few tokens
+// number of rows of a tile of 128 (32 sequences of 2,000 to 8,111 tokens, trees of up to 64, 40 heads on 8 of 64, int8: 377 us); for few tokens
 // the launch, a chain of dependent loads (lengths, page, tokens) and the join (8 nodes on 1,000 tokens: 15.6 us; 8 trees of 16 on up to
 // 4,093 in fp8: 40 us).  One group of softmax warps instead of two in turn: 20.9 and 50 us for the last two, 424 for the int8 case.
 #pragma once

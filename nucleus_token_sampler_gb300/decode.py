@@ -315,8 +315,9 @@ def tree_attention(q, cache: KVCache, page_table, seq_len, tree, *, nodes=None, 
     ``scale``: of q.k, by default D ** -0.5.  Returns the bfloat16 output of q's shape, or (output, log-sum-exp [B, N, Hq]
     float32) with ``want_lse``.  ``status``: an int32 [B] tensor that gets 3 for a sequence with a page outside the cache or
     impossible lengths (its outputs are NaN), 4 where a wait on the GPU ran out beside it (outputs it concerns are NaN), else 0.
-    ``workspace``: a uint8 tensor of at least ``tree_attention_workspace(...)`` bytes to use instead of the library's
-    memory pool."""
+    ``out`` must not overlap the inputs.  ``workspace``: a uint8 tensor of at least ``tree_attention_workspace(...)`` bytes to
+    use instead of the library's memory pool.  The kernel is chosen by the table's width, as only the GPU knows the lengths: a
+    table as wide as a long limit is best cut (``page_table[:, :n]``) to what the longest sequence of the batch may need."""
     c = _cache(cache)
     ops = _ops or _torch_ops()
     if stream is not None:
@@ -326,7 +327,8 @@ def tree_attention(q, cache: KVCache, page_table, seq_len, tree, *, nodes=None, 
 
 
 def tree_attention_workspace(q_shape, cache: KVCache, table_width: int) -> int:
-    """Bytes of workspace ``tree_attention`` needs for a query of this shape."""
+    """Bytes of workspace ``tree_attention`` needs for a query of this shape and a table of this width.  A smaller batch may
+    need more, by another kernel: for calls of several sizes take the largest."""
     from . import load
     B, N, Hq = q_shape[:3]
     t = _Tree(B=B, table_width=table_width, table_ld=table_width, n_nodes=N, n_q_heads=Hq, scale=1.0)
@@ -344,7 +346,7 @@ def prompt_attention(q, k, v, cu_seqlens, *, scale=None, want_lse: bool = False,
     ``q``: [T, Hq, D], ``k``, ``v``: [T, Hk, D] bfloat16 CUDA tensors, D 64 or 128, Hq a multiple of Hk (query head i
     reads key head i // (Hq // Hk)); token and head strides are free in steps of 8 elements, so all three may be cut
     out of one projection.  ``scale``: of q.k, by default D ** -0.5.  Returns the bfloat16 output [T, Hq, D], or (output,
-    log-sum-exp [T, Hq] float32) with ``want_lse``; ``out`` is written to if given.  Rows of no sequence are not written (in
+    log-sum-exp [T, Hq] float32) with ``want_lse``; ``out`` is written to if given (it must not overlap the inputs).  Rows of no sequence are not written (in
     new tensors they hold anything).  ``status``: an int32 [B] tensor that gets 3 for a sequence whose bounds are
     not in order (nothing of it is written), 4 where a wait on the GPU ran out (outputs it concerns are NaN), else 0."""
     ops = _ops or _torch_ops()
