@@ -524,7 +524,8 @@ int tps_kv_trim(const tps_kv_pages* pages, void* stream);
  *                TPS_ROW_TIMEOUT where a wait ran out (one second) beside any of the sequence's work (the
  *                outputs that it kept from being computed are NaN), else TPS_ROW_OK.
  *   workspace    device memory of tps_tree_attention_workspace bytes, 256-byte aligned, or NULL: taken from the
- *                library's stream-ordered pool and returned on the call's stream.
+ *                library's stream-ordered pool and returned on the call's stream.  Calls, or graphs, that may run at the
+ *                same time need one each.
  */
 typedef struct {
     const void* q;

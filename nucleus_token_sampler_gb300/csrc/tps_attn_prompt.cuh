@@ -48,9 +48,9 @@
 namespace tps {
 
 constexpr int kPromptThreads = 384, kPromptMma = 8, kPromptLoad = 9, kPromptHidden = 10;
-// Items of each tile whose marks are kept.  No product comes before the softmax of its tile's last item has ended, and the loads run at most
-// a ring of tiles ahead of the products: six items, counted for each tile by itself (prompts that fit one tile give tile 1 nothing to do,
-// and any number of them may go by while its softmax warps still have an output to write).
+// Items of each tile whose marks are kept.  An item's weights come after the output of the tile's item before, the second product waits
+// for them, and the loads run at most a ring of tiles ahead of it: six items, counted for each tile by itself (prompts that fit one
+// tile give tile 1 nothing to do, and any number of them may go by while its softmax warps still have an output to write).
 constexpr int kDirty = 8;
 constexpr uint64_t kLong = 64;   // waits for what may come after the whole of a long sequence, in limits of the others
 

@@ -316,7 +316,7 @@ def tree_attention(q, cache: KVCache, page_table, seq_len, tree, *, nodes=None, 
     float32) with ``want_lse``.  ``status``: an int32 [B] tensor that gets 3 for a sequence with a page outside the cache or
     impossible lengths (its outputs are NaN), 4 where a wait on the GPU ran out beside it (outputs it concerns are NaN), else 0.
     ``out`` must not overlap the inputs.  ``workspace``: a uint8 tensor of at least ``tree_attention_workspace(...)`` bytes to
-    use instead of the library's memory pool.  The kernel is chosen by the table's width, as only the GPU knows the lengths: a
+    use instead of the library's memory pool (calls, or graphs, that may run at the same time need one each).  The kernel is chosen by the table's width, as only the GPU knows the lengths: a
     table as wide as a long limit is best cut (``page_table[:, :n]``) to what the longest sequence of the batch may need."""
     c = _cache(cache)
     ops = _ops or _torch_ops()
